@@ -76,10 +76,13 @@ typedef enum convrot_status {
                                   (convrot_linear_noalloc) */
 } convrot_status;
 
-/* Element type of the floating-point activation input X. */
+/* Element type of a floating-point array. The convrot_pack*, convrot_linear*
+ * and convrot_mlp* inputs take the first two; the block norms and the fp8_*
+ * entry points take all three, for inputs and outputs. */
 typedef enum convrot_dtype {
   CONVROT_F32 = 0, /* IEEE binary32 */
-  CONVROT_F16 = 1  /* IEEE binary16 (converted exactly to fp32 on load) */
+  CONVROT_F16 = 1, /* IEEE binary16 (converted exactly to fp32 on load) */
+  CONVROT_BF16 = 2 /* bfloat16 (converted exactly to fp32 on load) */
 } convrot_dtype;
 
 /* Activation applied to a linear's output (convrot_mlp). */
@@ -513,6 +516,155 @@ int convrot_linear_swiglu(const void* X, int x_dtype, int64_t M, int64_t K, int 
                           const convrot_weight* gate_up, void* workspace, size_t workspace_bytes,
                           void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Block norms
+ * ---------------------------------------------------------------------------
+ */
+
+/* Longest row (K) of convrot_block_norm. */
+#define CONVROT_NORM_MAX_K 32768
+
+typedef enum convrot_norm {
+  CONVROT_NORM_NONE = 0, /* x */
+  CONVROT_NORM_RMS = 1,  /* x / sqrt(mean_k(x^2) + eps) */
+  CONVROT_NORM_LAYER = 2 /* (x - mean_k(x)) / sqrt(mean_k((x - mean)^2) + eps) */
+} convrot_norm;
+
+/*
+ * Arguments of convrot_block_norm. For row m of sample s:
+ *   v  = block_scale * (post(y) * post_weight + post_bias)
+ *   h' = residual_scale * h + gate[s] * v
+ *   u  = pre(h') * pre_weight + pre_bias
+ *   u  = u + u * scale[s] + shift[s]
+ * with absent vectors skipped (weights and gate 1, biases and shift 0). The
+ * arithmetic is fp32; h' and u are each rounded once, when they are stored,
+ * and u is formed from the unrounded h'.
+ * Every matrix is row-major with K contiguous; ld* is the distance between
+ * its rows in elements (>= K).
+ */
+typedef struct convrot_block_norm_args {
+  int64_t M, K;          /* rows, features; K <= CONVROT_NORM_MAX_K */
+  int dtype;             /* of H, Y and H_out (convrot_dtype) */
+  int u_dtype;           /* of U */
+  const void* H;         /* [M,K] residual stream */
+  const void* Y;         /* [M,K] block output, or NULL: h' = residual_scale * h */
+  int64_t ldh, ldy;
+  float residual_scale, block_scale;
+  int post_norm, pre_norm; /* convrot_norm */
+  float post_eps, pre_eps; /* >= 0, added under the square root */
+  const float* post_weight; /* [K] or NULL */
+  const float* post_bias;   /* [K] or NULL */
+  const float* pre_weight;  /* [K] or NULL */
+  const float* pre_bias;    /* [K] or NULL */
+  const float* gate;        /* [n_samples,K], rows ld_gate apart, or NULL */
+  const float* scale;       /* [n_samples,K], rows ld_mod apart, or NULL */
+  const float* shift;       /* [n_samples,K], rows ld_mod apart, or NULL */
+  int64_t ld_gate, ld_mod;
+  int64_t n_samples;        /* >= 1 where gate, scale or shift is given */
+  const int32_t* row_sample; /* [M] a row's sample, or NULL: m / rows_per_sample */
+  int64_t rows_per_sample;   /* without row_sample: > 0, or 0 for one sample */
+  void* H_out;           /* [M,K] h', or NULL; may be H itself (in place) */
+  void* U;               /* [M,K] u, or NULL */
+  int64_t ldho, ldu;
+  uint8_t* Q;            /* [M,K] e4m3 codes of u (dense), or NULL */
+  float* s;              /* [M, ceil(K/128)] their scales; with Q */
+} convrot_block_norm_args;
+
+/*
+ * convrot_block_norm -- the norms before and after a transformer block, its
+ * gate and its residual in one pass: see convrot_block_norm_args. u goes to U,
+ * or quantized (as by fp8_pack_activations, from the fp32 u) to Q and s, where
+ * an fp8_linear_packed reads it; U and Q are not given together, and H_out may
+ * be left out. One of H_out, U and Q is required. M = 0 is a no-op.
+ * Rows whose arrays all start on 16-byte boundaries, with ld a multiple of 16
+ * bytes and K a multiple of 8, take the fast path; any others are accepted.
+ * The sums of a row are taken in a fixed order: results repeat bit for bit.
+ * A row_sample outside [0, n_samples) is treated as gate 0 without modulation
+ * and reported by convrot_device_status as CONVROT_ERR_ARG.
+ * Errors: ERR_ARG (also a sample count that rows_per_sample overruns),
+ *         ERR_ALIGN (an array not aligned to its elements; Q: K % 16, Q not
+ *         16-byte aligned), ERR_ALIAS (an output overlaps an input or an
+ *         output, but for H_out = H with the same ld), ERR_UNSUPPORTED,
+ *         ERR_DEVICE, ERR_CUDA.
+ */
+int convrot_block_norm(const convrot_block_norm_args* args, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * 8-bit floating-point linears with a scale per block of 128
+ * ---------------------------------------------------------------------------
+ * Codes are e4m3 (4 exponent bits, 3 mantissa bits, largest value 448, no
+ * infinities), K contiguous. An activation has one fp32 scale per row and 128
+ * features, a weight one per 128 output x 128 input features:
+ *   s = max|x| / 448 over the block (IEEE fp32 division),
+ *   q = e4m3(x / s) (IEEE fp32 quotient, then round to nearest even),
+ * an all-zero block has scale 0 and codes 0. A block with an infinity or a
+ * NaN gets a scale that is one, so that every product it enters is NaN or
+ * infinite. K is a multiple of 16; the last block of a row may be shorter.
+ */
+
+/* Features (and weight rows) per scale. */
+#define CONVROT_FP8_BLOCK 128
+
+/*
+ * fp8_pack_activations -- X [M,K] (rows ldx elements apart) to codes Q_x [M,K]
+ * (dense) and scales s_x [M, ceil(K/128)]. X may have any alignment and ldx
+ * that suit its elements; 16-byte aligned rows are read fastest.
+ * Errors: ERR_ARG, ERR_ALIGN (K % 16, Q_x not 16-byte aligned, X or s_x not
+ *         aligned to its elements), ERR_ALIAS, ERR_UNSUPPORTED (more than
+ *         2^31 - 1 scales), ERR_DEVICE, ERR_CUDA.
+ */
+int fp8_pack_activations(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* Q_x,
+                         float* s_x, void* stream);
+
+/*
+ * fp8_prepare_weight -- offline: W [N,K] (dense) to codes Q_w [N,K] and scales
+ * s_w [ceil(N/128), ceil(K/128)].
+ * Errors: as fp8_pack_activations.
+ */
+int fp8_prepare_weight(const void* W, int w_dtype, int64_t N, int64_t K, uint8_t* Q_w, float* s_w,
+                       void* stream);
+
+/* One linear of an fp8_linear call. */
+typedef struct convrot_fp8_weight {
+  const uint8_t* q;   /* [N,K] e4m3 codes (fp8_prepare_weight) */
+  const float* scale; /* [ceil(N/128), ceil(K/128)] */
+  const float* bias;  /* [N] fp32, or NULL */
+  int64_t N;          /* output features */
+  void* Y;            /* [M,N] output of the call's y_dtype */
+  int64_t ldy;        /* distance between rows of Y in elements (>= N) */
+} convrot_fp8_weight;
+
+/* Device bytes fp8_linear needs: the packed activation. 0 for invalid sizes. */
+size_t fp8_linear_workspace_size(int64_t M, int64_t K);
+
+/*
+ * fp8_linear_packed -- for every linear j
+ *   Y_j[m,n] = sum_b s_x[m,b] s_wj[n/128,b] (sum_{k in block b} q_x[m,k] q_wj[n,k]) + bias_j[n],
+ * the inner sums on the tensor cores in fp32, the outer ones in fp32, one
+ * rounding to y_dtype at the end. One launch for all linears. Results repeat
+ * bit for bit. The N_j, ldy and the alignment of Y_j are free (a row pitch of
+ * Y that is a multiple of 16 bytes is stored fastest).
+ *   weights  host array of n_weights descriptors (1 <= n_weights <=
+ *            CONVROT_MAX_LINEARS); a linear with N = 0 is skipped.
+ * Errors: ERR_ARG, ERR_ALIGN (K % 16, codes not 16-byte aligned, other arrays
+ *         not aligned to their elements), ERR_ALIAS, ERR_UNSUPPORTED,
+ *         ERR_DEVICE, ERR_CUDA; ERR_TIMEOUT from convrot_device_status.
+ */
+int fp8_linear_packed(const uint8_t* Q_x, const float* s_x, int64_t M, int64_t K,
+                      const convrot_fp8_weight* weights, int n_weights, int y_dtype, void* stream);
+
+/*
+ * fp8_linear -- fp8_pack_activations of X into the workspace, then
+ * fp8_linear_packed.
+ *   workspace  at least fp8_linear_workspace_size(M, K) bytes, 16-byte aligned.
+ * Errors: those of both, and ERR_WORKSPACE.
+ */
+int fp8_linear(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx,
+               const convrot_fp8_weight* weights, int n_weights, int y_dtype, void* workspace,
+               size_t workspace_bytes, void* stream);
+
 /* Size of the fixed device array that convrot_linear_noalloc uses (32 MiB). */
 #define CONVROT_NOALLOC_SCRATCH_BYTES (32u << 20)
 
@@ -587,7 +739,8 @@ int convrot_test_unscale_sweep(const float* divisors, int n_divisors, int y_exp,
  * convrot_device_status -- synchronizes `stream`, then returns and clears the
  * device's sticky error word: CONVROT_OK, or CONVROT_ERR_TIMEOUT when a
  * kernel's bounded wait on a TMA or tensor-core completion barrier gave up
- * (the kernel then skipped its remaining work and released its resources).
+ * (the kernel then skipped its remaining work and released its resources), or
+ * CONVROT_ERR_ARG when convrot_block_norm met a row_sample out of range.
  */
 int convrot_device_status(void* stream);
 

@@ -58,6 +58,10 @@ bool device_is_sm103() {
 int read_and_clear_device_error(cudaStream_t stream);  // gemm.cu: syncs, then the GEMM's word
 int read_and_clear_w4_error();                         // gemm_w4.cu: the S8 x S4 GEMM's word
 int read_and_clear_pack_error();                       // pack.cu: the pack kernels' word
+namespace fp8 {
+int read_and_clear_fp8_error();                        // fp8_gemm.cu: the block-scaled GEMM's word
+int read_and_clear_norm_error();                       // block_norm.cu: the block norms' word
+}  // namespace fp8
 
 }  // namespace convrot
 
@@ -560,7 +564,11 @@ int convrot_device_status(void* stream) {
   const int gemm_st = read_and_clear_device_error(static_cast<cudaStream_t>(stream));
   const int w4_st = read_and_clear_w4_error();
   const int pack_st = read_and_clear_pack_error();
-  return gemm_st != CONVROT_OK ? gemm_st : (w4_st != CONVROT_OK ? w4_st : pack_st);
+  const int fp8_st = fp8::read_and_clear_fp8_error();
+  const int norm_st = fp8::read_and_clear_norm_error();
+  for (int st : {gemm_st, w4_st, pack_st, fp8_st})
+    if (st != CONVROT_OK) return st;
+  return norm_st;
 }
 
 size_t int8_gemm_s32_w4_workspace_size(int64_t M, int64_t K) {

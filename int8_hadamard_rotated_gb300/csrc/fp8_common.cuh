@@ -1,0 +1,192 @@
+// fp8_common.cuh -- helpers shared by the block norms (block_norm.cu), the
+// 8-bit floating-point pack (fp8_pack.cu) and the block-scaled GEMM
+// (fp8_gemm.cu): element conversion, the e4m3 block quantizer, bulk loads and
+// the host-side launchers.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace convrot {
+namespace fp8 {
+
+constexpr int QBLOCK = CONVROT_FP8_BLOCK;  // features that share one scale (128)
+constexpr float kE4M3Max = 448.0f;
+
+// ---------------------------------------------------------------------------
+// element types
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Two values as the bits of two consecutive 16-bit elements (round to nearest
+// even; a's at the lower address).
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+template <typename T> __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b);
+template <> __device__ __forceinline__ void unpack2<__half>(uint32_t w, float& a, float& b) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  a = f.x;
+  b = f.y;
+}
+template <> __device__ __forceinline__ void unpack2<__nv_bfloat16>(uint32_t w, float& a, float& b) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+
+// Eight consecutive elements at a 16-byte aligned address (global or shared).
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  unpack2<T>(v.x, x[0], x[1]);
+  unpack2<T>(v.y, x[2], x[3]);
+  unpack2<T>(v.z, x[4], x[5]);
+  unpack2<T>(v.w, x[6], x[7]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]),
+                                            pack2<T>(x[6], x[7]));
+}
+
+// ---------------------------------------------------------------------------
+// the e4m3 block quantizer
+// ---------------------------------------------------------------------------
+
+// The larger of two values; NaN if either is one, so that a block that holds
+// a NaN gets a NaN scale instead of a finite one that hides it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The codes of two values (a's in the low byte): round to nearest even,
+// saturating at +-448; NaN becomes the NaN code.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float e4m3_scale(float amax) { return __fdiv_rn(amax, kE4M3Max); }
+
+// Codes of NE values (NE % 4 == 0) with the scale s of their block: e4m3 of
+// the IEEE quotient RN(x / s), and 0 where s is 0.
+//
+// No division per element: with r = RN(1 / s), the products x r (1 -+ 2^-21)
+// enclose RN(x / s) (r, the two factors and the products are each off by at
+// most 2^-24 relative, together less than 2^-21), and rounding is monotone,
+// so where both products have the same code that code is the quotient's. The
+// rare others (a quotient within 2^-21 of a rounding border), and scales
+// whose reciprocal leaves the normal range, take the division. Two packed
+// multiplications and two conversions per two elements.
+template <int NE>
+__device__ __forceinline__ void e4m3_codes(const float (&x)[NE], float s, uint32_t (&out)[NE / 4]) {
+  if (s >= 0x1p-120f) {
+    const float r = __frcp_rn(s);
+    const float lo = r * (1.0f - 0x1p-21f), hi = r * (1.0f + 0x1p-21f);
+    const unsigned long long lo2 = f32x2_pack(lo, lo), hi2 = f32x2_pack(hi, hi);
+    uint32_t differ = 0;
+#pragma unroll
+    for (int i = 0; i < NE / 4; ++i) {
+      uint32_t w[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const unsigned long long p0 = f32x2_pack(x[4 * i], x[4 * i + 1]), p1 = f32x2_pack(x[4 * i + 2], x[4 * i + 3]);
+        float a, b, c, d;
+        f32x2_unpack(f32x2_mul(p0, k ? hi2 : lo2), a, b);
+        f32x2_unpack(f32x2_mul(p1, k ? hi2 : lo2), c, d);
+        w[k] = e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+      }
+      out[i] = w[0];
+      differ |= w[0] ^ w[1];
+    }
+    if (differ == 0) return;
+  }
+#pragma unroll
+  for (int i = 0; i < NE / 4; ++i) {
+    float q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q[k] = (s == 0.0f) ? 0.0f : __fdiv_rn(x[4 * i + k], s);
+    out[i] = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// untiled bulk loads
+// ---------------------------------------------------------------------------
+
+// Global -> shared, 16-byte aligned on both sides, bytes % 16 == 0, counted
+// on `bar`.
+__device__ __forceinline__ void bulk_load(void* sdst, const void* gsrc, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(sdst)), "l"(gsrc), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+inline size_t dtype_size(int dtype) { return dtype == CONVROT_F32 ? 4 : 2; }
+inline bool known_dtype(int dtype) { return dtype == CONVROT_F32 || dtype == CONVROT_F16 || dtype == CONVROT_BF16; }
+inline int64_t n_blocks(int64_t n) { return (n + QBLOCK - 1) / QBLOCK; }
+
+// A launch that may set itself up while the kernel before it in the stream
+// ends (every kernel here waits for that one before it touches global memory).
+struct Launch {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  Launch(unsigned grid, unsigned block, size_t smem, cudaStream_t stream, unsigned cluster = 1) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+  }
+};
+
+// fp8_pack.cu
+int launch_fp8_pack(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* Q, float* s,
+                    cudaStream_t stream);
+int launch_fp8_weight(const void* W, int w_dtype, int64_t N, int64_t K, uint8_t* Q, float* s, cudaStream_t stream);
+
+// block_norm.cu: arguments already checked; M > 0.
+int launch_block_norm(const convrot_block_norm_args& a, cudaStream_t stream);
+
+// fp8_gemm.cu: every linear has N > 0; M > 0.
+int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
+                    int n_weights, int y_dtype, cudaStream_t stream);
+
+}  // namespace fp8
+}  // namespace convrot

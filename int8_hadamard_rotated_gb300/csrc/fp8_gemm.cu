@@ -1,0 +1,863 @@
+// fp8_gemm.cu -- the block-scaled 8-bit floating-point GEMM on the sm_103a
+// tensor cores (tcgen05 kind::f8f6f4 + TMA + TMEM).
+//
+//   Y[m,n] = sum_b s_x[m,b] s_w[n/128,b] P_b[m,n] + bias[n],
+//   P_b[m,n] = sum of q_x[m,k] q_w[n,k] over the 128 features k of block b.
+//
+// The tensor cores sum one block, P_b, in an fp32 TMEM accumulator (the
+// instruction has no room for a factor per block); the epilogue warps read
+// it, multiply it by the two scales and add it to fp32 registers, which stay
+// for the whole tile. So every block costs the MMA a commit and the epilogue
+// one TMEM read and one multiply-add per output, and two or more accumulators
+// alternate so that the MMA of a block overlaps the reading of the one before.
+//
+// Both operands are K-major rows of e4m3 codes; one block of K is one 128-byte
+// swizzled row per operand row, so a pipeline stage is exactly one block. K
+// past the end is filled with zero codes by the tensor maps.
+#include "fp8_common.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+namespace convrot {
+namespace fp8 {
+
+// Sticky device error word of these kernels (timeouts of bounded waits).
+__device__ int g_fp8_error = 0;
+
+namespace {
+
+constexpr int MAX_LIN = CONVROT_MAX_LINEARS;
+constexpr int BK = QBLOCK;      // K per stage: 128 codes = 128 bytes
+constexpr int UMMA_K = 32;      // K of one kind::f8f6f4 MMA
+constexpr int LANES = 128;      // TMEM lanes: rows of the MMA's first operand per CTA
+
+struct GemmParams {
+  CUtensorMap tmap_x;             // codes [M,K]
+  CUtensorMap tmap_w[MAX_LIN];    // codes [N_j,K]
+  CUtensorMap tmap_y[MAX_LIN];    // Y_j [M,N_j], where tma_y
+  const float* s_x;               // [M,KB]
+  const float* s_w[MAX_LIN];      // [ceil(N_j/128),KB]
+  const float* bias[MAX_LIN];
+  void* out[MAX_LIN];
+  int64_t ldy[MAX_LIN];
+  int N[MAX_LIN];
+  int tile_start[MAX_LIN + 1];    // prefix sums of column tiles per linear
+  int M, KB;
+  int n_mtiles, n_lin, total_tiles;
+  int raster_mtiles;              // row tiles per raster group
+  int split;                      // CTAs (one cluster) that share a tile's K
+  bool tma_y;                     // every Y_j can be stored through its tensor map
+  bool vec_scales;                // the scales of a row can be read four at a time
+};
+
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (format 0, K-major),
+// fp32 D.
+//   bits 4-5 D format (1 = f32)   bits 7-9 A format   bits 10-12 B format
+//   bits 17-22 N >> 3             bits 24-28 M >> 4
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// The MMAs of one block of K on the operand tiles at `sa` and `sb`.
+template <int CG>
+__device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t sa, uint32_t sb, uint32_t idesc) {
+  const uint64_t a = smem_desc_sw128(sa), b = smem_desc_sw128(sb);
+#pragma unroll
+  for (int k = 0; k < BK / UMMA_K; ++k) {
+    const uint64_t off = static_cast<uint64_t>((k * UMMA_K) >> 4);
+    mma_f8<CG>(d_tmem, a + off, b + off, idesc, k > 0 ? 1u : 0u);
+  }
+}
+
+// 16 columns of the warp's 32 lanes, and the wait that hands them over (the
+// registers pass through the wait, so no use can be moved before it).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :: "memory");
+}
+__device__ __forceinline__ unsigned long long pair_bits(uint32_t a, uint32_t b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Four block scales of one row, from block kb on (0 past the last one).
+__device__ __forceinline__ void load_scales(const float* row, int kb, int KB, bool vec, float (&v)[4]) {
+  if (vec) {
+    const float4 t = __ldg(reinterpret_cast<const float4*>(row + kb));
+    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = kb + i < KB ? __ldg(row + kb + i) : 0.0f;
+  }
+}
+
+// 16 bytes of consecutive outputs, each rounded once.
+template <typename TY, int E>
+__device__ __forceinline__ uint4 pack16(const float (&v)[E]) {
+  static_assert(E * sizeof(TY) == 16, "sixteen bytes");
+  if constexpr (E == 4)
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  else
+    return make_uint4(pack2<TY>(v[0], v[1]), pack2<TY>(v[2], v[3]), pack2<TY>(v[4], v[5]), pack2<TY>(v[6], v[7]));
+}
+// Four consecutive outputs, each rounded once, at an address aligned to them.
+template <typename TY>
+__device__ __forceinline__ void store4(TY* p, const float (&v)[4]) {
+  if constexpr (sizeof(TY) == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<TY>(v[0], v[1]), pack2<TY>(v[2], v[3]));
+}
+
+struct Tile {
+  int lin, nt, mt;
+};
+// Tiles are taken in groups of raster_mtiles row tiles, and inside a group
+// column tile by column tile, so that the group's activation codes stay in L2
+// while the weights stream through.
+__device__ __forceinline__ Tile decode(const GemmParams& p, int t) {
+  const int n_cols = p.tile_start[p.n_lin];
+  const int per_group = p.raster_mtiles * n_cols;
+  const int g = t / per_group, idx = t - g * per_group;
+  const int gm = min(p.raster_mtiles, p.n_mtiles - g * p.raster_mtiles);
+  const int col = idx / gm;
+  Tile c;
+  c.mt = g * p.raster_mtiles + (idx - col * gm);
+  c.lin = 0;
+#pragma unroll 1
+  while (c.lin + 1 < p.n_lin && col >= p.tile_start[c.lin + 1]) ++c.lin;
+  c.nt = col - p.tile_start[c.lin];
+  return c;
+}
+
+// ---------------------------------------------------------------------------
+// many rows: CTA pairs, activation rows on the TMEM lanes
+// ---------------------------------------------------------------------------
+//
+// Persistent clusters of two CTAs; a tile is 256 activation rows x BN output
+// features, M = 256 MMAs issued by the even CTA, each CTA holding its 128 rows
+// x BN features. Activations take the lanes because a lane's row scale is then
+// one register, and the 128 features of a warp's half tile share one weight
+// scale: the promotion of a block is a single packed multiply-add per two
+// outputs with one factor. Twelve warps: 0-7 promote and store (quarter = warp
+// & 3 of the lanes, half = warp >> 2 of the features), 8 loads, 9 issues MMAs,
+// 10 and 11 only complete the control warpgroup.
+// Y leaves per warp through its own 4 KB of shared memory, 32 rows x 128
+// bytes at a time in the 128-byte swizzle (no barrier between warps), by
+// tensor-map stores where the rows of Y are 16-byte aligned, else by
+// coalesced element stores.
+
+constexpr int EPI_WARPS = 8;
+constexpr int PAIR_THREADS = (EPI_WARPS + 4) * 32;  // three warpgroups
+// Registers: 168 a thread at launch; the control warpgroup gives up what the
+// two epilogue warpgroups, which hold 128 accumulators a thread, take.
+constexpr int LAUNCH_REGS = 168, CONTROL_REGS = 56, EPI_REGS = 224;
+static_assert(2 * EPI_REGS + CONTROL_REGS <= 3 * LAUNCH_REGS, "within what the block was launched with");
+constexpr int STORE_BYTES = 32 * 128;  // one warp's store buffer
+
+template <int BN>
+struct PairGeom {
+  static constexpr int X_BYTES = LANES * BK;
+  static constexpr int W_BYTES = BN / 2 * BK;
+  static constexpr int STAGE_BYTES = X_BYTES + W_BYTES;
+  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int BUFS = 512 / BN;  // TMEM accumulators
+  static constexpr uint32_t IDESC = idesc_e4m3_f32(256, BN);
+  static constexpr int SMEM_OUT = STAGES * STAGE_BYTES;
+  static constexpr int SMEM_BARS = SMEM_OUT + EPI_WARPS * STORE_BYTES;
+  static constexpr int SMEM_ALLOC = SMEM_BARS + (2 * STAGES + 2 * BUFS + 1) * 8 + 16 + 1024;
+};
+static_assert(PairGeom<256>::SMEM_ALLOC <= 227 * 1024 && PairGeom<128>::SMEM_ALLOC <= 227 * 1024, "shared memory");
+
+template <typename TY, int BN>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+fp8_pair_kernel(const __grid_constant__ GemmParams p) {
+  using G = PairGeom<BN>;
+  constexpr int COLS = BN / 2;  // features per epilogue thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::SMEM_BARS);
+  uint64_t* empty = full + G::STAGES;
+  uint64_t* tfull = empty + G::STAGES;
+  uint64_t* tempty = tfull + G::BUFS;
+  uint64_t* drain = tempty + G::BUFS;
+  uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int unit = static_cast<int>(cluster_id_x()), n_units = static_cast<int>(cluster_count_x());
+  int* err = &g_fp8_error;
+
+  if (threadIdx.x == EPI_WARPS * 32) {
+    for (int s = 0; s < G::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < G::BUFS; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], EPI_WARPS * 2);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&p.tmap_x);
+    for (int j = 0; j < p.n_lin; ++j) tma_prefetch_desc(&p.tmap_w[j]);
+  }
+  if (warp == EPI_WARPS + 1) {
+    tmem_alloc_pair(tmem_base_smem, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_base_smem;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+
+  if (warp >= EPI_WARPS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONTROL_REGS));
+    if (warp == EPI_WARPS && lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+      uint32_t stage = 0, phase = 0, n_issued = 0;
+      bool ok = true;
+      for (int t = unit; ok && t < p.total_tiles; t += n_units) {
+        const Tile c = decode(p, t);
+        const int w_row = c.nt * BN + static_cast<int>(rank) * (BN / 2);
+        const int x_row = c.mt * 256 + static_cast<int>(rank) * LANES;
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
+          uint8_t* sx = smem + stage * G::STAGE_BYTES;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * G::STAGE_BYTES);
+          const uint32_t fb = full_leader + stage * 8u;
+          tma_load_2d_pair(sx, &p.tmap_x, fb, kb * BK, x_row, pol);
+          tma_load_2d_pair(sx + G::X_BYTES, &p.tmap_w[c.lin], fb, kb * BK, w_row, pol);
+          ++n_issued;
+          if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // no copy may land after the CTAs exit
+      if (rank == 0)
+        for (uint32_t s = 0; s < G::STAGES; ++s)
+          if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err);
+    }
+    if (warp == EPI_WARPS + 1 && lane == 0 && rank == 0) {
+      uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
+      bool ok = true;
+      for (int t = unit; ok && t < p.total_tiles; t += n_units) {
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err) ||
+              !mbar_wait(&full[stage], phase, abort_flag, err)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sx = smem_u32(smem + stage * G::STAGE_BYTES);
+          mma_block<2>(tmem_base + buf * BN, sx, sx + G::X_BYTES, G::IDESC);
+          mma_commit_pair(&empty[stage], 0x3u);
+          mma_commit_pair(&tfull[buf], 0x3u);
+          if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
+          if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
+        }
+      }
+      // all issued MMAs complete before TMEM is released
+      mma_commit_pair(drain, 0x1u);
+      mbar_wait(drain, 0, nullptr, err);
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + half * COLS;
+    const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
+    uint8_t* sout = smem + G::SMEM_OUT + warp * STORE_BYTES;
+    uint32_t buf = 0, bphase = 0;
+    bool ok = true;
+    for (int t = unit; ok && t < p.total_tiles; t += n_units) {
+      const Tile c = decode(p, t);
+      const int N = p.N[c.lin];
+      const int r0 = c.mt * 256 + static_cast<int>(rank) * LANES + 32 * quarter;  // the warp's first row
+      const int n0 = c.nt * BN + half * COLS;                                     // and first feature
+      // rows and features past the end read the last one's scales; their
+      // outputs are not stored
+      const float* xs = p.s_x + static_cast<int64_t>(min(r0 + lane, p.M - 1)) * p.KB;
+      const float* ws = p.s_w[c.lin] + static_cast<int64_t>(min(n0, N - 1) / QBLOCK) * p.KB;
+      unsigned long long acc[COLS / 2];
+#pragma unroll
+      for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
+      float nx[4], nw[4];  // the next four blocks' scales, loaded a group ahead
+      load_scales(xs, 0, p.KB, p.vec_scales, nx);
+      load_scales(ws, 0, p.KB, p.vec_scales, nw);
+      for (int kb0 = 0; ok && kb0 < p.KB; kb0 += 4) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = nx[i] * nw[i];
+        if (kb0 + 4 < p.KB) {
+          load_scales(xs, kb0 + 4, p.KB, p.vec_scales, nx);
+          load_scales(ws, kb0 + 4, p.KB, p.vec_scales, nw);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (kb0 + i >= p.KB) break;
+          if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) { ok = false; break; }
+          tc_fence_after();
+          const unsigned long long f2 = f32x2_pack(f[i], f[i]);
+          const uint32_t ta = t_addr + buf * BN;
+          uint32_t r[2][16];
+          tmem_ld16(ta, r[0]);
+#pragma unroll
+          for (int q = 0; q < COLS / 16; ++q) {
+            tmem_wait16(r[q & 1]);
+            if (q + 1 < COLS / 16) tmem_ld16(ta + (q + 1) * 16, r[(q + 1) & 1]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              acc[q * 8 + k] = f32x2_fma(pair_bits(r[q & 1][2 * k], r[q & 1][2 * k + 1]), f2, acc[q * 8 + k]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty_leader + buf * 8u);
+          if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
+        }
+      }
+      if (!ok) break;
+      // store: PER features of 128 bytes at a time
+      constexpr int PER = 128 / sizeof(TY);
+      const float* bias = p.bias[c.lin];
+      const bool bias_vec = bias && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0 && n0 + COLS <= N;
+#pragma unroll
+      for (int b = 0; b < COLS / PER; ++b) {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {  // 16-byte chunks
+          constexpr int E = 16 / sizeof(TY);
+          float v[E];
+          const int col = b * PER + ch * E;
+#pragma unroll
+          for (int k = 0; k < E; k += 2) f32x2_unpack(acc[(col + k) / 2], v[k], v[k + 1]);
+          if (bias_vec) {
+#pragma unroll
+            for (int k = 0; k < E; k += 4) {
+              const float4 bb = __ldg(reinterpret_cast<const float4*>(bias + n0 + col + k));
+              v[k] += bb.x;
+              v[k + 1] += bb.y;
+              v[k + 2] += bb.z;
+              v[k + 3] += bb.w;
+            }
+          } else if (bias) {
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+              if (n0 + col + k < N) v[k] += __ldg(bias + n0 + col + k);
+          }
+          *reinterpret_cast<uint4*>(sout + lane * 128 + ((ch ^ (lane & 7)) << 4)) = pack16<TY>(v);
+        }
+        const int n = n0 + b * PER;
+        if (p.tma_y) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (n < N && r0 < p.M) tma_store_2d(&p.tmap_y[c.lin], sout, n, r0);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          TY* Y = static_cast<TY*>(p.out[c.lin]);
+          const int rows = min(32, p.M - r0);
+          for (int r = 0; r < rows; ++r) {
+            TY* yr = Y + (r0 + r) * p.ldy[c.lin] + n;
+            for (int k = lane; k < PER && n + k < N; k += 32) {
+              const int byte = k * static_cast<int>(sizeof(TY));
+              yr[k] = *reinterpret_cast<const TY*>(sout + r * 128 + ((((byte >> 4) ^ (r & 7)) << 4) | (byte & 15)));
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  tc_fence_before();
+  cluster_sync();
+  if (warp == EPI_WARPS + 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// few rows: single CTAs, K split over a cluster
+// ---------------------------------------------------------------------------
+//
+// One tile per cluster: 128 output features x BN activation rows (SWAP: the
+// weight rows take the TMEM lanes, the activations the columns, down to 16 of
+// them), or 128 activation rows x 128 features. The CTAs of a cluster take
+// contiguous shares of K, so that with few tiles every SM still streams
+// weights; each leaves its fp32 partial tile in its own shared memory (the
+// stages are free by then) and, after a cluster barrier, sums a part of the
+// rows over all CTAs in rank order through distributed shared memory: no
+// workspace, no atomics, the same order every time.
+// Six warps: 0-3 promote (32 lanes each), 4 loads, 5 issues MMAs.
+
+constexpr int SOLO_THREADS = 6 * 32;
+
+template <int BN, bool SWAP>
+struct SoloGeom {
+  static constexpr int X_ROWS = SWAP ? BN : LANES;
+  static constexpr int W_ROWS = QBLOCK;
+  static constexpr int X_BYTES = X_ROWS * BK;
+  static constexpr int W_BYTES = W_ROWS * BK;
+  static constexpr int STAGE_BYTES = X_BYTES + W_BYTES;
+  static constexpr int SCALE_BYTES = SWAP ? 4 * 2 * 4 * BN * 4 : 0;  // [warp][2][4 blocks][BN]
+  static constexpr int STAGES = (200 * 1024) / STAGE_BYTES;
+  static constexpr int BUFS = BN == 128 ? 2 : 4;
+  static constexpr int TMEM_COLS = BUFS * BN;  // 64, 128, 256, 256
+  static constexpr uint32_t IDESC = idesc_e4m3_f32(LANES, BN);
+  static constexpr int TILE_ROWS = X_ROWS;             // activation rows of a tile
+  static constexpr int PITCH = SWAP ? QBLOCK : QBLOCK + 4;  // of the partial tile, floats
+  static constexpr int SMEM_SCALES = STAGES * STAGE_BYTES;
+  static constexpr int SMEM_BARS = SMEM_SCALES + SCALE_BYTES;
+  static constexpr int SMEM_ALLOC = SMEM_BARS + (2 * STAGES + 2 * BUFS + 1) * 8 + 16 + 1024;
+  static_assert(TILE_ROWS * PITCH * 4 <= STAGES * STAGE_BYTES, "the partial tile fits the stages");
+  static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+template <typename TY, int BN, bool SWAP>
+__global__ void __launch_bounds__(SOLO_THREADS, 1)
+fp8_solo_kernel(const __grid_constant__ GemmParams p) {
+  using G = SoloGeom<BN, SWAP>;
+  extern __shared__ uint8_t smem_raw[];
+  // the offset to the next 1024-byte boundary is the same in every CTA of a cluster
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::SMEM_BARS);
+  uint64_t* empty = full + G::STAGES;
+  uint64_t* tfull = empty + G::STAGES;
+  uint64_t* tempty = tfull + G::BUFS;
+  uint64_t* drain = tempty + G::BUFS;
+  uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* err = &g_fp8_error;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const Tile c = decode(p, static_cast<int>(blockIdx.x) / p.split);
+  const int N = p.N[c.lin];
+  const int m0 = c.mt * G::TILE_ROWS, n0 = c.nt * QBLOCK;
+  const int kb_begin = p.KB * rank / p.split, kb_end = p.KB * (rank + 1) / p.split;
+
+  if (threadIdx.x == 4 * 32) {
+    for (int s = 0; s < G::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < G::BUFS; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&p.tmap_x);
+    tma_prefetch_desc(&p.tmap_w[c.lin]);
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_base_smem, G::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_base_smem;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+
+  if (warp == 4) {
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      uint32_t stage = 0, phase = 0, n_issued = 0;
+      for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) break;
+        uint8_t* sx = smem + stage * G::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full[stage], G::STAGE_BYTES);
+        tma_load_2d(sx + G::X_BYTES, &p.tmap_w[c.lin], &full[stage], kb * BK, n0, pol);
+        tma_load_2d(sx, &p.tmap_x, &full[stage], kb * BK, m0, pol);
+        ++n_issued;
+        if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
+      }
+      // no copy may land once the stages hold partial sums, or after the exit
+      for (uint32_t s = 0; s < G::STAGES; ++s)
+        if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
+      for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err) ||
+            !mbar_wait(&full[stage], phase, abort_flag, err)) break;
+        tc_fence_after();
+        const uint32_t sx = smem_u32(smem + stage * G::STAGE_BYTES), sw = sx + G::X_BYTES;
+        mma_block<1>(tmem_base + buf * BN, SWAP ? sw : sx, SWAP ? sx : sw, G::IDESC);
+        mma_commit(&empty[stage]);
+        mma_commit(&tfull[buf]);
+        if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
+        if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
+      }
+      mma_commit(drain);
+      mbar_wait(drain, 0, nullptr, err);
+    }
+    __syncwarp();
+  } else {
+    const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
+    const float* ws = p.s_w[c.lin] + static_cast<int64_t>(c.nt) * p.KB;
+    // SWAP: lane l scales the activation rows (columns) l and l + 32; else
+    // its own row
+    constexpr int XR = SWAP ? (BN + 31) / 32 : 1;
+    const float* xs[XR];
+#pragma unroll
+    for (int i = 0; i < XR; ++i) {
+      const int r = SWAP ? m0 + (32 * i + lane) % BN : m0 + 32 * warp + lane;
+      xs[i] = p.s_x + static_cast<int64_t>(min(r, p.M - 1)) * p.KB;
+    }
+    float* sc = reinterpret_cast<float*>(smem + G::SMEM_SCALES) + warp * (2 * 4 * BN);
+    unsigned long long acc[BN / 2];
+#pragma unroll
+    for (int i = 0; i < BN / 2; ++i) acc[i] = 0ull;
+    uint32_t buf = 0, bphase = 0;
+    bool ok = true;
+    const bool vec = p.vec_scales && kb_begin % 4 == 0;
+    float nx[XR][4], nw[4];
+#pragma unroll
+    for (int i = 0; i < XR; ++i) load_scales(xs[i], kb_begin, p.KB, vec, nx[i]);
+    load_scales(ws, kb_begin, p.KB, vec, nw);
+    int flip = 0;
+    for (int kb0 = kb_begin; ok && kb0 < kb_end; kb0 += 4) {
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] = nx[0][i] * nw[i];
+        if (SWAP) {
+#pragma unroll
+          for (int j = 0; j < XR; ++j)
+            if (BN >= 32 || lane < BN) sc[(flip * 4 + i) * BN + 32 * j + lane] = nx[j][i] * nw[i];
+        }
+      }
+      if (SWAP) __syncwarp();
+      if (kb0 + 4 < kb_end) {
+#pragma unroll
+        for (int i = 0; i < XR; ++i) load_scales(xs[i], kb0 + 4, p.KB, vec, nx[i]);
+        load_scales(ws, kb0 + 4, p.KB, vec, nw);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (kb0 + i >= kb_end) break;
+        if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) { ok = false; break; }
+        tc_fence_after();
+        const unsigned long long f2 = f32x2_pack(f[i], f[i]);
+        const float* s4 = sc + (flip * 4 + i) * BN;
+        const uint32_t ta = t_addr + buf * BN;
+        uint32_t r[2][16];
+        tmem_ld16(ta, r[0]);
+#pragma unroll
+        for (int q = 0; q < BN / 16; ++q) {
+          tmem_wait16(r[q & 1]);
+          if (q + 1 < BN / 16) tmem_ld16(ta + (q + 1) * 16, r[(q + 1) & 1]);
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            unsigned long long fa = f2, fb = f2;
+            if (SWAP) {
+              const float4 s = *reinterpret_cast<const float4*>(s4 + q * 16 + 2 * k);
+              fa = f32x2_pack(s.x, s.y);
+              fb = f32x2_pack(s.z, s.w);
+            }
+            acc[q * 8 + k] = f32x2_fma(pair_bits(r[q & 1][2 * k], r[q & 1][2 * k + 1]), fa, acc[q * 8 + k]);
+            acc[q * 8 + k + 1] =
+                f32x2_fma(pair_bits(r[q & 1][2 * k + 2], r[q & 1][2 * k + 3]), fb, acc[q * 8 + k + 1]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[buf]);
+        if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
+      }
+      flip ^= 1;
+    }
+    // The partial tile, activation row by activation row. Every MMA of this
+    // CTA has completed (the last block's commit was seen), so no stage is
+    // read or filled any more.
+    float* part = reinterpret_cast<float*>(smem);
+    if (SWAP) {
+#pragma unroll
+      for (int i = 0; i < BN / 2; ++i) {
+        float a, b;
+        f32x2_unpack(acc[i], a, b);
+        part[(2 * i) * G::PITCH + 32 * warp + lane] = a;
+        part[(2 * i + 1) * G::PITCH + 32 * warp + lane] = b;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < BN / 4; ++i) {
+        float4 v;
+        f32x2_unpack(acc[2 * i], v.x, v.y);
+        f32x2_unpack(acc[2 * i + 1], v.z, v.w);
+        *reinterpret_cast<float4*>(part + (32 * warp + lane) * G::PITCH + 4 * i) = v;
+      }
+    }
+  }
+  tc_fence_before();
+  if (p.split > 1) cluster_sync(); else __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, G::TMEM_COLS);
+  }
+  // one activation row of 128 features per warp at a time
+  const int rows = min(G::TILE_ROWS, p.M - m0);
+  const int n = n0 + lane * 4;
+  const float* bias = p.bias[c.lin];
+  float bv[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) bv[k] = (bias && n + k < N) ? __ldg(bias + n + k) : 0.0f;
+  TY* Y = static_cast<TY*>(p.out[c.lin]);
+  const int64_t ldy = p.ldy[c.lin];
+  const bool vec_out = n + 4 <= N && ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * sizeof(TY) - 1)) == 0;
+  for (int r = warp * p.split + rank; r < rows; r += (SOLO_THREADS / 32) * p.split) {
+    const uint32_t at = smem_u32(smem) + (r * G::PITCH + lane * 4) * 4;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < p.split; ++j) {
+      const float4 s = p.split > 1 ? ld_cluster_v4(mapa_shared(at, j))
+                                   : *reinterpret_cast<const float4*>(smem + (r * G::PITCH + lane * 4) * 4);
+      v[0] += s.x;
+      v[1] += s.y;
+      v[2] += s.z;
+      v[3] += s.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += bv[k];
+    TY* yr = Y + (m0 + r) * ldy + n;
+    if (vec_out) {
+      store4(yr, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (n + k < N) yr[k] = from_f32<TY>(v[k]);
+    }
+  }
+  if (p.split > 1) cluster_sync();  // the others' reads of this CTA's partial sums
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// e4m3 codes [rows,K] (dense), box box_rows x 128 codes, 128-byte swizzle.
+int make_tmap_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return set_cuda_error(cudaErrorNotSupported);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(BK), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? CONVROT_OK : set_cuda_error(cudaErrorInvalidValue);
+}
+
+// Y [rows,cols], box 32 rows x 128 bytes, 128-byte swizzle.
+int make_tmap_out(CUtensorMap* m, void* base, int y_dtype, int64_t rows, int64_t cols, int64_t ldy) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return set_cuda_error(cudaErrorNotSupported);
+  const cuuint64_t size = dtype_size(y_dtype);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldy) * size};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType type = y_dtype == CONVROT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : y_dtype == CONVROT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult r = enc(m, type, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? CONVROT_OK : set_cuda_error(cudaErrorInvalidValue);
+}
+
+// Raises the kernel's shared-memory limit, once per device. `regs`: the
+// registers a thread that the kernel's own redistribution counts on (it would
+// wait forever for more than the launch has).
+template <typename F>
+int allow_smem(F* kernel, int bytes, uint64_t& done, std::mutex& mu, int regs = 0) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 64 || !((done >> dev) & 1u)) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    if (attr.numRegs < regs) return CONVROT_ERR_UNSUPPORTED;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    if (dev < 64) done |= 1ull << dev;
+  }
+  return CONVROT_OK;
+}
+
+constexpr int64_t RASTER_L2_BYTES = 48ll << 20;  // activation codes a raster group keeps in L2
+
+// Everything of a launch but the tensor maps of Y: tiles of tile_rows
+// activation rows x tile_cols features, operand boxes x_box and w_box rows.
+int fill(GemmParams& p, const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
+         int tile_rows, int tile_cols, int x_box, int w_box) {
+  if (int st = make_tmap_codes(&p.tmap_x, Qx, M, K, x_box)) return st;
+  int64_t cols = 0;
+  const int64_t KB = n_blocks(K);
+  p.vec_scales = KB % 4 == 0 && aligned16(s_x);
+  for (int j = 0; j < n; ++j) {
+    if (int st = make_tmap_codes(&p.tmap_w[j], w[j].q, w[j].N, K, w_box)) return st;
+    p.s_w[j] = w[j].scale;
+    p.bias[j] = w[j].bias;
+    p.out[j] = w[j].Y;
+    p.ldy[j] = w[j].ldy;
+    p.N[j] = static_cast<int>(w[j].N);
+    p.tile_start[j] = static_cast<int>(cols);
+    cols += (w[j].N + tile_cols - 1) / tile_cols;
+    p.vec_scales = p.vec_scales && aligned16(w[j].scale);
+  }
+  p.n_mtiles = static_cast<int>((M + tile_rows - 1) / tile_rows);
+  if (cols * p.n_mtiles > 0x7fffffff / 8) return CONVROT_ERR_UNSUPPORTED;
+  p.tile_start[n] = static_cast<int>(cols);
+  p.total_tiles = static_cast<int>(cols * p.n_mtiles);
+  p.raster_mtiles =
+      static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(p.n_mtiles, RASTER_L2_BYTES / (tile_rows * K))));
+  p.s_x = s_x;
+  p.M = static_cast<int>(M);
+  p.KB = static_cast<int>(KB);
+  p.n_lin = n;
+  p.split = 1;
+  p.tma_y = false;
+  return CONVROT_OK;
+}
+
+template <typename TY, int BN>
+int launch_pair(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
+                int y_dtype, cudaStream_t stream) {
+  using G = PairGeom<BN>;
+  GemmParams p;
+  if (int st = fill(p, Qx, s_x, M, K, w, n, 256, BN, LANES, BN / 2)) return st;
+  p.tma_y = true;
+  for (int j = 0; j < n; ++j) p.tma_y = p.tma_y && aligned16(w[j].Y) && w[j].ldy * sizeof(TY) % 16 == 0;
+  if (p.tma_y)
+    for (int j = 0; j < n; ++j)
+      if (int st = make_tmap_out(&p.tmap_y[j], w[j].Y, y_dtype, M, w[j].N, w[j].ldy)) return st;
+  static std::mutex mu;
+  static uint64_t done = 0;
+  auto kernel = fp8_pair_kernel<TY, BN>;
+  if (int st = allow_smem(kernel, G::SMEM_ALLOC, done, mu, LAUNCH_REGS)) return st;
+  const int pairs = std::min(p.total_tiles, device_sm_count() / 2);
+  Launch l(2 * pairs, PAIR_THREADS, G::SMEM_ALLOC, stream, 2);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, p);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+template <typename TY, int BN, bool SWAP>
+int launch_solo(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
+                int split, cudaStream_t stream) {
+  using G = SoloGeom<BN, SWAP>;
+  GemmParams p;
+  if (int st = fill(p, Qx, s_x, M, K, w, n, G::TILE_ROWS, QBLOCK, G::X_ROWS, G::W_ROWS)) return st;
+  p.split = split;
+  static std::mutex mu;
+  static uint64_t done = 0;
+  auto kernel = fp8_solo_kernel<TY, BN, SWAP>;
+  if (int st = allow_smem(kernel, G::SMEM_ALLOC, done, mu)) return st;
+  Launch l(p.total_tiles * split, SOLO_THREADS, G::SMEM_ALLOC, stream, split);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, p);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+// The largest cluster (of 1, 2, 4, 8 CTAs) that keeps `tiles` clusters within
+// one wave of the SMs and leaves every CTA a block of K.
+int pick_split(int64_t tiles, int64_t KB, int sms) {
+  int s = 1;
+  while (s < 8 && tiles * (2 * s) <= sms && 2 * s <= KB) s *= 2;
+  return s;
+}
+
+template <typename TY>
+int launch_as(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
+              int y_dtype, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  const int64_t KB = n_blocks(K);
+  int64_t cols = 0, wide = 0;  // features in tiles of 128 and of 256
+  for (int j = 0; j < n; ++j) {
+    cols += n_blocks(w[j].N);
+    wide += (w[j].N + 255) / 256;
+  }
+  if (M <= 64) {
+    const int split = pick_split(cols, KB, sms);
+    if (M <= 16) return launch_solo<TY, 16, true>(Qx, s_x, M, K, w, n, split, stream);
+    if (M <= 32) return launch_solo<TY, 32, true>(Qx, s_x, M, K, w, n, split, stream);
+    return launch_solo<TY, 64, true>(Qx, s_x, M, K, w, n, split, stream);
+  }
+  const int64_t solo = (M + 127) / 128 * cols;
+  const int64_t pair_wide = (M + 255) / 256 * wide, pair_narrow = (M + 255) / 256 * cols;
+  if (solo <= sms) return launch_solo<TY, 128, false>(Qx, s_x, M, K, w, n, pick_split(solo, KB, sms), stream);
+  if (pair_wide < sms / 2 && pair_narrow <= sms / 2)
+    return launch_pair<TY, 128>(Qx, s_x, M, K, w, n, y_dtype, stream);
+  return launch_pair<TY, 256>(Qx, s_x, M, K, w, n, y_dtype, stream);
+}
+
+}  // namespace
+
+int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
+                    int n_weights, int y_dtype, cudaStream_t stream) {
+  if (y_dtype == CONVROT_F32) return launch_as<float>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
+  if (y_dtype == CONVROT_F16) return launch_as<__half>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
+  return launch_as<__nv_bfloat16>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
+}
+
+int read_and_clear_fp8_error() {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_fp8_error, sizeof(int));
+  if (e != cudaSuccess) return set_cuda_error(e);
+  if (v != 0) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbol(g_fp8_error, &zero, sizeof(int));
+    if (e != cudaSuccess) return set_cuda_error(e);
+  }
+  return v;
+}
+
+}  // namespace fp8
+}  // namespace convrot

@@ -37,8 +37,13 @@ ACT_NONE = 0
 ACT_GELU = 1
 ACT_SWIGLU = 2
 
+NORM_NONE = 0
+NORM_RMS = 1
+NORM_LAYER = 2
+
 F32 = 0
 F16 = 1
+BF16 = 2
 MAX_LINEARS = 8
 PACK_MAX_K = 32768
 MAX_K = 133144
@@ -46,6 +51,8 @@ W4_MAX_K = 16384
 CHUNK_ROWS = 128
 NOALLOC_SCRATCH_BYTES = 32 << 20
 GEMM_SYNC_BYTES = 4096
+NORM_MAX_K = 32768
+FP8_BLOCK = 128
 
 
 class ConvrotError(RuntimeError):
@@ -68,6 +75,26 @@ class convrot_weight(ctypes.Structure):
                 ("bias", ctypes.c_void_p), ("N", ctypes.c_int64),
                 ("Y", ctypes.c_void_p), ("kchunk", ctypes.c_void_p),
                 ("q4", ctypes.c_void_p)]
+
+
+class convrot_block_norm_args(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("K", ctypes.c_int64), ("dtype", ctypes.c_int), ("u_dtype", ctypes.c_int),
+                ("H", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float),
+                ("post_norm", ctypes.c_int), ("pre_norm", ctypes.c_int),
+                ("post_eps", ctypes.c_float), ("pre_eps", ctypes.c_float),
+                ("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p),
+                ("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p),
+                ("ld_gate", ctypes.c_int64), ("ld_mod", ctypes.c_int64), ("n_samples", ctypes.c_int64),
+                ("row_sample", ctypes.c_void_p), ("rows_per_sample", ctypes.c_int64),
+                ("H_out", ctypes.c_void_p), ("U", ctypes.c_void_p), ("ldho", ctypes.c_int64), ("ldu", ctypes.c_int64),
+                ("Q", ctypes.c_void_p), ("s", ctypes.c_void_p)]
+
+
+class convrot_fp8_weight(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("N", ctypes.c_int64), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
 
 
 _LIB = None
@@ -109,6 +136,12 @@ SIGNATURES = {
                          ctypes.POINTER(convrot_weight), _VP, _SZ, _VP]),
     "convrot_linear_noalloc": (_I, [_VP, _I, _I64, _I64, _I, ctypes.POINTER(convrot_weight), _I, _VP]),
     "convrot_linear_swiglu": (_I, [_VP, _I, _I64, _I64, _I, ctypes.POINTER(convrot_weight), _VP, _SZ, _VP]),
+    "convrot_block_norm": (_I, [ctypes.POINTER(convrot_block_norm_args), _VP]),
+    "fp8_pack_activations": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _VP]),
+    "fp8_prepare_weight": (_I, [_VP, _I, _I64, _I64, _VP, _VP, _VP]),
+    "fp8_linear_workspace_size": (_SZ, [_I64, _I64]),
+    "fp8_linear_packed": (_I, [_VP, _VP, _I64, _I64, ctypes.POINTER(convrot_fp8_weight), _I, _I, _VP]),
+    "fp8_linear": (_I, [_VP, _I, _I64, _I64, _I64, ctypes.POINTER(convrot_fp8_weight), _I, _I, _VP, _SZ, _VP]),
     "convrot_device_status": (_I, [_VP]),
     "convrot_test_handover_timeout": (_I, [_VP, _VP, _I64, _I64, ctypes.POINTER(convrot_weight), _I, _VP, _SZ,
                                            ctypes.c_uint64, _VP]),
@@ -644,3 +677,275 @@ def convrot_linear_swiglu(X: torch.Tensor, G: int, gate: Tuple, up: Tuple, H: Op
            "convrot_linear_swiglu")
     return H
 
+
+# ---------------------------------------------------------------------------
+# block norms and 8-bit floating-point linears
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+_E4M3 = torch.float8_e4m3fn
+
+
+class _On:
+    """The stream a call runs on: its handle for the library, and memory that
+    belongs to it. Buffers made inside a call are allocated on that stream, so
+    that neither their earlier nor their later use elsewhere overlaps it."""
+
+    __slots__ = ("device", "handle", "_stream")
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.device = t.get_device()
+        if self.device < 0:
+            raise ValueError("the inputs must be CUDA tensors")
+        if self.device != torch.cuda.current_device():
+            raise ValueError("the inputs must be on the current CUDA device")
+        self._stream = stream
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(self.device)
+        else:
+            self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        dev = torch.device("cuda", self.device)
+        if self._stream is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        s = self._stream if isinstance(self._stream, torch.cuda.Stream) else torch.cuda.ExternalStream(self.handle, dev)
+        with torch.cuda.stream(s):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _rows(t: torch.Tensor, name: str, on: _On, shape=None, dtype=None) -> int:
+    """Checks a matrix whose rows are contiguous; the distance between them."""
+    if t.get_device() != on.device:
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be a matrix" + (f" of shape {tuple(shape)}" if shape is not None else ""))
+    if t.dtype not in _DTYPES if dtype is None else t.dtype != dtype:
+        raise ValueError(f"{name} must be " + (f"{dtype}" if dtype is not None else "float32, float16 or bfloat16")
+                         + f", got {t.dtype}")
+    M, K = t.shape
+    ld, inner = t.stride()
+    if inner != 1 and K > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if M <= 1 or K == 0:
+        return K
+    if ld < K:
+        raise ValueError(f"the rows of {name} overlap")
+    return ld
+
+
+def _dense(t: torch.Tensor, name: str, on: _On, shape, dtype):
+    """Checks a contiguous array of a given shape and type."""
+    if t.get_device() != on.device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the device of the "
+                         f"other tensors, got {t.dtype} {tuple(t.shape)}")
+
+
+def _n_blocks(n: int) -> int:
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def fp8_pack_activations(X: torch.Tensor, Q_x: Optional[torch.Tensor] = None, s_x: Optional[torch.Tensor] = None,
+                         stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """X [M,K] (float32, float16 or bfloat16, rows contiguous) -> (Q_x
+    float8_e4m3fn [M,K], s_x float32 [M, ceil(K/128)])."""
+    on = _On(X, stream)
+    ldx = _rows(X, "X", on)
+    M, K = X.shape
+    if Q_x is None:
+        Q_x = on.empty((M, K), _E4M3)
+    if s_x is None:
+        s_x = on.empty((M, _n_blocks(K)), torch.float32)
+    _dense(Q_x, "Q_x", on, (M, K), _E4M3)
+    _dense(s_x, "s_x", on, (M, _n_blocks(K)), torch.float32)
+    _check(lib().fp8_pack_activations(X.data_ptr(), _DTYPES[X.dtype], M, K, ldx, Q_x.data_ptr(), s_x.data_ptr(),
+                                      on.handle), "fp8_pack_activations")
+    return Q_x, s_x
+
+
+def fp8_prepare_weight(W: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Offline weight path: W [N,K] (float32, float16 or bfloat16) -> (Q_w
+    float8_e4m3fn [N,K], s_w float32 [ceil(N/128), ceil(K/128)])."""
+    on = _On(W, stream)
+    if _rows(W, "W", on) != W.shape[1]:
+        raise ValueError("W must be contiguous")
+    N, K = W.shape
+    Q_w = on.empty((N, K), _E4M3)
+    s_w = on.empty((_n_blocks(N), _n_blocks(K)), torch.float32)
+    _check(lib().fp8_prepare_weight(W.data_ptr(), _DTYPES[W.dtype], N, K, Q_w.data_ptr(), s_w.data_ptr(), on.handle),
+           "fp8_prepare_weight")
+    return Q_w, s_w
+
+
+def _fp8_weights(on: _On, M: int, K: int, qs, scales, biases, Ys, out_dtype):
+    """(descriptors, outputs, y_dtype) of an fp8 linear call."""
+    n = len(qs)
+    if not 1 <= n <= MAX_LINEARS or len(scales) != n or (biases is not None and len(biases) != n) or \
+            (Ys is not None and len(Ys) != n):
+        raise ValueError(f"1 to {MAX_LINEARS} weights, with as many scales, biases and outputs")
+    if Ys is None:
+        Ys = [on.empty((M, q.shape[0]), out_dtype) for q in qs]
+    arr = (convrot_fp8_weight * n)()
+    for j in range(n):
+        q, s, b, y = qs[j], scales[j], None if biases is None else biases[j], Ys[j]
+        N = q.shape[0]
+        _dense(q, "a weight", on, (N, K), _E4M3)
+        _dense(s, "a weight's scales", on, (_n_blocks(N), _n_blocks(K)), torch.float32)
+        if b is not None:
+            _dense(b, "a bias", on, (N,), torch.float32)
+        ldy = _rows(y, "an output", on, (M, N))
+        if y.dtype != Ys[0].dtype:
+            raise ValueError("the outputs of one call have one type")
+        w = arr[j]
+        w.q, w.scale, w.N, w.Y, w.ldy = q.data_ptr(), s.data_ptr(), N, y.data_ptr(), ldy
+        if b is not None:
+            w.bias = b.data_ptr()
+    return arr, Ys, _DTYPES[Ys[0].dtype]
+
+
+def fp8_linear_packed(Q_x: torch.Tensor, s_x: torch.Tensor, qs: Sequence[torch.Tensor], scales: Sequence[torch.Tensor],
+                      biases: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                      Ys: Optional[List[torch.Tensor]] = None, out_dtype: torch.dtype = torch.bfloat16,
+                      stream=None) -> List[torch.Tensor]:
+    """Every Y_j = X W_j^T + b_j on an activation packed by
+    fp8_pack_activations or convrot_block_norm_fp8; weights (codes `qs`,
+    `scales`) from fp8_prepare_weight. Ys: outputs to write (float32, float16
+    or bfloat16, rows contiguous), or new ones of out_dtype."""
+    on = _On(Q_x, stream)
+    if Q_x.dim() != 2:
+        raise ValueError("Q_x must be a matrix")
+    M, K = Q_x.shape
+    _dense(Q_x, "Q_x", on, (M, K), _E4M3)
+    _dense(s_x, "s_x", on, (M, _n_blocks(K)), torch.float32)
+    arr, Ys, y_dtype = _fp8_weights(on, M, K, qs, scales, biases, Ys, out_dtype)
+    _check(lib().fp8_linear_packed(Q_x.data_ptr(), s_x.data_ptr(), M, K, arr, len(arr), y_dtype, on.handle),
+           "fp8_linear_packed")
+    return Ys
+
+
+def fp8_linear_workspace_size(M: int, K: int) -> int:
+    return int(lib().fp8_linear_workspace_size(M, K))
+
+
+def fp8_linear(X: torch.Tensor, qs: Sequence[torch.Tensor], scales: Sequence[torch.Tensor],
+               biases: Optional[Sequence[Optional[torch.Tensor]]] = None, Ys: Optional[List[torch.Tensor]] = None,
+               out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> List[torch.Tensor]:
+    """Pack X once (fp8_pack_activations), then every Y_j = X W_j^T + b_j as
+    fp8_linear_packed. New outputs are of out_dtype (X's own by default)."""
+    on = _On(X, stream)
+    ldx = _rows(X, "X", on)
+    M, K = X.shape
+    arr, Ys, y_dtype = _fp8_weights(on, M, K, qs, scales, biases, Ys, X.dtype if out_dtype is None else out_dtype)
+    need = fp8_linear_workspace_size(M, K)
+    ws = on.empty((max(need, 1),), torch.uint8) if workspace is None else workspace
+    if ws.get_device() != on.device or not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of the other tensors")
+    _check(lib().fp8_linear(X.data_ptr(), _DTYPES[X.dtype], M, K, ldx, arr, len(arr), y_dtype, ws.data_ptr(),
+                            ws.numel() * ws.element_size(), on.handle), "fp8_linear")
+    return Ys
+
+
+def _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_weight, post_bias, gate, pre_norm,
+                pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, on: _On):
+    """The arguments of convrot_block_norm up to the form of u."""
+    a = convrot_block_norm_args()
+    a.ldh = _rows(H, "H", on)
+    M, K = H.shape
+    a.M, a.K, a.dtype, a.H = M, K, _DTYPES[H.dtype], H.data_ptr()
+    if Y is not None:
+        a.ldy = _rows(Y, "Y", on, (M, K), H.dtype)
+        a.Y = Y.data_ptr()
+    a.residual_scale, a.block_scale = residual_scale, block_scale
+    a.post_norm, a.pre_norm, a.post_eps, a.pre_eps = post_norm, pre_norm, post_eps, pre_eps
+    if post_weight is not None:
+        _dense(post_weight, "post_weight", on, (K,), torch.float32)
+        a.post_weight = post_weight.data_ptr()
+    if post_bias is not None:
+        _dense(post_bias, "post_bias", on, (K,), torch.float32)
+        a.post_bias = post_bias.data_ptr()
+    if pre_weight is not None:
+        _dense(pre_weight, "pre_weight", on, (K,), torch.float32)
+        a.pre_weight = pre_weight.data_ptr()
+    if pre_bias is not None:
+        _dense(pre_bias, "pre_bias", on, (K,), torch.float32)
+        a.pre_bias = pre_bias.data_ptr()
+    samples = None
+    for name, v in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if v is None:
+            continue
+        samples = v.shape[0] if samples is None else samples
+        ld = _rows(v, name, on, (samples, K), torch.float32)
+        setattr(a, name, v.data_ptr())
+        if name == "gate":
+            a.ld_gate = ld
+        elif name == "shift" and scale is not None and a.ld_mod != ld:
+            raise ValueError("scale and shift must have the same distance between rows")
+        else:
+            a.ld_mod = ld
+    if samples is not None:
+        a.n_samples, a.rows_per_sample = samples, rows_per_sample
+        if row_sample is not None:
+            _dense(row_sample, "row_sample", on, (M,), torch.int32)
+            a.row_sample = row_sample.data_ptr()
+        elif rows_per_sample == 0 and samples > 1:
+            raise ValueError("several samples need row_sample or rows_per_sample")
+    if H_out is not None:
+        a.ldho = _rows(H_out, "H_out", on, (M, K), H.dtype)
+        a.H_out = H_out.data_ptr()
+    return a
+
+
+def convrot_block_norm(H: torch.Tensor, Y: Optional[torch.Tensor] = None, *, residual_scale: float = 1.0,
+                       block_scale: float = 1.0, post_norm: int = NORM_NONE, post_eps: float = 1e-6, post_weight=None,
+                       post_bias=None, gate=None, pre_norm: int = NORM_RMS, pre_eps: float = 1e-6, pre_weight=None,
+                       pre_bias=None, scale=None, shift=None, row_sample=None, rows_per_sample: int = 0,
+                       H_out: Optional[torch.Tensor] = None, U: Optional[torch.Tensor] = None,
+                       u_dtype: Optional[torch.dtype] = None, want_h: bool = True, want_u: bool = True, stream=None):
+    """The norms before and after a block with its gate and residual, one pass:
+        h' = residual_scale H + gate * block_scale * post(Y),
+        u = modulate(pre(h')),  modulate(u) = u + u * scale + shift.
+    H, Y [M,K] (one type, rows contiguous); weights and biases float32 [K];
+    gate, scale, shift float32 [samples, K], the row m taking the sample
+    row_sample[m] (int32) or m // rows_per_sample. Returns (h', u): H_out and U
+    where given (H_out may be H), new tensors where not (u of u_dtype, H's own
+    by default), None for what want_h or want_u leaves out."""
+    on = _On(H, stream)
+    if H_out is None and want_h:
+        H_out = on.empty(H.shape, H.dtype)
+    if U is None and want_u:
+        U = on.empty(H.shape, H.dtype if u_dtype is None else u_dtype)
+    a = _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_weight, post_bias, gate, pre_norm,
+                    pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, on)
+    if U is not None:
+        a.ldu = _rows(U, "U", on, H.shape)
+        a.U, a.u_dtype = U.data_ptr(), _DTYPES[U.dtype]
+    _check(lib().convrot_block_norm(ctypes.byref(a), on.handle), "convrot_block_norm")
+    return H_out, U
+
+
+def convrot_block_norm_fp8(H: torch.Tensor, Y: Optional[torch.Tensor] = None, *, residual_scale: float = 1.0,
+                           block_scale: float = 1.0, post_norm: int = NORM_NONE, post_eps: float = 1e-6,
+                           post_weight=None, post_bias=None, gate=None, pre_norm: int = NORM_RMS,
+                           pre_eps: float = 1e-6, pre_weight=None, pre_bias=None, scale=None, shift=None,
+                           row_sample=None, rows_per_sample: int = 0, H_out: Optional[torch.Tensor] = None,
+                           Q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None, want_h: bool = True,
+                           stream=None):
+    """convrot_block_norm with u quantized as it is formed: returns (h', Q, s),
+    Q float8_e4m3fn [M,K] and s float32 [M, ceil(K/128)] as
+    fp8_pack_activations gives them, for fp8_linear_packed."""
+    on = _On(H, stream)
+    if H_out is None and want_h:
+        H_out = on.empty(H.shape, H.dtype)
+    a = _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_weight, post_bias, gate, pre_norm,
+                    pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, on)
+    M, K = H.shape
+    if Q is None:
+        Q = on.empty((M, K), _E4M3)
+    if s is None:
+        s = on.empty((M, _n_blocks(K)), torch.float32)
+    _dense(Q, "Q", on, (M, K), _E4M3)
+    _dense(s, "s", on, (M, _n_blocks(K)), torch.float32)
+    a.Q, a.s = Q.data_ptr(), s.data_ptr()
+    _check(lib().convrot_block_norm(ctypes.byref(a), on.handle), "convrot_block_norm")
+    return H_out, Q, s
