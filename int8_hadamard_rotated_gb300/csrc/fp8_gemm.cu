@@ -182,7 +182,8 @@ constexpr int PAIR_THREADS = (EPI_WARPS + 4) * 32;  // three warpgroups
 // two epilogue warpgroups, which hold 128 accumulators a thread, take.
 constexpr int LAUNCH_REGS = 168, CONTROL_REGS = 56, EPI_REGS = 224;
 static_assert(2 * EPI_REGS + CONTROL_REGS <= 3 * LAUNCH_REGS, "within what the block was launched with");
-constexpr int STORE_BYTES = 32 * 128;  // one warp's store buffer
+constexpr int STORE_ROW = 128;               // bytes of a row that one store takes
+constexpr int STORE_BYTES = 32 * STORE_ROW;  // one warp's store buffer
 
 template <int BN>
 struct PairGeom {
@@ -197,6 +198,37 @@ struct PairGeom {
   static constexpr int SMEM_ALLOC = SMEM_BARS + (2 * STAGES + 2 * BUFS + 1) * 8 + 16 + 1024;
 };
 static_assert(PairGeom<256>::SMEM_ALLOC <= 227 * 1024 && PairGeom<128>::SMEM_ALLOC <= 227 * 1024, "shared memory");
+
+// Where the store's 128-byte swizzle puts 16-byte piece `ch` of row `row`.
+__device__ __forceinline__ int swizzled(int ch, int row) { return ch ^ (row & 7); }
+
+// The sums start from the bias (0 without one, and past the last feature).
+template <int COLS>
+__device__ __forceinline__ void init_acc(unsigned long long (&acc)[COLS / 2], const float* bias, int n0, int N) {
+  if (bias && n0 + COLS <= N && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0) {
+#pragma unroll
+    for (int i = 0; i < COLS / 4; ++i) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(bias + n0) + i);
+      acc[2 * i] = f32x2_pack(b.x, b.y);
+      acc[2 * i + 1] = f32x2_pack(b.z, b.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < COLS / 2; ++i) {
+      const int n = n0 + 2 * i;
+      acc[i] = f32x2_pack(bias && n < N ? __ldg(bias + n) : 0.0f, bias && n + 1 < N ? __ldg(bias + n + 1) : 0.0f);
+    }
+  }
+}
+
+// Arrive on an mbarrier of either CTA of the pair with a CTA-scope release.
+// What is handed over is an accumulator that this thread has read (the wait
+// for the tcgen05 loads came before), no memory that another CTA would have to
+// see: a cluster-scope release, which orders every earlier access of the
+// thread at the cluster, costs about 0.5 us for each block here.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 
 template <typename TY, int BN>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
@@ -309,8 +341,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       const float* xs = p.s_x + static_cast<int64_t>(min(r0 + lane, p.M - 1)) * p.KB;
       const float* ws = p.s_w[c.lin] + static_cast<int64_t>(min(n0, N - 1) / QBLOCK) * p.KB;
       unsigned long long acc[COLS / 2];
-#pragma unroll
-      for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
+      init_acc<COLS>(acc, p.bias[c.lin], n0, N);
       float nx[4], nw[4];  // the next four blocks' scales, loaded a group ahead
       load_scales(xs, 0, p.KB, p.vec_scales, nx);
       load_scales(ws, 0, p.KB, p.vec_scales, nw);
@@ -341,41 +372,24 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty_leader + buf * 8u);
+          if (lane == 0) mbar_arrive_remote(tempty_leader + buf * 8u);
           if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
         }
       }
       if (!ok) break;
-      // store: PER features of 128 bytes at a time
-      constexpr int PER = 128 / sizeof(TY);
-      const float* bias = p.bias[c.lin];
-      const bool bias_vec = bias && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0 && n0 + COLS <= N;
+      // store: PER features of a row at a time
+      constexpr int PER = STORE_ROW / sizeof(TY);
+      constexpr int E = 16 / sizeof(TY);  // of them in 16 bytes
 #pragma unroll
       for (int b = 0; b < COLS / PER; ++b) {
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {  // 16-byte chunks
-          constexpr int E = 16 / sizeof(TY);
+        for (int ch = 0; ch < PER / E; ++ch) {
           float v[E];
-          const int col = b * PER + ch * E;
 #pragma unroll
-          for (int k = 0; k < E; k += 2) f32x2_unpack(acc[(col + k) / 2], v[k], v[k + 1]);
-          if (bias_vec) {
-#pragma unroll
-            for (int k = 0; k < E; k += 4) {
-              const float4 bb = __ldg(reinterpret_cast<const float4*>(bias + n0 + col + k));
-              v[k] += bb.x;
-              v[k + 1] += bb.y;
-              v[k + 2] += bb.z;
-              v[k + 3] += bb.w;
-            }
-          } else if (bias) {
-#pragma unroll
-            for (int k = 0; k < E; ++k)
-              if (n0 + col + k < N) v[k] += __ldg(bias + n0 + col + k);
-          }
-          *reinterpret_cast<uint4*>(sout + lane * 128 + ((ch ^ (lane & 7)) << 4)) = pack16<TY>(v);
+          for (int k = 0; k < E; k += 2) f32x2_unpack(acc[(b * PER + ch * E + k) / 2], v[k], v[k + 1]);
+          *reinterpret_cast<uint4*>(sout + lane * STORE_ROW + (swizzled(ch, lane) << 4)) = pack16<TY>(v);
         }
         const int n = n0 + b * PER;
         if (p.tma_y) {
@@ -393,7 +407,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
             TY* yr = Y + (r0 + r) * p.ldy[c.lin] + n;
             for (int k = lane; k < PER && n + k < N; k += 32) {
               const int byte = k * static_cast<int>(sizeof(TY));
-              yr[k] = *reinterpret_cast<const TY*>(sout + r * 128 + ((((byte >> 4) ^ (r & 7)) << 4) | (byte & 15)));
+              yr[k] = *reinterpret_cast<const TY*>(sout + r * STORE_ROW + ((swizzled(byte >> 4, r) << 4) | (byte & 15)));
             }
           }
           __syncwarp();
@@ -701,7 +715,7 @@ int make_tmap_out(CUtensorMap* m, void* base, int y_dtype, int64_t rows, int64_t
   const cuuint64_t size = dtype_size(y_dtype);
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldy) * size};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), 32};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(STORE_ROW / size), 32};
   const cuuint32_t estr[2] = {1, 1};
   const CUtensorMapDataType type = y_dtype == CONVROT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : y_dtype == CONVROT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
