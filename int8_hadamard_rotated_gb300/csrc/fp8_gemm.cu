@@ -109,14 +109,27 @@ __device__ __forceinline__ unsigned long long pair_bits(uint32_t a, uint32_t b) 
   return r;
 }
 
+// Loads that stay where they are written (the compiler would move plain ones
+// down to their first use, next to it in time).
+__device__ __forceinline__ float ldg_now(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ldg_now4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.nc.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+
 // Four block scales of one row, from block kb on (0 past the last one).
 __device__ __forceinline__ void load_scales(const float* row, int kb, int KB, bool vec, float (&v)[4]) {
   if (vec) {
-    const float4 t = __ldg(reinterpret_cast<const float4*>(row + kb));
+    const float4 t = ldg_now4(row + kb);
     v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = kb + i < KB ? __ldg(row + kb + i) : 0.0f;
+    for (int i = 0; i < 4; ++i) v[i] = kb + i < KB ? ldg_now(row + kb + i) : 0.0f;
   }
 }
 
@@ -170,7 +183,8 @@ __device__ __forceinline__ Tile decode(const GemmParams& p, int t) {
 // scale: the promotion of a block is a single packed multiply-add per two
 // outputs with one factor. Twelve warps: 0-7 promote and store (quarter = warp
 // & 3 of the lanes, half = warp >> 2 of the features), 8 loads, 9 issues MMAs,
-// 10 and 11 only complete the control warpgroup.
+// 10 looks up each tile's place, scales and bias ahead of the epilogue, 11
+// only completes the control warpgroup.
 // Y leaves per warp through its own 4 KB of shared memory, 32 rows x 128
 // bytes at a time in the 128-byte swizzle (no barrier between warps), by
 // tensor-map stores where the rows of Y are 16-byte aligned, else by
@@ -182,41 +196,98 @@ constexpr int PAIR_THREADS = (EPI_WARPS + 4) * 32;  // three warpgroups
 // two epilogue warpgroups, which hold 128 accumulators a thread, take.
 constexpr int LAUNCH_REGS = 168, CONTROL_REGS = 56, EPI_REGS = 224;
 static_assert(2 * EPI_REGS + CONTROL_REGS <= 3 * LAUNCH_REGS, "within what the block was launched with");
-constexpr int STORE_ROW = 128;               // bytes of a row that one store takes
-constexpr int STORE_BYTES = 32 * STORE_ROW;  // one warp's store buffer
+constexpr int STORE_ROW = 128;                 // bytes of a row that one store takes
+constexpr int STORE_BLOCK = 32 * STORE_ROW;    // one store: 32 rows
+constexpr int STORE_BYTES = 2 * STORE_BLOCK;   // one warp's two store buffers
+
+// What the epilogue needs to know of a tile, prepared by a warp of its own.
+struct __align__(16) TileInfo {
+  int lin, row, col, N;  // the linear, the tile's first row and feature, the linear's features
+  const float* ws;       // the weight scales of the tile's first block of features
+};
+static_assert(sizeof(TileInfo) == 32, "as laid out in shared memory");
 
 template <int BN>
 struct PairGeom {
   static constexpr int X_BYTES = LANES * BK;
   static constexpr int W_BYTES = BN / 2 * BK;
   static constexpr int STAGE_BYTES = X_BYTES + W_BYTES;
-  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int STAGES = BN == 256 ? 5 : 6;
   static constexpr int BUFS = 512 / BN;  // TMEM accumulators
   static constexpr uint32_t IDESC = idesc_e4m3_f32(256, BN);
   static constexpr int SMEM_OUT = STAGES * STAGE_BYTES;
-  static constexpr int SMEM_BARS = SMEM_OUT + EPI_WARPS * STORE_BYTES;
-  static constexpr int SMEM_ALLOC = SMEM_BARS + (2 * STAGES + 2 * BUFS + 1) * 8 + 16 + 1024;
+  static constexpr int SMEM_BIAS = SMEM_OUT + EPI_WARPS * STORE_BYTES;  // [BN] fp32
+  static constexpr int SMEM_INFO = SMEM_BIAS + BN * 4;                  // [2] TileInfo
+  static constexpr int SMEM_BARS = SMEM_INFO + 2 * 32;
+  static constexpr int SMEM_ALLOC = SMEM_BARS + (2 * STAGES + 2 * BUFS + 7) * 8 + 16 + 1024;
 };
 static_assert(PairGeom<256>::SMEM_ALLOC <= 227 * 1024 && PairGeom<128>::SMEM_ALLOC <= 227 * 1024, "shared memory");
 
 // Where the store's 128-byte swizzle puts 16-byte piece `ch` of row `row`.
 __device__ __forceinline__ int swizzled(int ch, int row) { return ch ^ (row & 7); }
 
-// The sums start from the bias (0 without one, and past the last feature).
-template <int COLS>
-__device__ __forceinline__ void init_acc(unsigned long long (&acc)[COLS / 2], const float* bias, int n0, int N) {
-  if (bias && n0 + COLS <= N && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0) {
-#pragma unroll
-    for (int i = 0; i < COLS / 4; ++i) {
-      const float4 b = __ldg(reinterpret_cast<const float4*>(bias + n0) + i);
-      acc[2 * i] = f32x2_pack(b.x, b.y);
-      acc[2 * i + 1] = f32x2_pack(b.z, b.w);
+// A staged block to rows of Y that no tensor map covers, element by element.
+// Out of line: the unrolled epilogue carries one call of it per block.
+template <typename TY>
+__device__ __noinline__ void store_rows(const uint8_t* sb, TY* y, int64_t ldy, int rows, int cols) {
+  const int lane = threadIdx.x & 31;
+  constexpr int PER = STORE_ROW / sizeof(TY);
+  for (int r = 0; r < rows; ++r, y += ldy)
+    for (int k = lane; k < PER && k < cols; k += 32) {
+      const int byte = k * static_cast<int>(sizeof(TY));
+      y[k] = *reinterpret_cast<const TY*>(sb + r * STORE_ROW + ((swizzled(byte >> 4, r) << 4) | (byte & 15)));
     }
-  } else {
+}
+
+// mbar_wait by a warp that is in no hurry: one lane looks, now and then.
+__device__ __forceinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+      __nanosleep(400);
+      if (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs) {
+        if (!*abort_flag) record_error(err, CONVROT_ERR_TIMEOUT);
+        *abort_flag = 1;
+        ok = 0;
+        break;
+      }
+    }
+  }
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  return ok != 0 && mbar_try_wait(bar, parity);
+}
+
+// Adds f times the accumulator at `ta` (COLS columns of the warp's lanes) to acc.
+template <int COLS>
+__device__ __forceinline__ void drain(unsigned long long (&acc)[COLS / 2], uint32_t ta, unsigned long long f2) {
+  uint32_t r[2][16];
+  tmem_ld16(ta, r[0]);
 #pragma unroll
-    for (int i = 0; i < COLS / 2; ++i) {
-      const int n = n0 + 2 * i;
-      acc[i] = f32x2_pack(bias && n < N ? __ldg(bias + n) : 0.0f, bias && n + 1 < N ? __ldg(bias + n + 1) : 0.0f);
+  for (int q = 0; q < COLS / 16; ++q) {
+    tmem_wait16(r[q & 1]);
+    if (q + 1 < COLS / 16) tmem_ld16(ta + (q + 1) * 16, r[(q + 1) & 1]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      acc[q * 8 + k] = f32x2_fma(pair_bits(r[q & 1][2 * k], r[q & 1][2 * k + 1]), f2, acc[q * 8 + k]);
+  }
+}
+
+// The same with a factor per column, read from shared memory.
+template <int COLS>
+__device__ __forceinline__ void drain_scaled(unsigned long long (&acc)[COLS / 2], uint32_t ta, const float* f) {
+  uint32_t r[2][16];
+  tmem_ld16(ta, r[0]);
+#pragma unroll
+  for (int q = 0; q < COLS / 16; ++q) {
+    tmem_wait16(r[q & 1]);
+    if (q + 1 < COLS / 16) tmem_ld16(ta + (q + 1) * 16, r[(q + 1) & 1]);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const float4 s = *reinterpret_cast<const float4*>(f + q * 16 + 2 * k);
+      acc[q * 8 + k] = f32x2_fma(pair_bits(r[q & 1][2 * k], r[q & 1][2 * k + 1]), f32x2_pack(s.x, s.y), acc[q * 8 + k]);
+      acc[q * 8 + k + 1] =
+          f32x2_fma(pair_bits(r[q & 1][2 * k + 2], r[q & 1][2 * k + 3]), f32x2_pack(s.z, s.w), acc[q * 8 + k + 1]);
     }
   }
 }
@@ -241,8 +312,14 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
   uint64_t* empty = full + G::STAGES;
   uint64_t* tfull = empty + G::STAGES;
   uint64_t* tempty = tfull + G::BUFS;
-  uint64_t* drain = tempty + G::BUFS;
-  uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* done = tempty + G::BUFS;
+  uint64_t* ifull = done + 1;    // [2] a tile's info is in shared memory
+  uint64_t* iempty = ifull + 2;   // [2] and has been read
+  uint64_t* bfull = iempty + 2;   // the same for its bias
+  uint64_t* bempty = bfull + 1;
+  TileInfo* info = reinterpret_cast<TileInfo*>(smem + G::SMEM_INFO);
+  float* sbias = reinterpret_cast<float*>(smem + G::SMEM_BIAS);
+  uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(bempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -258,7 +335,13 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], EPI_WARPS * 2);
     }
-    mbar_init(drain, 1);
+    mbar_init(done, 1);
+    for (int e = 0; e < 2; ++e) {
+      mbar_init(&ifull[e], 1);
+      mbar_init(&iempty[e], EPI_WARPS);
+    }
+    mbar_init(bfull, 1);
+    mbar_init(bempty, EPI_WARPS);
     *abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&p.tmap_x);
@@ -307,20 +390,43 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       bool ok = true;
       for (int t = unit; ok && t < p.total_tiles; t += n_units) {
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err) ||
-              !mbar_wait(&full[stage], phase, abort_flag, err)) { ok = false; break; }
+          if (!mbar_wait(&full[stage], phase, abort_flag, err) ||
+              !mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sx = smem_u32(smem + stage * G::STAGE_BYTES);
           mma_block<2>(tmem_base + buf * BN, sx, sx + G::X_BYTES, G::IDESC);
-          mma_commit_pair(&empty[stage], 0x3u);
           mma_commit_pair(&tfull[buf], 0x3u);
+          mma_commit_pair(&empty[stage], 0x3u);
           if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
           if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
         }
       }
       // all issued MMAs complete before TMEM is released
-      mma_commit_pair(drain, 0x1u);
-      mbar_wait(drain, 0, nullptr, err);
+      mma_commit_pair(done, 0x1u);
+      mbar_wait(done, 0, nullptr, err);
+    }
+    if (warp == EPI_WARPS + 2) {
+      int i = 0;
+      for (int t = unit; t < p.total_tiles; t += n_units, ++i) {
+        const Tile c = decode(p, t);
+        const int N = p.N[c.lin], n0 = c.nt * BN;
+        const float* b = p.bias[c.lin];
+        float v[BN / 32];
+#pragma unroll
+        for (int k = 0; k < BN / 32; ++k) v[k] = b && n0 + 32 * k + lane < N ? __ldg(b + n0 + 32 * k + lane) : 0.0f;
+        if (!wait_slowly(&iempty[i & 1], ((i >> 1) & 1) ^ 1u, abort_flag, err)) break;
+        if (lane == 0) {
+          info[i & 1] = TileInfo{c.lin, c.mt * 256 + static_cast<int>(rank) * LANES, n0, N,
+                                 p.s_w[c.lin] + static_cast<int64_t>(n0 / QBLOCK) * p.KB};
+          mbar_arrive(&ifull[i & 1]);
+        }
+        __syncwarp();
+        if (!wait_slowly(bempty, (i & 1) ^ 1u, abort_flag, err)) break;
+#pragma unroll
+        for (int k = 0; k < BN / 32; ++k) sbias[32 * k + lane] = v[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bfull);
+      }
     }
     __syncwarp();
   } else {
@@ -331,88 +437,101 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
     uint8_t* sout = smem + G::SMEM_OUT + warp * STORE_BYTES;
     uint32_t buf = 0, bphase = 0;
     bool ok = true;
-    for (int t = unit; ok && t < p.total_tiles; t += n_units) {
-      const Tile c = decode(p, t);
-      const int N = p.N[c.lin];
-      const int r0 = c.mt * 256 + static_cast<int>(rank) * LANES + 32 * quarter;  // the warp's first row
-      const int n0 = c.nt * BN + half * COLS;                                     // and first feature
+    // a tile's info is read, and its first scales are loaded, before the
+    // stores of the tile before it
+    TileInfo c{};
+    const float *xs = nullptr, *ws = nullptr;
+    float nx[4], nw[4];
+    auto start = [&](int i) {  // the CTA's tile i
+      if (!mbar_wait(&ifull[i & 1], (i >> 1) & 1u, abort_flag, err)) return false;
+      c = info[i & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[i & 1]);
+      c.row += 32 * quarter;  // the warp's first row
+      c.col += half * COLS;   // and first feature
       // rows and features past the end read the last one's scales; their
       // outputs are not stored
-      const float* xs = p.s_x + static_cast<int64_t>(min(r0 + lane, p.M - 1)) * p.KB;
-      const float* ws = p.s_w[c.lin] + static_cast<int64_t>(min(n0, N - 1) / QBLOCK) * p.KB;
-      unsigned long long acc[COLS / 2];
-      init_acc<COLS>(acc, p.bias[c.lin], n0, N);
-      float nx[4], nw[4];  // the next four blocks' scales, loaded a group ahead
+      xs = p.s_x + static_cast<int64_t>(min(c.row + lane, p.M - 1)) * p.KB;
+      ws = c.ws + (BN > QBLOCK && half * COLS >= QBLOCK && c.col < c.N ? p.KB : 0);
       load_scales(xs, 0, p.KB, p.vec_scales, nx);
       load_scales(ws, 0, p.KB, p.vec_scales, nw);
-      for (int kb0 = 0; ok && kb0 < p.KB; kb0 += 4) {
-        float f[4];
+      return true;
+    };
+    int seq = 0, sbuf = 0;
+    if (unit < p.total_tiles) ok = start(0);
+    for (int t = unit; ok && t < p.total_tiles; t += n_units, ++seq) {
+      unsigned long long acc[COLS / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = nx[i] * nw[i];
-        if (kb0 + 4 < p.KB) {
-          load_scales(xs, kb0 + 4, p.KB, p.vec_scales, nx);
-          load_scales(ws, kb0 + 4, p.KB, p.vec_scales, nw);
-        }
+      for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
+      // One block of K a turn, not unrolled: the loop stays small enough for
+      // the instruction caches that it shares with the other warps.
+      float f[4];  // the factors of this block and the next three at most
+#pragma unroll 1
+      for (int kb = 0; kb < p.KB; ++kb) {
+        if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) { ok = false; break; }
+        tc_fence_after();
+        if ((kb & 3) == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (kb0 + i >= p.KB) break;
-          if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) { ok = false; break; }
-          tc_fence_after();
-          const unsigned long long f2 = f32x2_pack(f[i], f[i]);
-          const uint32_t ta = t_addr + buf * BN;
-          uint32_t r[2][16];
-          tmem_ld16(ta, r[0]);
-#pragma unroll
-          for (int q = 0; q < COLS / 16; ++q) {
-            tmem_wait16(r[q & 1]);
-            if (q + 1 < COLS / 16) tmem_ld16(ta + (q + 1) * 16, r[(q + 1) & 1]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              acc[q * 8 + k] = f32x2_fma(pair_bits(r[q & 1][2 * k], r[q & 1][2 * k + 1]), f2, acc[q * 8 + k]);
+          for (int i = 0; i < 4; ++i) f[i] = nx[i] * nw[i];
+          if (kb + 4 < p.KB) {
+            load_scales(xs, kb + 4, p.KB, p.vec_scales, nx);
+            load_scales(ws, kb + 4, p.KB, p.vec_scales, nw);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(tempty_leader + buf * 8u);
-          if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
         }
+        drain<COLS>(acc, t_addr + buf * BN, f32x2_pack(f[0], f[0]));
+        f[0] = f[1];
+        f[1] = f[2];
+        f[2] = f[3];
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_leader + buf * 8u);
+        if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
       }
       if (!ok) break;
+      const int lin = c.lin, N = c.N, y_row = c.row, y_col = c.col;
+      if (t + n_units < p.total_tiles) ok = start(seq + 1);
+      if (!mbar_wait(bfull, seq & 1u, abort_flag, err)) break;
       // store: PER features of a row at a time
       constexpr int PER = STORE_ROW / sizeof(TY);
       constexpr int E = 16 / sizeof(TY);  // of them in 16 bytes
 #pragma unroll
       for (int b = 0; b < COLS / PER; ++b) {
-        if (lane == 0) bulk_wait_read<0>();
+        // the two buffers in turn: the store before the last has been read
+        uint8_t* sb = sout + sbuf * STORE_BLOCK;
+        sbuf ^= 1;
+        if (lane == 0) bulk_wait_read<1>();
         __syncwarp();
 #pragma unroll
         for (int ch = 0; ch < PER / E; ++ch) {
           float v[E];
 #pragma unroll
           for (int k = 0; k < E; k += 2) f32x2_unpack(acc[(b * PER + ch * E + k) / 2], v[k], v[k + 1]);
-          *reinterpret_cast<uint4*>(sout + lane * STORE_ROW + (swizzled(ch, lane) << 4)) = pack16<TY>(v);
+#pragma unroll
+          for (int k = 0; k < E; k += 4) {
+            const float4 bb = *reinterpret_cast<const float4*>(sbias + half * COLS + b * PER + ch * E + k);
+            v[k] += bb.x;
+            v[k + 1] += bb.y;
+            v[k + 2] += bb.z;
+            v[k + 3] += bb.w;
+          }
+          *reinterpret_cast<uint4*>(sb + lane * STORE_ROW + (swizzled(ch, lane) << 4)) = pack16<TY>(v);
         }
-        const int n = n0 + b * PER;
+        const int n = y_col + b * PER;
         if (p.tma_y) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (n < N && r0 < p.M) tma_store_2d(&p.tmap_y[c.lin], sout, n, r0);
+            if (n < N && y_row < p.M) tma_store_2d(&p.tmap_y[lin], sb, n, y_row);
             bulk_commit();
           }
         } else {
           __syncwarp();
-          TY* Y = static_cast<TY*>(p.out[c.lin]);
-          const int rows = min(32, p.M - r0);
-          for (int r = 0; r < rows; ++r) {
-            TY* yr = Y + (r0 + r) * p.ldy[c.lin] + n;
-            for (int k = lane; k < PER && n + k < N; k += 32) {
-              const int byte = k * static_cast<int>(sizeof(TY));
-              yr[k] = *reinterpret_cast<const TY*>(sout + r * STORE_ROW + ((swizzled(byte >> 4, r) << 4) | (byte & 15)));
-            }
-          }
+          store_rows<TY>(sb, static_cast<TY*>(p.out[lin]) + y_row * p.ldy[lin] + n, p.ldy[lin], min(32, p.M - y_row), N - n);
           __syncwarp();
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bempty);
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -479,8 +598,8 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
   uint64_t* empty = full + G::STAGES;
   uint64_t* tfull = empty + G::STAGES;
   uint64_t* tempty = tfull + G::BUFS;
-  uint64_t* drain = tempty + G::BUFS;
-  uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* done = tempty + G::BUFS;
+  uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = &g_fp8_error;
@@ -499,7 +618,7 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 4);
     }
-    mbar_init(drain, 1);
+    mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&p.tmap_x);
@@ -515,6 +634,12 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
   const uint32_t tmem_base = *tmem_base_smem;
   pdl_wait_prerequisites();
   pdl_launch_dependents();
+  // the bias of this lane's four features, for the end
+  const int n = n0 + lane * 4;
+  const float* bias = p.bias[c.lin];
+  float bv[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) bv[k] = (bias && n + k < N) ? ldg_now(bias + n + k) : 0.0f;
 
   if (warp == 4) {
     if (lane == 0) {
@@ -548,8 +673,8 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
         if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
         if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
       }
-      mma_commit(drain);
-      mbar_wait(drain, 0, nullptr, err);
+      mma_commit(done);
+      mbar_wait(done, 0, nullptr, err);
     }
     __syncwarp();
   } else {
@@ -569,63 +694,45 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
 #pragma unroll
     for (int i = 0; i < BN / 2; ++i) acc[i] = 0ull;
     uint32_t buf = 0, bphase = 0;
-    bool ok = true;
     const bool vec = p.vec_scales && kb_begin % 4 == 0;
     float nx[XR][4], nw[4];
 #pragma unroll
     for (int i = 0; i < XR; ++i) load_scales(xs[i], kb_begin, p.KB, vec, nx[i]);
     load_scales(ws, kb_begin, p.KB, vec, nw);
-    int flip = 0;
-    for (int kb0 = kb_begin; ok && kb0 < kb_end; kb0 += 4) {
-      float f[4];
+    float f[4];
+    int flip = 1;
+#pragma unroll 1
+    for (int kb = kb_begin, i = 0; kb < kb_end; ++kb, i = (i + 1) & 3) {
+      if (i == 0) {  // the factors of four blocks; the next four's scales are on their way meanwhile
+        flip ^= 1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] = nx[0][i] * nw[i];
-        if (SWAP) {
+        for (int j = 0; j < 4; ++j) {
+          f[j] = nx[0][j] * nw[j];
+          if (SWAP) {
 #pragma unroll
-          for (int j = 0; j < XR; ++j)
-            if (BN >= 32 || lane < BN) sc[(flip * 4 + i) * BN + 32 * j + lane] = nx[j][i] * nw[i];
-        }
-      }
-      if (SWAP) __syncwarp();
-      if (kb0 + 4 < kb_end) {
-#pragma unroll
-        for (int i = 0; i < XR; ++i) load_scales(xs[i], kb0 + 4, p.KB, vec, nx[i]);
-        load_scales(ws, kb0 + 4, p.KB, vec, nw);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (kb0 + i >= kb_end) break;
-        if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) { ok = false; break; }
-        tc_fence_after();
-        const unsigned long long f2 = f32x2_pack(f[i], f[i]);
-        const float* s4 = sc + (flip * 4 + i) * BN;
-        const uint32_t ta = t_addr + buf * BN;
-        uint32_t r[2][16];
-        tmem_ld16(ta, r[0]);
-#pragma unroll
-        for (int q = 0; q < BN / 16; ++q) {
-          tmem_wait16(r[q & 1]);
-          if (q + 1 < BN / 16) tmem_ld16(ta + (q + 1) * 16, r[(q + 1) & 1]);
-#pragma unroll
-          for (int k = 0; k < 8; k += 2) {
-            unsigned long long fa = f2, fb = f2;
-            if (SWAP) {
-              const float4 s = *reinterpret_cast<const float4*>(s4 + q * 16 + 2 * k);
-              fa = f32x2_pack(s.x, s.y);
-              fb = f32x2_pack(s.z, s.w);
-            }
-            acc[q * 8 + k] = f32x2_fma(pair_bits(r[q & 1][2 * k], r[q & 1][2 * k + 1]), fa, acc[q * 8 + k]);
-            acc[q * 8 + k + 1] =
-                f32x2_fma(pair_bits(r[q & 1][2 * k + 2], r[q & 1][2 * k + 3]), fb, acc[q * 8 + k + 1]);
+            for (int k = 0; k < XR; ++k)
+              if (BN >= 32 || lane < BN) sc[(flip * 4 + j) * BN + 32 * k + lane] = nx[k][j] * nw[j];
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[buf]);
-        if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
+        if (SWAP) __syncwarp();
+        if (kb + 4 < kb_end) {
+#pragma unroll
+          for (int k = 0; k < XR; ++k) load_scales(xs[k], kb + 4, p.KB, vec, nx[k]);
+          load_scales(ws, kb + 4, p.KB, vec, nw);
+        }
       }
-      flip ^= 1;
+      if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) break;
+      tc_fence_after();
+      const uint32_t ta = t_addr + buf * BN;
+      if (SWAP) drain_scaled<BN>(acc, ta, sc + (flip * 4 + i) * BN);
+      else drain<BN>(acc, ta, f32x2_pack(f[0], f[0]));
+      f[0] = f[1];
+      f[1] = f[2];
+      f[2] = f[3];
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[buf]);
+      if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
     }
     // The partial tile, activation row by activation row. Every MMA of this
     // CTA has completed (the last block's commit was seen), so no stage is
@@ -657,11 +764,6 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
   }
   // one activation row of 128 features per warp at a time
   const int rows = min(G::TILE_ROWS, p.M - m0);
-  const int n = n0 + lane * 4;
-  const float* bias = p.bias[c.lin];
-  float bv[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) bv[k] = (bias && n + k < N) ? __ldg(bias + n + k) : 0.0f;
   TY* Y = static_cast<TY*>(p.out[c.lin]);
   const int64_t ldy = p.ldy[c.lin];
   const bool vec_out = n + 4 <= N && ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * sizeof(TY) - 1)) == 0;
