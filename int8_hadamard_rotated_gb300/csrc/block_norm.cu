@@ -45,7 +45,9 @@ struct NormParams {
   int rows_per_sample, n_samples;
   int post, pre;
   float post_eps, pre_eps, residual_scale, block_scale;
-  int stages;
+  // of the kernels for aligned rows
+  int warps_per_row, stages;
+  uint32_t coef_smem;  // bytes of the coefficients, a multiple of 128
   uint32_t row_smem;  // bytes of one staged row, a multiple of 128
 };
 
@@ -55,7 +57,7 @@ __device__ __forceinline__ int sample_of(const NormParams& p, int row) {
   if (p.row_sample) {
     const int s = __ldg(p.row_sample + row);
     if (s >= 0 && s < p.n_samples) return s;
-    if (threadIdx.x == 0) record_error(&g_norm_error, CONVROT_ERR_ARG);
+    record_error(&g_norm_error, CONVROT_ERR_ARG);
     return -1;
   }
   return p.rows_per_sample > 0 ? row / p.rows_per_sample : 0;
@@ -144,104 +146,359 @@ struct Stats {
   float mean, rstd;
 };
 
-// Statistics of a row of K elements spread over the CTA, V * 8 per thread
-// (units of eight, `on` where the unit lies inside the row). One barrier;
-// `red` holds 2 x 32 floats and alternates between two such buffers from one
-// call to the next, so that the reads after one barrier are over before the
-// next but one call writes.
-template <int V>
-__device__ __forceinline__ Stats row_stats(const float (&x)[V][8], const bool (&on)[V], int kind, float eps, int K,
-                                           int n_warp, float* red) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
+// Barrier of the W warps that share a row (one warp: only itself).
+__device__ __forceinline__ void group_sync(int W, int group) {
+  if (W == 1) __syncwarp();
+  else named_bar_sync(1 + group, W * 32);
+}
+
+// Sums of a and b over the group's warps, in warp order, from each warp's own
+// (the same in all lanes). `red` holds 2 floats per warp of the group and
+// alternates between two such buffers from one call to the next, so that the
+// reads after one barrier are over before the next but one call writes.
+__device__ __forceinline__ void group_sum2(float& a, float& b, int W, int group, int warp_in_group, float2* red) {
+  if (W == 1) return;
+  if ((threadIdx.x & 31) == 0) red[warp_in_group] = make_float2(a, b);
+  group_sync(W, group);
+  a = b = 0.0f;
+  for (int w = 0; w < W; ++w) {
+    const float2 v = red[w];
+    a += v.x;
+    b += v.y;
+  }
+}
+
+// Statistics of a row of K elements spread over a group of W warps; `get(u)`
+// yields a thread's unit u of eight (zeros past the end), `count(w)` the
+// elements that warp w of the group holds.
+template <int V, typename Get, typename Count>
+__device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float eps, int K, int W, int group,
+                                           int warp_in_group, float2* red) {
   Stats st{0.0f, 1.0f};
-  float acc = 0.0f;
+  float acc = 0.0f, none = 0.0f;
   if (kind == CONVROT_NORM_RMS) {
 #pragma unroll
-    for (int u = 0; u < V; ++u)
-      if (on[u]) {
+    for (int u = 0; u < V; ++u) {
+      float x[8];
+      get(u, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc = fmaf(x[u][i], x[u][i], acc);
-      }
+      for (int i = 0; i < 8; ++i) acc = fmaf(x[i], x[i], acc);
+    }
     acc = warp_sum(acc);
-    if (lane == 0) red[warp] = acc;
-    __syncthreads();
-    const float total = warp_sum(lane < n_warps ? red[lane] : 0.0f);
-    st.rstd = 1.0f / sqrtf(total / static_cast<float>(K) + eps);
+    group_sum2(acc, none, W, group, warp_in_group, red);
+    st.rstd = 1.0f / sqrtf(acc / static_cast<float>(K) + eps);
     return st;
   }
 #pragma unroll
-  for (int u = 0; u < V; ++u)
-    if (on[u]) {
+  for (int u = 0; u < V; ++u) {
+    float x[8];
+    get(u, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc += x[u][i];
-    }
-  const float sum = warp_sum(acc);
-  const float mean_w = n_warp > 0 ? sum / static_cast<float>(n_warp) : 0.0f;
+    for (int i = 0; i < 8; ++i) acc += x[i];
+  }
+  float sum = warp_sum(acc);
+  const int n = count(warp_in_group);
+  const float mean_w = n > 0 ? sum / static_cast<float>(n) : 0.0f;
   acc = 0.0f;
 #pragma unroll
-  for (int u = 0; u < V; ++u)
-    if (on[u]) {
+  for (int u = 0; u < V; ++u) {
+    float x[8];
+    const bool on = get(u, x);
+    if (on) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = x[u][i] - mean_w;
+        const float d = x[i] - mean_w;
         acc = fmaf(d, d, acc);
       }
     }
-  const float m2 = warp_sum(acc);
-  if (lane == 0) {
-    red[warp] = sum;
-    red[32 + warp] = m2;
   }
-  __syncthreads();
-  // lane w recomputes warp w's count and mean
-  int n_l = 0;
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int lo = (u * n_warps + lane) * 32 * 8;
-    if (lane < n_warps) n_l += min(max(K - lo, 0), 32 * 8);
+  float m2 = warp_sum(acc);
+  if (W == 1) {
+    st.mean = mean_w;
+  } else {
+    // the warps' sums and squared distances: around each warp's own mean,
+    // then that mean's distance from the row's
+    if ((threadIdx.x & 31) == 0) red[warp_in_group] = make_float2(sum, m2);
+    group_sync(W, group);
+    sum = m2 = 0.0f;
+    for (int w = 0; w < W; ++w) sum += red[w].x;
+    st.mean = sum / static_cast<float>(K);
+    for (int w = 0; w < W; ++w) {
+      const int nw = count(w);
+      const float d = nw > 0 ? red[w].x / static_cast<float>(nw) - st.mean : 0.0f;
+      m2 += fmaf(static_cast<float>(nw) * d, d, red[w].y);
+    }
   }
-  const float sum_l = lane < n_warps ? red[lane] : 0.0f;
-  const float m2_l = lane < n_warps ? red[32 + lane] : 0.0f;
-  st.mean = warp_sum(sum_l) / static_cast<float>(K);
-  const float d = n_l > 0 ? sum_l / static_cast<float>(n_l) - st.mean : 0.0f;
-  const float var = warp_sum(fmaf(static_cast<float>(n_l) * d, d, m2_l)) / static_cast<float>(K);
-  st.rstd = 1.0f / sqrtf(var + eps);
+  st.rstd = 1.0f / sqrtf(m2 / static_cast<float>(K) + eps);
   return st;
 }
 
-// Rows whose every part is a whole number of aligned 16-byte units.
+// The thread's part of a row, V units of eight features (unit u at e0 + u *
+// stride), from its arrival in shared memory to its last store: see the two
+// kernels that use it. The coefficients come from `post(u, e, a, b)` and
+// `pre(u, e, a, b)`; `loaded()` is called once the staged row has been read
+// and the group has passed a barrier.
+template <typename T, typename TU, int V, bool FP8, typename Post, typename Pre, typename Loaded>
+__device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh, const T* sy, int e0, int stride, int W,
+                                       int group, int wg, float2* red_post, float2* red_pre, Post post, Pre pre,
+                                       Loaded loaded) {
+  auto count = [&](int w) {  // features of the row that warp w of the group holds
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < V; ++u) n += min(max(p.K - u * stride - w * 32 * 8, 0), 32 * 8);
+    return n;
+  };
+  float x[V][8];
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    const int e = e0 + u * stride;
+    if (e < p.K) {
+      load8(sh + e, x[u]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[u][i] *= p.residual_scale;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[u][i] = 0.0f;
+    }
+  }
+  if (p.Y) {
+    Stats ps{0.0f, 1.0f};
+    if (p.post != CONVROT_NORM_NONE) {
+      auto get = [&](int u, float (&v)[8]) {
+        const int e = e0 + u * stride;
+        if (e < p.K) {
+          load8(sy + e, v);
+          return true;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        return false;
+      };
+      ps = row_stats<V>(get, count, p.post, p.post_eps, p.K, W, group, wg, red_post);
+    }
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const int e = e0 + u * stride;
+      if (e < p.K) {
+        float y[8], a[8], b[8];
+        load8(sy + e, y);
+        post(u, e, a, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] = fmaf((y[i] - ps.mean) * ps.rstd, a[i], x[u][i] + b[i]);
+      }
+    }
+  }
+  group_sync(W, group);
+  loaded();
+  if (p.H_out) {
+    T* out = static_cast<T*>(p.H_out) + row * p.ldho;
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      if (e0 + u * stride < p.K) store8(out + e0 + u * stride, x[u]);
+  }
+  if (!FP8 && !p.U) return;
+  Stats us{0.0f, 1.0f};
+  if (p.pre != CONVROT_NORM_NONE) {
+    auto get = [&](int u, float (&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x[u][i];
+      return e0 + u * stride < p.K;
+    };
+    us = row_stats<V>(get, count, p.pre, p.pre_eps, p.K, W, group, wg, red_pre);
+  }
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    const int e = e0 + u * stride;
+    if (e < p.K) {
+      float a[8], b[8];
+      pre(u, e, a, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[u][i] = fmaf((x[u][i] - us.mean) * us.rstd, a[i], b[i]);
+    }
+    if (FP8) {
+      // sixteen lanes hold a block of 128
+      float m = fabsf(x[u][0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(x[u][i]));
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float sc = e4m3_scale(m);
+      uint32_t c[2];
+      e4m3_codes(x[u], sc, c);
+      if (e < p.K) {
+        *reinterpret_cast<uint2*>(p.Q + static_cast<int64_t>(row) * p.K + e) = make_uint2(c[0], c[1]);
+        if ((threadIdx.x & 15) == 0) p.s[static_cast<int64_t>(row) * p.KB + e / QBLOCK] = sc;
+      }
+    } else if (e < p.K) {
+      store8(static_cast<TU*>(p.U) + row * p.ldu + e, x[u]);
+    }
+  }
+}
+
+// A ring of staged rows of h and y: one lane issues bulk copies a few rows
+// ahead, so that enough bytes are in flight whatever the sums wait for.
+template <typename T>
+struct Ring {
+  const NormParams& p;
+  uint8_t* smem;
+  uint64_t* full;
+  int st = 0, phase = 0;
+  __device__ uint32_t stage_bytes() const { return p.row_smem * (p.Y ? 2u : 1u); }
+  __device__ void fetch(int row, int stage) {
+    const uint32_t bytes = static_cast<uint32_t>(p.K) * sizeof(T);
+    uint8_t* dst = smem + stage * stage_bytes();
+    mbar_arrive_expect_tx(&full[stage], bytes * (p.Y ? 2u : 1u));
+    bulk_load(dst, static_cast<const T*>(p.H) + row * p.ldh, bytes, &full[stage]);
+    if (p.Y) bulk_load(dst + p.row_smem, static_cast<const T*>(p.Y) + row * p.ldy, bytes, &full[stage]);
+  }
+  __device__ const T* h() const { return reinterpret_cast<const T*>(smem + st * stage_bytes()); }
+  __device__ const T* y() const { return reinterpret_cast<const T*>(smem + st * stage_bytes() + p.row_smem); }
+  __device__ void next() {
+    if (++st == p.stages) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+constexpr int WARPS = 8;  // per CTA of the grouped kernel
+constexpr int MAX_STAGES = 8;
+
+// Rows whose every part is a whole number of aligned 16-byte units, and whose
+// coefficients fit in shared memory.
 //
-// Persistent CTAs, each over a contiguous range of rows, one row at a time
-// with V units of eight features per thread (unit u * blockDim + thread), the
-// row in registers from its arrival to its last store. The rows of h and y
-// come through a ring of shared-memory stages, filled by bulk copies that one
-// thread issues several rows ahead, so that enough bytes are in flight
-// whatever the reductions wait for; a stage is refilled after the row's first
-// barrier, when every thread holds its part. With V = 1 a thread's
-// coefficients (norm weights, gate, modulation) stay in registers and are
-// read again only when the sample changes.
+// W warps share a row (1, 2, 4 or 8; a CTA has 8 / W such groups), so that a
+// lane has up to 96 features to spread the per-row work (sums over lanes and
+// warps, square roots) over. CTAs are persistent, each over a contiguous range
+// of rows, its groups taking them in turn; the affine coefficients of the
+// current sample (norm weights, gate and modulation folded, only those that
+// are not 0 or 1) lie in shared memory, the two halves of every unit of eight
+// apart so that a warp reads them without bank conflicts, and are formed again
+// when the sample changes.
+//
+// (One thread block per row with one unit per thread and its coefficients in
+// registers: 49 us for bf16 [4608, 3072] with gate, LayerNorm and modulation,
+// 53 instructions per feature, most of them per row and thread; coefficients
+// read through L1 for every row: 60 us.)
 template <typename T, typename TU, int V, bool FP8>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(WARPS * 32, V <= 2 ? 3 : V <= 4 ? 2 : 1)
 block_norm_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full[8];
-  __shared__ float red[2][64];
+  __shared__ __align__(8) uint64_t full[WARPS * MAX_STAGES];
+  __shared__ float2 red[2][WARPS];
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, n_warps = blockDim.x >> 5;
-  const uint32_t row_bytes = static_cast<uint32_t>(p.K) * sizeof(T);
-  const uint32_t stage_bytes = p.row_smem * (p.Y ? 2u : 1u);
-  const int r0 = static_cast<int>(static_cast<int64_t>(p.M) * blockIdx.x / gridDim.x);
-  const int r1 = static_cast<int>(static_cast<int64_t>(p.M) * (blockIdx.x + 1) / gridDim.x);
-  const T* H = static_cast<const T*>(p.H);
-  const T* Y = static_cast<const T*>(p.Y);
-  auto fetch = [&](int row, int st) {
-    uint8_t* dst = smem + st * stage_bytes;
-    mbar_arrive_expect_tx(&full[st], row_bytes * (Y ? 2u : 1u));
-    bulk_load(dst, H + row * p.ldh, row_bytes, &full[st]);
-    if (Y) bulk_load(dst + p.row_smem, Y + row * p.ldy, row_bytes, &full[st]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int W = p.warps_per_row, G = WARPS / W, group = warp / W, wg = warp - group * W;
+  const int c0 = static_cast<int>(static_cast<int64_t>(p.M) * blockIdx.x / gridDim.x);
+  const int c1 = static_cast<int>(static_cast<int64_t>(p.M) * (blockIdx.x + 1) / gridDim.x);
+  const int half = p.K / 2, n_coef = p.K;  // floats: a coefficient vector as two halves
+  const bool has_pa = p.Y && (p.gate || p.post_weight), has_pb = p.Y && p.post_bias;
+  const bool has_qa = p.pre_weight || p.scale, has_qb = p.pre_bias || p.shift;
+  float* cpa = reinterpret_cast<float*>(smem);
+  float* cpb = cpa + (has_pa ? n_coef : 0);
+  float* cqa = cpb + (has_pb ? n_coef : 0);
+  float* cqb = cqa + (has_qa ? n_coef : 0);
+  Ring<T> ring{p, smem + p.coef_smem, full + group * MAX_STAGES};
+  ring.smem += group * p.stages * ring.stage_bytes();
+  const bool leader = wg == 0 && lane == 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < WARPS * MAX_STAGES; ++i) mbar_init(&full[i], 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  int row = c0 + group;  // the group's next row
+  if (leader)
+    for (int i = 0; i < p.stages && row + i * G < c1; ++i) ring.fetch(row + i * G, i);
+
+  auto put = [&](float* c, int unit, const float (&v)[8]) {
+    *reinterpret_cast<float4*>(c + unit * 4) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(c + half + unit * 4) = make_float4(v[4], v[5], v[6], v[7]);
   };
+  auto take = [&](const float* c, bool has, int e, float otherwise, float (&v)[8]) {
+    if (has) {
+      const float4 a = *reinterpret_cast<const float4*>(c + e / 2), b = *reinterpret_cast<const float4*>(c + half + e / 2);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = otherwise;
+    }
+  };
+  const int stride = W * 32 * 8;
+  for (int start = c0; start < c1;) {
+    // the rows from `start` on that share its sample
+    const int s = sample_of(p, start);
+    int end = c1;
+    if (p.row_sample) {
+      for (end = start + 1; end < c1; end += 32) {
+        const unsigned other = __ballot_sync(0xffffffffu, end + lane >= c1 || sample_of(p, end + lane) != s);
+        if (other) {
+          end = min(c1, end + __ffs(other) - 1);
+          break;
+        }
+      }
+      end = min(end, c1);
+    } else if (p.rows_per_sample > 0) {
+      end = static_cast<int>(min(static_cast<int64_t>(c1), (static_cast<int64_t>(s) + 1) * p.rows_per_sample));
+    }
+    if (has_pa || has_pb || has_qa || has_qb) {
+      __syncthreads();  // the rows before may still read theirs
+      for (int unit = threadIdx.x; unit < p.K / 8; unit += WARPS * 32) {
+        float a[8], b[8];
+        if (has_pa || has_pb) {
+          post_coef8(p, s, unit * 8, a, b);
+          if (has_pa) put(cpa, unit, a);
+          if (has_pb) put(cpb, unit, b);
+        }
+        pre_coef8(p, s, unit * 8, a, b);
+        if (has_qa) put(cqa, unit, a);
+        if (has_qb) put(cqb, unit, b);
+      }
+      __syncthreads();
+    }
+    for (; row < end; row += G) {
+      mbar_wait(&ring.full[ring.st], ring.phase, &abort_flag, &g_norm_error);
+      do_row<T, TU, V, FP8>(
+          p, row, ring.h(), ring.y(), (wg * 32 + lane) * 8, stride, W, group, wg, red[0] + group * W,
+          red[1] + group * W,
+          [&](int, int e, float (&a)[8], float (&b)[8]) {
+            take(cpa, has_pa, e, p.block_scale, a);
+            take(cpb, has_pb, e, 0.0f, b);
+          },
+          [&](int, int e, float (&a)[8], float (&b)[8]) {
+            take(cqa, has_qa, e, 1.0f, a);
+            take(cqb, has_qb, e, 0.0f, b);
+          },
+          [&] {
+            if (leader && row + p.stages * G < c1) ring.fetch(row + p.stages * G, ring.st);
+          });
+      ring.next();
+    }
+    start = end;
+  }
+}
+
+// The same for rows whose coefficients do not fit beside the staged rows: one
+// row per CTA of up to sixteen warps, at most 32 features per thread; a
+// thread's weights and scales stay in registers while the sample stays.
+constexpr int WIDE_WARPS = 16;
+
+template <typename T, typename TU, int V, bool FP8>
+__global__ void __launch_bounds__(WIDE_WARPS * 32, 1)
+block_norm_wide_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[MAX_STAGES];
+  __shared__ float2 red[2][WIDE_WARPS];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const int c0 = static_cast<int>(static_cast<int64_t>(p.M) * blockIdx.x / gridDim.x);
+  const int c1 = static_cast<int>(static_cast<int64_t>(p.M) * (blockIdx.x + 1) / gridDim.x);
+  Ring<T> ring{p, smem, full};
   if (tid == 0) {
-    for (int i = 0; i < p.stages; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < MAX_STAGES; ++i) mbar_init(&full[i], 1);
     abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -249,120 +506,49 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   if (tid == 0)
-    for (int i = 0; i < p.stages && r0 + i < r1; ++i) fetch(r0 + i, i);
-
-  bool on[V];
-  int n_warp = 0;  // elements of the row that this warp holds
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    on[u] = (u * static_cast<int>(blockDim.x) + tid) * 8 < p.K;
-    n_warp += min(max(p.K - (u * n_warps + (tid >> 5)) * 32 * 8, 0), 32 * 8);
-  }
-  float pa[8], pb[8], qa[8], qb[8];  // V = 1: the thread's coefficients of sample `cur`
+    for (int i = 0; i < p.stages && c0 + i < c1; ++i) ring.fetch(c0 + i, i);
+  const int W = blockDim.x >> 5, stride = blockDim.x * 8;
+  float pa[V][8], qa[V][8];
   int cur = -2;
-  int st = 0, phase = 0, flip = 0;
-  for (int row = r0; row < r1; ++row) {
+  for (int row = c0; row < c1; ++row) {
     const int s = sample_of(p, row);
-    if (V == 1 && s != cur) {
+    if (s != cur) {
       cur = s;
-      if (on[0]) {
-        if (Y) post_coef8(p, s, tid * 8, pa, pb);
-        pre_coef8(p, s, tid * 8, qa, qb);
-      }
-    }
-    float h[V][8], y[V][8];
-    mbar_wait(&full[st], phase, &abort_flag, &g_norm_error);
-    const T* sh = reinterpret_cast<const T*>(smem + st * stage_bytes);
-    const T* sy = reinterpret_cast<const T*>(smem + st * stage_bytes + p.row_smem);
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-      const int e = (u * blockDim.x + tid) * 8;
-      if (on[u]) {
-        load8(sh + e, h[u]);
-        if (Y) load8(sy + e, y[u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[u][i] = y[u][i] = 0.0f;
-      }
-    }
-    // the next row of this stage, once a barrier has passed that follows every read above
-    auto refill = [&] {
-      if (tid == 0 && row + p.stages < r1) fetch(row + p.stages, st);
-    };
-    bool refilled = false;
-    if (Y) {
-      Stats ps{0.0f, 1.0f};
-      if (p.post != CONVROT_NORM_NONE) {
-        ps = row_stats<V>(y, on, p.post, p.post_eps, p.K, n_warp, red[flip]);
-        flip ^= 1;
-        refill();
-        refilled = true;
-      }
-#pragma unroll
-      for (int u = 0; u < V; ++u)
-        if (on[u]) {
-          if (V > 1) post_coef8(p, s, (u * blockDim.x + tid) * 8, pa, pb);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            h[u][i] = fmaf((y[u][i] - ps.mean) * ps.rstd, pa[i], fmaf(p.residual_scale, h[u][i], pb[i]));
-        }
-    } else {
-#pragma unroll
-      for (int u = 0; u < V; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[u][i] *= p.residual_scale;
-    }
-    if (p.H_out) {
-      T* out = static_cast<T*>(p.H_out) + row * p.ldho;
-#pragma unroll
-      for (int u = 0; u < V; ++u)
-        if (on[u]) store8(out + (u * blockDim.x + tid) * 8, h[u]);
-    }
-    Stats us{0.0f, 1.0f};
-    if (p.pre != CONVROT_NORM_NONE) {
-      us = row_stats<V>(h, on, p.pre, p.pre_eps, p.K, n_warp, red[flip]);
-      flip ^= 1;
-      if (!refilled) refill();
-    } else if (!refilled) {
-      __syncthreads();
-      refill();
-    }
-    if (FP8 || p.U) {
 #pragma unroll
       for (int u = 0; u < V; ++u) {
-        const int e = (u * blockDim.x + tid) * 8;
-        float o[8];
-        if (on[u]) {
-          if (V > 1) pre_coef8(p, s, e, qa, qb);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = fmaf((h[u][i] - us.mean) * us.rstd, qa[i], qb[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-        }
-        if (FP8) {
-          // sixteen lanes hold a block of 128
-          float m = fabsf(o[0]);
-#pragma unroll
-          for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(o[i]));
-#pragma unroll
-          for (int d = 1; d < 16; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-          const float sc = e4m3_scale(m);
-          uint32_t c[2];
-          e4m3_codes(o, sc, c);
-          if (on[u]) {
-            *reinterpret_cast<uint2*>(p.Q + static_cast<int64_t>(row) * p.K + e) = make_uint2(c[0], c[1]);
-            if ((tid & 15) == 0) p.s[static_cast<int64_t>(row) * p.KB + e / QBLOCK] = sc;
-          }
-        } else if (on[u]) {
-          store8(static_cast<TU*>(p.U) + row * p.ldu + e, o);
+        const int e = tid * 8 + u * stride;
+        float b[8];
+        if (e < p.K) {
+          if (p.Y) post_coef8(p, s, e, pa[u], b);
+          pre_coef8(p, s, e, qa[u], b);
         }
       }
     }
-    if (++st == p.stages) {
-      st = 0;
-      phase ^= 1;
-    }
+    mbar_wait(&ring.full[ring.st], ring.phase, &abort_flag, &g_norm_error);
+    do_row<T, TU, V, FP8>(
+        p, row, ring.h(), ring.y(), tid * 8, stride, W, 0, warp, red[0], red[1],
+        [&](int u, int e, float (&a)[8], float (&b)[8]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] = pa[u][i];
+          float c[8];
+          if (p.post_bias) post_coef8(p, s, e, c, b);
+          else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+        },
+        [&](int u, int e, float (&a)[8], float (&b)[8]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] = qa[u][i];
+          float c[8];
+          if (p.pre_bias || p.shift) pre_coef8(p, s, e, c, b);
+          else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+        },
+        [&] {
+          if (tid == 0 && row + p.stages < c1) ring.fetch(row + p.stages, ring.st);
+        });
+    ring.next();
   }
 }
 
@@ -456,8 +642,6 @@ block_norm_any_kernel(const __grid_constant__ NormParams p) {
 }
 
 constexpr int MAX_SMEM = 227 * 1024 - 2048;
-constexpr size_t RING_BYTES = 48 * 1024;  // of staged rows that a CTA keeps in flight, where they fit
-
 // Shared memory beyond 48 KB, once per kernel and device.
 template <typename F>
 int allow_smem(F* kernel, uint64_t& done, std::mutex& mu) {
@@ -480,37 +664,69 @@ int launch_rows(F* kernel, const NormParams& p, unsigned grid, unsigned threads,
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
+size_t stage_bytes(const NormParams& p) { return static_cast<size_t>(p.row_smem) * (p.Y ? 2 : 1); }
+
 template <typename T, typename TU, int V, bool FP8>
-int launch_vec(NormParams& p, int threads, cudaStream_t stream) {
+int launch_grouped(NormParams& p, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;
   auto kernel = block_norm_kernel<T, TU, V, FP8>;
   if (int st = allow_smem(kernel, done, mu)) return st;
-  const size_t stage = static_cast<size_t>(p.row_smem) * (p.Y ? 2 : 1);
-  p.stages = static_cast<int>(std::min<size_t>(8, std::max<size_t>(2, RING_BYTES / stage)));
-  while (p.stages > 1 && p.stages * stage > MAX_SMEM) --p.stages;
-  const size_t smem = p.stages * stage;
-  const int sms = device_sm_count();
-  int per_sm = 1;
-  if (p.M > sms) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
-    if (e != cudaSuccess) return set_cuda_error(e);
+  const int groups = WARPS / p.warps_per_row, sms = device_sm_count();
+  const size_t stage = stage_bytes(p) * groups;
+  // as many CTAs per SM as the registers allow while each keeps two rows per
+  // group in flight; then as many rows as fit
+  int per_sm = V <= 2 ? 3 : V <= 4 ? 2 : 1;
+  auto room = [&](int n) { return static_cast<size_t>(MAX_SMEM) / n - (n > 1 ? 2048 : 0); };
+  while (per_sm > 1 && p.coef_smem + 2 * stage > room(per_sm)) --per_sm;
+  p.stages = static_cast<int>(std::min<size_t>(MAX_STAGES, (room(per_sm) - p.coef_smem) / stage));
+  const int64_t ctas = (static_cast<int64_t>(p.M) + groups - 1) / groups;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ctas, static_cast<int64_t>(per_sm) * sms));
+  return launch_rows(kernel, p, grid, WARPS * 32, p.coef_smem + p.stages * stage, stream);
+}
+
+template <typename T, typename TU, int V, bool FP8>
+int launch_wide(NormParams& p, cudaStream_t stream) {
+  static std::mutex mu;
+  static uint64_t done = 0;
+  auto kernel = block_norm_wide_kernel<T, TU, V, FP8>;
+  if (int st = allow_smem(kernel, done, mu)) return st;
+  p.stages = static_cast<int>(std::min<size_t>(MAX_STAGES, MAX_SMEM / stage_bytes(p)));
+  const int threads = ((p.K / 8 + V - 1) / V + 31) / 32 * 32;
+  const unsigned grid = static_cast<unsigned>(std::min(p.M, device_sm_count()));
+  return launch_rows(kernel, p, grid, threads, p.stages * stage_bytes(p), stream);
+}
+
+// Warps per row of the grouped kernel: enough that a lane has at most 12
+// units and that two rows of every group fit beside the coefficients, and more
+// while there are fewer rows than groups on the GPU. 0: nothing fits.
+int pick_warps(const NormParams& p) {
+  const int units = p.K / 8;
+  const int64_t sms = device_sm_count();
+  for (int W = 1; W <= WARPS; W *= 2) {
+    if (units > 12 * 32 * W || p.coef_smem + 2 * stage_bytes(p) * (WARPS / W) > MAX_SMEM) continue;
+    if (W < WARPS && units > 32 * W && p.M * static_cast<int64_t>(W) * 2 <= sms * WARPS) continue;
+    return W;
   }
-  const int grid = std::min(p.M, std::max(1, per_sm) * sms);
-  return launch_rows(kernel, p, grid, threads, smem, stream);
+  return 0;
 }
 
 template <typename T, typename TU, bool FP8>
 int launch_typed(NormParams& p, bool vec, cudaStream_t stream) {
   const int units = (p.K + 7) / 8;
-  const size_t stage = static_cast<size_t>(p.row_smem) * (p.Y ? 2 : 1);
-  if (vec && units <= 4 * 512 && stage <= MAX_SMEM) {
-    const int v = (units + 511) / 512;
-    const int threads = ((units + v - 1) / v + 31) / 32 * 32;
-    if (v == 1) return launch_vec<T, TU, 1, FP8>(p, threads, stream);
-    if (v == 2) return launch_vec<T, TU, 2, FP8>(p, threads, stream);
-    if (v == 3) return launch_vec<T, TU, 3, FP8>(p, threads, stream);
-    return launch_vec<T, TU, 4, FP8>(p, threads, stream);
+  if (const int W = vec ? pick_warps(p) : 0) {
+    p.warps_per_row = W;
+    const int v = (units + 32 * W - 1) / (32 * W);
+    if (v <= 1) return launch_grouped<T, TU, 1, FP8>(p, stream);
+    if (v <= 2) return launch_grouped<T, TU, 2, FP8>(p, stream);
+    if (v <= 4) return launch_grouped<T, TU, 4, FP8>(p, stream);
+    if (v <= 6) return launch_grouped<T, TU, 6, FP8>(p, stream);
+    return launch_grouped<T, TU, 12, FP8>(p, stream);
+  }
+  if (vec && units <= 4 * WIDE_WARPS * 32 && stage_bytes(p) <= MAX_SMEM) {
+    if (units <= 2 * WIDE_WARPS * 32) return launch_wide<T, TU, 2, FP8>(p, stream);
+    if (units <= 3 * WIDE_WARPS * 32) return launch_wide<T, TU, 3, FP8>(p, stream);
+    return launch_wide<T, TU, 4, FP8>(p, stream);
   }
   static std::mutex mu;
   static uint64_t done = 0;
@@ -566,6 +782,9 @@ int launch_block_norm(const convrot_block_norm_args& a, cudaStream_t stream) {
   p.block_scale = a.block_scale;
   const size_t sz = dtype_size(a.dtype), usz = dtype_size(a.u_dtype);
   p.row_smem = static_cast<uint32_t>((a.K * sz + 127) / 128 * 128);
+  const int n_coef = (a.Y && (a.gate || a.post_weight)) + (a.Y && a.post_bias) + (a.pre_weight || a.scale) +
+                     (a.pre_bias || a.shift);
+  p.coef_smem = static_cast<uint32_t>((n_coef * a.K * 4 + 127) / 128 * 128);
   auto row_ok = [](const void* ptr, int64_t ld, size_t size) { return !ptr || (aligned16(ptr) && ld * size % 16 == 0); };
   const bool vec = a.K % 8 == 0 && row_ok(a.H, a.ldh, sz) && row_ok(a.Y, a.ldy, sz) && row_ok(a.H_out, a.ldho, sz) &&
                    row_ok(a.U, a.ldu, usz) && row_ok(a.gate, a.ld_gate, 4) && row_ok(a.scale, a.ld_mod, 4) &&
