@@ -44,7 +44,7 @@ struct NormParams {
   int M, K, KB;
   int rows_per_sample, n_samples;
   int post, pre;
-  float post_eps, pre_eps, residual_scale, block_scale;
+  float post_eps, pre_eps, residual_scale, block_scale, inv_k;
   // of the kernels for aligned rows
   int warps_per_row, stages;
   uint32_t coef_smem;  // bytes of the coefficients, a multiple of 128
@@ -94,50 +94,53 @@ __device__ __forceinline__ Coef pre_coef(const NormParams& p, int s, int e) {
   return c;
 }
 
-__device__ __forceinline__ void load8_vec(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
+__device__ __forceinline__ Pair both(float v) { return f32x2_pack(v, v); }
+
 // The same for eight consecutive features at a 16-byte aligned place.
-__device__ __forceinline__ void post_coef8(const NormParams& p, int s, int e, float (&a)[8], float (&b)[8]) {
-  float v[8];
+__device__ __forceinline__ void post_coef8(const NormParams& p, int s, int e, Pair (&a)[4], Pair (&b)[4]) {
+  Pair v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) { a[i] = p.block_scale; b[i] = 0.0f; }
+  for (int i = 0; i < 4; ++i) { a[i] = both(p.block_scale); b[i] = 0ull; }
   if (p.gate) {
-    if (s >= 0) load8_vec(p.gate + s * p.ld_gate + e, v);
+    if (s >= 0) load8(p.gate + s * p.ld_gate + e, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] *= s < 0 ? 0.0f : v[i];
+    for (int i = 0; i < 4; ++i) a[i] = s < 0 ? 0ull : f32x2_mul(a[i], v[i]);
   }
   if (p.post_bias) {
-    load8_vec(p.post_bias + e, v);
+    load8(p.post_bias + e, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = a[i] * v[i];
+    for (int i = 0; i < 4; ++i) b[i] = f32x2_mul(a[i], v[i]);
   }
   if (p.post_weight) {
-    load8_vec(p.post_weight + e, v);
+    load8(p.post_weight + e, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] *= v[i];
+    for (int i = 0; i < 4; ++i) a[i] = f32x2_mul(a[i], v[i]);
   }
 }
-__device__ __forceinline__ void pre_coef8(const NormParams& p, int s, int e, float (&a)[8], float (&b)[8]) {
-  float v[8];
+__device__ __forceinline__ void pre_coef8(const NormParams& p, int s, int e, Pair (&a)[4], Pair (&b)[4]) {
+  Pair v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) { a[i] = 1.0f; b[i] = 0.0f; }
-  if (p.pre_weight) load8_vec(p.pre_weight + e, a);
-  if (p.pre_bias) load8_vec(p.pre_bias + e, b);
+  for (int i = 0; i < 4; ++i) { a[i] = both(1.0f); b[i] = 0ull; }
+  if (p.pre_weight) load8(p.pre_weight + e, a);
+  if (p.pre_bias) load8(p.pre_bias + e, b);
   if (p.scale && s >= 0) {
-    load8_vec(p.scale + s * p.ld_mod + e, v);
+    load8(p.scale + s * p.ld_mod + e, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      a[i] *= 1.0f + v[i];
-      b[i] *= 1.0f + v[i];
+    for (int i = 0; i < 4; ++i) {
+      v[i] = add2(v[i], both(1.0f));
+      a[i] = f32x2_mul(a[i], v[i]);
+      b[i] = f32x2_mul(b[i], v[i]);
     }
   }
   if (p.shift && s >= 0) {
-    load8_vec(p.shift + s * p.ld_mod + e, v);
+    load8(p.shift + s * p.ld_mod + e, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] += v[i];
+    for (int i = 0; i < 4; ++i) b[i] = add2(b[i], v[i]);
   }
 }
 
@@ -168,51 +171,65 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, int W, int group,
   }
 }
 
-// Statistics of a row of K elements spread over a group of W warps; `get(u)`
-// yields a thread's unit u of eight (zeros past the end), `count(w)` the
-// elements that warp w of the group holds.
+// 1 / sqrt(v): the hardware's approximation (relative error under 2^-22) and
+// one Newton step, which squares it; 0 and infinity are kept as they are.
+__device__ __forceinline__ float inverse_root(float v) {
+  float r;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  const float better = fmaf(fmaf(-v * r, r, 1.0f), 0.5f * r, r);
+  return (r > 0.0f && r < INFINITY) ? better : r;
+}
+
+// Statistics of a row of K elements spread over a group of W warps; `get(u,
+// x)` yields a thread's unit u of eight (zeros past the end, and whether it
+// lies inside), `count(w)` the elements that warp w of the group holds.
 template <int V, typename Get, typename Count>
-__device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float eps, int K, int W, int group,
+__device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float eps, int K, float inv_k, int W, int group,
                                            int warp_in_group, float2* red) {
   Stats st{0.0f, 1.0f};
-  float acc = 0.0f, none = 0.0f;
+  auto total = [](const Pair (&acc)[2]) {
+    float a, b;
+    f32x2_unpack(add2(acc[0], acc[1]), a, b);
+    return warp_sum(a + b);
+  };
+  Pair acc[2] = {0ull, 0ull};
   if (kind == CONVROT_NORM_RMS) {
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      float x[8];
+      Pair x[4];
       get(u, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc = fmaf(x[i], x[i], acc);
+      for (int i = 0; i < 4; ++i) acc[i & 1] = f32x2_fma(x[i], x[i], acc[i & 1]);
     }
-    acc = warp_sum(acc);
-    group_sum2(acc, none, W, group, warp_in_group, red);
-    st.rstd = 1.0f / sqrtf(acc / static_cast<float>(K) + eps);
+    float sum = total(acc), none = 0.0f;
+    group_sum2(sum, none, W, group, warp_in_group, red);
+    st.rstd = inverse_root(fmaf(sum, inv_k, eps));
     return st;
   }
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    float x[8];
+    Pair x[4];
     get(u, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc += x[i];
+    for (int i = 0; i < 4; ++i) acc[i & 1] = add2(acc[i & 1], x[i]);
   }
-  float sum = warp_sum(acc);
+  float sum = total(acc);
   const int n = count(warp_in_group);
   const float mean_w = n > 0 ? sum / static_cast<float>(n) : 0.0f;
-  acc = 0.0f;
+  const Pair minus = both(-mean_w);
+  acc[0] = acc[1] = 0ull;
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    float x[8];
-    const bool on = get(u, x);
-    if (on) {
+    Pair x[4];
+    if (get(u, x)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = x[i] - mean_w;
-        acc = fmaf(d, d, acc);
+      for (int i = 0; i < 4; ++i) {
+        const Pair d = add2(x[i], minus);
+        acc[i & 1] = f32x2_fma(d, d, acc[i & 1]);
       }
     }
   }
-  float m2 = warp_sum(acc);
+  float m2 = total(acc);
   if (W == 1) {
     st.mean = mean_w;
   } else {
@@ -229,7 +246,7 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
       m2 += fmaf(static_cast<float>(nw) * d, d, red[w].y);
     }
   }
-  st.rstd = 1.0f / sqrtf(m2 / static_cast<float>(K) + eps);
+  st.rstd = inverse_root(fmaf(m2, inv_k, eps));
   return st;
 }
 
@@ -248,43 +265,52 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
     for (int u = 0; u < V; ++u) n += min(max(p.K - u * stride - w * 32 * 8, 0), 32 * 8);
     return n;
   };
-  float x[V][8];
+  auto normalized = [](Pair x, const Stats& st) { return f32x2_mul(add2(x, both(-st.mean)), both(st.rstd)); };
+  Pair x[V][4];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const int e = e0 + u * stride;
     if (e < p.K) {
       load8(sh + e, x[u]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] *= p.residual_scale;
+      for (int i = 0; i < 4; ++i) x[u][i] = f32x2_mul(x[u][i], both(p.residual_scale));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) x[u][i] = 0ull;
     }
   }
   if (p.Y) {
     Stats ps{0.0f, 1.0f};
     if (p.post != CONVROT_NORM_NONE) {
-      auto get = [&](int u, float (&v)[8]) {
+      auto get = [&](int u, Pair (&v)[4]) {
         const int e = e0 + u * stride;
         if (e < p.K) {
           load8(sy + e, v);
           return true;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int i = 0; i < 4; ++i) v[i] = 0ull;
         return false;
       };
-      ps = row_stats<V>(get, count, p.post, p.post_eps, p.K, W, group, wg, red_post);
+      ps = row_stats<V>(get, count, p.post, p.post_eps, p.K, p.inv_k, W, group, wg, red_post);
     }
 #pragma unroll
     for (int u = 0; u < V; ++u) {
       const int e = e0 + u * stride;
       if (e < p.K) {
-        float y[8], a[8], b[8];
+        Pair y[4], a[4], b[4];
         load8(sy + e, y);
         post(u, e, a, b);
+        if (p.post_bias) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] = fmaf((y[i] - ps.mean) * ps.rstd, a[i], x[u][i] + b[i]);
+          for (int i = 0; i < 4; ++i) x[u][i] = add2(x[u][i], b[i]);
+        }
+        if (p.post != CONVROT_NORM_NONE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = normalized(y[i], ps);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[u][i] = f32x2_fma(y[i], a[i], x[u][i]);
       }
     }
   }
@@ -299,27 +325,29 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
   if (!FP8 && !p.U) return;
   Stats us{0.0f, 1.0f};
   if (p.pre != CONVROT_NORM_NONE) {
-    auto get = [&](int u, float (&v)[8]) {
+    auto get = [&](int u, Pair (&v)[4]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = x[u][i];
+      for (int i = 0; i < 4; ++i) v[i] = x[u][i];
       return e0 + u * stride < p.K;
     };
-    us = row_stats<V>(get, count, p.pre, p.pre_eps, p.K, W, group, wg, red_pre);
+    us = row_stats<V>(get, count, p.pre, p.pre_eps, p.K, p.inv_k, W, group, wg, red_pre);
   }
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const int e = e0 + u * stride;
     if (e < p.K) {
-      float a[8], b[8];
+      Pair a[4], b[4];
       pre(u, e, a, b);
+      if (p.pre != CONVROT_NORM_NONE) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = fmaf((x[u][i] - us.mean) * us.rstd, a[i], b[i]);
+        for (int i = 0; i < 4; ++i) x[u][i] = normalized(x[u][i], us);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[u][i] = f32x2_fma(x[u][i], a[i], b[i]);
     }
     if (FP8) {
       // sixteen lanes hold a block of 128
-      float m = fabsf(x[u][0]);
-#pragma unroll
-      for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(x[u][i]));
+      float m = max_magnitude(x[u]);
 #pragma unroll
       for (int d = 1; d < 16; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
       const float sc = e4m3_scale(m);
@@ -413,18 +441,21 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
   if (leader)
     for (int i = 0; i < p.stages && row + i * G < c1; ++i) ring.fetch(row + i * G, i);
 
-  auto put = [&](float* c, int unit, const float (&v)[8]) {
-    *reinterpret_cast<float4*>(c + unit * 4) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(c + half + unit * 4) = make_float4(v[4], v[5], v[6], v[7]);
+  auto put = [&](float* c, int unit, const Pair (&v)[4]) {
+    *reinterpret_cast<ulonglong2*>(c + unit * 4) = make_ulonglong2(v[0], v[1]);
+    *reinterpret_cast<ulonglong2*>(c + half + unit * 4) = make_ulonglong2(v[2], v[3]);
   };
-  auto take = [&](const float* c, bool has, int e, float otherwise, float (&v)[8]) {
+  auto take = [&](const float* c, bool has, int e, float otherwise, Pair (&v)[4]) {
     if (has) {
-      const float4 a = *reinterpret_cast<const float4*>(c + e / 2), b = *reinterpret_cast<const float4*>(c + half + e / 2);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(c + e / 2);
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(c + half + e / 2);
+      v[0] = a.x;
+      v[1] = a.y;
+      v[2] = b.x;
+      v[3] = b.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = otherwise;
+      for (int i = 0; i < 4; ++i) v[i] = both(otherwise);
     }
   };
   const int stride = W * 32 * 8;
@@ -447,7 +478,7 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
     if (has_pa || has_pb || has_qa || has_qb) {
       __syncthreads();  // the rows before may still read theirs
       for (int unit = threadIdx.x; unit < p.K / 8; unit += WARPS * 32) {
-        float a[8], b[8];
+        Pair a[4], b[4];
         if (has_pa || has_pb) {
           post_coef8(p, s, unit * 8, a, b);
           if (has_pa) put(cpa, unit, a);
@@ -464,11 +495,11 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
       do_row<T, TU, V, FP8>(
           p, row, ring.h(), ring.y(), (wg * 32 + lane) * 8, stride, W, group, wg, red[0] + group * W,
           red[1] + group * W,
-          [&](int, int e, float (&a)[8], float (&b)[8]) {
+          [&](int, int e, Pair (&a)[4], Pair (&b)[4]) {
             take(cpa, has_pa, e, p.block_scale, a);
             take(cpb, has_pb, e, 0.0f, b);
           },
-          [&](int, int e, float (&a)[8], float (&b)[8]) {
+          [&](int, int e, Pair (&a)[4], Pair (&b)[4]) {
             take(cqa, has_qa, e, 1.0f, a);
             take(cqb, has_qb, e, 0.0f, b);
           },
@@ -508,7 +539,7 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
   if (tid == 0)
     for (int i = 0; i < p.stages && c0 + i < c1; ++i) ring.fetch(c0 + i, i);
   const int W = blockDim.x >> 5, stride = blockDim.x * 8;
-  float pa[V][8], qa[V][8];
+  Pair pa[V][4], qa[V][4];
   int cur = -2;
   for (int row = c0; row < c1; ++row) {
     const int s = sample_of(p, row);
@@ -517,7 +548,7 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
 #pragma unroll
       for (int u = 0; u < V; ++u) {
         const int e = tid * 8 + u * stride;
-        float b[8];
+        Pair b[4];
         if (e < p.K) {
           if (p.Y) post_coef8(p, s, e, pa[u], b);
           pre_coef8(p, s, e, qa[u], b);
@@ -527,23 +558,23 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
     mbar_wait(&ring.full[ring.st], ring.phase, &abort_flag, &g_norm_error);
     do_row<T, TU, V, FP8>(
         p, row, ring.h(), ring.y(), tid * 8, stride, W, 0, warp, red[0], red[1],
-        [&](int u, int e, float (&a)[8], float (&b)[8]) {
+        [&](int u, int e, Pair (&a)[4], Pair (&b)[4]) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = pa[u][i];
-          float c[8];
+          for (int i = 0; i < 4; ++i) a[i] = pa[u][i];
+          Pair c[4];
           if (p.post_bias) post_coef8(p, s, e, c, b);
           else
 #pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+            for (int i = 0; i < 4; ++i) b[i] = 0ull;
         },
-        [&](int u, int e, float (&a)[8], float (&b)[8]) {
+        [&](int u, int e, Pair (&a)[4], Pair (&b)[4]) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = qa[u][i];
-          float c[8];
+          for (int i = 0; i < 4; ++i) a[i] = qa[u][i];
+          Pair c[4];
           if (p.pre_bias || p.shift) pre_coef8(p, s, e, c, b);
           else
 #pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+            for (int i = 0; i < 4; ++i) b[i] = 0ull;
         },
         [&] {
           if (tid == 0 && row + p.stages < c1) ring.fetch(row + p.stages, ring.st);
@@ -619,14 +650,12 @@ block_norm_any_kernel(const __grid_constant__ NormParams p) {
         const int lane = threadIdx.x & 31;
         for (int kb = threadIdx.x >> 5; kb < p.KB; kb += blockDim.x >> 5) {
           const int e = kb * QBLOCK + lane * 4;  // K is a multiple of 16: whole groups of four
-          float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          Pair o[2] = {0ull, 0ull};
           if (e < p.K) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = x[e + i];
+            o[0] = f32x2_pack(x[e], x[e + 1]);
+            o[1] = f32x2_pack(x[e + 2], x[e + 3]);
           }
-          float m = fabsf(o[0]);
-#pragma unroll
-          for (int i = 1; i < 4; ++i) m = max_nan(m, fabsf(o[i]));
+          float m = max_magnitude(o);
 #pragma unroll
           for (int d = 1; d < 32; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
           const float sc = e4m3_scale(m);
@@ -697,14 +726,18 @@ int launch_wide(NormParams& p, cudaStream_t stream) {
   return launch_rows(kernel, p, grid, threads, p.stages * stage_bytes(p), stream);
 }
 
-// Warps per row of the grouped kernel: enough that a lane has at most 12
-// units and that two rows of every group fit beside the coefficients, and more
-// while there are fewer rows than groups on the GPU. 0: nothing fits.
+// Warps per row of the grouped kernel: enough that a lane has at most four
+// units (two CTAs per SM; six with all eight warps) and that two rows of every
+// group fit beside the coefficients, and more while there are fewer rows than
+// groups on the GPU. 0: nothing fits. bf16 [4608, 3072] to codes: 40 us with
+// four warps and three units against 52 us with two warps and six, [8192,
+// 1280]: 25 us with two warps and three units, 26 with one and five, 29 with
+// four.
 int pick_warps(const NormParams& p) {
   const int units = p.K / 8;
   const int64_t sms = device_sm_count();
   for (int W = 1; W <= WARPS; W *= 2) {
-    if (units > 12 * 32 * W || p.coef_smem + 2 * stage_bytes(p) * (WARPS / W) > MAX_SMEM) continue;
+    if (units > (W == WARPS ? 6 : 4) * 32 * W || p.coef_smem + 2 * stage_bytes(p) * (WARPS / W) > MAX_SMEM) continue;
     if (W < WARPS && units > 32 * W && p.M * static_cast<int64_t>(W) * 2 <= sms * WARPS) continue;
     return W;
   }
@@ -719,9 +752,9 @@ int launch_typed(NormParams& p, bool vec, cudaStream_t stream) {
     const int v = (units + 32 * W - 1) / (32 * W);
     if (v <= 1) return launch_grouped<T, TU, 1, FP8>(p, stream);
     if (v <= 2) return launch_grouped<T, TU, 2, FP8>(p, stream);
+    if (v <= 3) return launch_grouped<T, TU, 3, FP8>(p, stream);
     if (v <= 4) return launch_grouped<T, TU, 4, FP8>(p, stream);
-    if (v <= 6) return launch_grouped<T, TU, 6, FP8>(p, stream);
-    return launch_grouped<T, TU, 12, FP8>(p, stream);
+    return launch_grouped<T, TU, 6, FP8>(p, stream);
   }
   if (vec && units <= 4 * WIDE_WARPS * 32 && stage_bytes(p) <= MAX_SMEM) {
     if (units <= 2 * WIDE_WARPS * 32) return launch_wide<T, TU, 2, FP8>(p, stream);
@@ -780,6 +813,7 @@ int launch_block_norm(const convrot_block_norm_args& a, cudaStream_t stream) {
   p.pre_eps = a.pre_eps;
   p.residual_scale = a.residual_scale;
   p.block_scale = a.block_scale;
+  p.inv_k = 1.0f / static_cast<float>(a.K);
   const size_t sz = dtype_size(a.dtype), usz = dtype_size(a.u_dtype);
   p.row_smem = static_cast<uint32_t>((a.K * sz + 127) / 128 * 128);
   const int n_coef = (a.Y && (a.gate || a.post_weight)) + (a.Y && a.post_bias) + (a.pre_weight || a.scale) +

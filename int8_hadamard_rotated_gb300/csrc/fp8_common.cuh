@@ -50,28 +50,44 @@ template <> __device__ __forceinline__ void unpack2<__nv_bfloat16>(uint32_t w, f
   b = __uint_as_float(w & 0xffff0000u);
 }
 
-// Eight consecutive elements at a 16-byte aligned address (global or shared).
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+// Eight consecutive elements at a 16-byte aligned address (global or shared),
+// as four lane-wise pairs.
+typedef unsigned long long Pair;
+__device__ __forceinline__ void load8(const float* p, Pair (&x)[4]) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  x[0] = f32x2_pack(a.x, a.y);
+  x[1] = f32x2_pack(a.z, a.w);
+  x[2] = f32x2_pack(b.x, b.y);
+  x[3] = f32x2_pack(b.z, b.w);
 }
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+__device__ __forceinline__ void load8(const T* p, Pair (&x)[4]) {
   const uint4 v = *reinterpret_cast<const uint4*>(p);
-  unpack2<T>(v.x, x[0], x[1]);
-  unpack2<T>(v.y, x[2], x[3]);
-  unpack2<T>(v.z, x[4], x[5]);
-  unpack2<T>(v.w, x[6], x[7]);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack2<T>(w[i], a, b);
+    x[i] = f32x2_pack(a, b);
+  }
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store8(float* p, const Pair (&x)[4]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f32x2_unpack(x[i], v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]),
-                                            pack2<T>(x[6], x[7]));
+__device__ __forceinline__ void store8(T* p, const Pair (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f32x2_unpack(x[i], a, b);
+    w[i] = pack2<T>(a, b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -92,50 +108,80 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ float e4m3_scale(float amax) { return __fdiv_rn(amax, kE4M3Max); }
+// The codes of four values that are quotients already.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) { return e4m3x2(a, b) | (e4m3x2(c, d) << 16); }
 
-// Codes of NE values (NE % 4 == 0) with the scale s of their block: e4m3 of
-// the IEEE quotient RN(x / s), and 0 where s is 0.
+// RN(x / s) without a division: Markstein's correction step ("IA-64 and
+// Elementary Functions", 2000). With r = RN(1 / s) and q0 = RN(x r), which
+// lies within one ulp of x / s, the remainder x - q0 s is exact in one FMA and
+// RN(q0 + (x - q0 s) r) = RN(x / s), as long as everything stays normal.
+
+// The scale of a block, RN(amax / 448).
+static __device__ __noinline__ float e4m3_scale_divided(float amax) { return __fdiv_rn(amax, kE4M3Max); }
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  if (amax >= 0x1p-90f && amax <= 3.0e38f) {
+    constexpr float r = 1.0f / kE4M3Max;
+    const float q0 = __fmul_rn(amax, r);
+    return __fmaf_rn(__fmaf_rn(-q0, kE4M3Max, amax), r, q0);
+  }
+  return e4m3_scale_divided(amax);  // 0, tiny, infinite, NaN
+}
+
+// Codes of four values with the scale s of their block by division: scales
+// outside the correction step's range. Out of line, so that unrolled code
+// does not carry a division per element.
+static __device__ __noinline__ uint32_t e4m3_codes_divided(float a, float b, float c, float d, float s) {
+  if (s == 0.0f) return 0u;
+  return e4m3x4(__fdiv_rn(a, s), __fdiv_rn(b, s), __fdiv_rn(c, s), __fdiv_rn(d, s));
+}
+
+// Codes of 2 * NP values, as lane-wise pairs, with the scale s of their block:
+// e4m3 of the IEEE quotient RN(x / s), and 0 where s is 0.
 //
-// No division per element: Markstein's correction step ("IA-64 and Elementary
-// Functions", 2000): with r = RN(1 / s) and q0 = RN(x r), which lies within
-// one ulp of x / s, the remainder x - q0 s is exact in one FMA and
-// RN(q0 + (x - q0 s) r) = RN(x / s). It is taken where s and r are normal and
-// every x whose code is not 0 (|x| >= 2^-10 s) leaves the remainder normal:
-// s >= 2^-90; other scales (tiny, infinite, NaN) take the division. On the
-// negated values, so that zeros keep their sign; the codes' sign bits are
-// flipped at the end. Three packed operations and a conversion per two
-// elements. (Two products that enclose the quotient, and the division where
-// their codes differ, cost the same without ties, but 16-bit inputs are full
-// of exact ties: 51 us against 27 us for bf16 [4608, 12288].)
-template <int NE>
-__device__ __forceinline__ void e4m3_codes(const float (&x)[NE], float s, uint32_t (&out)[NE / 4]) {
+// The correction step is taken where s and 1 / s are normal and every x whose
+// code is not 0 (|x| >= 2^-10 s) leaves the remainder normal: s >= 2^-90. It
+// runs on the negated values, so that zeros keep their sign; the codes' sign
+// bits are flipped at the end. Three packed operations and a conversion per
+// two elements. (Two products that enclose the quotient, and the division
+// where their codes differ, cost the same without ties, but 16-bit inputs are
+// full of exact ties: 51 us against 35 us for bf16 [4608, 12288].)
+template <int NP>
+__device__ __forceinline__ void e4m3_codes(const unsigned long long (&x)[NP], float s, uint32_t (&out)[NP / 2]) {
   if (s >= 0x1p-90f && s <= 3.0e38f) {
     const float nr = -__frcp_rn(s);
     const unsigned long long nr2 = f32x2_pack(nr, nr), s2 = f32x2_pack(s, s);
 #pragma unroll
-    for (int i = 0; i < NE / 4; ++i) {
-      uint32_t w[2];
+    for (int i = 0; i < NP / 2; ++i) {
+      float q[4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const unsigned long long v = f32x2_pack(x[4 * i + 2 * k], x[4 * i + 2 * k + 1]);
-        const unsigned long long nq0 = f32x2_mul(v, nr2);
-        const unsigned long long nq = f32x2_fma(f32x2_fma(nq0, s2, v), nr2, nq0);
-        float a, b;
-        f32x2_unpack(nq, a, b);
-        w[k] = e4m3x2(a, b);
+        const unsigned long long nq0 = f32x2_mul(x[2 * i + k], nr2);
+        f32x2_unpack(f32x2_fma(f32x2_fma(nq0, s2, x[2 * i + k]), nr2, nq0), q[2 * k], q[2 * k + 1]);
       }
-      out[i] = (w[0] | (w[1] << 16)) ^ 0x80808080u;
+      out[i] = e4m3x4(q[0], q[1], q[2], q[3]) ^ 0x80808080u;
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < NE / 4; ++i) {
-    float q[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) q[k] = (s == 0.0f) ? 0.0f : __fdiv_rn(x[4 * i + k], s);
-    out[i] = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
+    for (int i = 0; i < NP / 2; ++i) {
+      float q[4];
+      f32x2_unpack(x[2 * i], q[0], q[1]);
+      f32x2_unpack(x[2 * i + 1], q[2], q[3]);
+      out[i] = e4m3_codes_divided(q[0], q[1], q[2], q[3], s);
+    }
   }
+}
+
+// The largest magnitude of 2 * NP values (NaN if one is).
+template <int NP>
+__device__ __forceinline__ float max_magnitude(const unsigned long long (&x)[NP]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    float a, b;
+    f32x2_unpack(x[i], a, b);
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(a), "f"(b));
+  }
+  return m;
 }
 
 // ---------------------------------------------------------------------------

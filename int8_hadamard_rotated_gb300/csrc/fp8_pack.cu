@@ -13,20 +13,20 @@ namespace convrot {
 namespace fp8 {
 namespace {
 
-// Sixteen consecutive elements; `vec`: the address is 16-byte aligned.
+// Sixteen consecutive elements as pairs; `vec`: the address is 16-byte aligned.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, bool vec, float (&x)[16]) {
+__device__ __forceinline__ void load16(const T* p, bool vec, Pair (&x)[8]) {
   if (vec) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float v[8];
+      Pair v[4];
       load8(p + 8 * h, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[8 * h + i] = v[i];
+      for (int i = 0; i < 4; ++i) x[4 * h + i] = v[i];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = to_f32(p[i]);
+    for (int i = 0; i < 8; ++i) x[i] = f32x2_pack(to_f32(p[2 * i]), to_f32(p[2 * i + 1]));
   }
 }
 
@@ -43,7 +43,7 @@ fp8_pack_kernel(const T* __restrict__ X, int64_t ldx, uint32_t n_qblocks, uint32
   pdl_launch_dependents();
   const uint32_t sub = threadIdx.x & 7;
   const uint32_t first = blockIdx.x * (PACK_THREADS / 8 * UNITS) + (threadIdx.x >> 3);
-  float x[UNITS][16];
+  Pair x[UNITS][8];
   uint32_t row[UNITS], col[UNITS];
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
@@ -54,14 +54,12 @@ fp8_pack_kernel(const T* __restrict__ X, int64_t ldx, uint32_t n_qblocks, uint32
       load16(X + row[u] * ldx + col[u], vec, x[u]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[u][i] = 0.0f;
+      for (int i = 0; i < 8; ++i) x[u][i] = 0ull;
     }
   }
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
-    float m = fabsf(x[u][0]);
-#pragma unroll
-    for (int i = 1; i < 16; ++i) m = max_nan(m, fabsf(x[u][i]));
+    float m = max_magnitude(x[u]);
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float sc = e4m3_scale(m);
@@ -86,7 +84,7 @@ fp8_weight_kernel(const T* __restrict__ W, int64_t N, int64_t K, bool vec, uint8
   __shared__ float part[8];
   const int64_t KB = (K + QBLOCK - 1) / QBLOCK;
   const int64_t nb = blockIdx.x / KB, kb = blockIdx.x - nb * KB;
-  float x[4][16];
+  Pair x[4][8];
   float m = 0.0f;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
@@ -96,10 +94,9 @@ fp8_weight_kernel(const T* __restrict__ W, int64_t N, int64_t K, bool vec, uint8
       load16(W + row * K + col, vec, x[u]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[u][i] = 0.0f;
+      for (int i = 0; i < 8; ++i) x[u][i] = 0ull;
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = max_nan(m, fabsf(x[u][i]));
+    m = max_nan(m, max_magnitude(x[u]));
   }
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
