@@ -28,7 +28,8 @@ LIB_PATH = os.path.join(LIB_DIR, "libconvrot.so")
 BENCH_LIB_PATH = os.path.join(LIB_DIR, "libconvrot_bench.so")
 
 SOURCES = ["api.cu", "pack.cu", "gemm.cu", "gemm_w4.cu", "noalloc.cu", "host_pipeline.cu", "mlp.cu",
-           "fp8_api.cu", "fp8_pack.cu", "fp8_gemm.cu", "block_norm.cu"]
+           "fp8_api.cu", "fp8_pack.cu", "fp8_gemm.cu",
+           "block_norm_f32.cu", "block_norm_f16.cu", "block_norm_bf16.cu"]
 BENCH_CSRC = os.path.join(PKG, "bench_csrc")
 BENCH_SOURCES = ["copy_ceiling.cu", "mma_s8_probe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

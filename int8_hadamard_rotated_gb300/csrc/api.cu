@@ -60,7 +60,7 @@ int read_and_clear_w4_error();                         // gemm_w4.cu: the S8 x S
 int read_and_clear_pack_error();                       // pack.cu: the pack kernels' word
 namespace fp8 {
 int read_and_clear_fp8_error();                        // fp8_gemm.cu: the block-scaled GEMM's word
-int read_and_clear_norm_error();                       // block_norm.cu: the block norms' word
+int read_and_clear_norm_error();                       // fp8_api.cu: the block norms' words
 }  // namespace fp8
 
 }  // namespace convrot

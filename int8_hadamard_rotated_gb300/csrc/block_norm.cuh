@@ -1,4 +1,4 @@
-// block_norm.cu -- the norms before and after a transformer block fused with
+// block_norm.cuh -- the norms before and after a transformer block fused with
 // the block's gate and its residual, in one pass over the rows:
 //
 //   v  = block_scale * post(y)                  y: the block's output
@@ -16,6 +16,10 @@
 // large common offset does not cancel.
 //
 // Bound by HBM: per row h and y in, h' and u out, once each.
+//
+// Compiled once per type of the residual stream (block_norm_*.cu).
+#pragma once
+
 #include "fp8_common.cuh"
 
 #include <algorithm>
@@ -24,12 +28,12 @@
 namespace convrot {
 namespace fp8 {
 
-// Sticky device error word of the block norms: a bounded wait that gave up
+namespace {
+
+// Sticky device error word of this type's kernels: a bounded wait that gave up
 // (CONVROT_ERR_TIMEOUT) or a row's sample outside [0, n_samples)
 // (CONVROT_ERR_ARG).
 __device__ int g_norm_error = 0;
-
-namespace {
 
 struct NormParams {
   const void* H;
@@ -101,46 +105,46 @@ __device__ __forceinline__ Pair add2(Pair a, Pair b) {
 }
 __device__ __forceinline__ Pair both(float v) { return f32x2_pack(v, v); }
 
-// The same for eight consecutive features at a 16-byte aligned place.
-__device__ __forceinline__ void post_coef8(const NormParams& p, int s, int e, Pair (&a)[4], Pair (&b)[4]) {
-  Pair v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) { a[i] = both(p.block_scale); b[i] = 0ull; }
+// The same for four consecutive features at a 16-byte aligned place.
+__device__ __forceinline__ void post_coef4(const NormParams& p, int s, int e, Pair (&a)[2], Pair (&b)[2]) {
+  Pair v[2];
+  a[0] = a[1] = both(p.block_scale);
+  b[0] = b[1] = 0ull;
   if (p.gate) {
-    if (s >= 0) load8(p.gate + s * p.ld_gate + e, v);
+    if (s >= 0) load4(p.gate + s * p.ld_gate + e, v[0], v[1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = s < 0 ? 0ull : f32x2_mul(a[i], v[i]);
+    for (int i = 0; i < 2; ++i) a[i] = s < 0 ? 0ull : f32x2_mul(a[i], v[i]);
   }
   if (p.post_bias) {
-    load8(p.post_bias + e, v);
+    load4(p.post_bias + e, v[0], v[1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = f32x2_mul(a[i], v[i]);
+    for (int i = 0; i < 2; ++i) b[i] = f32x2_mul(a[i], v[i]);
   }
   if (p.post_weight) {
-    load8(p.post_weight + e, v);
+    load4(p.post_weight + e, v[0], v[1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = f32x2_mul(a[i], v[i]);
+    for (int i = 0; i < 2; ++i) a[i] = f32x2_mul(a[i], v[i]);
   }
 }
-__device__ __forceinline__ void pre_coef8(const NormParams& p, int s, int e, Pair (&a)[4], Pair (&b)[4]) {
-  Pair v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) { a[i] = both(1.0f); b[i] = 0ull; }
-  if (p.pre_weight) load8(p.pre_weight + e, a);
-  if (p.pre_bias) load8(p.pre_bias + e, b);
+__device__ __forceinline__ void pre_coef4(const NormParams& p, int s, int e, Pair (&a)[2], Pair (&b)[2]) {
+  Pair v[2];
+  a[0] = a[1] = both(1.0f);
+  b[0] = b[1] = 0ull;
+  if (p.pre_weight) load4(p.pre_weight + e, a[0], a[1]);
+  if (p.pre_bias) load4(p.pre_bias + e, b[0], b[1]);
   if (p.scale && s >= 0) {
-    load8(p.scale + s * p.ld_mod + e, v);
+    load4(p.scale + s * p.ld_mod + e, v[0], v[1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       v[i] = add2(v[i], both(1.0f));
       a[i] = f32x2_mul(a[i], v[i]);
       b[i] = f32x2_mul(b[i], v[i]);
     }
   }
   if (p.shift && s >= 0) {
-    load8(p.shift + s * p.ld_mod + e, v);
+    load4(p.shift + s * p.ld_mod + e, v[0], v[1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = add2(b[i], v[i]);
+    for (int i = 0; i < 2; ++i) b[i] = add2(b[i], v[i]);
   }
 }
 
@@ -181,8 +185,8 @@ __device__ __forceinline__ float inverse_root(float v) {
 }
 
 // Statistics of a row of K elements spread over a group of W warps; `get(u,
-// x)` yields a thread's unit u of eight (zeros past the end, and whether it
-// lies inside), `count(w)` the elements that warp w of the group holds.
+// x, on)` yields a thread's unit u (four pairs; zeros past the end, and which
+// halves lie inside), `count(w)` the elements that warp w of the group holds.
 template <int V, typename Get, typename Count>
 __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float eps, int K, float inv_k, int W, int group,
                                            int warp_in_group, float2* red) {
@@ -197,7 +201,8 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
 #pragma unroll
     for (int u = 0; u < V; ++u) {
       Pair x[4];
-      get(u, x);
+      bool on[2];
+      get(u, x, on);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i & 1] = f32x2_fma(x[i], x[i], acc[i & 1]);
     }
@@ -209,7 +214,8 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     Pair x[4];
-    get(u, x);
+    bool on[2];
+    get(u, x, on);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i & 1] = add2(acc[i & 1], x[i]);
   }
@@ -221,12 +227,12 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     Pair x[4];
-    if (get(u, x)) {
+    bool on[2];
+    get(u, x, on);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Pair d = add2(x[i], minus);
-        acc[i & 1] = f32x2_fma(d, d, acc[i & 1]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const Pair d = add2(x[i], minus);
+      if (on[i / 2]) acc[i & 1] = f32x2_fma(d, d, acc[i & 1]);
     }
   }
   float m2 = total(acc);
@@ -250,68 +256,123 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
   return st;
 }
 
-// The thread's part of a row, V units of eight features (unit u at e0 + u *
-// stride), from its arrival in shared memory to its last store: see the two
-// kernels that use it. The coefficients come from `post(u, e, a, b)` and
-// `pre(u, e, a, b)`; `loaded()` is called once the staged row has been read
-// and the group has passed a barrier.
+// How a warp takes 256 consecutive features, a unit of eight per lane in two
+// halves of four: 16-bit elements are one 16-byte piece per lane, 32-bit ones
+// two, 128 features apart, so that a warp's accesses are always contiguous.
+template <typename T>
+struct Unit {
+  int lo, hi;  // first features of the two halves
+  bool on[2];  // which lie inside the row
+  __device__ __forceinline__ Unit(int chunk, int K) {
+    const int lane = threadIdx.x & 31;
+    lo = chunk * 256 + lane * (sizeof(T) == 4 ? 4 : 8);
+    hi = lo + (sizeof(T) == 4 ? 128 : 4);
+    on[0] = lo < K;
+    on[1] = sizeof(T) == 4 ? hi < K : on[0];
+  }
+  __device__ __forceinline__ void load(const T* row, Pair (&x)[4]) const {
+    if constexpr (sizeof(T) == 4) {
+      if (on[0]) load4(row + lo, x[0], x[1]);
+      if (on[1]) load4(row + hi, x[2], x[3]);
+    } else {
+      if (on[0]) load8(row + lo, x);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!on[i / 2]) x[i] = 0ull;
+  }
+  template <typename TU>
+  __device__ __forceinline__ void store(TU* row, const Pair (&x)[4]) const {
+    if constexpr (sizeof(T) == 4) {
+      if (on[0]) store4(row + lo, x[0], x[1]);
+      if (on[1]) store4(row + hi, x[2], x[3]);
+    } else {
+      if (on[0]) store8(row + lo, x);
+    }
+  }
+  // Codes and scales of the unit's features: a block of 128 is the same half
+  // of all lanes (32-bit elements) or both halves of sixteen lanes.
+  __device__ __forceinline__ void store_codes(uint8_t* q, float* s, const Pair (&x)[4]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const Pair v[2] = {x[2 * h], x[2 * h + 1]};
+        float m = max_magnitude(v);
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float sc = e4m3_scale(m);
+        uint32_t c[1];
+        e4m3_codes(v, sc, c);
+        if (on[h]) {
+          *reinterpret_cast<uint32_t*>(q + (h ? hi : lo)) = c[0];
+          if ((threadIdx.x & 31) == 0) s[(h ? hi : lo) / QBLOCK] = sc;
+        }
+      }
+    } else {
+      float m = max_magnitude(x);
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float sc = e4m3_scale(m);
+      uint32_t c[2];
+      e4m3_codes(x, sc, c);
+      if (on[0]) {
+        *reinterpret_cast<uint2*>(q + lo) = make_uint2(c[0], c[1]);
+        if ((threadIdx.x & 15) == 0) s[lo / QBLOCK] = sc;
+      }
+    }
+  }
+};
+
+// The thread's part of a row, V units (unit u of chunk u * W + wg), from its
+// arrival in shared memory to its last store: see the two kernels that use it.
+// The coefficients come from `post(u, unit, a, b)` and `pre(u, unit, a, b)`;
+// `loaded()` is called once the staged row has been read and the group has
+// passed a barrier.
 template <typename T, typename TU, int V, bool FP8, typename Post, typename Pre, typename Loaded>
-__device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh, const T* sy, int e0, int stride, int W,
-                                       int group, int wg, float2* red_post, float2* red_pre, Post post, Pre pre,
-                                       Loaded loaded) {
+__device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh, const T* sy, int W, int group, int wg,
+                                       float2* red_post, float2* red_pre, Post post, Pre pre, Loaded loaded) {
   auto count = [&](int w) {  // features of the row that warp w of the group holds
     int n = 0;
 #pragma unroll
-    for (int u = 0; u < V; ++u) n += min(max(p.K - u * stride - w * 32 * 8, 0), 32 * 8);
+    for (int u = 0; u < V; ++u) n += min(max(p.K - (u * W + w) * 256, 0), 256);
     return n;
   };
   auto normalized = [](Pair x, const Stats& st) { return f32x2_mul(add2(x, both(-st.mean)), both(st.rstd)); };
   Pair x[V][4];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const int e = e0 + u * stride;
-    if (e < p.K) {
-      load8(sh + e, x[u]);
+    Unit<T>(u * W + wg, p.K).load(sh, x[u]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[u][i] = f32x2_mul(x[u][i], both(p.residual_scale));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[u][i] = 0ull;
-    }
+    for (int i = 0; i < 4; ++i) x[u][i] = f32x2_mul(x[u][i], both(p.residual_scale));
   }
   if (p.Y) {
     Stats ps{0.0f, 1.0f};
     if (p.post != CONVROT_NORM_NONE) {
-      auto get = [&](int u, Pair (&v)[4]) {
-        const int e = e0 + u * stride;
-        if (e < p.K) {
-          load8(sy + e, v);
-          return true;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = 0ull;
-        return false;
+      auto get = [&](int u, Pair (&v)[4], bool (&on)[2]) {
+        const Unit<T> unit(u * W + wg, p.K);
+        unit.load(sy, v);
+        on[0] = unit.on[0];
+        on[1] = unit.on[1];
       };
       ps = row_stats<V>(get, count, p.post, p.post_eps, p.K, p.inv_k, W, group, wg, red_post);
     }
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      const int e = e0 + u * stride;
-      if (e < p.K) {
-        Pair y[4], a[4], b[4];
-        load8(sy + e, y);
-        post(u, e, a, b);
-        if (p.post_bias) {
+      const Unit<T> unit(u * W + wg, p.K);
+      Pair y[4], a[4], b[4];
+      unit.load(sy, y);
+      post(u, unit, a, b);
+      if (p.post_bias) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[u][i] = add2(x[u][i], b[i]);
-        }
-        if (p.post != CONVROT_NORM_NONE) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = normalized(y[i], ps);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[u][i] = f32x2_fma(y[i], a[i], x[u][i]);
+        for (int i = 0; i < 4; ++i) x[u][i] = add2(x[u][i], b[i]);
       }
+      if (p.post != CONVROT_NORM_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = normalized(y[i], ps);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (unit.on[i / 2]) x[u][i] = f32x2_fma(y[i], a[i], x[u][i]);
     }
   }
   group_sync(W, group);
@@ -319,47 +380,36 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
   if (p.H_out) {
     T* out = static_cast<T*>(p.H_out) + row * p.ldho;
 #pragma unroll
-    for (int u = 0; u < V; ++u)
-      if (e0 + u * stride < p.K) store8(out + e0 + u * stride, x[u]);
+    for (int u = 0; u < V; ++u) Unit<T>(u * W + wg, p.K).store(out, x[u]);
   }
   if (!FP8 && !p.U) return;
   Stats us{0.0f, 1.0f};
   if (p.pre != CONVROT_NORM_NONE) {
-    auto get = [&](int u, Pair (&v)[4]) {
+    auto get = [&](int u, Pair (&v)[4], bool (&on)[2]) {
+      const Unit<T> unit(u * W + wg, p.K);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = x[u][i];
-      return e0 + u * stride < p.K;
+      for (int i = 0; i < 4; ++i) v[i] = unit.on[i / 2] ? x[u][i] : 0ull;
+      on[0] = unit.on[0];
+      on[1] = unit.on[1];
     };
     us = row_stats<V>(get, count, p.pre, p.pre_eps, p.K, p.inv_k, W, group, wg, red_pre);
   }
+  uint8_t* q = FP8 ? p.Q + static_cast<int64_t>(row) * p.K : nullptr;
+  float* s = FP8 ? p.s + static_cast<int64_t>(row) * p.KB : nullptr;
+  TU* out = FP8 ? nullptr : static_cast<TU*>(p.U) + row * p.ldu;
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const int e = e0 + u * stride;
-    if (e < p.K) {
-      Pair a[4], b[4];
-      pre(u, e, a, b);
-      if (p.pre != CONVROT_NORM_NONE) {
+    const Unit<T> unit(u * W + wg, p.K);
+    Pair a[4], b[4];
+    pre(u, unit, a, b);
+    if (p.pre != CONVROT_NORM_NONE) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[u][i] = normalized(x[u][i], us);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[u][i] = f32x2_fma(x[u][i], a[i], b[i]);
+      for (int i = 0; i < 4; ++i) x[u][i] = normalized(x[u][i], us);
     }
-    if (FP8) {
-      // sixteen lanes hold a block of 128
-      float m = max_magnitude(x[u]);
 #pragma unroll
-      for (int d = 1; d < 16; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const float sc = e4m3_scale(m);
-      uint32_t c[2];
-      e4m3_codes(x[u], sc, c);
-      if (e < p.K) {
-        *reinterpret_cast<uint2*>(p.Q + static_cast<int64_t>(row) * p.K + e) = make_uint2(c[0], c[1]);
-        if ((threadIdx.x & 15) == 0) p.s[static_cast<int64_t>(row) * p.KB + e / QBLOCK] = sc;
-      }
-    } else if (e < p.K) {
-      store8(static_cast<TU*>(p.U) + row * p.ldu + e, x[u]);
-    }
+    for (int i = 0; i < 4; ++i) x[u][i] = unit.on[i / 2] ? f32x2_fma(x[u][i], a[i], b[i]) : 0ull;
+    if (FP8) unit.store_codes(q, s, x[u]);
+    else unit.store(out, x[u]);
   }
 }
 
@@ -400,9 +450,7 @@ constexpr int MAX_STAGES = 8;
 // warps, square roots) over. CTAs are persistent, each over a contiguous range
 // of rows, its groups taking them in turn; the affine coefficients of the
 // current sample (norm weights, gate and modulation folded, only those that
-// are not 0 or 1) lie in shared memory, the two halves of every unit of eight
-// apart so that a warp reads them without bank conflicts, and are formed again
-// when the sample changes.
+// are not 0 or 1) lie in shared memory and are formed again when it changes.
 //
 // (One thread block per row with one unit per thread and its coefficients in
 // registers: 49 us for bf16 [4608, 3072] with gate, LayerNorm and modulation,
@@ -419,7 +467,7 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
   const int W = p.warps_per_row, G = WARPS / W, group = warp / W, wg = warp - group * W;
   const int c0 = static_cast<int>(static_cast<int64_t>(p.M) * blockIdx.x / gridDim.x);
   const int c1 = static_cast<int>(static_cast<int64_t>(p.M) * (blockIdx.x + 1) / gridDim.x);
-  const int half = p.K / 2, n_coef = p.K;  // floats: a coefficient vector as two halves
+  const int n_coef = (p.K + 255) / 256 * 256;  // floats of a coefficient vector
   const bool has_pa = p.Y && (p.gate || p.post_weight), has_pb = p.Y && p.post_bias;
   const bool has_qa = p.pre_weight || p.scale, has_qb = p.pre_bias || p.shift;
   float* cpa = reinterpret_cast<float*>(smem);
@@ -441,31 +489,26 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
   if (leader)
     for (int i = 0; i < p.stages && row + i * G < c1; ++i) ring.fetch(row + i * G, i);
 
-  auto put = [&](float* c, int unit, const Pair (&v)[4]) {
-    *reinterpret_cast<ulonglong2*>(c + unit * 4) = make_ulonglong2(v[0], v[1]);
-    *reinterpret_cast<ulonglong2*>(c + half + unit * 4) = make_ulonglong2(v[2], v[3]);
-  };
-  auto take = [&](const float* c, bool has, int e, float otherwise, Pair (&v)[4]) {
-    if (has) {
-      const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(c + e / 2);
-      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(c + half + e / 2);
-      v[0] = a.x;
-      v[1] = a.y;
-      v[2] = b.x;
-      v[3] = b.y;
+  // A unit's coefficients: in every 256 floats the first halves of the lanes,
+  // then the second ones, so that a warp reads them without bank conflicts.
+  const int n_chunks = (p.K + 255) / 256;
+  auto take = [&](const float* c, bool has, int chunk, float otherwise, Pair (&v)[4]) {
+    if (has && chunk < n_chunks) {
+      load4(c + chunk * 256 + lane * 4, v[0], v[1]);
+      load4(c + chunk * 256 + 128 + lane * 4, v[2], v[3]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = both(otherwise);
     }
   };
-  const int stride = W * 32 * 8;
   for (int start = c0; start < c1;) {
     // the rows from `start` on that share its sample
-    const int s = sample_of(p, start);
-    int end = c1;
+    int s = 0, end = c1;
     if (p.row_sample) {
-      for (end = start + 1; end < c1; end += 32) {
-        const unsigned other = __ballot_sync(0xffffffffu, end + lane >= c1 || sample_of(p, end + lane) != s);
+      for (end = start; end < c1; end += 32) {
+        const int mine = sample_of(p, min(end + lane, c1 - 1));
+        if (end == start) s = __shfl_sync(0xffffffffu, mine, 0);
+        const unsigned other = __ballot_sync(0xffffffffu, mine != s);
         if (other) {
           end = min(c1, end + __ffs(other) - 1);
           break;
@@ -473,35 +516,41 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
       }
       end = min(end, c1);
     } else if (p.rows_per_sample > 0) {
+      s = start / p.rows_per_sample;
       end = static_cast<int>(min(static_cast<int64_t>(c1), (static_cast<int64_t>(s) + 1) * p.rows_per_sample));
     }
     if (has_pa || has_pb || has_qa || has_qb) {
       __syncthreads();  // the rows before may still read theirs
-      for (int unit = threadIdx.x; unit < p.K / 8; unit += WARPS * 32) {
-        Pair a[4], b[4];
-        if (has_pa || has_pb) {
-          post_coef8(p, s, unit * 8, a, b);
-          if (has_pa) put(cpa, unit, a);
-          if (has_pb) put(cpb, unit, b);
+      for (int chunk = warp; chunk < n_chunks; chunk += WARPS) {
+        const Unit<T> unit(chunk, p.K);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!unit.on[h]) continue;
+          const int e = h ? unit.hi : unit.lo, at = chunk * 256 + h * 128 + lane * 4;
+          Pair a[2], b[2];
+          if (has_pa || has_pb) {
+            post_coef4(p, s, e, a, b);
+            if (has_pa) store4(cpa + at, a[0], a[1]);
+            if (has_pb) store4(cpb + at, b[0], b[1]);
+          }
+          pre_coef4(p, s, e, a, b);
+          if (has_qa) store4(cqa + at, a[0], a[1]);
+          if (has_qb) store4(cqb + at, b[0], b[1]);
         }
-        pre_coef8(p, s, unit * 8, a, b);
-        if (has_qa) put(cqa, unit, a);
-        if (has_qb) put(cqb, unit, b);
       }
       __syncthreads();
     }
     for (; row < end; row += G) {
       mbar_wait(&ring.full[ring.st], ring.phase, &abort_flag, &g_norm_error);
       do_row<T, TU, V, FP8>(
-          p, row, ring.h(), ring.y(), (wg * 32 + lane) * 8, stride, W, group, wg, red[0] + group * W,
-          red[1] + group * W,
-          [&](int, int e, Pair (&a)[4], Pair (&b)[4]) {
-            take(cpa, has_pa, e, p.block_scale, a);
-            take(cpb, has_pb, e, 0.0f, b);
+          p, row, ring.h(), ring.y(), W, group, wg, red[0] + group * W, red[1] + group * W,
+          [&](int u, const Unit<T>&, Pair (&a)[4], Pair (&b)[4]) {
+            take(cpa, has_pa, u * W + wg, p.block_scale, a);
+            take(cpb, has_pb, u * W + wg, 0.0f, b);
           },
-          [&](int, int e, Pair (&a)[4], Pair (&b)[4]) {
-            take(cqa, has_qa, e, 1.0f, a);
-            take(cqb, has_qb, e, 0.0f, b);
+          [&](int u, const Unit<T>&, Pair (&a)[4], Pair (&b)[4]) {
+            take(cqa, has_qa, u * W + wg, 1.0f, a);
+            take(cqb, has_qb, u * W + wg, 0.0f, b);
           },
           [&] {
             if (leader && row + p.stages * G < c1) ring.fetch(row + p.stages * G, ring.st);
@@ -513,16 +562,19 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
 }
 
 // The same for rows whose coefficients do not fit beside the staged rows: one
-// row per CTA of up to sixteen warps, at most 32 features per thread; a
-// thread's weights and scales stay in registers while the sample stays.
-constexpr int WIDE_WARPS = 16;
+// row per CTA of up to 24 warps; a thread's coefficients stay in registers
+// while the sample stays, but for a bias of the first norm (and, with four
+// units per thread, what is added after the second), which is read again for
+// every row.
+template <int V>
+constexpr int WIDE_WARPS = V <= 2 ? 24 : 16;
 
 template <typename T, typename TU, int V, bool FP8>
-__global__ void __launch_bounds__(WIDE_WARPS * 32, 1)
+__global__ void __launch_bounds__(WIDE_WARPS<V> * 32, 1)
 block_norm_wide_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[MAX_STAGES];
-  __shared__ float2 red[2][WIDE_WARPS];
+  __shared__ float2 red[2][WIDE_WARPS<V>];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, tid = threadIdx.x;
   const int c0 = static_cast<int>(static_cast<int64_t>(p.M) * blockIdx.x / gridDim.x);
@@ -538,8 +590,24 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
   pdl_launch_dependents();
   if (tid == 0)
     for (int i = 0; i < p.stages && c0 + i < c1; ++i) ring.fetch(c0 + i, i);
-  const int W = blockDim.x >> 5, stride = blockDim.x * 8;
-  Pair pa[V][4], qa[V][4];
+  const int W = blockDim.x >> 5;
+  constexpr bool HOLD_B = V <= 2;
+  Pair pa[V][4], qa[V][4], qb[HOLD_B ? V : 1][4];
+  auto coefs = [&](int s, const Unit<T>& unit, bool pre, Pair (&a)[4], Pair (&b)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Pair va[2] = {0ull, 0ull}, vb[2] = {0ull, 0ull};
+      if (unit.on[h]) {
+        if (pre) pre_coef4(p, s, h ? unit.hi : unit.lo, va, vb);
+        else post_coef4(p, s, h ? unit.hi : unit.lo, va, vb);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[2 * h + i] = va[i];
+        b[2 * h + i] = vb[i];
+      }
+    }
+  };
   int cur = -2;
   for (int row = c0; row < c1; ++row) {
     const int s = sample_of(p, row);
@@ -547,34 +615,35 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
       cur = s;
 #pragma unroll
       for (int u = 0; u < V; ++u) {
-        const int e = tid * 8 + u * stride;
+        const Unit<T> unit(u * W + warp, p.K);
         Pair b[4];
-        if (e < p.K) {
-          if (p.Y) post_coef8(p, s, e, pa[u], b);
-          pre_coef8(p, s, e, qa[u], b);
+        if (p.Y) coefs(s, unit, false, pa[u], b);
+        coefs(s, unit, true, qa[u], b);
+        if (HOLD_B) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qb[HOLD_B ? u : 0][i] = b[i];
         }
       }
     }
     mbar_wait(&ring.full[ring.st], ring.phase, &abort_flag, &g_norm_error);
     do_row<T, TU, V, FP8>(
-        p, row, ring.h(), ring.y(), tid * 8, stride, W, 0, warp, red[0], red[1],
-        [&](int u, int e, Pair (&a)[4], Pair (&b)[4]) {
+        p, row, ring.h(), ring.y(), W, 0, warp, red[0], red[1],
+        [&](int u, const Unit<T>& unit, Pair (&a)[4], Pair (&b)[4]) {
+          Pair c[4];
+          if (p.post_bias) coefs(s, unit, false, c, b);
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[i] = pa[u][i];
-          Pair c[4];
-          if (p.post_bias) post_coef8(p, s, e, c, b);
-          else
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = 0ull;
         },
-        [&](int u, int e, Pair (&a)[4], Pair (&b)[4]) {
+        [&](int u, const Unit<T>& unit, Pair (&a)[4], Pair (&b)[4]) {
+          Pair c[4];
+          if (!HOLD_B && (p.pre_bias || p.shift)) {
+            coefs(s, unit, true, c, b);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = HOLD_B ? qb[HOLD_B ? u : 0][i] : 0ull;
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[i] = qa[u][i];
-          Pair c[4];
-          if (p.pre_bias || p.shift) pre_coef8(p, s, e, c, b);
-          else
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = 0ull;
         },
         [&] {
           if (tid == 0 && row + p.stages < c1) ring.fetch(row + p.stages, ring.st);
@@ -721,7 +790,7 @@ int launch_wide(NormParams& p, cudaStream_t stream) {
   auto kernel = block_norm_wide_kernel<T, TU, V, FP8>;
   if (int st = allow_smem(kernel, done, mu)) return st;
   p.stages = static_cast<int>(std::min<size_t>(MAX_STAGES, MAX_SMEM / stage_bytes(p)));
-  const int threads = ((p.K / 8 + V - 1) / V + 31) / 32 * 32;
+  const int threads = ((p.K + 255) / 256 + V - 1) / V * 32;
   const unsigned grid = static_cast<unsigned>(std::min(p.M, device_sm_count()));
   return launch_rows(kernel, p, grid, threads, p.stages * stage_bytes(p), stream);
 }
@@ -734,11 +803,11 @@ int launch_wide(NormParams& p, cudaStream_t stream) {
 // 1280]: 25 us with two warps and three units, 26 with one and five, 29 with
 // four.
 int pick_warps(const NormParams& p) {
-  const int units = p.K / 8;
+  const int chunks = (p.K + 255) / 256;
   const int64_t sms = device_sm_count();
   for (int W = 1; W <= WARPS; W *= 2) {
-    if (units > (W == WARPS ? 6 : 4) * 32 * W || p.coef_smem + 2 * stage_bytes(p) * (WARPS / W) > MAX_SMEM) continue;
-    if (W < WARPS && units > 32 * W && p.M * static_cast<int64_t>(W) * 2 <= sms * WARPS) continue;
+    if (chunks > (W == WARPS ? 6 : 4) * W || p.coef_smem + 2 * stage_bytes(p) * (WARPS / W) > MAX_SMEM) continue;
+    if (W < WARPS && chunks > W && p.M * static_cast<int64_t>(W) * 2 <= sms * WARPS) continue;
     return W;
   }
   return 0;
@@ -746,19 +815,18 @@ int pick_warps(const NormParams& p) {
 
 template <typename T, typename TU, bool FP8>
 int launch_typed(NormParams& p, bool vec, cudaStream_t stream) {
-  const int units = (p.K + 7) / 8;
+  const int chunks = (p.K + 255) / 256;
   if (const int W = vec ? pick_warps(p) : 0) {
     p.warps_per_row = W;
-    const int v = (units + 32 * W - 1) / (32 * W);
+    const int v = (chunks + W - 1) / W;
     if (v <= 1) return launch_grouped<T, TU, 1, FP8>(p, stream);
     if (v <= 2) return launch_grouped<T, TU, 2, FP8>(p, stream);
     if (v <= 3) return launch_grouped<T, TU, 3, FP8>(p, stream);
     if (v <= 4) return launch_grouped<T, TU, 4, FP8>(p, stream);
     return launch_grouped<T, TU, 6, FP8>(p, stream);
   }
-  if (vec && units <= 4 * WIDE_WARPS * 32 && stage_bytes(p) <= MAX_SMEM) {
-    if (units <= 2 * WIDE_WARPS * 32) return launch_wide<T, TU, 2, FP8>(p, stream);
-    if (units <= 3 * WIDE_WARPS * 32) return launch_wide<T, TU, 3, FP8>(p, stream);
+  if (vec && chunks <= 4 * WIDE_WARPS<4> && stage_bytes(p) <= MAX_SMEM) {
+    if (chunks <= 2 * WIDE_WARPS<2>) return launch_wide<T, TU, 2, FP8>(p, stream);
     return launch_wide<T, TU, 4, FP8>(p, stream);
   }
   static std::mutex mu;
@@ -770,17 +838,10 @@ int launch_typed(NormParams& p, bool vec, cudaStream_t stream) {
   return launch_rows(kernel, p, grid, threads, static_cast<size_t>(p.K) * 4, stream);
 }
 
-template <typename T>
-int launch_from(NormParams& p, int u_dtype, bool fp8, bool vec, cudaStream_t stream) {
-  if (fp8) return launch_typed<T, T, true>(p, vec, stream);
-  if (u_dtype == CONVROT_F32) return launch_typed<T, float, false>(p, vec, stream);
-  if (u_dtype == CONVROT_F16) return launch_typed<T, __half, false>(p, vec, stream);
-  return launch_typed<T, __nv_bfloat16, false>(p, vec, stream);
-}
-
 }  // namespace
 
-int launch_block_norm(const convrot_block_norm_args& a, cudaStream_t stream) {
+template <typename T>
+int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream) {
   NormParams p{};
   p.H = a.H;
   p.Y = a.Y;
@@ -814,23 +875,24 @@ int launch_block_norm(const convrot_block_norm_args& a, cudaStream_t stream) {
   p.residual_scale = a.residual_scale;
   p.block_scale = a.block_scale;
   p.inv_k = 1.0f / static_cast<float>(a.K);
-  const size_t sz = dtype_size(a.dtype), usz = dtype_size(a.u_dtype);
+  const size_t sz = sizeof(T), usz = dtype_size(a.u_dtype);
   p.row_smem = static_cast<uint32_t>((a.K * sz + 127) / 128 * 128);
   const int n_coef = (a.Y && (a.gate || a.post_weight)) + (a.Y && a.post_bias) + (a.pre_weight || a.scale) +
                      (a.pre_bias || a.shift);
-  p.coef_smem = static_cast<uint32_t>((n_coef * a.K * 4 + 127) / 128 * 128);
+  p.coef_smem = static_cast<uint32_t>(n_coef * ((a.K + 255) / 256 * 256) * 4);
   auto row_ok = [](const void* ptr, int64_t ld, size_t size) { return !ptr || (aligned16(ptr) && ld * size % 16 == 0); };
   const bool vec = a.K % 8 == 0 && row_ok(a.H, a.ldh, sz) && row_ok(a.Y, a.ldy, sz) && row_ok(a.H_out, a.ldho, sz) &&
                    row_ok(a.U, a.ldu, usz) && row_ok(a.gate, a.ld_gate, 4) && row_ok(a.scale, a.ld_mod, 4) &&
                    row_ok(a.shift, a.ld_mod, 4) && row_ok(a.post_weight, 0, 4) && row_ok(a.post_bias, 0, 4) &&
                    row_ok(a.pre_weight, 0, 4) && row_ok(a.pre_bias, 0, 4);
-  const bool fp8 = a.Q != nullptr;
-  if (a.dtype == CONVROT_F32) return launch_from<float>(p, a.u_dtype, fp8, vec, stream);
-  if (a.dtype == CONVROT_F16) return launch_from<__half>(p, a.u_dtype, fp8, vec, stream);
-  return launch_from<__nv_bfloat16>(p, a.u_dtype, fp8, vec, stream);
+  if (a.Q) return launch_typed<T, T, true>(p, vec, stream);
+  if (a.u_dtype == CONVROT_F32) return launch_typed<T, float, false>(p, vec, stream);
+  if (a.u_dtype == CONVROT_F16) return launch_typed<T, __half, false>(p, vec, stream);
+  return launch_typed<T, __nv_bfloat16, false>(p, vec, stream);
 }
 
-int read_and_clear_norm_error() {
+template <typename T>
+int read_and_clear_norm_error_as() {
   int v = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_error, sizeof(int));
   if (e != cudaSuccess) return set_cuda_error(e);

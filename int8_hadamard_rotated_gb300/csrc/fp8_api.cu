@@ -162,6 +162,18 @@ int norm_checks(const convrot_block_norm_args& a) {
 
 }  // namespace
 
+namespace convrot {
+namespace fp8 {
+
+int read_and_clear_norm_error() {
+  const int st[] = {read_and_clear_norm_error_as<float>(), read_and_clear_norm_error_as<__half>(),
+                    read_and_clear_norm_error_as<__nv_bfloat16>()};
+  return st[0] ? st[0] : st[1] ? st[1] : st[2];
+}
+
+}  // namespace fp8
+}  // namespace convrot
+
 extern "C" {
 
 int convrot_block_norm(const convrot_block_norm_args* args, void* stream) {
@@ -169,7 +181,10 @@ int convrot_block_norm(const convrot_block_norm_args* args, void* stream) {
   if (int st = norm_checks(*args)) return st;
   if (args->M == 0) return CONVROT_OK;
   if (int st = check_device()) return st;
-  return launch_block_norm(*args, static_cast<cudaStream_t>(stream));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (args->dtype == CONVROT_F32) return launch_block_norm_as<float>(*args, s);
+  if (args->dtype == CONVROT_F16) return launch_block_norm_as<__half>(*args, s);
+  return launch_block_norm_as<__nv_bfloat16>(*args, s);
 }
 
 int fp8_pack_activations(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* Q_x, float* s_x,

@@ -1,4 +1,4 @@
-// fp8_common.cuh -- helpers shared by the block norms (block_norm.cu), the
+// fp8_common.cuh -- helpers shared by the block norms (block_norm.cuh), the
 // 8-bit floating-point pack (fp8_pack.cu) and the block-scaled GEMM
 // (fp8_gemm.cu): element conversion, the e4m3 block quantizer, bulk loads and
 // the host-side launchers.
@@ -50,44 +50,53 @@ template <> __device__ __forceinline__ void unpack2<__nv_bfloat16>(uint32_t w, f
   b = __uint_as_float(w & 0xffff0000u);
 }
 
-// Eight consecutive elements at a 16-byte aligned address (global or shared),
-// as four lane-wise pairs.
+// Lane-wise pairs, and four or eight consecutive elements as pairs, at an
+// address (global or shared) aligned to their size, at most 16 bytes.
 typedef unsigned long long Pair;
+__device__ __forceinline__ void load4(const float* p, Pair& a, Pair& b) {
+  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+  a = v.x;
+  b = v.y;
+}
+template <typename T>
+__device__ __forceinline__ Pair widen2(uint32_t w) {
+  float a, b;
+  unpack2<T>(w, a, b);
+  return f32x2_pack(a, b);
+}
 __device__ __forceinline__ void load8(const float* p, Pair (&x)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = f32x2_pack(a.x, a.y);
-  x[1] = f32x2_pack(a.z, a.w);
-  x[2] = f32x2_pack(b.x, b.y);
-  x[3] = f32x2_pack(b.z, b.w);
+  load4(p, x[0], x[1]);
+  load4(p + 4, x[2], x[3]);
 }
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, Pair (&x)[4]) {
   const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b;
-    unpack2<T>(w[i], a, b);
-    x[i] = f32x2_pack(a, b);
-  }
+  x[0] = widen2<T>(v.x);
+  x[1] = widen2<T>(v.y);
+  x[2] = widen2<T>(v.z);
+  x[3] = widen2<T>(v.w);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t narrow2(Pair x) {
+  float a, b;
+  f32x2_unpack(x, a, b);
+  return pack2<T>(a, b);
+}
+__device__ __forceinline__ void store4(float* p, Pair a, Pair b) {
+  *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(a, b);
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, Pair a, Pair b) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(narrow2<T>(a), narrow2<T>(b));
 }
 __device__ __forceinline__ void store8(float* p, const Pair (&x)[4]) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f32x2_unpack(x[i], v[2 * i], v[2 * i + 1]);
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  store4(p, x[0], x[1]);
+  store4(p + 4, x[2], x[3]);
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const Pair (&x)[4]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b;
-    f32x2_unpack(x[i], a, b);
-    w[i] = pack2<T>(a, b);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(narrow2<T>(x[0]), narrow2<T>(x[1]), narrow2<T>(x[2]), narrow2<T>(x[3]));
 }
 
 // ---------------------------------------------------------------------------
@@ -229,8 +238,12 @@ int launch_fp8_pack(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ld
                     cudaStream_t stream);
 int launch_fp8_weight(const void* W, int w_dtype, int64_t N, int64_t K, uint8_t* Q, float* s, cudaStream_t stream);
 
-// block_norm.cu: arguments already checked; M > 0.
-int launch_block_norm(const convrot_block_norm_args& a, cudaStream_t stream);
+// block_norm_*.cu, one per type T of H, Y and H_out: arguments already checked;
+// M > 0. The second reads and clears the kernels' error word.
+template <typename T>
+int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream);
+template <typename T>
+int read_and_clear_norm_error_as();
 
 // fp8_gemm.cu: every linear has N > 0; M > 0.
 int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
