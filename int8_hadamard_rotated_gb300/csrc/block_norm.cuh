@@ -263,12 +263,14 @@ template <typename T>
 struct Unit {
   int lo, hi;  // first features of the two halves
   bool on[2];  // which lie inside the row
-  __device__ __forceinline__ Unit(int chunk, int K) {
+  // `whole`: the chunk is known to lie inside (every unit of a thread but its
+  // last, which spares them the tests)
+  __device__ __forceinline__ Unit(int chunk, int K, bool whole = false) {
     const int lane = threadIdx.x & 31;
     lo = chunk * 256 + lane * (sizeof(T) == 4 ? 4 : 8);
     hi = lo + (sizeof(T) == 4 ? 128 : 4);
-    on[0] = lo < K;
-    on[1] = sizeof(T) == 4 ? hi < K : on[0];
+    on[0] = whole || lo < K;
+    on[1] = sizeof(T) == 4 ? whole || hi < K : on[0];
   }
   __device__ __forceinline__ void load(const T* row, Pair (&x)[4]) const {
     if constexpr (sizeof(T) == 4) {
@@ -341,7 +343,7 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
   Pair x[V][4];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    Unit<T>(u * W + wg, p.K).load(sh, x[u]);
+    Unit<T>(u * W + wg, p.K, u < V - 1).load(sh, x[u]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[u][i] = f32x2_mul(x[u][i], both(p.residual_scale));
   }
@@ -349,7 +351,7 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
     Stats ps{0.0f, 1.0f};
     if (p.post != CONVROT_NORM_NONE) {
       auto get = [&](int u, Pair (&v)[4], bool (&on)[2]) {
-        const Unit<T> unit(u * W + wg, p.K);
+        const Unit<T> unit(u * W + wg, p.K, u < V - 1);
         unit.load(sy, v);
         on[0] = unit.on[0];
         on[1] = unit.on[1];
@@ -358,7 +360,7 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
     }
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      const Unit<T> unit(u * W + wg, p.K);
+      const Unit<T> unit(u * W + wg, p.K, u < V - 1);
       Pair y[4], a[4], b[4];
       unit.load(sy, y);
       post(u, unit, a, b);
@@ -380,13 +382,13 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
   if (p.H_out) {
     T* out = static_cast<T*>(p.H_out) + row * p.ldho;
 #pragma unroll
-    for (int u = 0; u < V; ++u) Unit<T>(u * W + wg, p.K).store(out, x[u]);
+    for (int u = 0; u < V; ++u) Unit<T>(u * W + wg, p.K, u < V - 1).store(out, x[u]);
   }
   if (!FP8 && !p.U) return;
   Stats us{0.0f, 1.0f};
   if (p.pre != CONVROT_NORM_NONE) {
     auto get = [&](int u, Pair (&v)[4], bool (&on)[2]) {
-      const Unit<T> unit(u * W + wg, p.K);
+      const Unit<T> unit(u * W + wg, p.K, u < V - 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = unit.on[i / 2] ? x[u][i] : 0ull;
       on[0] = unit.on[0];
@@ -399,7 +401,7 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
   TU* out = FP8 ? nullptr : static_cast<TU*>(p.U) + row * p.ldu;
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const Unit<T> unit(u * W + wg, p.K);
+    const Unit<T> unit(u * W + wg, p.K, u < V - 1);
     Pair a[4], b[4];
     pre(u, unit, a, b);
     if (p.pre != CONVROT_NORM_NONE) {
@@ -492,8 +494,9 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
   // A unit's coefficients: in every 256 floats the first halves of the lanes,
   // then the second ones, so that a warp reads them without bank conflicts.
   const int n_chunks = (p.K + 255) / 256;
-  auto take = [&](const float* c, bool has, int chunk, float otherwise, Pair (&v)[4]) {
-    if (has && chunk < n_chunks) {
+  auto take = [&](const float* c, bool has, int u, float otherwise, Pair (&v)[4]) {
+    const int chunk = u * W + wg;
+    if (has && (u < V - 1 || chunk < n_chunks)) {
       load4(c + chunk * 256 + lane * 4, v[0], v[1]);
       load4(c + chunk * 256 + 128 + lane * 4, v[2], v[3]);
     } else {
@@ -545,12 +548,12 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
       do_row<T, TU, V, FP8>(
           p, row, ring.h(), ring.y(), W, group, wg, red[0] + group * W, red[1] + group * W,
           [&](int u, const Unit<T>&, Pair (&a)[4], Pair (&b)[4]) {
-            take(cpa, has_pa, u * W + wg, p.block_scale, a);
-            take(cpb, has_pb, u * W + wg, 0.0f, b);
+            take(cpa, has_pa, u, p.block_scale, a);
+            take(cpb, has_pb, u, 0.0f, b);
           },
           [&](int u, const Unit<T>&, Pair (&a)[4], Pair (&b)[4]) {
-            take(cqa, has_qa, u * W + wg, 1.0f, a);
-            take(cqb, has_qb, u * W + wg, 0.0f, b);
+            take(cqa, has_qa, u, 1.0f, a);
+            take(cqb, has_qb, u, 0.0f, b);
           },
           [&] {
             if (leader && row + p.stages * G < c1) ring.fetch(row + p.stages * G, ring.st);
@@ -562,25 +565,26 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
 }
 
 // The same for rows whose coefficients do not fit beside the staged rows: one
-// row per CTA of up to 24 warps; a thread's coefficients stay in registers
-// while the sample stays, but for a bias of the first norm (and, with four
-// units per thread, what is added after the second), which is read again for
-// every row.
-template <int V>
-constexpr int WIDE_WARPS = V <= 2 ? 24 : 16;
-
-template <typename T, typename TU, int V, bool FP8>
-__global__ void __launch_bounds__(WIDE_WARPS<V> * 32, 1)
+// row per CTA; a thread's factors stay in registers while the sample stays,
+// what is added (a bias of the first norm; bias and shift of the second) in
+// shared memory where that fits (p.coef_smem) and else read again for every
+// row. Eight warps with up to six units per thread: fp32 [4608, 12288] between
+// two weighted RMS norms takes 214 us with 24 warps of two units.
+template <typename T, typename TU, int V, bool FP8, int NW>
+__global__ void __launch_bounds__(NW * 32, 1)
 block_norm_wide_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[MAX_STAGES];
-  __shared__ float2 red[2][WIDE_WARPS<V>];
+  __shared__ float2 red[2][NW];
   __shared__ int abort_flag;
-  const int warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = static_cast<int>(static_cast<int64_t>(p.M) * blockIdx.x / gridDim.x);
   const int c1 = static_cast<int>(static_cast<int64_t>(p.M) * (blockIdx.x + 1) / gridDim.x);
-  Ring<T> ring{p, smem, full};
-  if (tid == 0) {
+  const bool has_pb = p.Y && p.post_bias, has_qb = p.pre_bias || p.shift, staged = p.coef_smem > 0;
+  float* cpb = reinterpret_cast<float*>(smem);
+  float* cqb = cpb + (has_pb ? (p.K + 255) / 256 * 256 : 0);
+  Ring<T> ring{p, smem + p.coef_smem, full};
+  if (threadIdx.x == 0) {
     for (int i = 0; i < MAX_STAGES; ++i) mbar_init(&full[i], 1);
     abort_flag = 0;
     fence_mbarrier_init();
@@ -588,11 +592,9 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
   __syncthreads();
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  if (tid == 0)
+  if (threadIdx.x == 0)
     for (int i = 0; i < p.stages && c0 + i < c1; ++i) ring.fetch(c0 + i, i);
-  const int W = blockDim.x >> 5;
-  constexpr bool HOLD_B = V <= 2;
-  Pair pa[V][4], qa[V][4], qb[HOLD_B ? V : 1][4];
+  Pair pa[V][4], qa[V][4];
   auto coefs = [&](int s, const Unit<T>& unit, bool pre, Pair (&a)[4], Pair (&b)[4]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -608,6 +610,23 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
       }
     }
   };
+  // a thread reads back what it wrote itself: no barrier
+  auto put = [&](float* c, int u, const Pair (&v)[4]) {
+    float* at = c + (u * NW + warp) * 256 + lane * 4;
+    if (u < V - 1 || (u * NW + warp) * 256 < p.K) {
+      store4(at, v[0], v[1]);
+      store4(at + 128, v[2], v[3]);
+    }
+  };
+  auto take = [&](const float* c, int u, Pair (&v)[4]) {
+    const float* at = c + (u * NW + warp) * 256 + lane * 4;
+    if (u < V - 1 || (u * NW + warp) * 256 < p.K) {
+      load4(at, v[0], v[1]);
+      load4(at + 128, v[2], v[3]);
+    } else {
+      v[0] = v[1] = v[2] = v[3] = 0ull;
+    }
+  };
   int cur = -2;
   for (int row = c0; row < c1; ++row) {
     const int s = sample_of(p, row);
@@ -615,38 +634,39 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
       cur = s;
 #pragma unroll
       for (int u = 0; u < V; ++u) {
-        const Unit<T> unit(u * W + warp, p.K);
+        const Unit<T> unit(u * NW + warp, p.K, u < V - 1);
         Pair b[4];
-        if (p.Y) coefs(s, unit, false, pa[u], b);
-        coefs(s, unit, true, qa[u], b);
-        if (HOLD_B) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) qb[HOLD_B ? u : 0][i] = b[i];
+        if (p.Y) {
+          coefs(s, unit, false, pa[u], b);
+          if (staged && has_pb) put(cpb, u, b);
         }
+        coefs(s, unit, true, qa[u], b);
+        if (staged && has_qb) put(cqb, u, b);
       }
     }
     mbar_wait(&ring.full[ring.st], ring.phase, &abort_flag, &g_norm_error);
     do_row<T, TU, V, FP8>(
-        p, row, ring.h(), ring.y(), W, 0, warp, red[0], red[1],
+        p, row, ring.h(), ring.y(), NW, 0, warp, red[0], red[1],
         [&](int u, const Unit<T>& unit, Pair (&a)[4], Pair (&b)[4]) {
-          Pair c[4];
-          if (p.post_bias) coefs(s, unit, false, c, b);
+          if (has_pb) {
+            if (staged) take(cpb, u, b);
+            else coefs(s, unit, false, a, b);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[i] = pa[u][i];
         },
         [&](int u, const Unit<T>& unit, Pair (&a)[4], Pair (&b)[4]) {
-          Pair c[4];
-          if (!HOLD_B && (p.pre_bias || p.shift)) {
-            coefs(s, unit, true, c, b);
+          if (has_qb) {
+            if (staged) take(cqb, u, b);
+            else coefs(s, unit, true, a, b);
           } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = HOLD_B ? qb[HOLD_B ? u : 0][i] : 0ull;
+            b[0] = b[1] = b[2] = b[3] = 0ull;
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[i] = qa[u][i];
         },
         [&] {
-          if (tid == 0 && row + p.stages < c1) ring.fetch(row + p.stages, ring.st);
+          if (threadIdx.x == 0 && row + p.stages < c1) ring.fetch(row + p.stages, ring.st);
         });
     ring.next();
   }
@@ -783,16 +803,17 @@ int launch_grouped(NormParams& p, cudaStream_t stream) {
   return launch_rows(kernel, p, grid, WARPS * 32, p.coef_smem + p.stages * stage, stream);
 }
 
-template <typename T, typename TU, int V, bool FP8>
+template <typename T, typename TU, int V, bool FP8, int NW>
 int launch_wide(NormParams& p, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;
-  auto kernel = block_norm_wide_kernel<T, TU, V, FP8>;
+  auto kernel = block_norm_wide_kernel<T, TU, V, FP8, NW>;
   if (int st = allow_smem(kernel, done, mu)) return st;
-  p.stages = static_cast<int>(std::min<size_t>(MAX_STAGES, MAX_SMEM / stage_bytes(p)));
-  const int threads = ((p.K + 255) / 256 + V - 1) / V * 32;
+  const size_t added = static_cast<size_t>((p.Y && p.post_bias) + (p.pre_bias || p.shift)) * ((p.K + 255) / 256) * 1024;
+  p.coef_smem = added + 2 * stage_bytes(p) <= MAX_SMEM ? static_cast<uint32_t>(added) : 0;
+  p.stages = static_cast<int>(std::min<size_t>(MAX_STAGES, (MAX_SMEM - p.coef_smem) / stage_bytes(p)));
   const unsigned grid = static_cast<unsigned>(std::min(p.M, device_sm_count()));
-  return launch_rows(kernel, p, grid, threads, p.stages * stage_bytes(p), stream);
+  return launch_rows(kernel, p, grid, NW * 32, p.coef_smem + p.stages * stage_bytes(p), stream);
 }
 
 // Warps per row of the grouped kernel: enough that a lane has at most four
@@ -819,15 +840,18 @@ int launch_typed(NormParams& p, bool vec, cudaStream_t stream) {
   if (const int W = vec ? pick_warps(p) : 0) {
     p.warps_per_row = W;
     const int v = (chunks + W - 1) / W;
-    if (v <= 1) return launch_grouped<T, TU, 1, FP8>(p, stream);
-    if (v <= 2) return launch_grouped<T, TU, 2, FP8>(p, stream);
-    if (v <= 3) return launch_grouped<T, TU, 3, FP8>(p, stream);
-    if (v <= 4) return launch_grouped<T, TU, 4, FP8>(p, stream);
+    if (v == 1) return launch_grouped<T, TU, 1, FP8>(p, stream);
+    if (v == 2) return launch_grouped<T, TU, 2, FP8>(p, stream);
+    if (v == 3) return launch_grouped<T, TU, 3, FP8>(p, stream);
+    if (v == 4) return launch_grouped<T, TU, 4, FP8>(p, stream);
+    if (v == 5) return launch_grouped<T, TU, 5, FP8>(p, stream);
     return launch_grouped<T, TU, 6, FP8>(p, stream);
   }
-  if (vec && chunks <= 4 * WIDE_WARPS<4> && stage_bytes(p) <= MAX_SMEM) {
-    if (chunks <= 2 * WIDE_WARPS<2>) return launch_wide<T, TU, 2, FP8>(p, stream);
-    return launch_wide<T, TU, 4, FP8>(p, stream);
+  if (vec && chunks > 3 * WARPS && stage_bytes(p) <= MAX_SMEM) {
+    if (chunks <= 4 * WARPS) return launch_wide<T, TU, 4, FP8, WARPS>(p, stream);
+    if (chunks <= 5 * WARPS) return launch_wide<T, TU, 5, FP8, WARPS>(p, stream);
+    if (chunks <= 6 * WARPS) return launch_wide<T, TU, 6, FP8, WARPS>(p, stream);
+    if (chunks <= 8 * WARPS) return launch_wide<T, TU, 4, FP8, 2 * WARPS>(p, stream);
   }
   static std::mutex mu;
   static uint64_t done = 0;
