@@ -82,20 +82,12 @@ int linear_checks(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, con
   return CONVROT_OK;
 }
 
-// The launch of the linears that have outputs.
-int run_linears(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights, int n,
-                int y_dtype, cudaStream_t stream) {
-  convrot_fp8_weight w[CONVROT_MAX_LINEARS];
+// The linears that have outputs, to `w`; their number.
+int with_output(const convrot_fp8_weight* weights, int n, convrot_fp8_weight (&w)[CONVROT_MAX_LINEARS]) {
   int k = 0;
   for (int j = 0; j < n; ++j)
     if (weights[j].N > 0) w[k++] = weights[j];
-  return k == 0 ? CONVROT_OK : launch_fp8_gemm(Qx, s_x, M, K, w, k, y_dtype, stream);
-}
-
-bool any_output(const convrot_fp8_weight* weights, int n) {
-  for (int j = 0; j < n; ++j)
-    if (weights[j].N > 0) return true;
-  return false;
+  return k;
 }
 
 int norm_checks(const convrot_block_norm_args& a) {
@@ -212,9 +204,11 @@ size_t fp8_linear_workspace_size(int64_t M, int64_t K) {
 int fp8_linear_packed(const uint8_t* Q_x, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
                       int n_weights, int y_dtype, void* stream) {
   if (int st = linear_checks(Q_x, s_x, M, K, weights, n_weights, y_dtype, flat(nullptr, 0))) return st;
-  if (M == 0 || !any_output(weights, n_weights)) return CONVROT_OK;
+  convrot_fp8_weight w[CONVROT_MAX_LINEARS];
+  const int n = with_output(weights, n_weights, w);
+  if (M == 0 || n == 0) return CONVROT_OK;
   if (int st = check_device()) return st;
-  return run_linears(Q_x, s_x, M, K, weights, n_weights, y_dtype, static_cast<cudaStream_t>(stream));
+  return launch_fp8_gemm(Q_x, s_x, M, K, w, n, y_dtype, static_cast<cudaStream_t>(stream));
 }
 
 int fp8_linear(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,
@@ -233,7 +227,9 @@ int fp8_linear(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, co
   if (int st = pack_checks(X, x_dtype, M, K, ldx, q, s, M * n_blocks(K))) return st;
   const int64_t size = static_cast<int64_t>(dtype_size(x_dtype));
   if (int st = linear_checks(q, s, M, K, weights, n_weights, y_dtype, Region{X, M, K * size, ldx * size})) return st;
-  if (M == 0 || !any_output(weights, n_weights)) return CONVROT_OK;
+  convrot_fp8_weight lin[CONVROT_MAX_LINEARS];
+  const int n = with_output(weights, n_weights, lin);
+  if (M == 0 || n == 0) return CONVROT_OK;
   const Region ws = flat(workspace, static_cast<int64_t>(need));
   for (int j = 0; j < n_weights; ++j) {
     const convrot_fp8_weight& w = weights[j];
@@ -243,8 +239,11 @@ int fp8_linear(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, co
   }
   if (int st = check_device()) return st;
   const cudaStream_t str = static_cast<cudaStream_t>(stream);
+  bool launched = false;
+  if (int st = launch_fp8_token(X, x_dtype, M, K, ldx, lin, n, y_dtype, str, &launched)) return st;
+  if (launched) return CONVROT_OK;
   if (int st = launch_fp8_pack(X, x_dtype, M, K, ldx, q, s, str)) return st;
-  return run_linears(q, s, M, K, weights, n_weights, y_dtype, str);
+  return launch_fp8_gemm(q, s, M, K, lin, n, y_dtype, str);
 }
 
 }  // extern "C"

@@ -99,6 +99,23 @@ __device__ __forceinline__ void store8(T* p, const Pair (&x)[4]) {
       make_uint4(narrow2<T>(x[0]), narrow2<T>(x[1]), narrow2<T>(x[2]), narrow2<T>(x[3]));
 }
 
+// Sixteen consecutive elements as pairs; `vec`: the address is 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, bool vec, Pair (&x)[8]) {
+  if (vec) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Pair v[4];
+      load8(p + 8 * h, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[4 * h + i] = v[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = f32x2_pack(to_f32(p[2 * i]), to_f32(p[2 * i + 1]));
+  }
+}
+
 // ---------------------------------------------------------------------------
 // the e4m3 block quantizer
 // ---------------------------------------------------------------------------
@@ -245,7 +262,10 @@ int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream);
 template <typename T>
 int read_and_clear_norm_error_as();
 
-// fp8_gemm.cu: every linear has N > 0; M > 0.
+// fp8_gemm.cu: every linear has N > 0; M > 0. launch_fp8_token packs X itself,
+// for few rows; *launched says whether the call is of that kind.
+int launch_fp8_token(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,
+                     int n_weights, int y_dtype, cudaStream_t stream, bool* launched);
 int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
                     int n_weights, int y_dtype, cudaStream_t stream);
 

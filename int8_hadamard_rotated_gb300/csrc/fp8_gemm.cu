@@ -273,21 +273,30 @@ __device__ __forceinline__ void drain(unsigned long long (&acc)[COLS / 2], uint3
   }
 }
 
-// The same with a factor per column, read from shared memory.
-template <int COLS>
-__device__ __forceinline__ void drain_scaled(unsigned long long (&acc)[COLS / 2], uint32_t ta, const float* f) {
-  uint32_t r[2][16];
-  tmem_ld16(ta, r[0]);
+// The same for n <= KG accumulators of COLS columns side by side (KG * COLS
+// <= 64), each with a factor per column, read from shared memory at f + its
+// index * COLS. One wait for all of them.
+template <int COLS, int KG>
+__device__ __forceinline__ void drain_scaled(unsigned long long (&acc)[COLS / 2], uint32_t ta, const float* f, int n) {
+  constexpr int PER = COLS / 16;  // loads per accumulator
+  uint32_t r[KG * PER][16];
 #pragma unroll
-  for (int q = 0; q < COLS / 16; ++q) {
-    tmem_wait16(r[q & 1]);
-    if (q + 1 < COLS / 16) tmem_ld16(ta + (q + 1) * 16, r[(q + 1) & 1]);
+  for (int q = 0; q < KG * PER; ++q) tmem_ld16(ta + q * 16, r[q]);
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const float4 s = *reinterpret_cast<const float4*>(f + q * 16 + 2 * k);
-      acc[q * 8 + k] = f32x2_fma(pair_bits(r[q & 1][2 * k], r[q & 1][2 * k + 1]), f32x2_pack(s.x, s.y), acc[q * 8 + k]);
-      acc[q * 8 + k + 1] =
-          f32x2_fma(pair_bits(r[q & 1][2 * k + 2], r[q & 1][2 * k + 3]), f32x2_pack(s.z, s.w), acc[q * 8 + k + 1]);
+  for (int q = 0; q < KG * PER; ++q) tmem_wait16(r[q]);
+#pragma unroll
+  for (int g = 0; g < KG; ++g) {
+    if (g >= n) break;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const uint32_t(&v)[16] = r[g * PER + q];
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const float4 s = *reinterpret_cast<const float4*>(f + g * COLS + q * 16 + 2 * k);
+        acc[q * 8 + k] = f32x2_fma(pair_bits(v[2 * k], v[2 * k + 1]), f32x2_pack(s.x, s.y), acc[q * 8 + k]);
+        acc[q * 8 + k + 1] =
+            f32x2_fma(pair_bits(v[2 * k + 2], v[2 * k + 3]), f32x2_pack(s.z, s.w), acc[q * 8 + k + 1]);
+      }
     }
   }
 }
@@ -558,6 +567,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
 // Six warps: 0-3 promote (32 lanes each), 4 loads, 5 issues MMAs.
 
 constexpr int SOLO_THREADS = 6 * 32;
+constexpr int MAX_SPLIT = 8;  // CTAs of a cluster
 
 template <int BN, bool SWAP>
 struct SoloGeom {
@@ -568,8 +578,13 @@ struct SoloGeom {
   static constexpr int STAGE_BYTES = X_BYTES + W_BYTES;
   static constexpr int SCALE_BYTES = SWAP ? 4 * 2 * 4 * BN * 4 : 0;  // [warp][2][4 blocks][BN]
   static constexpr int STAGES = (200 * 1024) / STAGE_BYTES;
-  static constexpr int BUFS = BN == 128 ? 2 : 4;
-  static constexpr int TMEM_COLS = BUFS * BN;  // 64, 128, 256, 256
+  // With few columns, KG blocks of K, each in an accumulator of its own, are
+  // handed over together: a hand-over costs the epilogue about 0.3 us whatever
+  // its size (24 CTAs on [1, 12288] x [3072, 12288]: 38 us one block at a time).
+  static constexpr int KG = SWAP ? 64 / BN : 1;
+  static constexpr int BUF_COLS = KG * BN;
+  static constexpr int BUFS = SWAP ? 4 : 2;
+  static constexpr int TMEM_COLS = BUFS * BUF_COLS;  // 256
   static constexpr uint32_t IDESC = idesc_e4m3_f32(LANES, BN);
   static constexpr int TILE_ROWS = X_ROWS;             // activation rows of a tile
   static constexpr int PITCH = SWAP ? QBLOCK : QBLOCK + 4;  // of the partial tile, floats
@@ -585,6 +600,52 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
+}
+
+// Sums the partial tiles that the cluster's CTAs hold at `smem` (ROWS
+// activation rows x 128 features, PITCH floats apart) in rank order, adds the
+// bias bv of the lane's four features (from feature n on) and stores: one row
+// per warp at a time, the rows shared out over the CTAs. Every thread of the
+// cluster comes here after a barrier that follows the last write.
+template <typename TY, int ROWS, int PITCH>
+__device__ __forceinline__ void finish_tile(const GemmParams& p, const Tile& c, int m0, int n, int rank,
+                                            const uint8_t* smem, const float (&bv)[4]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = min(ROWS, p.M - m0), N = p.N[c.lin];
+  TY* Y = static_cast<TY*>(p.out[c.lin]);
+  const int64_t ldy = p.ldy[c.lin];
+  const bool vec_out = n + 4 <= N && ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * sizeof(TY) - 1)) == 0;
+  for (int r = warp * p.split + rank; r < rows; r += (SOLO_THREADS / 32) * p.split) {
+    const int off = (r * PITCH + lane * 4) * 4;
+    float4 s[MAX_SPLIT];
+    if (p.split > 1) {
+#pragma unroll
+      for (int j = 0; j < MAX_SPLIT; ++j)
+        if (j < p.split) s[j] = ld_cluster_v4(mapa_shared(smem_u32(smem) + off, j));
+    } else {
+      s[0] = *reinterpret_cast<const float4*>(smem + off);
+    }
+    float v[4] = {s[0].x, s[0].y, s[0].z, s[0].w};
+#pragma unroll
+    for (int j = 1; j < MAX_SPLIT; ++j)
+      if (j < p.split) {
+        v[0] += s[j].x;
+        v[1] += s[j].y;
+        v[2] += s[j].z;
+        v[3] += s[j].w;
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += bv[k];
+    TY* yr = Y + (m0 + r) * ldy + n;
+    if (vec_out) {
+      store4(yr, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (n + k < N) yr[k] = from_f32<TY>(v[k]);
+    }
+  }
+  if (p.split > 1) cluster_sync();  // the others' reads of this CTA's partial sums
 }
 
 template <typename TY, int BN, bool SWAP>
@@ -662,15 +723,19 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
   } else if (warp == 5) {
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
-      for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err) ||
-            !mbar_wait(&full[stage], phase, abort_flag, err)) break;
-        tc_fence_after();
-        const uint32_t sx = smem_u32(smem + stage * G::STAGE_BYTES), sw = sx + G::X_BYTES;
-        mma_block<1>(tmem_base + buf * BN, SWAP ? sw : sx, SWAP ? sx : sw, G::IDESC);
-        mma_commit(&empty[stage]);
+      bool ok = true;
+      for (int kb0 = kb_begin; ok && kb0 < kb_end; kb0 += G::KG) {
+        if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err)) break;
+        for (int kb = kb0; kb < min(kb0 + G::KG, kb_end); ++kb) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, err)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sx = smem_u32(smem + stage * G::STAGE_BYTES), sw = sx + G::X_BYTES;
+          mma_block<1>(tmem_base + buf * G::BUF_COLS + (kb - kb0) * BN, SWAP ? sw : sx, SWAP ? sx : sw, G::IDESC);
+          mma_commit(&empty[stage]);
+          if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
         mma_commit(&tfull[buf]);
-        if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
         if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
       }
       mma_commit(done);
@@ -702,7 +767,7 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
     float f[4];
     int flip = 1;
 #pragma unroll 1
-    for (int kb = kb_begin, i = 0; kb < kb_end; ++kb, i = (i + 1) & 3) {
+    for (int kb = kb_begin, i = 0; kb < kb_end; kb += G::KG, i = (i + G::KG) & 3) {
       if (i == 0) {  // the factors of four blocks; the next four's scales are on their way meanwhile
         flip ^= 1;
 #pragma unroll
@@ -723,8 +788,8 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
       }
       if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) break;
       tc_fence_after();
-      const uint32_t ta = t_addr + buf * BN;
-      if (SWAP) drain_scaled<BN>(acc, ta, sc + (flip * 4 + i) * BN);
+      const uint32_t ta = t_addr + buf * G::BUF_COLS;
+      if constexpr (SWAP) drain_scaled<BN, G::KG>(acc, ta, sc + (flip * 4 + i) * BN, kb_end - kb);
       else drain<BN>(acc, ta, f32x2_pack(f[0], f[0]));
       f[0] = f[1];
       f[1] = f[2];
@@ -762,34 +827,214 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
     tc_fence_after();
     tmem_dealloc(tmem_base, G::TMEM_COLS);
   }
-  // one activation row of 128 features per warp at a time
-  const int rows = min(G::TILE_ROWS, p.M - m0);
-  TY* Y = static_cast<TY*>(p.out[c.lin]);
-  const int64_t ldy = p.ldy[c.lin];
-  const bool vec_out = n + 4 <= N && ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * sizeof(TY) - 1)) == 0;
-  for (int r = warp * p.split + rank; r < rows; r += (SOLO_THREADS / 32) * p.split) {
-    const uint32_t at = smem_u32(smem) + (r * G::PITCH + lane * 4) * 4;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < p.split; ++j) {
-      const float4 s = p.split > 1 ? ld_cluster_v4(mapa_shared(at, j))
-                                   : *reinterpret_cast<const float4*>(smem + (r * G::PITCH + lane * 4) * 4);
-      v[0] += s.x;
-      v[1] += s.y;
-      v[2] += s.z;
-      v[3] += s.w;
+  finish_tile<TY, G::TILE_ROWS, G::PITCH>(p, c, m0, n, rank, smem, bv);
+}
+
+// ---------------------------------------------------------------------------
+// at most 16 rows, packed inside
+// ---------------------------------------------------------------------------
+//
+// The swapped form of the kernel above for up to 16 rows of X itself: every
+// CTA packs its share of K of all rows into shared memory (the quantizer of
+// fp8_pack.cu, so the same codes and scales), which is little next to its
+// share of the weights, and one launch and a round trip through memory are
+// saved. The weight tiles are asked for before the launch's predecessor has
+// ended (into L2 only: what it may still write is seen), and packing overlaps
+// their arrival. Shared memory is kept under half an SM's, so that the next
+// call's CTAs can set themselves up beside these.
+
+constexpr int TOKEN_ROWS = 16;
+constexpr int TOKEN_X_BYTES = TOKEN_ROWS * BK;  // codes of one block of K
+constexpr int TOKEN_STAGES = 4;
+constexpr int TOKEN_BUFS = 4;
+constexpr int TOKEN_MAX_KB = 20;  // blocks of K per CTA
+constexpr int TOKEN_KG = 4;  // blocks of K handed over together
+constexpr int TOKEN_TMEM_COLS = TOKEN_BUFS * TOKEN_KG * TOKEN_ROWS;
+
+// Byte layout: weight stages (later the partial tile), activation codes per
+// block, factors [block][16], barriers.
+constexpr int TOKEN_SMEM_X = TOKEN_STAGES * QBLOCK * BK;
+__host__ __device__ constexpr int token_smem_scales(int kbs) { return TOKEN_SMEM_X + kbs * TOKEN_X_BYTES; }
+__host__ __device__ constexpr int token_smem_bars(int kbs) { return token_smem_scales(kbs) + kbs * TOKEN_ROWS * 4; }
+__host__ __device__ constexpr int token_smem(int kbs) {
+  return token_smem_bars(kbs) + (2 * TOKEN_STAGES + 2 * TOKEN_BUFS + 2) * 8 + 16 + 1024;
+}
+static_assert(token_smem(TOKEN_MAX_KB) <= 112 * 1024, "two CTAs per SM");
+static_assert(TOKEN_SMEM_X >= TOKEN_ROWS * QBLOCK * 4, "the partial tile fits the stages");
+
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(x), "r"(y) : "memory");
+}
+
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(SOLO_THREADS, 2)
+fp8_token_kernel(const __grid_constant__ GemmParams p, const TX* X, int64_t ldx, int K, bool vec_x) {
+  constexpr int STAGE_BYTES = QBLOCK * BK, BN = TOKEN_ROWS, PITCH = QBLOCK;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int max_kbs = (p.KB + p.split - 1) / p.split;
+  uint8_t* sx = smem + TOKEN_SMEM_X;
+  float* scales = reinterpret_cast<float*>(smem + token_smem_scales(max_kbs));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + token_smem_bars(max_kbs));
+  uint64_t* empty = full + TOKEN_STAGES;
+  uint64_t* tfull = empty + TOKEN_STAGES;
+  uint64_t* tempty = tfull + TOKEN_BUFS;
+  uint64_t* packed = tempty + TOKEN_BUFS;
+  uint64_t* done = packed + 1;
+  uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* err = &g_fp8_error;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const Tile c = decode(p, static_cast<int>(blockIdx.x) / p.split);
+  const int N = p.N[c.lin], n0 = c.nt * QBLOCK;
+  const int kb_begin = p.KB * rank / p.split, kb_end = p.KB * (rank + 1) / p.split;
+  pdl_launch_dependents();
+
+  if (threadIdx.x == 4 * 32) {
+    for (int kb = kb_begin; kb < kb_end; ++kb) tma_prefetch_2d(&p.tmap_w[c.lin], kb * BK, n0);
+    for (int s = 0; s < TOKEN_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
+    for (int b = 0; b < TOKEN_BUFS; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+    }
+    mbar_init(packed, 4);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_base_smem, TOKEN_TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_base_smem;
+  pdl_wait_prerequisites();
+  const int n = n0 + lane * 4;
+  const float* bias = p.bias[c.lin];
+  float bv[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] += bv[k];
-    TY* yr = Y + (m0 + r) * ldy + n;
-    if (vec_out) {
-      store4(yr, v);
-    } else {
+  for (int k = 0; k < 4; ++k) bv[k] = (bias && n + k < N) ? ldg_now(bias + n + k) : 0.0f;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      uint32_t stage = 0, phase = 0, n_issued = 0;
+      for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) break;
+        mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+        tma_load_2d(smem + stage * STAGE_BYTES, &p.tmap_w[c.lin], &full[stage], kb * BK, n0, pol);
+        ++n_issued;
+        if (++stage == TOKEN_STAGES) { stage = 0; phase ^= 1u; }
+      }
+      for (uint32_t s = 0; s < TOKEN_STAGES; ++s)
+        if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / TOKEN_STAGES) & 1u, nullptr, err);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
+      bool ok = mbar_wait(packed, 0, abort_flag, err);
+      for (int kb0 = kb_begin; ok && kb0 < kb_end; kb0 += TOKEN_KG) {
+        if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err)) break;
+        for (int kb = kb0; kb < min(kb0 + TOKEN_KG, kb_end); ++kb) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, err)) { ok = false; break; }
+          tc_fence_after();
+          mma_block<1>(tmem_base + (buf * TOKEN_KG + kb - kb0) * BN, smem_u32(smem + stage * STAGE_BYTES),
+                       smem_u32(sx + (kb - kb_begin) * TOKEN_X_BYTES), idesc_e4m3_f32(LANES, BN));
+          mma_commit(&empty[stage]);
+          if (++stage == TOKEN_STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        mma_commit(&tfull[buf]);
+        if (++buf == TOKEN_BUFS) { buf = 0; bphase ^= 1u; }
+      }
+      mma_commit(done);
+      mbar_wait(done, 0, nullptr, err);
+    }
+    __syncwarp();
+  } else {
+    // Pack: eight lanes per block of 128 features, 16 features per lane, up to
+    // AHEAD blocks' loads in flight; the codes go where a 128-byte-swizzled
+    // tensor-map load would put them. The rows past M stay as they are: they
+    // only meet columns that are not stored.
+    const float* ws = p.s_w[c.lin] + static_cast<int64_t>(c.nt) * p.KB;
+    const int sub = lane & 7, items = (kb_end - kb_begin) * p.M;
+    constexpr int AHEAD = 4, GROUPS = 128 / 8;
+    for (int i0 = 0; i0 < items; i0 += AHEAD * GROUPS) {
+      Pair x[AHEAD][8];
+      int b[AHEAD], r[AHEAD];
+      float w[AHEAD];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (n + k < N) yr[k] = from_f32<TY>(v[k]);
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + u * GROUPS + (threadIdx.x >> 3);
+        b[u] = i / p.M;
+        r[u] = i - b[u] * p.M;
+        const int col = (kb_begin + b[u]) * BK + sub * 16;
+        if (i < items && col < K) {
+          load16(X + r[u] * ldx + col, vec_x, x[u]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[u][k] = 0ull;
+        }
+        w[u] = i < items ? __ldg(ws + kb_begin + b[u]) : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        float m = max_magnitude(x[u]);
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float sc = e4m3_scale(m);
+        uint32_t q[4];
+        e4m3_codes(x[u], sc, q);
+        if (i0 + u * GROUPS + (threadIdx.x >> 3) < items) {
+          *reinterpret_cast<uint4*>(sx + b[u] * TOKEN_X_BYTES + r[u] * BK + ((sub ^ (r[u] & 7)) << 4)) =
+              make_uint4(q[0], q[1], q[2], q[3]);
+          if (sub == 0) scales[b[u] * TOKEN_ROWS + r[u]] = sc * w[u];
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(1, 4 * 32);  // the factors are read by all four warps
+    if (lane == 0) mbar_arrive(packed);
+
+    const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
+    unsigned long long acc[BN / 2];
+#pragma unroll
+    for (int i = 0; i < BN / 2; ++i) acc[i] = 0ull;
+    uint32_t buf = 0, bphase = 0;
+#pragma unroll 1
+    for (int kb = kb_begin; kb < kb_end; kb += TOKEN_KG) {
+      if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) break;
+      tc_fence_after();
+      drain_scaled<BN, TOKEN_KG>(acc, t_addr + buf * TOKEN_KG * BN, scales + (kb - kb_begin) * TOKEN_ROWS, kb_end - kb);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[buf]);
+      if (++buf == TOKEN_BUFS) { buf = 0; bphase ^= 1u; }
+    }
+    // the partial tile, in the stages: every MMA has completed
+    float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < BN / 2; ++i) {
+      float a, b;
+      f32x2_unpack(acc[i], a, b);
+      part[(2 * i) * PITCH + 32 * warp + lane] = a;
+      part[(2 * i + 1) * PITCH + 32 * warp + lane] = b;
     }
   }
-  if (p.split > 1) cluster_sync();  // the others' reads of this CTA's partial sums
+  tc_fence_before();
+  if (p.split > 1) cluster_sync(); else __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TOKEN_TMEM_COLS);
+  }
+  finish_tile<TY, TOKEN_ROWS, PITCH>(p, c, 0, n, rank, smem, bv);
 }
 
 // ---------------------------------------------------------------------------
@@ -855,7 +1100,8 @@ constexpr int64_t RASTER_L2_BYTES = 48ll << 20;  // activation codes a raster gr
 // activation rows x tile_cols features, operand boxes x_box and w_box rows.
 int fill(GemmParams& p, const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
          int tile_rows, int tile_cols, int x_box, int w_box) {
-  if (int st = make_tmap_codes(&p.tmap_x, Qx, M, K, x_box)) return st;
+  if (Qx)
+    if (int st = make_tmap_codes(&p.tmap_x, Qx, M, K, x_box)) return st;
   int64_t cols = 0;
   const int64_t KB = n_blocks(K);
   p.vec_scales = KB % 4 == 0 && aligned16(s_x);
@@ -922,12 +1168,38 @@ int launch_solo(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
-// The largest cluster (of 1, 2, 4, 8 CTAs) that keeps `tiles` clusters within
-// one wave of the SMs and leaves every CTA a block of K.
+// CTAs per tile (a cluster of 1, 2, 4 or 8; others measured slower, 19 us for
+// six against 13 us for four on [24, 12288] x [3072, 12288]): as many as keep
+// all tiles within one wave of the SMs, and leave every CTA a block of K.
 int pick_split(int64_t tiles, int64_t KB, int sms) {
   int s = 1;
-  while (s < 8 && tiles * (2 * s) <= sms && 2 * s <= KB) s *= 2;
+  while (s < MAX_SPLIT && tiles * (2 * s) <= sms && 2 * s <= KB) s *= 2;
   return s;
+}
+
+template <typename TX, typename TY>
+int launch_token_as(const void* X, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* w, int n, int split,
+                    cudaStream_t stream) {
+  GemmParams p;
+  if (int st = fill(p, nullptr, nullptr, M, K, w, n, TOKEN_ROWS, QBLOCK, TOKEN_ROWS, QBLOCK)) return st;
+  p.split = split;
+  static std::mutex mu;
+  static uint64_t done = 0;
+  auto kernel = fp8_token_kernel<TX, TY>;
+  if (int st = allow_smem(kernel, token_smem(TOKEN_MAX_KB), done, mu)) return st;
+  const bool vec = aligned16(X) && (ldx * sizeof(TX)) % 16 == 0;
+  Launch l(p.total_tiles * split, SOLO_THREADS, token_smem((p.KB + split - 1) / split), stream, split);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&l.cfg, kernel, p, static_cast<const TX*>(X), ldx, static_cast<int>(K), vec);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+template <typename TX>
+int launch_token(const void* X, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* w, int n, int y_dtype,
+                 int split, cudaStream_t stream) {
+  if (y_dtype == CONVROT_F32) return launch_token_as<TX, float>(X, M, K, ldx, w, n, split, stream);
+  if (y_dtype == CONVROT_F16) return launch_token_as<TX, __half>(X, M, K, ldx, w, n, split, stream);
+  return launch_token_as<TX, __nv_bfloat16>(X, M, K, ldx, w, n, split, stream);
 }
 
 template <typename TY>
@@ -961,6 +1233,19 @@ int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, c
   if (y_dtype == CONVROT_F32) return launch_as<float>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
   if (y_dtype == CONVROT_F16) return launch_as<__half>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
   return launch_as<__nv_bfloat16>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
+}
+
+int launch_fp8_token(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,
+                     int n_weights, int y_dtype, cudaStream_t stream, bool* launched) {
+  const int64_t KB = n_blocks(K);
+  int64_t tiles = 0;
+  for (int j = 0; j < n_weights; ++j) tiles += n_blocks(weights[j].N);
+  const int split = pick_split(tiles, KB, device_sm_count());
+  *launched = M <= TOKEN_ROWS && (KB + split - 1) / split <= TOKEN_MAX_KB;
+  if (!*launched) return CONVROT_OK;
+  if (x_dtype == CONVROT_F32) return launch_token<float>(X, M, K, ldx, weights, n_weights, y_dtype, split, stream);
+  if (x_dtype == CONVROT_F16) return launch_token<__half>(X, M, K, ldx, weights, n_weights, y_dtype, split, stream);
+  return launch_token<__nv_bfloat16>(X, M, K, ldx, weights, n_weights, y_dtype, split, stream);
 }
 
 int read_and_clear_fp8_error() {

@@ -13,23 +13,6 @@ namespace convrot {
 namespace fp8 {
 namespace {
 
-// Sixteen consecutive elements as pairs; `vec`: the address is 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, bool vec, Pair (&x)[8]) {
-  if (vec) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      Pair v[4];
-      load8(p + 8 * h, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[4 * h + i] = v[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = f32x2_pack(to_f32(p[2 * i]), to_f32(p[2 * i + 1]));
-  }
-}
-
 constexpr int PACK_THREADS = 256;
 
 // Eight lanes per block of 128 features, 16 features per lane; UNITS blocks

@@ -136,12 +136,12 @@ SIGNATURES = {
                          ctypes.POINTER(convrot_weight), _VP, _SZ, _VP]),
     "convrot_linear_noalloc": (_I, [_VP, _I, _I64, _I64, _I, ctypes.POINTER(convrot_weight), _I, _VP]),
     "convrot_linear_swiglu": (_I, [_VP, _I, _I64, _I64, _I, ctypes.POINTER(convrot_weight), _VP, _SZ, _VP]),
-    "convrot_block_norm": (_I, [ctypes.POINTER(convrot_block_norm_args), _VP]),
+    "convrot_block_norm": (_I, [_VP, _VP]),
     "fp8_pack_activations": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _VP]),
     "fp8_prepare_weight": (_I, [_VP, _I, _I64, _I64, _VP, _VP, _VP]),
     "fp8_linear_workspace_size": (_SZ, [_I64, _I64]),
-    "fp8_linear_packed": (_I, [_VP, _VP, _I64, _I64, ctypes.POINTER(convrot_fp8_weight), _I, _I, _VP]),
-    "fp8_linear": (_I, [_VP, _I, _I64, _I64, _I64, ctypes.POINTER(convrot_fp8_weight), _I, _I, _VP, _SZ, _VP]),
+    "fp8_linear_packed": (_I, [_VP, _VP, _I64, _I64, _VP, _I, _I, _VP]),
+    "fp8_linear": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I, _I, _VP, _SZ, _VP]),
     "convrot_device_status": (_I, [_VP]),
     "convrot_test_handover_timeout": (_I, [_VP, _VP, _I64, _I64, ctypes.POINTER(convrot_weight), _I, _VP, _SZ,
                                            ctypes.c_uint64, _VP]),
@@ -680,50 +680,55 @@ def convrot_linear_swiglu(X: torch.Tensor, G: int, gate: Tuple, up: Tuple, H: Op
 
 # ---------------------------------------------------------------------------
 # block norms and 8-bit floating-point linears
+#
+# A single token's calls take a few microseconds on the GPU, so the checks
+# here are written to cost little: one condition per tensor, its description
+# formed only for a refusal, and the argument structs packed in one go.
 # ---------------------------------------------------------------------------
 
 _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _E4M3 = torch.float8_e4m3fn
+_F32 = torch.float32
+# convrot_block_norm_args and convrot_fp8_weight as the C compiler lays them out
+_NORM_ARGS = struct.Struct("@qqiiPPqqffiiffPPPPPPPqqqPqPPqqPP")
+_FP8_WEIGHTS = [None] + [struct.Struct("@" + "PPPqPq" * n) for n in range(1, MAX_LINEARS + 1)]
+assert _NORM_ARGS.size == ctypes.sizeof(convrot_block_norm_args)
+assert _FP8_WEIGHTS[2].size == 2 * ctypes.sizeof(convrot_fp8_weight)
 
 
-class _On:
-    """The stream a call runs on: its handle for the library, and memory that
-    belongs to it. Buffers made inside a call are allocated on that stream, so
-    that neither their earlier nor their later use elsewhere overlaps it."""
-
-    __slots__ = ("device", "handle", "_stream")
-
-    def __init__(self, t: torch.Tensor, stream):
-        self.device = t.get_device()
-        if self.device < 0:
-            raise ValueError("the inputs must be CUDA tensors")
-        if self.device != torch.cuda.current_device():
-            raise ValueError("the inputs must be on the current CUDA device")
-        self._stream = stream
-        if stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(self.device)
-        else:
-            self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-
-    def empty(self, shape, dtype) -> torch.Tensor:
-        dev = torch.device("cuda", self.device)
-        if self._stream is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
-        s = self._stream if isinstance(self._stream, torch.cuda.Stream) else torch.cuda.ExternalStream(self.handle, dev)
-        with torch.cuda.stream(s):
-            return torch.empty(shape, dtype=dtype, device=dev)
+def _start(t: torch.Tensor, stream):
+    """(device, stream handle) of a call whose first input is t."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("the inputs must be CUDA tensors")
+    if device != torch.cuda.current_device():
+        raise ValueError("the inputs must be on the current CUDA device")
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _rows(t: torch.Tensor, name: str, on: _On, shape=None, dtype=None) -> int:
-    """Checks a matrix whose rows are contiguous; the distance between them."""
-    if t.get_device() != on.device:
-        raise ValueError(f"{name} must be on the device of the other tensors")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must be a matrix" + (f" of shape {tuple(shape)}" if shape is not None else ""))
-    if t.dtype not in _DTYPES if dtype is None else t.dtype != dtype:
-        raise ValueError(f"{name} must be " + (f"{dtype}" if dtype is not None else "float32, float16 or bfloat16")
-                         + f", got {t.dtype}")
-    M, K = t.shape
+def _empty(shape, dtype, device: int, stream) -> torch.Tensor:
+    """Memory that belongs to the call's stream, so that neither its earlier
+    nor its later use elsewhere overlaps the call."""
+    dev = torch.device("cuda", device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream, dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _rows(t: torch.Tensor, name: str, device: int, shape, dtype=None) -> int:
+    """Checks a matrix whose rows are contiguous (of a float type, or dtype);
+    the distance between them."""
+    if t.get_device() != device or t.shape != shape or (t.dtype not in _DTYPES if dtype is None else t.dtype is not dtype):
+        raise ValueError(f"{name} must be a {dtype or 'float32, float16 or bfloat16'} matrix of shape {tuple(shape)} "
+                         f"on the device of the other tensors, got {t.dtype} {tuple(t.shape)}")
+    M, K = shape
+    if t.is_contiguous():
+        return K
     ld, inner = t.stride()
     if inner != 1 and K > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
@@ -734,11 +739,18 @@ def _rows(t: torch.Tensor, name: str, on: _On, shape=None, dtype=None) -> int:
     return ld
 
 
-def _dense(t: torch.Tensor, name: str, on: _On, shape, dtype):
-    """Checks a contiguous array of a given shape and type."""
-    if t.get_device() != on.device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _dense(t: torch.Tensor, name: str, device: int, shape, dtype) -> int:
+    """Checks a contiguous array of a given shape and type; its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the device of the "
                          f"other tensors, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape
 
 
 def _n_blocks(n: int) -> int:
@@ -749,58 +761,55 @@ def fp8_pack_activations(X: torch.Tensor, Q_x: Optional[torch.Tensor] = None, s_
                          stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """X [M,K] (float32, float16 or bfloat16, rows contiguous) -> (Q_x
     float8_e4m3fn [M,K], s_x float32 [M, ceil(K/128)])."""
-    on = _On(X, stream)
-    ldx = _rows(X, "X", on)
-    M, K = X.shape
+    device, handle = _start(X, stream)
+    M, K = shape = _matrix(X, "X")
+    ldx = _rows(X, "X", device, shape)
+    kb = (M, _n_blocks(K))
     if Q_x is None:
-        Q_x = on.empty((M, K), _E4M3)
+        Q_x = _empty(shape, _E4M3, device, stream)
     if s_x is None:
-        s_x = on.empty((M, _n_blocks(K)), torch.float32)
-    _dense(Q_x, "Q_x", on, (M, K), _E4M3)
-    _dense(s_x, "s_x", on, (M, _n_blocks(K)), torch.float32)
-    _check(lib().fp8_pack_activations(X.data_ptr(), _DTYPES[X.dtype], M, K, ldx, Q_x.data_ptr(), s_x.data_ptr(),
-                                      on.handle), "fp8_pack_activations")
+        s_x = _empty(kb, _F32, device, stream)
+    _check(lib().fp8_pack_activations(X.data_ptr(), _DTYPES[X.dtype], M, K, ldx,
+                                      _dense(Q_x, "Q_x", device, shape, _E4M3), _dense(s_x, "s_x", device, kb, _F32),
+                                      handle), "fp8_pack_activations")
     return Q_x, s_x
 
 
 def fp8_prepare_weight(W: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Offline weight path: W [N,K] (float32, float16 or bfloat16) -> (Q_w
     float8_e4m3fn [N,K], s_w float32 [ceil(N/128), ceil(K/128)])."""
-    on = _On(W, stream)
-    if _rows(W, "W", on) != W.shape[1]:
+    device, handle = _start(W, stream)
+    N, K = shape = _matrix(W, "W")
+    if _rows(W, "W", device, shape) != K:
         raise ValueError("W must be contiguous")
-    N, K = W.shape
-    Q_w = on.empty((N, K), _E4M3)
-    s_w = on.empty((_n_blocks(N), _n_blocks(K)), torch.float32)
-    _check(lib().fp8_prepare_weight(W.data_ptr(), _DTYPES[W.dtype], N, K, Q_w.data_ptr(), s_w.data_ptr(), on.handle),
+    Q_w = _empty(shape, _E4M3, device, stream)
+    s_w = _empty((_n_blocks(N), _n_blocks(K)), _F32, device, stream)
+    _check(lib().fp8_prepare_weight(W.data_ptr(), _DTYPES[W.dtype], N, K, Q_w.data_ptr(), s_w.data_ptr(), handle),
            "fp8_prepare_weight")
     return Q_w, s_w
 
 
-def _fp8_weights(on: _On, M: int, K: int, qs, scales, biases, Ys, out_dtype):
+def _fp8_weights(device: int, stream, M: int, K: int, qs, scales, biases, Ys, out_dtype):
     """(descriptors, outputs, y_dtype) of an fp8 linear call."""
     n = len(qs)
     if not 1 <= n <= MAX_LINEARS or len(scales) != n or (biases is not None and len(biases) != n) or \
             (Ys is not None and len(Ys) != n):
         raise ValueError(f"1 to {MAX_LINEARS} weights, with as many scales, biases and outputs")
     if Ys is None:
-        Ys = [on.empty((M, q.shape[0]), out_dtype) for q in qs]
-    arr = (convrot_fp8_weight * n)()
+        Ys = [_empty((M, q.shape[0]), out_dtype, device, stream) for q in qs]
+    y_dtype = Ys[0].dtype
+    kb = _n_blocks(K)
+    d = []
     for j in range(n):
-        q, s, b, y = qs[j], scales[j], None if biases is None else biases[j], Ys[j]
+        q, b, y = qs[j], None if biases is None else biases[j], Ys[j]
         N = q.shape[0]
-        _dense(q, "a weight", on, (N, K), _E4M3)
-        _dense(s, "a weight's scales", on, (_n_blocks(N), _n_blocks(K)), torch.float32)
-        if b is not None:
-            _dense(b, "a bias", on, (N,), torch.float32)
-        ldy = _rows(y, "an output", on, (M, N))
-        if y.dtype != Ys[0].dtype:
+        d += (_dense(q, "a weight", device, (N, K), _E4M3),
+              _dense(scales[j], "a weight's scales", device, (_n_blocks(N), kb), _F32),
+              0 if b is None else _dense(b, "a bias", device, (N,), _F32), N, y.data_ptr(),
+              _rows(y, "an output", device, (M, N)))
+        if y.dtype is not y_dtype:
             raise ValueError("the outputs of one call have one type")
-        w = arr[j]
-        w.q, w.scale, w.N, w.Y, w.ldy = q.data_ptr(), s.data_ptr(), N, y.data_ptr(), ldy
-        if b is not None:
-            w.bias = b.data_ptr()
-    return arr, Ys, _DTYPES[Ys[0].dtype]
+    return _FP8_WEIGHTS[n].pack(*d), Ys, _DTYPES[y_dtype]
 
 
 def fp8_linear_packed(Q_x: torch.Tensor, s_x: torch.Tensor, qs: Sequence[torch.Tensor], scales: Sequence[torch.Tensor],
@@ -811,15 +820,12 @@ def fp8_linear_packed(Q_x: torch.Tensor, s_x: torch.Tensor, qs: Sequence[torch.T
     fp8_pack_activations or convrot_block_norm_fp8; weights (codes `qs`,
     `scales`) from fp8_prepare_weight. Ys: outputs to write (float32, float16
     or bfloat16, rows contiguous), or new ones of out_dtype."""
-    on = _On(Q_x, stream)
-    if Q_x.dim() != 2:
-        raise ValueError("Q_x must be a matrix")
-    M, K = Q_x.shape
-    _dense(Q_x, "Q_x", on, (M, K), _E4M3)
-    _dense(s_x, "s_x", on, (M, _n_blocks(K)), torch.float32)
-    arr, Ys, y_dtype = _fp8_weights(on, M, K, qs, scales, biases, Ys, out_dtype)
-    _check(lib().fp8_linear_packed(Q_x.data_ptr(), s_x.data_ptr(), M, K, arr, len(arr), y_dtype, on.handle),
-           "fp8_linear_packed")
+    device, handle = _start(Q_x, stream)
+    M, K = shape = _matrix(Q_x, "Q_x")
+    q_ptr = _dense(Q_x, "Q_x", device, shape, _E4M3)
+    s_ptr = _dense(s_x, "s_x", device, (M, _n_blocks(K)), _F32)
+    weights, Ys, y_dtype = _fp8_weights(device, stream, M, K, qs, scales, biases, Ys, out_dtype)
+    _check(lib().fp8_linear_packed(q_ptr, s_ptr, M, K, weights, len(Ys), y_dtype, handle), "fp8_linear_packed")
     return Ys
 
 
@@ -833,67 +839,61 @@ def fp8_linear(X: torch.Tensor, qs: Sequence[torch.Tensor], scales: Sequence[tor
                stream=None) -> List[torch.Tensor]:
     """Pack X once (fp8_pack_activations), then every Y_j = X W_j^T + b_j as
     fp8_linear_packed. New outputs are of out_dtype (X's own by default)."""
-    on = _On(X, stream)
-    ldx = _rows(X, "X", on)
-    M, K = X.shape
-    arr, Ys, y_dtype = _fp8_weights(on, M, K, qs, scales, biases, Ys, X.dtype if out_dtype is None else out_dtype)
-    need = fp8_linear_workspace_size(M, K)
-    ws = on.empty((max(need, 1),), torch.uint8) if workspace is None else workspace
-    if ws.get_device() != on.device or not ws.is_contiguous():
+    device, handle = _start(X, stream)
+    M, K = shape = _matrix(X, "X")
+    ldx = _rows(X, "X", device, shape)
+    weights, Ys, y_dtype = _fp8_weights(device, stream, M, K, qs, scales, biases, Ys,
+                                        X.dtype if out_dtype is None else out_dtype)
+    ws = workspace
+    if ws is None:
+        ws = _empty((max(fp8_linear_workspace_size(M, K), 1),), torch.uint8, device, stream)
+    elif ws.get_device() != device or not ws.is_contiguous():
         raise ValueError("workspace must be contiguous and on the device of the other tensors")
-    _check(lib().fp8_linear(X.data_ptr(), _DTYPES[X.dtype], M, K, ldx, arr, len(arr), y_dtype, ws.data_ptr(),
-                            ws.numel() * ws.element_size(), on.handle), "fp8_linear")
+    _check(lib().fp8_linear(X.data_ptr(), _DTYPES[X.dtype], M, K, ldx, weights, len(Ys), y_dtype, ws.data_ptr(),
+                            ws.numel() * ws.element_size(), handle), "fp8_linear")
     return Ys
 
 
 def _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_weight, post_bias, gate, pre_norm,
-                pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, on: _On):
-    """The arguments of convrot_block_norm up to the form of u."""
-    a = convrot_block_norm_args()
-    a.ldh = _rows(H, "H", on)
-    M, K = H.shape
-    a.M, a.K, a.dtype, a.H = M, K, _DTYPES[H.dtype], H.data_ptr()
-    if Y is not None:
-        a.ldy = _rows(Y, "Y", on, (M, K), H.dtype)
-        a.Y = Y.data_ptr()
-    a.residual_scale, a.block_scale = residual_scale, block_scale
-    a.post_norm, a.pre_norm, a.post_eps, a.pre_eps = post_norm, pre_norm, post_eps, pre_eps
-    if post_weight is not None:
-        _dense(post_weight, "post_weight", on, (K,), torch.float32)
-        a.post_weight = post_weight.data_ptr()
-    if post_bias is not None:
-        _dense(post_bias, "post_bias", on, (K,), torch.float32)
-        a.post_bias = post_bias.data_ptr()
-    if pre_weight is not None:
-        _dense(pre_weight, "pre_weight", on, (K,), torch.float32)
-        a.pre_weight = pre_weight.data_ptr()
-    if pre_bias is not None:
-        _dense(pre_bias, "pre_bias", on, (K,), torch.float32)
-        a.pre_bias = pre_bias.data_ptr()
-    samples = None
-    for name, v in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if v is None:
-            continue
-        samples = v.shape[0] if samples is None else samples
-        ld = _rows(v, name, on, (samples, K), torch.float32)
-        setattr(a, name, v.data_ptr())
-        if name == "gate":
-            a.ld_gate = ld
-        elif name == "shift" and scale is not None and a.ld_mod != ld:
+                pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, U, u_dtype, ldu, Q, s,
+                device, handle):
+    """Checks what both forms of the block norm share and calls the library."""
+    M, K = shape = H.shape
+    dtype = H.dtype
+    ldh = _rows(H, "H", device, shape)
+    ldy = 0 if Y is None else _rows(Y, "Y", device, shape, dtype)
+    ldho = 0 if H_out is None else _rows(H_out, "H_out", device, shape, dtype)
+    vec = (K,)
+    samples = ld_gate = ld_mod = 0
+    if gate is not None:
+        samples = gate.shape[0]
+        ld_gate = _rows(gate, "gate", device, (samples, K), _F32)
+    if scale is not None:
+        samples = samples or scale.shape[0]
+        ld_mod = _rows(scale, "scale", device, (samples, K), _F32)
+    if shift is not None:
+        samples = samples or shift.shape[0]
+        ld = _rows(shift, "shift", device, (samples, K), _F32)
+        if scale is not None and ld != ld_mod:
             raise ValueError("scale and shift must have the same distance between rows")
-        else:
-            a.ld_mod = ld
-    if samples is not None:
-        a.n_samples, a.rows_per_sample = samples, rows_per_sample
+        ld_mod = ld
+    rows = 0
+    if samples:
         if row_sample is not None:
-            _dense(row_sample, "row_sample", on, (M,), torch.int32)
-            a.row_sample = row_sample.data_ptr()
+            rows = _dense(row_sample, "row_sample", device, (M,), torch.int32)
         elif rows_per_sample == 0 and samples > 1:
             raise ValueError("several samples need row_sample or rows_per_sample")
-    if H_out is not None:
-        a.ldho = _rows(H_out, "H_out", on, (M, K), H.dtype)
-        a.H_out = H_out.data_ptr()
-    return a
+    args = _NORM_ARGS.pack(
+        M, K, _DTYPES[dtype], u_dtype, H.data_ptr(), 0 if Y is None else Y.data_ptr(), ldh, ldy, residual_scale,
+        block_scale, post_norm, pre_norm, post_eps, pre_eps,
+        0 if post_weight is None else _dense(post_weight, "post_weight", device, vec, _F32),
+        0 if post_bias is None else _dense(post_bias, "post_bias", device, vec, _F32),
+        0 if pre_weight is None else _dense(pre_weight, "pre_weight", device, vec, _F32),
+        0 if pre_bias is None else _dense(pre_bias, "pre_bias", device, vec, _F32),
+        0 if gate is None else gate.data_ptr(), 0 if scale is None else scale.data_ptr(),
+        0 if shift is None else shift.data_ptr(), ld_gate, ld_mod, samples, rows, rows_per_sample,
+        0 if H_out is None else H_out.data_ptr(), U, ldho, ldu, Q, s)
+    _check(lib().convrot_block_norm(args, handle), "convrot_block_norm")
 
 
 def convrot_block_norm(H: torch.Tensor, Y: Optional[torch.Tensor] = None, *, residual_scale: float = 1.0,
@@ -910,17 +910,16 @@ def convrot_block_norm(H: torch.Tensor, Y: Optional[torch.Tensor] = None, *, res
     row_sample[m] (int32) or m // rows_per_sample. Returns (h', u): H_out and U
     where given (H_out may be H), new tensors where not (u of u_dtype, H's own
     by default), None for what want_h or want_u leaves out."""
-    on = _On(H, stream)
+    device, handle = _start(H, stream)
+    shape = _matrix(H, "H")
     if H_out is None and want_h:
-        H_out = on.empty(H.shape, H.dtype)
+        H_out = _empty(shape, H.dtype, device, stream)
     if U is None and want_u:
-        U = on.empty(H.shape, H.dtype if u_dtype is None else u_dtype)
-    a = _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_weight, post_bias, gate, pre_norm,
-                    pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, on)
-    if U is not None:
-        a.ldu = _rows(U, "U", on, H.shape)
-        a.U, a.u_dtype = U.data_ptr(), _DTYPES[U.dtype]
-    _check(lib().convrot_block_norm(ctypes.byref(a), on.handle), "convrot_block_norm")
+        U = _empty(shape, H.dtype if u_dtype is None else u_dtype, device, stream)
+    ldu = 0 if U is None else _rows(U, "U", device, shape)
+    _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_weight, post_bias, gate, pre_norm,
+                pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out,
+                0 if U is None else U.data_ptr(), 0 if U is None else _DTYPES[U.dtype], ldu, 0, 0, device, handle)
     return H_out, U
 
 
@@ -934,18 +933,16 @@ def convrot_block_norm_fp8(H: torch.Tensor, Y: Optional[torch.Tensor] = None, *,
     """convrot_block_norm with u quantized as it is formed: returns (h', Q, s),
     Q float8_e4m3fn [M,K] and s float32 [M, ceil(K/128)] as
     fp8_pack_activations gives them, for fp8_linear_packed."""
-    on = _On(H, stream)
+    device, handle = _start(H, stream)
+    M, K = shape = _matrix(H, "H")
+    kb = (M, _n_blocks(K))
     if H_out is None and want_h:
-        H_out = on.empty(H.shape, H.dtype)
-    a = _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_weight, post_bias, gate, pre_norm,
-                    pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, on)
-    M, K = H.shape
+        H_out = _empty(shape, H.dtype, device, stream)
     if Q is None:
-        Q = on.empty((M, K), _E4M3)
+        Q = _empty(shape, _E4M3, device, stream)
     if s is None:
-        s = on.empty((M, _n_blocks(K)), torch.float32)
-    _dense(Q, "Q", on, (M, K), _E4M3)
-    _dense(s, "s", on, (M, _n_blocks(K)), torch.float32)
-    a.Q, a.s = Q.data_ptr(), s.data_ptr()
-    _check(lib().convrot_block_norm(ctypes.byref(a), on.handle), "convrot_block_norm")
+        s = _empty(kb, _F32, device, stream)
+    _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_weight, post_bias, gate, pre_norm,
+                pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, 0, 0, 0,
+                _dense(Q, "Q", device, shape, _E4M3), _dense(s, "s", device, kb, _F32), device, handle)
     return H_out, Q, s

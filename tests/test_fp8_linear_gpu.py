@@ -254,3 +254,39 @@ def test_linear_refusals(ops):
     with pytest.raises(ops.ConvrotError) as e:
         ops.fp8_linear(X, [Qw], [sw], workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == ops.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("M", [1, 2, 7, 15, 16])
+@pytest.mark.parametrize("N,K", [(16, 16), (130, 656), (1283, 3072), (5000, 1040), (128, 12288)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f16")])
+def test_few_rows_are_packed_alike(ops, M, N, K, dtype, out):
+    """Up to 16 rows are packed inside the linear: the same result as of codes
+    packed before, at any alignment of X."""
+    Qw, sw, qw, w = packed(N + 1, N, K, 128)
+    b = torch.randn(N, generator=torch.Generator().manual_seed(N)).cuda()
+    wide = activations(M + N, M, K + 8, dtype)
+    for off in (0, 3):
+        X = wide[:, off:off + K]
+        ref, mag = bo.fp8_linear(*bo.fp8_pack(host(X.float().contiguous())), qw, w, host(b))
+        y = torch.full((M, N), float("nan"), dtype=DT[out], device="cuda")
+        ops.fp8_linear(X, [Qw], [sw], [b], Ys=[y])
+        assert_linear(y, ref, mag, K)
+    assert ops.convrot_device_status() == ops.OK
+
+
+def test_few_rows_non_finite(ops):
+    X = activations(3, 9, 512)
+    X[1, 300] = float("nan")
+    X[3, 5] = float("inf")
+    Qw, sw, _, _ = packed(3, 256, 512, 128)
+    (y,) = ops.fp8_linear(X, [Qw], [sw])
+    assert not torch.isfinite(y[[1, 3]]).any() and torch.isfinite(y[[0, 2, 4, 5, 6, 7, 8]]).all()
+
+
+def test_few_rows_of_a_long_k(ops):
+    """More blocks of K than the linear packs itself."""
+    M, N, K = 3, 128, 24576
+    X = activations(8, M, K)
+    Qw, sw, qw, w = packed(9, N, K, 128)
+    (y,) = ops.fp8_linear(X, [Qw], [sw])
+    assert_linear(y, *bo.fp8_linear(*bo.fp8_pack(host(X)), qw, w), K)
