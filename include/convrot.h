@@ -657,8 +657,8 @@ int fp8_linear_packed(const uint8_t* Q_x, const float* s_x, int64_t M, int64_t K
 
 /*
  * fp8_linear -- fp8_pack_activations of X into the workspace, then
- * fp8_linear_packed (up to 16 rows are packed by the linear's own launch, into
- * the same codes; the workspace is not touched then).
+ * fp8_linear_packed (up to 4 rows of up to 12288 features are packed by the
+ * linear's own launch, into the same codes; the workspace is not touched then).
  *   workspace  at least fp8_linear_workspace_size(M, K) bytes, 16-byte aligned.
  * Errors: those of both, and ERR_WORKSPACE.
  */

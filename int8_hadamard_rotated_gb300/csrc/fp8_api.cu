@@ -240,7 +240,7 @@ int fp8_linear(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, co
   if (int st = check_device()) return st;
   const cudaStream_t str = static_cast<cudaStream_t>(stream);
   bool launched = false;
-  if (int st = launch_fp8_token(X, x_dtype, M, K, ldx, lin, n, y_dtype, str, &launched)) return st;
+  if (int st = launch_fp8_packing(X, x_dtype, M, K, ldx, lin, n, y_dtype, str, &launched)) return st;
   if (launched) return CONVROT_OK;
   if (int st = launch_fp8_pack(X, x_dtype, M, K, ldx, q, s, str)) return st;
   return launch_fp8_gemm(q, s, M, K, lin, n, y_dtype, str);

@@ -262,10 +262,10 @@ int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream);
 template <typename T>
 int read_and_clear_norm_error_as();
 
-// fp8_gemm.cu: every linear has N > 0; M > 0. launch_fp8_token packs X itself,
-// for few rows; *launched says whether the call is of that kind.
-int launch_fp8_token(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,
-                     int n_weights, int y_dtype, cudaStream_t stream, bool* launched);
+// fp8_gemm.cu: every linear has N > 0; M > 0. launch_fp8_packing packs X
+// itself, for few rows; *launched says whether the call is of that kind.
+int launch_fp8_packing(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,
+                       int n_weights, int y_dtype, cudaStream_t stream, bool* launched);
 int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
                     int n_weights, int y_dtype, cudaStream_t stream);
 

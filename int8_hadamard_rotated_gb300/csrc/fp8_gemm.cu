@@ -567,7 +567,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
 // Six warps: 0-3 promote (32 lanes each), 4 loads, 5 issues MMAs.
 
 constexpr int SOLO_THREADS = 6 * 32;
-constexpr int MAX_SPLIT = 8;  // CTAs of a cluster
+constexpr int MAX_SPLIT = 4;  // CTAs of a cluster
 
 template <int BN, bool SWAP>
 struct SoloGeom {
@@ -577,7 +577,10 @@ struct SoloGeom {
   static constexpr int W_BYTES = W_ROWS * BK;
   static constexpr int STAGE_BYTES = X_BYTES + W_BYTES;
   static constexpr int SCALE_BYTES = SWAP ? 4 * 2 * 4 * BN * 4 : 0;  // [warp][2][4 blocks][BN]
-  static constexpr int STAGES = (200 * 1024) / STAGE_BYTES;
+  // Few columns: two CTAs per SM, so that one's set-up and sums overlap the
+  // other's loads (16 rows through three 3072 x 3072 linears, K split in four:
+  // 6.7 us against 7.7 us with one CTA per SM and K split in two).
+  static constexpr int STAGES = ((SWAP ? 96 : 200) * 1024) / STAGE_BYTES;
   // With few columns, KG blocks of K, each in an accumulator of its own, are
   // handed over together: a hand-over costs the epilogue about 0.3 us whatever
   // its size (24 CTAs on [1, 12288] x [3072, 12288]: 38 us one block at a time).
@@ -649,7 +652,7 @@ __device__ __forceinline__ void finish_tile(const GemmParams& p, const Tile& c, 
 }
 
 template <typename TY, int BN, bool SWAP>
-__global__ void __launch_bounds__(SOLO_THREADS, 1)
+__global__ void __launch_bounds__(SOLO_THREADS, SWAP ? 2 : 1)
 fp8_solo_kernel(const __grid_constant__ GemmParams p) {
   using G = SoloGeom<BN, SWAP>;
   extern __shared__ uint8_t smem_raw[];
@@ -831,210 +834,171 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// at most 16 rows, packed inside
+// at most 8 rows: weights streamed to registers
 // ---------------------------------------------------------------------------
 //
-// The swapped form of the kernel above for up to 16 rows of X itself: every
-// CTA packs its share of K of all rows into shared memory (the quantizer of
-// fp8_pack.cu, so the same codes and scales), which is little next to its
-// share of the weights, and one launch and a round trip through memory are
-// saved. The weight tiles are asked for before the launch's predecessor has
-// ended (into L2 only: what it may still write is seen), and packing overlaps
-// their arrival. Shared memory is kept under half an SM's, so that the next
-// call's CTAs can set themselves up beside these.
+// Bound by reading the weights once, so nothing stands between memory and the
+// multiply: a CTA takes 16 output features, its NW warps every NW-th block of K
+// each, and every lane loads its operands of mma.sync (m16n8k32, weights
+// first) straight to registers, 16 bytes at a time. The instruction wants
+// four codes of each of two places of K per thread; which four does not matter
+// as long as both operands agree, so a lane takes 16 consecutive codes of a
+// row and spends them on two instructions. The block's fp32 sums are scaled
+// into the warp's accumulators, and the warps' sums meet in shared memory, in
+// warp order. Several CTAs per SM keep enough bytes in flight, and there is no
+// tensor memory, barrier or cluster to set up. One token through three 3072 x
+// 3072 linears: 6.7 us against 8.8 us on tcgen05 with K split over clusters;
+// from 9 rows on that one is faster (16 rows: 9.4 against 6.7 us).
+//
+// TX: the activations come as codes and scales (uint8_t), or as they are, up
+// to PACK_ROWS rows; then every CTA packs them all into shared memory (the
+// quantizer of fp8_pack.cu, so the same codes), which saves a launch.
 
-constexpr int TOKEN_ROWS = 16;
-constexpr int TOKEN_X_BYTES = TOKEN_ROWS * BK;  // codes of one block of K
-constexpr int TOKEN_STAGES = 4;
-constexpr int TOKEN_BUFS = 4;
-constexpr int TOKEN_MAX_KB = 20;  // blocks of K per CTA
-constexpr int TOKEN_KG = 4;  // blocks of K handed over together
-constexpr int TOKEN_TMEM_COLS = TOKEN_BUFS * TOKEN_KG * TOKEN_ROWS;
+constexpr int STREAM_FEATURES = 16;
+constexpr int STREAM_ROWS = 8;                   // most rows
+constexpr int PACK_ROWS = 4;                     // most rows packed inside
+constexpr int64_t PACK_MAX_K = 12288;            // and their longest K
+static_assert(PACK_ROWS * PACK_MAX_K + PACK_ROWS * (PACK_MAX_K / QBLOCK) * 4 <= 56 * 1024, "several CTAs per SM");
 
-// Byte layout: weight stages (later the partial tile), activation codes per
-// block, factors [block][16], barriers.
-constexpr int TOKEN_SMEM_X = TOKEN_STAGES * QBLOCK * BK;
-__host__ __device__ constexpr int token_smem_scales(int kbs) { return TOKEN_SMEM_X + kbs * TOKEN_X_BYTES; }
-__host__ __device__ constexpr int token_smem_bars(int kbs) { return token_smem_scales(kbs) + kbs * TOKEN_ROWS * 4; }
-__host__ __device__ constexpr int token_smem(int kbs) {
-  return token_smem_bars(kbs) + (2 * TOKEN_STAGES + 2 * TOKEN_BUFS + 2) * 8 + 16 + 1024;
+// d += a b for 16 weight rows and 8 activation rows over 32 places of K.
+__device__ __forceinline__ void mma_sync_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-static_assert(token_smem(TOKEN_MAX_KB) <= 112 * 1024, "two CTAs per SM");
-static_assert(TOKEN_SMEM_X >= TOKEN_ROWS * QBLOCK * 4, "the partial tile fits the stages");
-
-__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t x, int32_t y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(x), "r"(y) : "memory");
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
 
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(SOLO_THREADS, 2)
-fp8_token_kernel(const __grid_constant__ GemmParams p, const TX* X, int64_t ldx, int K, bool vec_x) {
-  constexpr int STAGE_BYTES = QBLOCK * BK, BN = TOKEN_ROWS, PITCH = QBLOCK;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int max_kbs = (p.KB + p.split - 1) / p.split;
-  uint8_t* sx = smem + TOKEN_SMEM_X;
-  float* scales = reinterpret_cast<float*>(smem + token_smem_scales(max_kbs));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + token_smem_bars(max_kbs));
-  uint64_t* empty = full + TOKEN_STAGES;
-  uint64_t* tfull = empty + TOKEN_STAGES;
-  uint64_t* tempty = tfull + TOKEN_BUFS;
-  uint64_t* packed = tempty + TOKEN_BUFS;
-  uint64_t* done = packed + 1;
-  uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(done + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
+struct StreamParams {
+  const void* X;                // codes [M,K], or activations
+  const float* s_x;             // with codes
+  int64_t ldx;
+  const uint8_t* q[MAX_LIN];
+  const float* s_w[MAX_LIN];
+  const float* bias[MAX_LIN];
+  void* out[MAX_LIN];
+  int64_t ldy[MAX_LIN];
+  int N[MAX_LIN];
+  int tile_start[MAX_LIN + 1];
+  int M, K, KB, n_lin;
+  bool vec_x;
+};
+
+template <typename TX, typename TY, int NW>
+__global__ void __launch_bounds__(NW * 32, 32 / NW)
+fp8_stream_kernel(const __grid_constant__ StreamParams p) {
+  constexpr bool PACK = sizeof(TX) > 1;
+  extern __shared__ __align__(16) uint8_t sx[];  // PACK: codes [M][K rounded up to blocks], scales [M][KB]
+  __shared__ float part[NW][STREAM_ROWS][STREAM_FEATURES + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int* err = &g_fp8_error;
-  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const Tile c = decode(p, static_cast<int>(blockIdx.x) / p.split);
-  const int N = p.N[c.lin], n0 = c.nt * QBLOCK;
-  const int kb_begin = p.KB * rank / p.split, kb_end = p.KB * (rank + 1) / p.split;
-  pdl_launch_dependents();
-
-  if (threadIdx.x == 4 * 32) {
-    for (int kb = kb_begin; kb < kb_end; ++kb) tma_prefetch_2d(&p.tmap_w[c.lin], kb * BK, n0);
-    for (int s = 0; s < TOKEN_STAGES; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    for (int b = 0; b < TOKEN_BUFS; ++b) {
-      mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4);
-    }
-    mbar_init(packed, 4);
-    mbar_init(done, 1);
-    *abort_flag = 0;
-    fence_mbarrier_init();
-  }
-  if (warp == 5) {
-    tmem_alloc(tmem_base_smem, TOKEN_TMEM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_base_smem;
-  pdl_wait_prerequisites();
-  const int n = n0 + lane * 4;
-  const float* bias = p.bias[c.lin];
-  float bv[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) bv[k] = (bias && n + k < N) ? ldg_now(bias + n + k) : 0.0f;
-
-  if (warp == 4) {
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
-      uint32_t stage = 0, phase = 0, n_issued = 0;
-      for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) break;
-        mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
-        tma_load_2d(smem + stage * STAGE_BYTES, &p.tmap_w[c.lin], &full[stage], kb * BK, n0, pol);
-        ++n_issued;
-        if (++stage == TOKEN_STAGES) { stage = 0; phase ^= 1u; }
-      }
-      for (uint32_t s = 0; s < TOKEN_STAGES; ++s)
-        if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / TOKEN_STAGES) & 1u, nullptr, err);
-    }
-    __syncwarp();
-  } else if (warp == 5) {
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
-      bool ok = mbar_wait(packed, 0, abort_flag, err);
-      for (int kb0 = kb_begin; ok && kb0 < kb_end; kb0 += TOKEN_KG) {
-        if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err)) break;
-        for (int kb = kb0; kb < min(kb0 + TOKEN_KG, kb_end); ++kb) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, err)) { ok = false; break; }
-          tc_fence_after();
-          mma_block<1>(tmem_base + (buf * TOKEN_KG + kb - kb0) * BN, smem_u32(smem + stage * STAGE_BYTES),
-                       smem_u32(sx + (kb - kb_begin) * TOKEN_X_BYTES), idesc_e4m3_f32(LANES, BN));
-          mma_commit(&empty[stage]);
-          if (++stage == TOKEN_STAGES) { stage = 0; phase ^= 1u; }
-        }
-        if (!ok) break;
-        mma_commit(&tfull[buf]);
-        if (++buf == TOKEN_BUFS) { buf = 0; bphase ^= 1u; }
-      }
-      mma_commit(done);
-      mbar_wait(done, 0, nullptr, err);
-    }
-    __syncwarp();
-  } else {
-    // Pack: eight lanes per block of 128 features, 16 features per lane, up to
-    // AHEAD blocks' loads in flight; the codes go where a 128-byte-swizzled
-    // tensor-map load would put them. The rows past M stay as they are: they
-    // only meet columns that are not stored.
-    const float* ws = p.s_w[c.lin] + static_cast<int64_t>(c.nt) * p.KB;
-    const int sub = lane & 7, items = (kb_end - kb_begin) * p.M;
-    constexpr int AHEAD = 4, GROUPS = 128 / 8;
-    for (int i0 = 0; i0 < items; i0 += AHEAD * GROUPS) {
-      Pair x[AHEAD][8];
-      int b[AHEAD], r[AHEAD];
-      float w[AHEAD];
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        const int i = i0 + u * GROUPS + (threadIdx.x >> 3);
-        b[u] = i / p.M;
-        r[u] = i - b[u] * p.M;
-        const int col = (kb_begin + b[u]) * BK + sub * 16;
-        if (i < items && col < K) {
-          load16(X + r[u] * ldx + col, vec_x, x[u]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[u][k] = 0ull;
-        }
-        w[u] = i < items ? __ldg(ws + kb_begin + b[u]) : 0.0f;
-      }
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        float m = max_magnitude(x[u]);
-#pragma unroll
-        for (int d = 1; d < 8; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float sc = e4m3_scale(m);
-        uint32_t q[4];
-        e4m3_codes(x[u], sc, q);
-        if (i0 + u * GROUPS + (threadIdx.x >> 3) < items) {
-          *reinterpret_cast<uint4*>(sx + b[u] * TOKEN_X_BYTES + r[u] * BK + ((sub ^ (r[u] & 7)) << 4)) =
-              make_uint4(q[0], q[1], q[2], q[3]);
-          if (sub == 0) scales[b[u] * TOKEN_ROWS + r[u]] = sc * w[u];
-        }
-      }
-    }
-    fence_proxy_async_smem();
-    named_bar_sync(1, 4 * 32);  // the factors are read by all four warps
-    if (lane == 0) mbar_arrive(packed);
-
-    const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
-    unsigned long long acc[BN / 2];
-#pragma unroll
-    for (int i = 0; i < BN / 2; ++i) acc[i] = 0ull;
-    uint32_t buf = 0, bphase = 0;
+  const int g = lane >> 2, t = lane & 3;
+  int lin = 0;
 #pragma unroll 1
-    for (int kb = kb_begin; kb < kb_end; kb += TOKEN_KG) {
-      if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) break;
-      tc_fence_after();
-      drain_scaled<BN, TOKEN_KG>(acc, t_addr + buf * TOKEN_KG * BN, scales + (kb - kb_begin) * TOKEN_ROWS, kb_end - kb);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[buf]);
-      if (++buf == TOKEN_BUFS) { buf = 0; bphase ^= 1u; }
-    }
-    // the partial tile, in the stages: every MMA has completed
-    float* part = reinterpret_cast<float*>(smem);
+  while (lin + 1 < p.n_lin && static_cast<int>(blockIdx.x) >= p.tile_start[lin + 1]) ++lin;
+  const int N = p.N[lin], n0 = (static_cast<int>(blockIdx.x) - p.tile_start[lin]) * STREAM_FEATURES;
+  // this lane's two weight rows (past the last one: the last one again, not stored)
+  const uint8_t* w0 = p.q[lin] + static_cast<int64_t>(min(n0 + g, N - 1)) * p.K;
+  const uint8_t* w1 = p.q[lin] + static_cast<int64_t>(min(n0 + g + 8, N - 1)) * p.K;
+  pdl_launch_dependents();
+  // ask for the weights while the launch before this one ends (into L2 only:
+  // what it may still write is seen)
+  for (int k = (warp * 4 + t) * 128; k < p.K; k += NW * 4 * 128) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 + k));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(w1 + k));
+  }
+  pdl_wait_prerequisites();
+
+  // The weights of one block: [half of 64 codes][row]; zeros past K.
+  auto load_w = [&](int kb, uint4 (&a)[2][2]) {
 #pragma unroll
-    for (int i = 0; i < BN / 2; ++i) {
-      float a, b;
-      f32x2_unpack(acc[i], a, b);
-      part[(2 * i) * PITCH + 32 * warp + lane] = a;
-      part[(2 * i + 1) * PITCH + 32 * warp + lane] = b;
+    for (int h = 0; h < 2; ++h) {
+      const int k = kb * BK + h * 64 + t * 16;
+      const bool on = k < p.K;
+      a[h][0] = on ? ldg_stream(w0 + k) : make_uint4(0, 0, 0, 0);
+      a[h][1] = on ? ldg_stream(w1 + k) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint4 a[2][2], next[2][2];
+  if (warp < p.KB) load_w(warp, a);
+  const int Kp = p.KB * BK;
+  float* ssx = reinterpret_cast<float*>(sx + p.M * Kp);
+  if (PACK) {
+    // eight lanes per block of 128 features, 16 features per lane; a warp's
+    // lanes all take the same turns
+    const int sub = lane & 7, items = p.KB * p.M;
+    for (int i0 = warp * 4; i0 < items; i0 += NW * 4) {
+      const int i = i0 + (lane >> 3), kb = i / p.M, r = i - kb * p.M, col = kb * BK + sub * 16;
+      Pair x[8];
+      if (i < items && col < p.K) {
+        load16(static_cast<const TX*>(p.X) + r * p.ldx + col, p.vec_x, x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = 0ull;
+      }
+      float m = max_magnitude(x);
+#pragma unroll
+      for (int d = 1; d < 8; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float sc = e4m3_scale(m);
+      uint32_t q[4];
+      e4m3_codes(x, sc, q);
+      if (i < items) {
+        *reinterpret_cast<uint4*>(sx + r * Kp + col) = make_uint4(q[0], q[1], q[2], q[3]);
+        if (sub == 0) ssx[r * p.KB + kb] = sc;
+      }
+    }
+    __syncthreads();
+  }
+
+  const float* ws = p.s_w[lin] + static_cast<int64_t>(n0 / QBLOCK) * p.KB;
+  // the activation row that this lane holds, and the scales of the two whose
+  // results it has (past the last row: the last one again, not stored)
+  const int r = min(g, p.M - 1), r0 = min(2 * t, p.M - 1), r1 = min(2 * t + 1, p.M - 1);
+  const uint8_t* xr = static_cast<const uint8_t*>(p.X) + static_cast<int64_t>(r) * p.K;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int kb = warp; kb < p.KB; kb += NW) {
+    if (kb + NW < p.KB) load_w(kb + NW, next);
+    uint4 b[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = kb * BK + h * 64 + t * 16;
+      if (PACK) b[h] = *reinterpret_cast<const uint4*>(sx + r * Kp + k);
+      else b[h] = k < p.K ? __ldg(reinterpret_cast<const uint4*>(xr + k)) : make_uint4(0, 0, 0, 0);
+    }
+    const float sw = __ldg(ws + kb);
+    const float f0 = sw * (PACK ? ssx[r0 * p.KB + kb] : __ldg(p.s_x + static_cast<int64_t>(r0) * p.KB + kb));
+    const float f1 = sw * (PACK ? ssx[r1 * p.KB + kb] : __ldg(p.s_x + static_cast<int64_t>(r1) * p.KB + kb));
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mma_sync_e4m3(d, a[h][0].x, a[h][1].x, a[h][0].y, a[h][1].y, b[h].x, b[h].y);
+      mma_sync_e4m3(d, a[h][0].z, a[h][1].z, a[h][0].w, a[h][1].w, b[h].z, b[h].w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], i & 1 ? f1 : f0, acc[i]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      a[h][0] = next[h][0];
+      a[h][1] = next[h][1];
     }
   }
-  tc_fence_before();
-  if (p.split > 1) cluster_sync(); else __syncthreads();
-  if (warp == 5) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, TOKEN_TMEM_COLS);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[warp][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[i];
+  __syncthreads();
+  const float* bias = p.bias[lin];
+  for (int i = threadIdx.x; i < p.M * STREAM_FEATURES; i += NW * 32) {
+    const int m = i / STREAM_FEATURES, n = i % STREAM_FEATURES;
+    if (n0 + n >= N) continue;
+    float y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) y += part[w][m][n];
+    if (bias) y += __ldg(bias + n0 + n);
+    static_cast<TY*>(p.out[lin])[m * p.ldy[lin] + n0 + n] = from_f32<TY>(y);
   }
-  finish_tile<TY, TOKEN_ROWS, PITCH>(p, c, 0, n, rank, smem, bv);
 }
 
 // ---------------------------------------------------------------------------
@@ -1168,38 +1132,67 @@ int launch_solo(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
-// CTAs per tile (a cluster of 1, 2, 4 or 8; others measured slower, 19 us for
-// six against 13 us for four on [24, 12288] x [3072, 12288]): as many as keep
-// all tiles within one wave of the SMs, and leave every CTA a block of K.
-int pick_split(int64_t tiles, int64_t KB, int sms) {
+// CTAs per tile (a cluster of 1, 2, 4 or at most `most`): as many as keep all
+// tiles within one wave of `slots` CTAs and leave every CTA a block of K.
+// Clusters of six and eight measured slower than four on [24, 12288] x [3072,
+// 12288] although they use more SMs: 19 and 17 us against 13 us.
+int pick_split(int64_t tiles, int64_t KB, int64_t slots, int most) {
   int s = 1;
-  while (s < MAX_SPLIT && tiles * (2 * s) <= sms && 2 * s <= KB) s *= 2;
+  while (s < most && tiles * (2 * s) <= slots && 2 * s <= KB) s *= 2;
   return s;
 }
 
-template <typename TX, typename TY>
-int launch_token_as(const void* X, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* w, int n, int split,
-                    cudaStream_t stream) {
-  GemmParams p;
-  if (int st = fill(p, nullptr, nullptr, M, K, w, n, TOKEN_ROWS, QBLOCK, TOKEN_ROWS, QBLOCK)) return st;
-  p.split = split;
+template <typename TX, typename TY, int NW>
+int launch_stream_of(const StreamParams& p, size_t smem, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;
-  auto kernel = fp8_token_kernel<TX, TY>;
-  if (int st = allow_smem(kernel, token_smem(TOKEN_MAX_KB), done, mu)) return st;
-  const bool vec = aligned16(X) && (ldx * sizeof(TX)) % 16 == 0;
-  Launch l(p.total_tiles * split, SOLO_THREADS, token_smem((p.KB + split - 1) / split), stream, split);
-  const cudaError_t e =
-      cudaLaunchKernelEx(&l.cfg, kernel, p, static_cast<const TX*>(X), ldx, static_cast<int>(K), vec);
+  auto kernel = fp8_stream_kernel<TX, TY, NW>;
+  if (int st = allow_smem(kernel, 64 * 1024, done, mu)) return st;
+  Launch l(p.tile_start[p.n_lin], NW * 32, smem, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, p);
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
+// Sixteen warps per CTA where the tiles alone would leave the SMs few, and K
+// is long enough for them.
+template <typename TX, typename TY>
+int launch_stream_as(const StreamParams& p, size_t smem, cudaStream_t stream) {
+  if (p.tile_start[p.n_lin] <= 2 * device_sm_count() && p.KB >= 16)
+    return launch_stream_of<TX, TY, 16>(p, smem, stream);
+  return launch_stream_of<TX, TY, 8>(p, smem, stream);
+}
+
+StreamParams stream_params(const void* X, const float* s_x, int64_t M, int64_t K, int64_t ldx,
+                           const convrot_fp8_weight* w, int n) {
+  StreamParams p{};
+  p.X = X;
+  p.s_x = s_x;
+  p.ldx = ldx;
+  p.M = static_cast<int>(M);
+  p.K = static_cast<int>(K);
+  p.KB = static_cast<int>(n_blocks(K));
+  p.n_lin = n;
+  for (int j = 0; j < n; ++j) {
+    p.q[j] = w[j].q;
+    p.s_w[j] = w[j].scale;
+    p.bias[j] = w[j].bias;
+    p.out[j] = w[j].Y;
+    p.ldy[j] = w[j].ldy;
+    p.N[j] = static_cast<int>(w[j].N);
+    p.tile_start[j + 1] = p.tile_start[j] + static_cast<int>((w[j].N + STREAM_FEATURES - 1) / STREAM_FEATURES);
+  }
+  return p;
+}
+
 template <typename TX>
-int launch_token(const void* X, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* w, int n, int y_dtype,
-                 int split, cudaStream_t stream) {
-  if (y_dtype == CONVROT_F32) return launch_token_as<TX, float>(X, M, K, ldx, w, n, split, stream);
-  if (y_dtype == CONVROT_F16) return launch_token_as<TX, __half>(X, M, K, ldx, w, n, split, stream);
-  return launch_token_as<TX, __nv_bfloat16>(X, M, K, ldx, w, n, split, stream);
+int launch_packing_stream(const void* X, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* w, int n,
+                          int y_dtype, cudaStream_t stream) {
+  StreamParams p = stream_params(X, nullptr, M, K, ldx, w, n);
+  p.vec_x = aligned16(X) && (ldx * sizeof(TX)) % 16 == 0;
+  const size_t smem = static_cast<size_t>(M) * p.KB * (BK + 4);
+  if (y_dtype == CONVROT_F32) return launch_stream_as<TX, float>(p, smem, stream);
+  if (y_dtype == CONVROT_F16) return launch_stream_as<TX, __half>(p, smem, stream);
+  return launch_stream_as<TX, __nv_bfloat16>(p, smem, stream);
 }
 
 template <typename TY>
@@ -1212,15 +1205,16 @@ int launch_as(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const c
     cols += n_blocks(w[j].N);
     wide += (w[j].N + 255) / 256;
   }
+  if (M <= STREAM_ROWS) return launch_stream_as<uint8_t, TY>(stream_params(Qx, s_x, M, K, K, w, n), 0, stream);
   if (M <= 64) {
-    const int split = pick_split(cols, KB, sms);
+    const int split = pick_split(cols, KB, 2 * sms, 4);
     if (M <= 16) return launch_solo<TY, 16, true>(Qx, s_x, M, K, w, n, split, stream);
     if (M <= 32) return launch_solo<TY, 32, true>(Qx, s_x, M, K, w, n, split, stream);
     return launch_solo<TY, 64, true>(Qx, s_x, M, K, w, n, split, stream);
   }
   const int64_t solo = (M + 127) / 128 * cols;
   const int64_t pair_wide = (M + 255) / 256 * wide, pair_narrow = (M + 255) / 256 * cols;
-  if (solo <= sms) return launch_solo<TY, 128, false>(Qx, s_x, M, K, w, n, pick_split(solo, KB, sms), stream);
+  if (solo <= sms) return launch_solo<TY, 128, false>(Qx, s_x, M, K, w, n, pick_split(solo, KB, sms, 4), stream);
   if (pair_wide < sms / 2 && pair_narrow <= sms / 2)
     return launch_pair<TY, 128>(Qx, s_x, M, K, w, n, y_dtype, stream);
   return launch_pair<TY, 256>(Qx, s_x, M, K, w, n, y_dtype, stream);
@@ -1235,17 +1229,13 @@ int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, c
   return launch_as<__nv_bfloat16>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
 }
 
-int launch_fp8_token(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,
-                     int n_weights, int y_dtype, cudaStream_t stream, bool* launched) {
-  const int64_t KB = n_blocks(K);
-  int64_t tiles = 0;
-  for (int j = 0; j < n_weights; ++j) tiles += n_blocks(weights[j].N);
-  const int split = pick_split(tiles, KB, device_sm_count());
-  *launched = M <= TOKEN_ROWS && (KB + split - 1) / split <= TOKEN_MAX_KB;
+int launch_fp8_packing(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,
+                       int n_weights, int y_dtype, cudaStream_t stream, bool* launched) {
+  *launched = M <= PACK_ROWS && K <= PACK_MAX_K;
   if (!*launched) return CONVROT_OK;
-  if (x_dtype == CONVROT_F32) return launch_token<float>(X, M, K, ldx, weights, n_weights, y_dtype, split, stream);
-  if (x_dtype == CONVROT_F16) return launch_token<__half>(X, M, K, ldx, weights, n_weights, y_dtype, split, stream);
-  return launch_token<__nv_bfloat16>(X, M, K, ldx, weights, n_weights, y_dtype, split, stream);
+  if (x_dtype == CONVROT_F32) return launch_packing_stream<float>(X, M, K, ldx, weights, n_weights, y_dtype, stream);
+  if (x_dtype == CONVROT_F16) return launch_packing_stream<__half>(X, M, K, ldx, weights, n_weights, y_dtype, stream);
+  return launch_packing_stream<__nv_bfloat16>(X, M, K, ldx, weights, n_weights, y_dtype, stream);
 }
 
 int read_and_clear_fp8_error() {
