@@ -185,8 +185,8 @@ __device__ __forceinline__ float inverse_root(float v) {
 }
 
 // Statistics of a row of K elements spread over a group of W warps; `get(u,
-// x, on)` yields a thread's unit u (four pairs; zeros past the end, and which
-// halves lie inside), `count(w)` the elements that warp w of the group holds.
+// x)` yields a thread's unit u (four pairs, zeros past the end) and returns its
+// place, `count(w)` the elements that warp w of the group holds.
 template <int V, typename Get, typename Count>
 __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float eps, int K, float inv_k, int W, int group,
                                            int warp_in_group, float2* red) {
@@ -201,8 +201,7 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
 #pragma unroll
     for (int u = 0; u < V; ++u) {
       Pair x[4];
-      bool on[2];
-      get(u, x, on);
+      get(u, x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i & 1] = f32x2_fma(x[i], x[i], acc[i & 1]);
     }
@@ -214,8 +213,7 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     Pair x[4];
-    bool on[2];
-    get(u, x, on);
+    get(u, x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i & 1] = add2(acc[i & 1], x[i]);
   }
@@ -227,12 +225,11 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     Pair x[4];
-    bool on[2];
-    get(u, x, on);
+    const auto unit = get(u, x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const Pair d = add2(x[i], minus);
-      if (on[i / 2]) acc[i & 1] = f32x2_fma(d, d, acc[i & 1]);
+      const Pair d = unit.inside(i, add2(x[i], minus));
+      acc[i & 1] = f32x2_fma(d, d, acc[i & 1]);
     }
   }
   float m2 = total(acc);
@@ -283,6 +280,8 @@ struct Unit {
     for (int i = 0; i < 4; ++i)
       if (!on[i / 2]) x[i] = 0ull;
   }
+  // pair i with what lies past the end replaced by zeros
+  __device__ __forceinline__ Pair inside(int i, Pair x) const { return on[i / 2] ? x : 0ull; }
   template <typename TU>
   __device__ __forceinline__ void store(TU* row, const Pair (&x)[4]) const {
     if constexpr (sizeof(T) == 4) {
@@ -330,7 +329,7 @@ struct Unit {
 // The coefficients come from `post(u, unit, a, b)` and `pre(u, unit, a, b)`;
 // `loaded()` is called once the staged row has been read and the group has
 // passed a barrier.
-template <typename T, typename TU, int V, bool FP8, typename Post, typename Pre, typename Loaded>
+template <typename T, typename TU, int V, bool FP8, typename Place, typename Post, typename Pre, typename Loaded>
 __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh, const T* sy, int W, int group, int wg,
                                        float2* red_post, float2* red_pre, Post post, Pre pre, Loaded loaded) {
   auto count = [&](int w) {  // features of the row that warp w of the group holds
@@ -343,24 +342,23 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
   Pair x[V][4];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    Unit<T>(u * W + wg, p.K, u < V - 1).load(sh, x[u]);
+    Place(u * W + wg, p.K, u < V - 1).load(sh, x[u]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[u][i] = f32x2_mul(x[u][i], both(p.residual_scale));
   }
   if (p.Y) {
     Stats ps{0.0f, 1.0f};
     if (p.post != CONVROT_NORM_NONE) {
-      auto get = [&](int u, Pair (&v)[4], bool (&on)[2]) {
-        const Unit<T> unit(u * W + wg, p.K, u < V - 1);
+      auto get = [&](int u, Pair (&v)[4]) {
+        const Place unit(u * W + wg, p.K, u < V - 1);
         unit.load(sy, v);
-        on[0] = unit.on[0];
-        on[1] = unit.on[1];
+        return unit;
       };
       ps = row_stats<V>(get, count, p.post, p.post_eps, p.K, p.inv_k, W, group, wg, red_post);
     }
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      const Unit<T> unit(u * W + wg, p.K, u < V - 1);
+      const Place unit(u * W + wg, p.K, u < V - 1);
       Pair y[4], a[4], b[4];
       unit.load(sy, y);
       post(u, unit, a, b);
@@ -373,8 +371,7 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
         for (int i = 0; i < 4; ++i) y[i] = normalized(y[i], ps);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (unit.on[i / 2]) x[u][i] = f32x2_fma(y[i], a[i], x[u][i]);
+      for (int i = 0; i < 4; ++i) x[u][i] = unit.inside(i, f32x2_fma(y[i], a[i], x[u][i]));
     }
   }
   group_sync(W, group);
@@ -382,17 +379,16 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
   if (p.H_out) {
     T* out = static_cast<T*>(p.H_out) + row * p.ldho;
 #pragma unroll
-    for (int u = 0; u < V; ++u) Unit<T>(u * W + wg, p.K, u < V - 1).store(out, x[u]);
+    for (int u = 0; u < V; ++u) Place(u * W + wg, p.K, u < V - 1).store(out, x[u]);
   }
   if (!FP8 && !p.U) return;
   Stats us{0.0f, 1.0f};
   if (p.pre != CONVROT_NORM_NONE) {
-    auto get = [&](int u, Pair (&v)[4], bool (&on)[2]) {
-      const Unit<T> unit(u * W + wg, p.K, u < V - 1);
+    auto get = [&](int u, Pair (&v)[4]) {
+      const Place unit(u * W + wg, p.K, u < V - 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = unit.on[i / 2] ? x[u][i] : 0ull;
-      on[0] = unit.on[0];
-      on[1] = unit.on[1];
+      for (int i = 0; i < 4; ++i) v[i] = x[u][i];
+      return unit;
     };
     us = row_stats<V>(get, count, p.pre, p.pre_eps, p.K, p.inv_k, W, group, wg, red_pre);
   }
@@ -401,7 +397,7 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
   TU* out = FP8 ? nullptr : static_cast<TU*>(p.U) + row * p.ldu;
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const Unit<T> unit(u * W + wg, p.K, u < V - 1);
+    const Place unit(u * W + wg, p.K, u < V - 1);
     Pair a[4], b[4];
     pre(u, unit, a, b);
     if (p.pre != CONVROT_NORM_NONE) {
@@ -409,7 +405,7 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
       for (int i = 0; i < 4; ++i) x[u][i] = normalized(x[u][i], us);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[u][i] = unit.on[i / 2] ? f32x2_fma(x[u][i], a[i], b[i]) : 0ull;
+    for (int i = 0; i < 4; ++i) x[u][i] = unit.inside(i, f32x2_fma(x[u][i], a[i], b[i]));
     if (FP8) unit.store_codes(q, s, x[u]);
     else unit.store(out, x[u]);
   }
@@ -545,7 +541,7 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
     }
     for (; row < end; row += G) {
       mbar_wait(&ring.full[ring.st], ring.phase, &abort_flag, &g_norm_error);
-      do_row<T, TU, V, FP8>(
+      do_row<T, TU, V, FP8, Unit<T>>(
           p, row, ring.h(), ring.y(), W, group, wg, red[0] + group * W, red[1] + group * W,
           [&](int u, const Unit<T>&, Pair (&a)[4], Pair (&b)[4]) {
             take(cpa, has_pa, u, p.block_scale, a);
@@ -645,7 +641,7 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
       }
     }
     mbar_wait(&ring.full[ring.st], ring.phase, &abort_flag, &g_norm_error);
-    do_row<T, TU, V, FP8>(
+    do_row<T, TU, V, FP8, Unit<T>>(
         p, row, ring.h(), ring.y(), NW, 0, warp, red[0], red[1],
         [&](int u, const Unit<T>& unit, Pair (&a)[4], Pair (&b)[4]) {
           if (has_pb) {
@@ -672,9 +668,124 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
   }
 }
 
-// Rows of any width, alignment and stride: one row per CTA at a time, kept
-// as fp32 in shared memory, elements taken one by one (thread t owns the
-// elements t, t + blockDim, ...).
+// Rows of any width, alignment and stride up to 12288 features: the same with
+// the elements of 256 features dealt out one by one (element i of a lane is
+// feature 32 i + lane), so that a warp's accesses are contiguous however the
+// row starts; everything is read from global memory, the coefficients and the
+// second reading of y through L1.
+template <typename T>
+struct Scattered {
+  int e0, K;
+  __device__ __forceinline__ Scattered(int chunk, int K_, bool) : e0(chunk * 256 + (threadIdx.x & 31)), K(K_) {}
+  template <typename TV>
+  __device__ __forceinline__ void load(const TV* row, Pair (&x)[4]) const {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = e0 + 32 * i < K ? to_f32(row[e0 + 32 * i]) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = f32x2_pack(v[2 * i], v[2 * i + 1]);
+  }
+  __device__ __forceinline__ Pair inside(int i, Pair x) const {
+    float a, b;
+    f32x2_unpack(x, a, b);
+    return f32x2_pack(e0 + 64 * i < K ? a : 0.0f, e0 + 64 * i + 32 < K ? b : 0.0f);
+  }
+  template <typename TU>
+  __device__ __forceinline__ void store(TU* row, const Pair (&x)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      f32x2_unpack(x[i], a, b);
+      if (e0 + 64 * i < K) row[e0 + 64 * i] = from_f32<TU>(a);
+      if (e0 + 64 * i + 32 < K) row[e0 + 64 * i + 32] = from_f32<TU>(b);
+    }
+  }
+  // a block of 128 is half of every lane's elements
+  __device__ __forceinline__ void store_codes(uint8_t* q, float* s, const Pair (&x)[4]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const Pair v[2] = {x[2 * h], x[2 * h + 1]};
+      float m = max_magnitude(v);
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float sc = e4m3_scale(m);
+      uint32_t c[1];
+      e4m3_codes(v, sc, c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e0 + 128 * h + 32 * i < K) q[e0 + 128 * h + 32 * i] = static_cast<uint8_t>(c[0] >> (8 * i));
+      if ((threadIdx.x & 31) == 0 && e0 + 128 * h < K) s[(e0 + 128 * h) / QBLOCK] = sc;
+    }
+  }
+};
+
+template <typename T, typename TU, int V, bool FP8>
+__global__ void __launch_bounds__(WARPS * 32, V <= 2 ? 3 : 1)
+block_norm_scattered_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float2 red[2][WARPS];
+  const int warp = threadIdx.x >> 5;
+  const int W = p.warps_per_row, G = WARPS / W, group = warp / W, wg = warp - group * W;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * G + group; row < p.M; row += static_cast<int64_t>(gridDim.x) * G) {
+    const int s = sample_of(p, static_cast<int>(row));
+    // one vector at a time, so that its loads are on their way together
+    auto fold = [](Pair (&a)[4], const Pair (&v)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = f32x2_mul(a[i], v[i]);
+    };
+    auto post = [&](int, const Scattered<T>& unit, Pair (&a)[4], Pair (&b)[4]) {
+      Pair v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = both(p.gate && s < 0 ? 0.0f : p.block_scale);
+        b[i] = 0ull;
+      }
+      if (p.gate && s >= 0) {
+        unit.load(p.gate + s * p.ld_gate, v);
+        fold(a, v);
+      }
+      if (p.post_bias) {
+        unit.load(p.post_bias, b);
+        fold(b, a);
+      }
+      if (p.post_weight) {
+        unit.load(p.post_weight, v);
+        fold(a, v);
+      }
+    };
+    auto pre = [&](int, const Scattered<T>& unit, Pair (&a)[4], Pair (&b)[4]) {
+      Pair v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = both(1.0f);
+        b[i] = 0ull;
+      }
+      if (p.pre_weight) unit.load(p.pre_weight, a);
+      if (p.pre_bias) unit.load(p.pre_bias, b);
+      if (p.scale && s >= 0) {
+        unit.load(p.scale + s * p.ld_mod, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(1.0f));
+        fold(a, v);
+        fold(b, v);
+      }
+      if (p.shift && s >= 0) {
+        unit.load(p.shift + s * p.ld_mod, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = add2(b[i], v[i]);
+      }
+    };
+    do_row<T, TU, V, FP8, Scattered<T>>(
+        p, static_cast<int>(row), static_cast<const T*>(p.H) + row * p.ldh,
+        p.Y ? static_cast<const T*>(p.Y) + row * p.ldy : nullptr, W, group, wg, red[0] + group * W, red[1] + group * W,
+        post, pre, [] {});
+  }
+}
+
+// Rows longer than the kernels above hold in registers: one row per CTA at a
+// time, kept as fp32 in shared memory, elements taken one by one (thread t
+// owns the elements t, t + blockDim, ...).
 __device__ float block_sum(float v, float* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
   v = warp_sum(v);
@@ -834,6 +945,17 @@ int pick_warps(const NormParams& p) {
   return 0;
 }
 
+template <typename T, typename TU, int V, bool FP8>
+int launch_scattered(NormParams& p, int chunks, cudaStream_t stream) {
+  const int64_t sms = device_sm_count();
+  int W = 1;
+  while (W < WARPS && (chunks > V * W || (chunks > W && p.M * static_cast<int64_t>(W) * 2 <= sms * WARPS))) W *= 2;
+  p.warps_per_row = W;
+  const int64_t ctas = (p.M + static_cast<int64_t>(WARPS / W) - 1) / (WARPS / W);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ctas, (V <= 2 ? 3 : 1) * sms));
+  return launch_rows(block_norm_scattered_kernel<T, TU, V, FP8>, p, grid, WARPS * 32, 0, stream);
+}
+
 template <typename T, typename TU, bool FP8>
 int launch_typed(NormParams& p, bool vec, cudaStream_t stream) {
   const int chunks = (p.K + 255) / 256;
@@ -853,6 +975,8 @@ int launch_typed(NormParams& p, bool vec, cudaStream_t stream) {
     if (chunks <= 6 * WARPS) return launch_wide<T, TU, 6, FP8, WARPS>(p, stream);
     if (chunks <= 8 * WARPS) return launch_wide<T, TU, 4, FP8, 2 * WARPS>(p, stream);
   }
+  if (chunks <= 6 * WARPS) return chunks <= 2 * WARPS ? launch_scattered<T, TU, 2, FP8>(p, chunks, stream)
+                                                       : launch_scattered<T, TU, 6, FP8>(p, chunks, stream);
   static std::mutex mu;
   static uint64_t done = 0;
   auto kernel = block_norm_any_kernel<T, TU, FP8>;

@@ -176,9 +176,9 @@ __device__ __forceinline__ Tile decode(const GemmParams& p, int t) {
 // many rows: CTA pairs, activation rows on the TMEM lanes
 // ---------------------------------------------------------------------------
 //
-// Persistent clusters of two CTAs; a tile is 256 activation rows x BN output
+// Persistent clusters of two CTAs; a tile is 256 activation rows x 256 output
 // features, M = 256 MMAs issued by the even CTA, each CTA holding its 128 rows
-// x BN features. Activations take the lanes because a lane's row scale is then
+// x 256 features. Activations take the lanes because a lane's row scale is then
 // one register, and the 128 features of a warp's half tile share one weight
 // scale: the promotion of a block is a single packed multiply-add per two
 // outputs with one factor. Twelve warps: 0-7 promote and store (quarter = warp
@@ -207,12 +207,12 @@ struct __align__(16) TileInfo {
 };
 static_assert(sizeof(TileInfo) == 32, "as laid out in shared memory");
 
-template <int BN>
 struct PairGeom {
+  static constexpr int BN = 256;  // features of a tile
   static constexpr int X_BYTES = LANES * BK;
   static constexpr int W_BYTES = BN / 2 * BK;
   static constexpr int STAGE_BYTES = X_BYTES + W_BYTES;
-  static constexpr int STAGES = BN == 256 ? 5 : 6;
+  static constexpr int STAGES = 5;
   static constexpr int BUFS = 512 / BN;  // TMEM accumulators
   static constexpr uint32_t IDESC = idesc_e4m3_f32(256, BN);
   static constexpr int SMEM_OUT = STAGES * STAGE_BYTES;
@@ -221,7 +221,7 @@ struct PairGeom {
   static constexpr int SMEM_BARS = SMEM_INFO + 2 * 32;
   static constexpr int SMEM_ALLOC = SMEM_BARS + (2 * STAGES + 2 * BUFS + 7) * 8 + 16 + 1024;
 };
-static_assert(PairGeom<256>::SMEM_ALLOC <= 227 * 1024 && PairGeom<128>::SMEM_ALLOC <= 227 * 1024, "shared memory");
+static_assert(PairGeom::SMEM_ALLOC <= 227 * 1024, "shared memory");
 
 // Where the store's 128-byte swizzle puts 16-byte piece `ch` of row `row`.
 __device__ __forceinline__ int swizzled(int ch, int row) { return ch ^ (row & 7); }
@@ -310,10 +310,11 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-template <typename TY, int BN>
+template <typename TY>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
 fp8_pair_kernel(const __grid_constant__ GemmParams p) {
-  using G = PairGeom<BN>;
+  using G = PairGeom;
+  constexpr int BN = G::BN;
   constexpr int COLS = BN / 2;  // features per epilogue thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -461,7 +462,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       // rows and features past the end read the last one's scales; their
       // outputs are not stored
       xs = p.s_x + static_cast<int64_t>(min(c.row + lane, p.M - 1)) * p.KB;
-      ws = c.ws + (BN > QBLOCK && half * COLS >= QBLOCK && c.col < c.N ? p.KB : 0);
+      ws = c.ws + (half && c.col < c.N ? p.KB : 0);
       load_scales(xs, 0, p.KB, p.vec_scales, nx);
       load_scales(ws, 0, p.KB, p.vec_scales, nw);
       return true;
@@ -1095,12 +1096,12 @@ int fill(GemmParams& p, const uint8_t* Qx, const float* s_x, int64_t M, int64_t 
   return CONVROT_OK;
 }
 
-template <typename TY, int BN>
+template <typename TY>
 int launch_pair(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
                 int y_dtype, cudaStream_t stream) {
-  using G = PairGeom<BN>;
+  using G = PairGeom;
   GemmParams p;
-  if (int st = fill(p, Qx, s_x, M, K, w, n, 256, BN, LANES, BN / 2)) return st;
+  if (int st = fill(p, Qx, s_x, M, K, w, n, 256, G::BN, LANES, G::BN / 2)) return st;
   p.tma_y = true;
   for (int j = 0; j < n; ++j) p.tma_y = p.tma_y && aligned16(w[j].Y) && w[j].ldy * sizeof(TY) % 16 == 0;
   if (p.tma_y)
@@ -1108,7 +1109,7 @@ int launch_pair(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const
       if (int st = make_tmap_out(&p.tmap_y[j], w[j].Y, y_dtype, M, w[j].N, w[j].ldy)) return st;
   static std::mutex mu;
   static uint64_t done = 0;
-  auto kernel = fp8_pair_kernel<TY, BN>;
+  auto kernel = fp8_pair_kernel<TY>;
   if (int st = allow_smem(kernel, G::SMEM_ALLOC, done, mu, LAUNCH_REGS)) return st;
   const int pairs = std::min(p.total_tiles, device_sm_count() / 2);
   Launch l(2 * pairs, PAIR_THREADS, G::SMEM_ALLOC, stream, 2);
@@ -1200,11 +1201,8 @@ int launch_as(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const c
               int y_dtype, cudaStream_t stream) {
   const int sms = device_sm_count();
   const int64_t KB = n_blocks(K);
-  int64_t cols = 0, wide = 0;  // features in tiles of 128 and of 256
-  for (int j = 0; j < n; ++j) {
-    cols += n_blocks(w[j].N);
-    wide += (w[j].N + 255) / 256;
-  }
+  int64_t cols = 0;  // tiles of 128 features
+  for (int j = 0; j < n; ++j) cols += n_blocks(w[j].N);
   if (M <= STREAM_ROWS) return launch_stream_as<uint8_t, TY>(stream_params(Qx, s_x, M, K, K, w, n), 0, stream);
   if (M <= 64) {
     const int split = pick_split(cols, KB, 2 * sms, 4);
@@ -1213,11 +1211,12 @@ int launch_as(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const c
     return launch_solo<TY, 64, true>(Qx, s_x, M, K, w, n, split, stream);
   }
   const int64_t solo = (M + 127) / 128 * cols;
-  const int64_t pair_wide = (M + 255) / 256 * wide, pair_narrow = (M + 255) / 256 * cols;
+  // Whole waves of single-CTA tiles while one wave holds them all: measured at
+  // 65 to 2304 rows on five weight shapes, within 2 % of the faster of the two
+  // kernels everywhere (1024 rows, 3072 x 3072: 26 us here, 16 us in pairs;
+  // 700 rows: 13.6 us here, 15.2 us in pairs).
   if (solo <= sms) return launch_solo<TY, 128, false>(Qx, s_x, M, K, w, n, pick_split(solo, KB, sms, 4), stream);
-  if (pair_wide < sms / 2 && pair_narrow <= sms / 2)
-    return launch_pair<TY, 128>(Qx, s_x, M, K, w, n, y_dtype, stream);
-  return launch_pair<TY, 256>(Qx, s_x, M, K, w, n, y_dtype, stream);
+  return launch_pair<TY>(Qx, s_x, M, K, w, n, y_dtype, stream);
 }
 
 }  // namespace
