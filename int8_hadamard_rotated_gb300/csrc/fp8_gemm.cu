@@ -467,7 +467,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       load_scales(ws, 0, p.KB, p.vec_scales, nw);
       return true;
     };
-    int seq = 0, sbuf = 0;
+    int seq = 0;
     if (unit < p.total_tiles) ok = start(0);
     for (int t = unit; ok && t < p.total_tiles; t += n_units, ++seq) {
       unsigned long long acc[COLS / 2];
@@ -504,11 +504,12 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       // store: PER features of a row at a time
       constexpr int PER = STORE_ROW / sizeof(TY);
       constexpr int E = 16 / sizeof(TY);  // of them in 16 bytes
+      static_assert((COLS / PER) % 2 == 0, "both store buffers equally often");
 #pragma unroll
       for (int b = 0; b < COLS / PER; ++b) {
-        // the two buffers in turn: the store before the last has been read
-        uint8_t* sb = sout + sbuf * STORE_BLOCK;
-        sbuf ^= 1;
+        // the two buffers in turn (an even number of blocks per tile): the
+        // store before the last has been read
+        uint8_t* sb = sout + (b & 1) * STORE_BLOCK;
         if (lane == 0) bulk_wait_read<1>();
         __syncwarp();
 #pragma unroll
@@ -928,7 +929,7 @@ fp8_stream_kernel(const __grid_constant__ StreamParams p) {
   if (warp < p.KB) load_w(warp, a);
   const int Kp = p.KB * BK;
   float* ssx = reinterpret_cast<float*>(sx + p.M * Kp);
-  if (PACK) {
+  if constexpr (PACK) {
     // eight lanes per block of 128 features, 16 features per lane; a warp's
     // lanes all take the same turns
     const int sub = lane & 7, items = p.KB * p.M;
