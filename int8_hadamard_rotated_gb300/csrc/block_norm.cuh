@@ -418,10 +418,11 @@ struct Ring {
   const NormParams& p;
   uint8_t* smem;
   uint64_t* full;
-  int st = 0, phase = 0;
+  int st = 0, phase = 0, issued = 0;  // issued: by the lane that fetches
   __device__ uint32_t stage_bytes() const { return p.row_smem * (p.Y ? 2u : 1u); }
   __device__ void fetch(int row, int stage) {
     const uint32_t bytes = static_cast<uint32_t>(p.K) * sizeof(T);
+    ++issued;
     uint8_t* dst = smem + stage * stage_bytes();
     mbar_arrive_expect_tx(&full[stage], bytes * (p.Y ? 2u : 1u));
     bulk_load(dst, static_cast<const T*>(p.H) + row * p.ldh, bytes, &full[stage]);
@@ -429,6 +430,12 @@ struct Ring {
   }
   __device__ const T* h() const { return reinterpret_cast<const T*>(smem + st * stage_bytes()); }
   __device__ const T* y() const { return reinterpret_cast<const T*>(smem + st * stage_bytes() + p.row_smem); }
+  // No copy may land after the CTA has gone (if a wait for one gave up): the
+  // lane that fetched waits for the last use of every stage.
+  __device__ void drain() const {
+    for (int i = 0; i < p.stages; ++i)
+      if (issued > i) mbar_wait(&full[i], ((issued - 1 - i) / p.stages) & 1, nullptr, &g_norm_error);
+  }
   __device__ void next() {
     if (++st == p.stages) {
       st = 0;
@@ -558,6 +565,7 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
     }
     start = end;
   }
+  if (leader && *static_cast<volatile int*>(&abort_flag)) ring.drain();
 }
 
 // The same for rows whose coefficients do not fit beside the staged rows: one
@@ -666,6 +674,7 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
         });
     ring.next();
   }
+  if (threadIdx.x == 0 && *static_cast<volatile int*>(&abort_flag)) ring.drain();
 }
 
 // Rows of any width, alignment and stride up to 12288 features: the same with
@@ -1004,7 +1013,8 @@ int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream) 
   p.gate = a.gate;
   p.scale = a.scale;
   p.shift = a.shift;
-  p.row_sample = a.row_sample;
+  const bool sampled = a.gate || a.scale || a.shift;
+  p.row_sample = sampled ? a.row_sample : nullptr;
   p.ldh = a.ldh;
   p.ldy = a.ldy;
   p.ldho = a.ldho;
@@ -1014,7 +1024,7 @@ int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream) 
   p.M = static_cast<int>(a.M);
   p.K = static_cast<int>(a.K);
   p.KB = static_cast<int>(n_blocks(a.K));
-  p.rows_per_sample = static_cast<int>(std::min<int64_t>(a.rows_per_sample, 0x7fffffff));
+  p.rows_per_sample = sampled ? static_cast<int>(std::min<int64_t>(a.rows_per_sample, 0x7fffffff)) : 0;
   p.n_samples = static_cast<int>(a.n_samples);
   p.post = a.Y ? a.post_norm : CONVROT_NORM_NONE;
   p.pre = a.pre_norm;

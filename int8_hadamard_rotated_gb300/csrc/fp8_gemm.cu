@@ -1104,7 +1104,10 @@ int launch_pair(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const
   GemmParams p;
   if (int st = fill(p, Qx, s_x, M, K, w, n, 256, G::BN, LANES, G::BN / 2)) return st;
   p.tma_y = true;
-  for (int j = 0; j < n; ++j) p.tma_y = p.tma_y && aligned16(w[j].Y) && w[j].ldy * sizeof(TY) % 16 == 0;
+  for (int j = 0; j < n; ++j) {
+    const uint64_t pitch = static_cast<uint64_t>(w[j].ldy) * sizeof(TY);
+    p.tma_y = p.tma_y && aligned16(w[j].Y) && pitch % 16 == 0 && pitch < (1ull << 40);
+  }
   if (p.tma_y)
     for (int j = 0; j < n; ++j)
       if (int st = make_tmap_out(&p.tmap_y[j], w[j].Y, y_dtype, M, w[j].N, w[j].ldy)) return st;

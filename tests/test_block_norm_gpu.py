@@ -202,6 +202,23 @@ def test_sample_out_of_range_is_reported(ops):
         assert_near(U[fine], u, um, "u")
 
 
+def test_samples_without_vectors_are_not_read(ops):
+    """A row's sample means nothing without gate, scale or shift."""
+    import ctypes
+    for K in (256, 259):
+        h = torch.randn(6, K, device="cuda")
+        u = torch.empty_like(h)
+        a = ops.convrot_block_norm_args()
+        a.M, a.K, a.dtype, a.u_dtype, a.H, a.ldh, a.U, a.ldu = 6, K, ops.F32, ops.F32, h.data_ptr(), K, u.data_ptr(), K
+        a.residual_scale, a.pre_norm, a.pre_eps = 1.0, ops.NORM_RMS, 1e-6
+        sample = torch.full((6,), 77, dtype=torch.int32, device="cuda")
+        a.row_sample = sample.data_ptr()
+        assert ops.lib().convrot_block_norm(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == ops.OK
+        assert ops.convrot_device_status() == ops.OK
+        _, ref, _, mag = bo.block_norm(host(h))
+        assert_near(u, ref, mag, "u")
+
+
 def test_many_rows_repeat_bit_for_bit(ops):
     t, sample = case(8, 5000, 768)
     H, U = ops.convrot_block_norm(**t, post_norm=2, pre_norm=2)

@@ -166,6 +166,23 @@ def test_linears_share_a_pack(ops, M):
     assert ops.convrot_device_status() == ops.OK
 
 
+@pytest.mark.parametrize("M", [3, 40, 300, 2500])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_outputs_inside_a_wider_array(ops, M, out):
+    """Slices whose rows are 16-byte aligned (the bulk stores): what lies
+    around them is left alone."""
+    K, Ns = 400, [200, 1000]
+    Qx, sx, qx, x = packed(M, M, K)
+    ws = [packed(50 + n, n, K, 128) for n in Ns]
+    wide = torch.full((M + 2, 1600), 5.0, dtype=DT[out], device="cuda")
+    Ys = [wide[1:M + 1, 16:216], wide[1:M + 1, 232:1232]]
+    ops.fp8_linear_packed(Qx, sx, [w[0] for w in ws], [w[1] for w in ws], Ys=Ys)
+    for y, w in zip(Ys, ws):
+        assert_linear(y, *bo.fp8_linear(qx, x, w[2], w[3]), K)
+        y.fill_(5.0)
+    assert (wide == 5.0).all()
+
+
 def test_linear_is_repeatable_and_rows_are_independent(ops):
     """The same rows give the same bits, again and whatever rows follow within
     one kernel's range; every split of K adds in a fixed order."""
