@@ -585,8 +585,9 @@ typedef struct convrot_block_norm_args {
  * Errors: ERR_ARG (also a sample count that rows_per_sample overruns),
  *         ERR_ALIGN (an array not aligned to its elements; Q: K % 16, Q not
  *         16-byte aligned), ERR_ALIAS (an output overlaps an input or an
- *         output, but for H_out = H with the same ld), ERR_UNSUPPORTED,
- *         ERR_DEVICE, ERR_CUDA.
+ *         output, but for H_out = H with the same ld), ERR_UNSUPPORTED (K
+ *         over CONVROT_NORM_MAX_K, more than 2^31 - 2^16 rows), ERR_DEVICE,
+ *         ERR_CUDA.
  */
 int convrot_block_norm(const convrot_block_norm_args* args, void* stream);
 
@@ -613,7 +614,7 @@ int convrot_block_norm(const convrot_block_norm_args* args, void* stream);
  * that suit its elements; 16-byte aligned rows are read fastest.
  * Errors: ERR_ARG, ERR_ALIGN (K % 16, Q_x not 16-byte aligned, X or s_x not
  *         aligned to its elements), ERR_ALIAS, ERR_UNSUPPORTED (more than
- *         2^31 - 1 scales), ERR_DEVICE, ERR_CUDA.
+ *         2^31 - 1 scales or 2^31 - 2^16 rows), ERR_DEVICE, ERR_CUDA.
  */
 int fp8_pack_activations(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* Q_x,
                          float* s_x, void* stream);

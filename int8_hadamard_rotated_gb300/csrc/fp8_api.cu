@@ -30,8 +30,12 @@ bool meet(const Region& a, const Region& b) {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Most rows of a matrix: the kernels count them in 32 bits and may look as far
+// as a tile or a ring of staged rows past the last one.
+constexpr int64_t MAX_ROWS = 0x7fff0000;
+
 // Whether rows * pitch (elements) stays far inside 63 bits.
-bool sane(int64_t rows, int64_t pitch) { return pitch <= (1ll << 40) && rows <= (1ll << 31) - 1; }
+bool sane(int64_t rows, int64_t pitch) { return pitch <= (1ll << 40) && rows <= MAX_ROWS; }
 
 int pack_checks(const void* X, int dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* Q, const float* s,
                 int64_t n_scales) {
@@ -59,12 +63,12 @@ int linear_checks(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, con
     if (!w.q || !w.scale || !w.Y || w.ldy < w.N) return CONVROT_ERR_ARG;
     if (!aligned16(w.q) || !aligned_to(w.scale, 4) || !aligned_to(w.bias, 4) || !aligned_to(w.Y, size))
       return CONVROT_ERR_ALIGN;
-    if (!sane(M, w.ldy) || w.N > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+    if (!sane(M, w.ldy) || w.N > MAX_ROWS) return CONVROT_ERR_UNSUPPORTED;
   }
   if (M == 0) return CONVROT_OK;
   if (!Qx || !s_x) return CONVROT_ERR_ARG;
   if (K % 16 != 0 || !aligned16(Qx) || !aligned_to(s_x, 4)) return CONVROT_ERR_ALIGN;
-  if (M > 0x7fffffff || K > 0x7fffffff || M * n_blocks(K) > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+  if (M > MAX_ROWS || K > 0x7fffffff || M * n_blocks(K) > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
   const Region qx = flat(Qx, M * K), sx = flat(s_x, M * n_blocks(K) * 4);
   for (int j = 0; j < n; ++j) {
     if (weights[j].N == 0) continue;
@@ -181,7 +185,7 @@ int convrot_block_norm(const convrot_block_norm_args* args, void* stream) {
 
 int fp8_pack_activations(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* Q_x, float* s_x,
                          void* stream) {
-  if (M > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+  if (M > MAX_ROWS) return CONVROT_ERR_UNSUPPORTED;
   if (int st = pack_checks(X, x_dtype, M, K, ldx, Q_x, s_x, M * n_blocks(K))) return st;
   if (M == 0) return CONVROT_OK;
   if (int st = check_device()) return st;
@@ -189,7 +193,7 @@ int fp8_pack_activations(const void* X, int x_dtype, int64_t M, int64_t K, int64
 }
 
 int fp8_prepare_weight(const void* W, int w_dtype, int64_t N, int64_t K, uint8_t* Q_w, float* s_w, void* stream) {
-  if (N > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+  if (N > MAX_ROWS) return CONVROT_ERR_UNSUPPORTED;
   if (int st = pack_checks(W, w_dtype, N, K, K, Q_w, s_w, n_blocks(N) * n_blocks(K))) return st;
   if (N == 0) return CONVROT_OK;
   if (int st = check_device()) return st;
@@ -197,7 +201,7 @@ int fp8_prepare_weight(const void* W, int w_dtype, int64_t N, int64_t K, uint8_t
 }
 
 size_t fp8_linear_workspace_size(int64_t M, int64_t K) {
-  if (M < 0 || K <= 0 || M > 0x7fffffff || K > 0x7fffffff) return 0;
+  if (M < 0 || K <= 0 || M > MAX_ROWS || K > 0x7fffffff) return 0;
   return round256(static_cast<size_t>(M) * K) + round256(static_cast<size_t>(M) * n_blocks(K) * 4);
 }
 
@@ -216,7 +220,7 @@ int fp8_linear(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, co
   if (M < 0 || K <= 0 || !known_dtype(x_dtype) || ldx < K || !weights || n_weights < 1 ||
       n_weights > CONVROT_MAX_LINEARS || !known_dtype(y_dtype))
     return CONVROT_ERR_ARG;
-  if (M > 0x7fffffff || K > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+  if (M > MAX_ROWS || K > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
   const size_t need = fp8_linear_workspace_size(M, K);
   uint8_t* q = static_cast<uint8_t*>(workspace);
   if (M > 0) {

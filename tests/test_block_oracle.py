@@ -193,3 +193,22 @@ def test_binding_refuses_host_tensors():
         ops.fp8_pack_activations(torch.zeros(4, 32))
     with pytest.raises(ValueError, match="CUDA"):
         ops.convrot_block_norm(torch.zeros(4, 32))
+
+
+def test_row_limit(L):
+    # rows are counted in 32 bits, with room for looking a tile past the last
+    from int8_hadamard_rotated_gb300 import ops
+    import ctypes
+    W = ops.convrot_fp8_weight
+    most, over = 0x7fff0000, 0x7fff0001
+    for rows in (over, (1 << 31) - 1):
+        assert L.fp8_pack_activations(A[0], ops.F32, rows, 16, 16, A[1], A[2], None) == ops.ERR_UNSUPPORTED
+        assert L.fp8_prepare_weight(A[0], ops.F32, rows, 16, A[1], A[2], None) == ops.ERR_UNSUPPORTED
+        assert L.fp8_linear_workspace_size(rows, 16) == 0
+        w = (W * 1)(W(A[2], A[3], None, 64, A[5], 64))
+        assert L.fp8_linear_packed(A[0], A[1], rows, 16, w, 1, ops.F32, None) == ops.ERR_UNSUPPORTED
+        assert L.fp8_linear(A[0], ops.F32, rows, 16, 16, w, 1, ops.F32, A[6], 0, None) == ops.ERR_UNSUPPORTED
+        w[0].N = w[0].ldy = rows
+        assert L.fp8_linear_packed(A[0], A[1], 1, 16, w, 1, ops.F32, None) == ops.ERR_UNSUPPORTED
+        assert L.convrot_block_norm(ctypes.byref(norm_args(M=rows, K=8)), None) == ops.ERR_UNSUPPORTED
+    assert L.fp8_linear_workspace_size(most, 16) == most * 16 + most * 4
