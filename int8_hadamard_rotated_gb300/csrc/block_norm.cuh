@@ -159,20 +159,37 @@ __device__ __forceinline__ void group_sync(int W, int group) {
   else named_bar_sync(1 + group, W * 32);
 }
 
-// Sums of a and b over the group's warps, in warp order, from each warp's own
-// (the same in all lanes). `red` holds 2 floats per warp of the group and
-// alternates between two such buffers from one call to the next, so that the
-// reads after one barrier are over before the next but one call writes.
-__device__ __forceinline__ void group_sum2(float& a, float& b, int W, int group, int warp_in_group, float2* red) {
-  if (W == 1) return;
-  if ((threadIdx.x & 31) == 0) red[warp_in_group] = make_float2(a, b);
+// The sum of v over W neighbouring lanes (W a power of two up to 16), the same
+// in all of them.
+__device__ __forceinline__ float lanes_sum(float v, int W) {
+  if (W > 1) v += __shfl_xor_sync(0xffffffffu, v, 1);
+  if (W > 2) v += __shfl_xor_sync(0xffffffffu, v, 2);
+  if (W > 4) v += __shfl_xor_sync(0xffffffffu, v, 4);
+  if (W > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v;
+}
+
+// What each warp of the group has put into its place of `red`, one warp's per
+// lane. `red` alternates between two such arrays from one call to the next, so
+// that the reads after one barrier are over before the next but one call
+// writes.
+__device__ __forceinline__ float2 exchange(float2 mine, int W, int group, int warp_in_group, float2* red) {
+  if (W == 1) return mine;
+  if ((threadIdx.x & 31) == 0) red[warp_in_group] = mine;
   group_sync(W, group);
-  a = b = 0.0f;
-  for (int w = 0; w < W; ++w) {
-    const float2 v = red[w];
-    a += v.x;
-    b += v.y;
-  }
+  return red[threadIdx.x & (W - 1)];
+}
+
+// s / n by the hardware's reciprocal r of n (or a better one) and a correction
+// step, within an ulp; 0 where n is 0.
+__device__ __forceinline__ float quotient(float s, float n, float r) {
+  const float q = s * r;
+  return n > 0.0f ? fmaf(fmaf(-q, n, s), r, q) : 0.0f;
+}
+__device__ __forceinline__ float quotient(float s, float n) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(n));
+  return quotient(s, n, r);
 }
 
 // 1 / sqrt(v): the hardware's approximation (relative error under 2^-22) and
@@ -205,8 +222,7 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i & 1] = f32x2_fma(x[i], x[i], acc[i & 1]);
     }
-    float sum = total(acc), none = 0.0f;
-    group_sum2(sum, none, W, group, warp_in_group, red);
+    const float sum = lanes_sum(exchange(make_float2(total(acc), 0.0f), W, group, warp_in_group, red).x, W);
     st.rstd = inverse_root(fmaf(sum, inv_k, eps));
     return st;
   }
@@ -217,9 +233,8 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i & 1] = add2(acc[i & 1], x[i]);
   }
-  float sum = total(acc);
-  const int n = count(warp_in_group);
-  const float mean_w = n > 0 ? sum / static_cast<float>(n) : 0.0f;
+  // around the warp's own mean, then that mean's distance from the row's
+  const float mean_w = quotient(total(acc), static_cast<float>(count(warp_in_group)));
   const Pair minus = both(-mean_w);
   acc[0] = acc[1] = 0ull;
 #pragma unroll
@@ -233,21 +248,13 @@ __device__ __forceinline__ Stats row_stats(Get get, Count count, int kind, float
     }
   }
   float m2 = total(acc);
-  if (W == 1) {
-    st.mean = mean_w;
-  } else {
-    // the warps' sums and squared distances: around each warp's own mean,
-    // then that mean's distance from the row's
-    if ((threadIdx.x & 31) == 0) red[warp_in_group] = make_float2(sum, m2);
-    group_sync(W, group);
-    sum = m2 = 0.0f;
-    for (int w = 0; w < W; ++w) sum += red[w].x;
-    st.mean = sum / static_cast<float>(K);
-    for (int w = 0; w < W; ++w) {
-      const int nw = count(w);
-      const float d = nw > 0 ? red[w].x / static_cast<float>(nw) - st.mean : 0.0f;
-      m2 += fmaf(static_cast<float>(nw) * d, d, red[w].y);
-    }
+  st.mean = mean_w;
+  if (W > 1) {
+    const float2 of_warp = exchange(make_float2(mean_w, m2), W, group, warp_in_group, red);
+    const float n = static_cast<float>(count(threadIdx.x & (W - 1)));
+    st.mean = quotient(lanes_sum(n * of_warp.x, W), static_cast<float>(K), inv_k);
+    const float d = of_warp.x - st.mean;
+    m2 = lanes_sum(fmaf(n * d, d, of_warp.y), W);
   }
   st.rstd = inverse_root(fmaf(m2, inv_k, eps));
   return st;
@@ -291,38 +298,83 @@ struct Unit {
       if (on[0]) store8(row + lo, x);
     }
   }
-  // Codes and scales of the unit's features: a block of 128 is the same half
-  // of all lanes (32-bit elements) or both halves of sixteen lanes.
-  __device__ __forceinline__ void store_codes(uint8_t* q, float* s, const Pair (&x)[4]) const {
-    if constexpr (sizeof(T) == 4) {
+  // Blocks of 128 of the unit's features: the same half of all lanes (32-bit
+  // elements) or both halves of sixteen lanes.
+  static constexpr int BLOCKS = sizeof(T) == 4 ? 2 : 1, SPAN = sizeof(T) == 4 ? 32 : 16;
+  __device__ __forceinline__ void maxima(const Pair (&x)[4], float* m) const {
+    if constexpr (BLOCKS == 2) {
+      m[0] = max_magnitude({x[0], x[1]});
+      m[1] = max_magnitude({x[2], x[3]});
+    } else {
+      m[0] = max_magnitude(x);
+    }
+  }
+  // `sc`, `nr`: the blocks' scales and factors
+  __device__ __forceinline__ void store_codes(uint8_t* q, float* s, const Pair (&x)[4], const float (&sc)[BLOCKS],
+                                              const float (&nr)[BLOCKS]) const {
+    if constexpr (BLOCKS == 2) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const Pair v[2] = {x[2 * h], x[2 * h + 1]};
-        float m = max_magnitude(v);
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float sc = e4m3_scale(m);
         uint32_t c[1];
-        e4m3_codes(v, sc, c);
+        e4m3_codes({x[2 * h], x[2 * h + 1]}, sc[h], nr[h], c);
         if (on[h]) {
           *reinterpret_cast<uint32_t*>(q + (h ? hi : lo)) = c[0];
-          if ((threadIdx.x & 31) == 0) s[(h ? hi : lo) / QBLOCK] = sc;
+          if ((threadIdx.x & 31) == 0) s[(h ? hi : lo) / QBLOCK] = sc[h];
         }
       }
     } else {
-      float m = max_magnitude(x);
-#pragma unroll
-      for (int d = 1; d < 16; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const float sc = e4m3_scale(m);
       uint32_t c[2];
-      e4m3_codes(x, sc, c);
+      e4m3_codes(x, sc[0], nr[0], c);
       if (on[0]) {
         *reinterpret_cast<uint2*>(q + lo) = make_uint2(c[0], c[1]);
-        if ((threadIdx.x & 15) == 0) s[lo / QBLOCK] = sc;
+        if ((threadIdx.x & 15) == 0) s[lo / QBLOCK] = sc[0];
       }
     }
   }
 };
+
+// The maxima of N values over SPAN neighbouring lanes, value j in lane j of
+// them: while several are left, each step hands half of them to the other lane.
+template <int N, int SPAN, int D = 1>
+__device__ __forceinline__ float spread_max(const float (&m)[N]) {
+  if constexpr (D == SPAN) {
+    static_assert(N == 1, "at most a value per lane");
+    return m[0];
+  } else {
+    const bool odd = threadIdx.x & D;
+    float next[(N + 1) / 2];
+#pragma unroll
+    for (int i = 0; i < (N + 1) / 2; ++i) {
+      if (2 * i + 1 < N)
+        next[i] = max_nan(odd ? m[2 * i + 1] : m[2 * i],
+                          __shfl_xor_sync(0xffffffffu, odd ? m[2 * i] : m[2 * i + 1], D));
+      else
+        next[i] = max_nan(m[2 * i], __shfl_xor_sync(0xffffffffu, m[2 * i], D));
+    }
+    return spread_max<(N + 1) / 2, SPAN, 2 * D>(next);
+  }
+}
+
+// The codes of a thread's V units, with the scales of their blocks: each scale
+// is computed in one lane and handed round.
+template <int V, typename Place, typename At>
+__device__ __forceinline__ void quantize_row(At at, uint8_t* q, float* s, const Pair (&x)[V][4]) {
+  constexpr int B = Place::BLOCKS;
+  float m[V * B];
+#pragma unroll
+  for (int u = 0; u < V; ++u) at(u).maxima(x[u], m + u * B);
+  const float scale = e4m3_scale(spread_max<V * B, Place::SPAN>(m)), factor = e4m3_factor(scale);
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    float sc[B], nr[B];
+#pragma unroll
+    for (int h = 0; h < B; ++h) {
+      sc[h] = __shfl_sync(0xffffffffu, scale, u * B + h, Place::SPAN);
+      nr[h] = __shfl_sync(0xffffffffu, factor, u * B + h, Place::SPAN);
+    }
+    at(u).store_codes(q, s, x[u], sc, nr);
+  }
+}
 
 // The thread's part of a row, V units (unit u of chunk u * W + wg), from its
 // arrival in shared memory to its last store: see the two kernels that use it.
@@ -406,9 +458,9 @@ __device__ __forceinline__ void do_row(const NormParams& p, int row, const T* sh
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[u][i] = unit.inside(i, f32x2_fma(x[u][i], a[i], b[i]));
-    if (FP8) unit.store_codes(q, s, x[u]);
-    else unit.store(out, x[u]);
+    if (!FP8) unit.store(out, x[u]);
   }
+  if constexpr (FP8) quantize_row<V, Place>([&](int u) { return Place(u * W + wg, p.K, u < V - 1); }, q, s, x);
 }
 
 // A ring of staged rows of h and y: one lane issues bulk copies a few rows
@@ -710,20 +762,21 @@ struct Scattered {
     }
   }
   // a block of 128 is half of every lane's elements
-  __device__ __forceinline__ void store_codes(uint8_t* q, float* s, const Pair (&x)[4]) const {
+  static constexpr int BLOCKS = 2, SPAN = 32;
+  __device__ __forceinline__ void maxima(const Pair (&x)[4], float* m) const {
+    m[0] = max_magnitude({x[0], x[1]});
+    m[1] = max_magnitude({x[2], x[3]});
+  }
+  __device__ __forceinline__ void store_codes(uint8_t* q, float* s, const Pair (&x)[4], const float (&sc)[2],
+                                              const float (&nr)[2]) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const Pair v[2] = {x[2 * h], x[2 * h + 1]};
-      float m = max_magnitude(v);
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const float sc = e4m3_scale(m);
       uint32_t c[1];
-      e4m3_codes(v, sc, c);
+      e4m3_codes({x[2 * h], x[2 * h + 1]}, sc[h], nr[h], c);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (e0 + 128 * h + 32 * i < K) q[e0 + 128 * h + 32 * i] = static_cast<uint8_t>(c[0] >> (8 * i));
-      if ((threadIdx.x & 31) == 0 && e0 + 128 * h < K) s[(e0 + 128 * h) / QBLOCK] = sc;
+      if ((threadIdx.x & 31) == 0 && e0 + 128 * h < K) s[(e0 + 128 * h) / QBLOCK] = sc[h];
     }
   }
 };
@@ -869,7 +922,7 @@ block_norm_any_kernel(const __grid_constant__ NormParams p) {
           for (int d = 1; d < 32; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
           const float sc = e4m3_scale(m);
           uint32_t c[1];
-          e4m3_codes(o, sc, c);
+          e4m3_codes(o, sc, e4m3_factor(sc), c);
           if (e < p.K) *reinterpret_cast<uint32_t*>(p.Q + row * p.K + e) = c[0];
           if (lane == 0) p.s[row * p.KB + kb] = sc;
         }

@@ -171,10 +171,13 @@ static __device__ __noinline__ uint32_t e4m3_codes_divided(float a, float b, flo
 // two elements. (Two products that enclose the quotient, and the division
 // where their codes differ, cost the same without ties, but 16-bit inputs are
 // full of exact ties: 51 us against 35 us for bf16 [4608, 12288].)
+// `nr` is -RN(1 / s) in that range.
+__device__ __forceinline__ bool e4m3_corrected(float s) { return s >= 0x1p-90f && s <= 3.0e38f; }
+__device__ __forceinline__ float e4m3_factor(float s) { return e4m3_corrected(s) ? -__frcp_rn(s) : 0.0f; }
 template <int NP>
-__device__ __forceinline__ void e4m3_codes(const unsigned long long (&x)[NP], float s, uint32_t (&out)[NP / 2]) {
-  if (s >= 0x1p-90f && s <= 3.0e38f) {
-    const float nr = -__frcp_rn(s);
+__device__ __forceinline__ void e4m3_codes(const unsigned long long (&x)[NP], float s, float nr,
+                                           uint32_t (&out)[NP / 2]) {
+  if (e4m3_corrected(s)) {
     const unsigned long long nr2 = f32x2_pack(nr, nr), s2 = f32x2_pack(s, s);
 #pragma unroll
     for (int i = 0; i < NP / 2; ++i) {

@@ -947,7 +947,7 @@ fp8_stream_kernel(const __grid_constant__ StreamParams p) {
       for (int d = 1; d < 8; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
       const float sc = e4m3_scale(m);
       uint32_t q[4];
-      e4m3_codes(x, sc, q);
+      e4m3_codes(x, sc, e4m3_factor(sc), q);
       if (i < items) {
         *reinterpret_cast<uint4*>(sx + r * Kp + col) = make_uint4(q[0], q[1], q[2], q[3]);
         if (sub == 0) ssx[r * p.KB + kb] = sc;

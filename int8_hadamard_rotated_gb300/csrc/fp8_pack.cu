@@ -42,7 +42,7 @@ fp8_pack_kernel(const T* __restrict__ X, int64_t ldx, uint32_t n_qblocks, uint32
   for (int d = 1; d < 8; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float sc = e4m3_scale(m);
   uint32_t c[4];
-  e4m3_codes(x, sc, c);
+  e4m3_codes(x, sc, e4m3_factor(sc), c);
   if (on) {
     *reinterpret_cast<uint4*>(Q + static_cast<int64_t>(row) * K + col) = make_uint4(c[0], c[1], c[2], c[3]);
     if (sub == 0) s[b] = sc;
@@ -80,13 +80,13 @@ fp8_weight_kernel(const T* __restrict__ W, int64_t N, int64_t K, bool vec, uint8
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 8; ++w) m = max_nan(m, part[w]);
-  const float sc = e4m3_scale(m);
+  const float sc = e4m3_scale(m), nr = e4m3_factor(sc);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int unit = threadIdx.x + 256 * u;
     const int64_t row = nb * QBLOCK + unit / 8, col = kb * QBLOCK + (unit & 7) * 16;
     uint32_t c[4];
-    e4m3_codes(x[u], sc, c);
+    e4m3_codes(x[u], sc, nr, c);
     if (row < N && col < K) *reinterpret_cast<uint4*>(Q + row * K + col) = make_uint4(c[0], c[1], c[2], c[3]);
   }
   if (threadIdx.x == 0) s[blockIdx.x] = sc;
