@@ -105,46 +105,53 @@ __device__ __forceinline__ Pair add2(Pair a, Pair b) {
 }
 __device__ __forceinline__ Pair both(float v) { return f32x2_pack(v, v); }
 
-// The same for four consecutive features at a 16-byte aligned place.
-__device__ __forceinline__ void post_coef4(const NormParams& p, int s, int e, Pair (&a)[2], Pair (&b)[2]) {
-  Pair v[2];
-  a[0] = a[1] = both(p.block_scale);
-  b[0] = b[1] = 0ull;
-  if (p.gate) {
-    if (s >= 0) load4(p.gate + s * p.ld_gate + e, v[0], v[1]);
+// The same for four consecutive features at a 16-byte aligned place, in two
+// steps: first every vector's values, so that all loads of a thread's places
+// are on their way together, then the arithmetic, with 1 and 0 for what is
+// absent. (With a wait after every load, at the start of a kernel and at every
+// change of sample: bf16 [4608, 3072] to codes with seven samples 36.8 us
+// instead of 34.1 us, fp32 [4608, 12288] between weighted RMS norms with a gate
+// 169 us instead of 161 us. All loads of eight features together spill: 167 us
+// instead of 135 us for bf16 [4608, 16384] with gate and modulation.)
+struct PostVectors {
+  Pair gate[2], weight[2], bias[2];
+};
+__device__ __forceinline__ void load_or(const float* v, bool has, int64_t at, float otherwise, Pair (&x)[2]) {
+  x[0] = x[1] = both(otherwise);
+  if (has) load4(v + at, x[0], x[1]);
+}
+__device__ __forceinline__ PostVectors post_vectors(const NormParams& p, int s, int e) {
+  PostVectors v;
+  load_or(p.gate, p.gate && s >= 0, s * p.ld_gate + e, p.gate ? 0.0f : 1.0f, v.gate);
+  load_or(p.post_weight, p.post_weight, e, 1.0f, v.weight);
+  load_or(p.post_bias, p.post_bias, e, 0.0f, v.bias);
+  return v;
+}
+__device__ __forceinline__ void fold(const NormParams& p, const PostVectors& v, Pair (&a)[2], Pair (&b)[2]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) a[i] = s < 0 ? 0ull : f32x2_mul(a[i], v[i]);
-  }
-  if (p.post_bias) {
-    load4(p.post_bias + e, v[0], v[1]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) b[i] = f32x2_mul(a[i], v[i]);
-  }
-  if (p.post_weight) {
-    load4(p.post_weight + e, v[0], v[1]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) a[i] = f32x2_mul(a[i], v[i]);
+  for (int i = 0; i < 2; ++i) {
+    const Pair g = f32x2_mul(both(p.block_scale), v.gate[i]);
+    b[i] = f32x2_mul(g, v.bias[i]);
+    a[i] = f32x2_mul(g, v.weight[i]);
   }
 }
-__device__ __forceinline__ void pre_coef4(const NormParams& p, int s, int e, Pair (&a)[2], Pair (&b)[2]) {
-  Pair v[2];
-  a[0] = a[1] = both(1.0f);
-  b[0] = b[1] = 0ull;
-  if (p.pre_weight) load4(p.pre_weight + e, a[0], a[1]);
-  if (p.pre_bias) load4(p.pre_bias + e, b[0], b[1]);
-  if (p.scale && s >= 0) {
-    load4(p.scale + s * p.ld_mod + e, v[0], v[1]);
+struct PreVectors {
+  Pair weight[2], bias[2], scale[2], shift[2];
+};
+__device__ __forceinline__ PreVectors pre_vectors(const NormParams& p, int s, int e) {
+  PreVectors v;
+  load_or(p.pre_weight, p.pre_weight, e, 1.0f, v.weight);
+  load_or(p.pre_bias, p.pre_bias, e, 0.0f, v.bias);
+  load_or(p.scale, p.scale && s >= 0, s * p.ld_mod + e, 0.0f, v.scale);
+  load_or(p.shift, p.shift && s >= 0, s * p.ld_mod + e, 0.0f, v.shift);
+  return v;
+}
+__device__ __forceinline__ void fold(const NormParams&, const PreVectors& v, Pair (&a)[2], Pair (&b)[2]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      v[i] = add2(v[i], both(1.0f));
-      a[i] = f32x2_mul(a[i], v[i]);
-      b[i] = f32x2_mul(b[i], v[i]);
-    }
-  }
-  if (p.shift && s >= 0) {
-    load4(p.shift + s * p.ld_mod + e, v[0], v[1]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) b[i] = add2(b[i], v[i]);
+  for (int i = 0; i < 2; ++i) {
+    const Pair f = add2(v.scale[i], both(1.0f));
+    a[i] = f32x2_mul(v.weight[i], f);
+    b[i] = add2(f32x2_mul(v.bias[i], f), v.shift[i]);
   }
 }
 
@@ -509,10 +516,15 @@ constexpr int MAX_STAGES = 8;
 // current sample (norm weights, gate and modulation folded, only those that
 // are not 0 or 1) lie in shared memory and are formed again when it changes.
 //
+// bf16 [4608, 3072] with gate, LayerNorm and modulation, two samples: 24.6 us
+// = 4.61 TB/s (a copy with as many bytes 5.7 TB/s); RMS norms on both sides to
+// codes, seven samples: 34.1 us. What is left is the chain from a row's arrival
+// over two sums to its last store with 16 warps per SM to cover it (registers
+// and the coefficients take the SM), issuing in 40 % of the cycles.
 // (One thread block per row with one unit per thread and its coefficients in
-// registers: 49 us for bf16 [4608, 3072] with gate, LayerNorm and modulation,
-// 53 instructions per feature, most of them per row and thread; coefficients
-// read through L1 for every row: 60 us.)
+// registers: 49 us, 53 instructions per feature, most of them per row and
+// thread; coefficients read through L1 for every row: 60 us; three CTAs per SM
+// at three units: 12 % slower, spilling, and the rows divide worse.)
 template <typename T, typename TU, int V, bool FP8>
 __global__ void __launch_bounds__(WARPS * 32, V <= 2 ? 3 : V <= 4 ? 2 : 1)
 block_norm_kernel(const __grid_constant__ NormParams p) {
@@ -579,22 +591,26 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
     }
     if (has_pa || has_pb || has_qa || has_qb) {
       __syncthreads();  // the rows before may still read theirs
-      for (int chunk = warp; chunk < n_chunks; chunk += WARPS) {
-        const Unit<T> unit(chunk, p.K);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!unit.on[h]) continue;
-          const int e = h ? unit.hi : unit.lo, at = chunk * 256 + h * 128 + lane * 4;
-          Pair a[2], b[2];
-          if (has_pa || has_pb) {
-            post_coef4(p, s, e, a, b);
-            if (has_pa) store4(cpa + at, a[0], a[1]);
-            if (has_pb) store4(cpb + at, b[0], b[1]);
-          }
-          pre_coef4(p, s, e, a, b);
-          if (has_qa) store4(cqa + at, a[0], a[1]);
-          if (has_qb) store4(cqb + at, b[0], b[1]);
+      // pieces of four features per lane, one half of a unit; one at a time, for
+      // the registers' sake
+#pragma unroll 1
+      for (int piece = warp; piece < 2 * n_chunks; piece += WARPS) {
+        const Unit<T> unit(piece / 2, p.K);
+        const bool second = piece & 1;
+        if (!(second ? unit.on[1] : unit.on[0])) continue;
+        const int e = second ? unit.hi : unit.lo, at = piece * 128 + lane * 4;
+        PostVectors post;
+        if (has_pa || has_pb) post = post_vectors(p, s, e);
+        const PreVectors pre = pre_vectors(p, s, e);
+        Pair a[2], b[2];
+        if (has_pa || has_pb) {
+          fold(p, post, a, b);
+          if (has_pa) store4(cpa + at, a[0], a[1]);
+          if (has_pb) store4(cpb + at, b[0], b[1]);
         }
+        fold(p, pre, a, b);
+        if (has_qa) store4(cqa + at, a[0], a[1]);
+        if (has_qb) store4(cqb + at, b[0], b[1]);
       }
       __syncthreads();
     }
@@ -625,7 +641,8 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
 // what is added (a bias of the first norm; bias and shift of the second) in
 // shared memory where that fits (p.coef_smem) and else read again for every
 // row. Eight warps with up to six units per thread: fp32 [4608, 12288] between
-// two weighted RMS norms takes 214 us with 24 warps of two units.
+// two weighted RMS norms with a gate 161 us = 5.65 TB/s, with 24 warps of two
+// units 214 us.
 template <typename T, typename TU, int V, bool FP8, int NW>
 __global__ void __launch_bounds__(NW * 32, 1)
 block_norm_wide_kernel(const __grid_constant__ NormParams p) {
@@ -656,8 +673,8 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
     for (int h = 0; h < 2; ++h) {
       Pair va[2] = {0ull, 0ull}, vb[2] = {0ull, 0ull};
       if (unit.on[h]) {
-        if (pre) pre_coef4(p, s, h ? unit.hi : unit.lo, va, vb);
-        else post_coef4(p, s, h ? unit.hi : unit.lo, va, vb);
+        if (pre) fold(p, pre_vectors(p, s, h ? unit.hi : unit.lo), va, vb);
+        else fold(p, post_vectors(p, s, h ? unit.hi : unit.lo), va, vb);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -992,10 +1009,10 @@ int launch_wide(NormParams& p, cudaStream_t stream) {
 // Warps per row of the grouped kernel: enough that a lane has at most four
 // units (two CTAs per SM; six with all eight warps) and that two rows of every
 // group fit beside the coefficients, and more while there are fewer rows than
-// groups on the GPU. 0: nothing fits. bf16 [4608, 3072] to codes: 40 us with
-// four warps and three units against 52 us with two warps and six, [8192,
-// 1280]: 25 us with two warps and three units, 26 with one and five, 29 with
-// four.
+// groups on the GPU. 0: nothing fits. Measured before the sums went across
+// lanes: bf16 [4608, 3072] to codes 40 us with four warps and three units, 52
+// us with two warps and six; [8192, 1280] 25 us with two warps and three units,
+// 26 with one and five, 29 with four.
 int pick_warps(const NormParams& p) {
   const int chunks = (p.K + 255) / 256;
   const int64_t sms = device_sm_count();
