@@ -189,6 +189,16 @@ __device__ __forceinline__ Tile decode(const GemmParams& p, int t) {
 // bytes at a time in the 128-byte swizzle (no barrier between warps), by
 // tensor-map stores where the rows of Y are 16-byte aligned, else by
 // coalesced element stores.
+//
+// [4608, 3072] through three [3072, 3072] weights to bf16: 113 us = 2.3
+// PFLOP/s; [4608, 12288] through [3072, 12288] to fp32: 144 us = 2.4 PFLOP/s
+// (154 us under sustained load). Two chains bound it about equally. The MMAs
+// with no loads and no promotion take 82 us on the first shape; with the loads
+// 116 us, since a pair's operands (64 KB per block of K, all from L2) arrive at
+// some 12 TB/s over the GPU; with the promotion and no loads 117 us: reading
+// an accumulator out of TMEM and handing it back takes as long as a block's
+// MMAs, and only two fit beside each other. The last tile's promotion and
+// stores, and 648 tiles over 76 pairs (8.5 waves), cost another 10 %.
 
 constexpr int EPI_WARPS = 8;
 constexpr int PAIR_THREADS = (EPI_WARPS + 4) * 32;  // three warpgroups
@@ -566,6 +576,12 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
 // stages are free by then) and, after a cluster barrier, sums a part of the
 // rows over all CTAs in rank order through distributed shared memory: no
 // workspace, no atomics, the same order every time.
+// Bound by the chain of a CTA's blocks, about 0.3 us each from the last load to
+// the promoted sums, against the time its weights take from HBM: 24 rows
+// through [3072, 12288] take 12.9 us = 2.98 TB/s, 331 rows through [1283,
+// 1280] 8.8 us with their pack. (Asking for the weights in L2 before the wait
+// for the kernel ahead: 7.1 us instead of 6.6 us for 16 rows through three
+// 3072 x 3072 linears.)
 // Six warps: 0-3 promote (32 lanes each), 4 loads, 5 issues MMAs.
 
 constexpr int SOLO_THREADS = 6 * 32;
@@ -849,7 +865,7 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
 // into the warp's accumulators, and the warps' sums meet in shared memory, in
 // warp order. Several CTAs per SM keep enough bytes in flight, and there is no
 // tensor memory, barrier or cluster to set up. One token through three 3072 x
-// 3072 linears: 6.7 us against 8.8 us on tcgen05 with K split over clusters;
+// 3072 linears, packed here too: 6.7 us = 4.2 TB/s against 8.8 us on tcgen05 with K split over clusters;
 // from 9 rows on that one is faster (16 rows: 9.4 against 6.7 us).
 //
 // TX: the activations come as codes and scales (uint8_t), or as they are, up
