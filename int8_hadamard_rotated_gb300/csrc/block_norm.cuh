@@ -750,7 +750,10 @@ block_norm_wide_kernel(const __grid_constant__ NormParams p) {
 // the elements of 256 features dealt out one by one (element i of a lane is
 // feature 32 i + lane), so that a warp's accesses are contiguous however the
 // row starts; everything is read from global memory, the coefficients and the
-// second reading of y through L1.
+// second reading of y through L1. Bound by issuing element-wise accesses: bf16
+// [4000, 3071] with gate and modulation 56 us = 1.75 TB/s, fp16 [1003, 1283]
+// 8.6 us; loading the coefficients element by element as they are used, not one
+// vector at a time, more than doubled it.
 template <typename T>
 struct Scattered {
   int e0, K;
@@ -864,7 +867,10 @@ block_norm_scattered_kernel(const __grid_constant__ NormParams p) {
 
 // Rows longer than the kernels above hold in registers: one row per CTA at a
 // time, kept as fp32 in shared memory, elements taken one by one (thread t
-// owns the elements t, t + blockDim, ...).
+// owns the elements t, t + blockDim, ...). Bound by the latency of its loads:
+// with gate and modulation bf16 [512, 32768] 251 us, [512, 24001] 102 us; four
+// loads of each array together need 59 registers, which leaves one CTA per SM:
+// 236 and 173 us.
 __device__ float block_sum(float v, float* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
   v = warp_sum(v);
