@@ -282,3 +282,43 @@ def test_refusals(ops):
         with pytest.raises(ops.ConvrotError) as e:
             bad()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("M,K", [(11, 8200), (400, 9000), (7, 10240), (3, 9001)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vectors", [True, False])
+def test_widths_between_8192_and_10240(ops, M, K, dtype, vectors):
+    """Five units of eight features per lane, with and without vectors beside
+    the staged rows, to u and to codes."""
+    t, sample = case(M + K, M, K, dtype, vectors=vectors)
+    h, u, hm, um = oracle(t, sample, 2, 1)
+    H, U = ops.convrot_block_norm(**t, post_norm=2, pre_norm=1)
+    assert_near(H, h, hm, "h")
+    assert_near(U, u, um, "u")
+    if K % 16 == 0:
+        H, Q, s = ops.convrot_block_norm_fp8(**t, post_norm=2, pre_norm=1)
+        assert_near(H, h, hm, "h")
+        assert_codes(Q, s, u, um)
+    assert ops.convrot_device_status() == ops.OK
+
+
+@pytest.mark.parametrize("M", [1, 260])
+def test_u_feeds_the_int8_linears(ops, M):
+    """A bfloat16 residual stream in front of an INT8 linear: u leaves as
+    binary16 or fp32, which the INT8 pack takes; the result is that of the same
+    u held by the caller."""
+    K, N, G = 1024, 256, 64
+    t, sample = case(M, M, K, "bf16")
+    W = torch.randn(N, K, generator=torch.Generator().manual_seed(5)).cuda()
+    Q_w, s_w, Q16 = ops.convrot_prepare_weight(W, G)
+    _, u, _, um = oracle(t, sample, 1, 2)
+    for u_dtype in ("f16", "f32"):
+        _, U = ops.convrot_block_norm(**t, post_norm=1, pre_norm=2, want_h=False, u_dtype=DT[u_dtype])
+        assert_near(U, u, um, "u")
+        (y,) = ops.convrot_linear(U, G, [Q16], [s_w], [None])
+        # each operand is rounded to 8 bits: by up to 1 / 254 of its row's
+        # largest rotated value, 1 / (254 sqrt 3) in the root mean square; that
+        # largest of 1024 is within 6 times the row's root mean square
+        ref = U.double() @ W.double().t()
+        assert float((y.double() - ref).norm() / ref.norm()) < 2 * 6 / (254 * 3 ** 0.5)
+    assert ops.convrot_device_status() == ops.OK

@@ -307,3 +307,54 @@ def test_few_rows_of_a_long_k(ops):
     Qw, sw, qw, w = packed(9, N, K, 128)
     (y,) = ops.fp8_linear(X, [Qw], [sw])
     assert_linear(y, *bo.fp8_linear(*bo.fp8_pack(host(X)), qw, w), K)
+
+
+# one kernel each: streamed weights (up to 8 rows), few rows, one wave of
+# tiles, CTA pairs
+@pytest.mark.parametrize("M,K", [(1, 3072), (3, 3072), (8, 3072), (1, 12288), (3, 12288), (8, 12288), (9, 12288),
+                                 (300, 3072), (1500, 3072)])
+def test_sums_are_fp32(ops, M, K):
+    """The error of fp32 outputs against the 64-bit statement, root mean square
+    over root mean square. Rounding the running sum to nearest after each of
+    K / 128 <= 96 blocks gives sqrt(96) 2^-24 / sqrt 3 times the sum's own mean
+    growth (0.71), 2.4e-7; eight steps of a block, each cut at 2^-23 of a block
+    sum that is sqrt(128 / K) >= 0.1 of the result, give 3.4e-7 over 96 blocks;
+    together 4.2e-7, doubled. Sums that keep 14 to 16 bits come to 1e-5 and
+    more."""
+    N = 2048
+    Qx, sx, qx, x = packed(M, M, K)
+    Qw, sw, qw, w = packed(N, N, K, 128)
+    ref, _ = bo.fp8_linear(qx, x, qw, w)
+    (y,) = ops.fp8_linear_packed(Qx, sx, [Qw], [sw], out_dtype=torch.float32)
+    off = np.sqrt(np.mean((host(y).astype(np.float64) - ref) ** 2) / np.mean(ref ** 2))
+    assert off <= 1e-6, off
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("N,K", [(16, 16), (130, 656), (1283, 3072), (5000, 1040), (128, 12288), (128, 12304)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f16", "bf16"), ("f32", "f16")])
+def test_packing_in_the_call_equals_packing_before_it(ops, M, N, K, dtype, out):
+    """Bit for bit: up to 4 rows of up to 12288 features are packed by the
+    linear's own launch, more rows or features by a launch before it."""
+    Qw, sw, qw, w = packed(N + 1, N, K, 128)
+    b = torch.randn(N, generator=torch.Generator().manual_seed(N)).cuda()
+    X = activations(M + N, M, K, dtype)
+    (y,) = ops.fp8_linear(X, [Qw], [sw], [b], out_dtype=DT[out])
+    Q, s = ops.fp8_pack_activations(X)
+    (z,) = ops.fp8_linear_packed(Q, s, [Qw], [sw], [b], out_dtype=DT[out])
+    assert torch.equal(y, z)
+    assert_linear(y, *bo.fp8_linear(*bo.fp8_pack(host(X.float())), qw, w, host(b)), K)
+    assert ops.convrot_device_status() == ops.OK
+
+
+@pytest.mark.parametrize("M", [1, 8, 16, 200])
+def test_nan_codes_of_finite_scales(ops, M):
+    """A NaN code reaches the outputs that it enters, and no others."""
+    Qx, sx, _, _ = packed(M, M, 256)
+    Qw, sw, _, _ = packed(3, 64, 256, 128)
+    Qw.view(torch.uint8)[7, 130] = 0x7f
+    Qw.view(torch.uint8)[9, 3] = 0xff
+    (y,) = ops.fp8_linear_packed(Qx, sx, [Qw], [sw], out_dtype=torch.float32)
+    bad = torch.zeros(64, dtype=torch.bool, device="cuda")
+    bad[[7, 9]] = True
+    assert torch.isnan(y[:, bad]).all() and torch.isfinite(y[:, ~bad]).all()
