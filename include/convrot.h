@@ -718,6 +718,22 @@ int convrot_test_handover_timeout(const uint16_t* Q_x16, const float* s_x, int64
                                   size_t workspace_bytes, uint64_t wait_ns, void* stream);
 
 /*
+ * convrot_test_block_norm_timeout -- a test of the block norms' timeout path,
+ * not part of the method: convrot_block_norm with every bounded device wait of
+ * the launch limited to wait_ns nanoseconds, and no copy into shared memory of
+ * the rows from `row` (0 <= row < M) on. The waits for them give up: the kernel
+ * records CONVROT_ERR_TIMEOUT, stores nothing for them, waits (bounded) for its
+ * copies in flight and exits. Every row of the outputs is either complete or
+ * untouched; rows before `row` may be left out too, where they share a block of
+ * threads with later ones.
+ * Errors: those of convrot_block_norm, ERR_ARG (also wait_ns == 0), and
+ *         ERR_UNSUPPORTED for rows that the kernels without waits take
+ *         (unaligned, or longer than 16384 features).
+ */
+int convrot_test_block_norm_timeout(const convrot_block_norm_args* args, int64_t row, uint64_t wait_ns,
+                                    void* stream);
+
+/*
  * convrot_test_unscale_sweep -- a test of the GEMM epilogue's unscaling step,
  * not part of the method. The epilogue divides by a linear's input scale a
  * without a division per element (Markstein's correction step: r = RN(1/a),

@@ -4,7 +4,8 @@
 namespace convrot {
 namespace fp8 {
 
-template int launch_block_norm_as<__nv_bfloat16>(const convrot_block_norm_args& a, cudaStream_t stream);
+template int launch_block_norm_as<__nv_bfloat16>(const convrot_block_norm_args& a, cudaStream_t stream,
+                                                 NormTimeoutTest test);
 template int read_and_clear_norm_error_as<__nv_bfloat16>();
 
 }  // namespace fp8

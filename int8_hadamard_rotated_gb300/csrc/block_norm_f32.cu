@@ -4,7 +4,8 @@
 namespace convrot {
 namespace fp8 {
 
-template int launch_block_norm_as<float>(const convrot_block_norm_args& a, cudaStream_t stream);
+template int launch_block_norm_as<float>(const convrot_block_norm_args& a, cudaStream_t stream,
+                                         NormTimeoutTest test);
 template int read_and_clear_norm_error_as<float>();
 
 }  // namespace fp8

@@ -156,6 +156,14 @@ int norm_checks(const convrot_block_norm_args& a) {
   return CONVROT_OK;
 }
 
+int launch_norm(const convrot_block_norm_args& a, void* stream, NormTimeoutTest test) {
+  if (int st = check_device()) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a.dtype == CONVROT_F32) return launch_block_norm_as<float>(a, s, test);
+  if (a.dtype == CONVROT_F16) return launch_block_norm_as<__half>(a, s, test);
+  return launch_block_norm_as<__nv_bfloat16>(a, s, test);
+}
+
 }  // namespace
 
 namespace convrot {
@@ -176,11 +184,14 @@ int convrot_block_norm(const convrot_block_norm_args* args, void* stream) {
   if (!args) return CONVROT_ERR_ARG;
   if (int st = norm_checks(*args)) return st;
   if (args->M == 0) return CONVROT_OK;
-  if (int st = check_device()) return st;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (args->dtype == CONVROT_F32) return launch_block_norm_as<float>(*args, s);
-  if (args->dtype == CONVROT_F16) return launch_block_norm_as<__half>(*args, s);
-  return launch_block_norm_as<__nv_bfloat16>(*args, s);
+  return launch_norm(*args, stream, NormTimeoutTest());
+}
+
+int convrot_test_block_norm_timeout(const convrot_block_norm_args* args, int64_t row, uint64_t wait_ns, void* stream) {
+  if (!args || wait_ns == 0) return CONVROT_ERR_ARG;
+  if (int st = norm_checks(*args)) return st;
+  if (row < 0 || row >= args->M) return CONVROT_ERR_ARG;
+  return launch_norm(*args, stream, NormTimeoutTest{wait_ns, row});
 }
 
 int fp8_pack_activations(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* Q_x, float* s_x,

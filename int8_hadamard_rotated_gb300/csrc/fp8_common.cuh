@@ -259,10 +259,18 @@ int launch_fp8_pack(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ld
                     cudaStream_t stream);
 int launch_fp8_weight(const void* W, int w_dtype, int64_t N, int64_t K, uint8_t* Q, float* s, cudaStream_t stream);
 
+// Test of the block norms' timeout (convrot_test_block_norm_timeout): a limit
+// for the launch's waits (0: none of this) and the row from which on no row is
+// copied in.
+struct NormTimeoutTest {
+  uint64_t wait_ns = 0;
+  int64_t row = -1;
+};
+
 // block_norm_*.cu, one per type T of H, Y and H_out: arguments already checked;
 // M > 0. The second reads and clears the kernels' error word.
 template <typename T>
-int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream);
+int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream, NormTimeoutTest test);
 template <typename T>
 int read_and_clear_norm_error_as();
 

@@ -212,3 +212,16 @@ def test_row_limit(L):
         assert L.fp8_linear_packed(A[0], A[1], 1, 16, w, 1, ops.F32, None) == ops.ERR_UNSUPPORTED
         assert L.convrot_block_norm(ctypes.byref(norm_args(M=rows, K=8)), None) == ops.ERR_UNSUPPORTED
     assert L.fp8_linear_workspace_size(most, 16) == most * 16 + most * 4
+
+
+def test_norm_timeout_test_checks(L):
+    import ctypes
+    from int8_hadamard_rotated_gb300 import ops
+    f = L.convrot_test_block_norm_timeout
+    a = norm_args()
+    assert f(None, 0, 1000, None) == ops.ERR_ARG
+    assert f(ctypes.byref(a), 0, 0, None) == ops.ERR_ARG             # no limit
+    assert f(ctypes.byref(a), 8, 1000, None) == ops.ERR_ARG          # no such row
+    assert f(ctypes.byref(a), -1, 1000, None) == ops.ERR_ARG
+    a.U = a.H
+    assert f(ctypes.byref(a), 0, 1000, None) == ops.ERR_ALIAS
