@@ -734,6 +734,21 @@ int convrot_test_block_norm_timeout(const convrot_block_norm_args* args, int64_t
                                     void* stream);
 
 /*
+ * fp8_test_linear_timeout -- a test of the fp8 linears' timeout path, not part
+ * of the method: fp8_linear_packed with every bounded device wait of the launch
+ * limited to wait_ns nanoseconds, and the last block of K of its last tile not
+ * loaded. The waits of the blocks of threads that compute that tile give up: the
+ * kernel records CONVROT_ERR_TIMEOUT, waits (bounded) for its copies and
+ * multiplications in flight, releases its tensor memory and exits. The other
+ * tiles are complete.
+ * Errors: those of fp8_linear_packed, ERR_ARG (also wait_ns == 0), and
+ *         ERR_UNSUPPORTED for M <= 8 (that kernel has no waits).
+ */
+int fp8_test_linear_timeout(const uint8_t* Q_x, const float* s_x, int64_t M, int64_t K,
+                            const convrot_fp8_weight* weights, int n_weights, int y_dtype, uint64_t wait_ns,
+                            void* stream);
+
+/*
  * convrot_test_unscale_sweep -- a test of the GEMM epilogue's unscaling step,
  * not part of the method. The epilogue divides by a linear's input scale a
  * without a division per element (Markstein's correction step: r = RN(1/a),

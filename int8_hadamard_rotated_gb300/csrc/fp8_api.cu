@@ -156,6 +156,16 @@ int norm_checks(const convrot_block_norm_args& a) {
   return CONVROT_OK;
 }
 
+int linear_packed(const uint8_t* Q_x, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
+                  int n_weights, int y_dtype, uint64_t test_wait_ns, void* stream) {
+  if (int st = linear_checks(Q_x, s_x, M, K, weights, n_weights, y_dtype, flat(nullptr, 0))) return st;
+  convrot_fp8_weight w[CONVROT_MAX_LINEARS];
+  const int n = with_output(weights, n_weights, w);
+  if (M == 0 || n == 0) return CONVROT_OK;
+  if (int st = check_device()) return st;
+  return launch_fp8_gemm(Q_x, s_x, M, K, w, n, y_dtype, static_cast<cudaStream_t>(stream), test_wait_ns);
+}
+
 int launch_norm(const convrot_block_norm_args& a, void* stream, NormTimeoutTest test) {
   if (int st = check_device()) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -218,12 +228,14 @@ size_t fp8_linear_workspace_size(int64_t M, int64_t K) {
 
 int fp8_linear_packed(const uint8_t* Q_x, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
                       int n_weights, int y_dtype, void* stream) {
-  if (int st = linear_checks(Q_x, s_x, M, K, weights, n_weights, y_dtype, flat(nullptr, 0))) return st;
-  convrot_fp8_weight w[CONVROT_MAX_LINEARS];
-  const int n = with_output(weights, n_weights, w);
-  if (M == 0 || n == 0) return CONVROT_OK;
-  if (int st = check_device()) return st;
-  return launch_fp8_gemm(Q_x, s_x, M, K, w, n, y_dtype, static_cast<cudaStream_t>(stream));
+  return linear_packed(Q_x, s_x, M, K, weights, n_weights, y_dtype, 0, stream);
+}
+
+int fp8_test_linear_timeout(const uint8_t* Q_x, const float* s_x, int64_t M, int64_t K,
+                            const convrot_fp8_weight* weights, int n_weights, int y_dtype, uint64_t wait_ns,
+                            void* stream) {
+  if (wait_ns == 0) return CONVROT_ERR_ARG;
+  return linear_packed(Q_x, s_x, M, K, weights, n_weights, y_dtype, wait_ns, stream);
 }
 
 int fp8_linear(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,

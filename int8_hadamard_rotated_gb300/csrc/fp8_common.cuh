@@ -276,10 +276,12 @@ int read_and_clear_norm_error_as();
 
 // fp8_gemm.cu: every linear has N > 0; M > 0. launch_fp8_packing packs X
 // itself, for few rows; *launched says whether the call is of that kind.
+// test_wait_ns: a limit for the waits of a test of the timeout
+// (fp8_test_linear_timeout), whose last tile is not loaded to its end; else 0.
 int launch_fp8_packing(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,
                        int n_weights, int y_dtype, cudaStream_t stream, bool* launched);
 int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
-                    int n_weights, int y_dtype, cudaStream_t stream);
+                    int n_weights, int y_dtype, cudaStream_t stream, uint64_t test_wait_ns = 0);
 
 }  // namespace fp8
 }  // namespace convrot

@@ -49,6 +49,8 @@ struct GemmParams {
   int split;                      // CTAs (one cluster) that share a tile's K
   bool tma_y;                     // every Y_j can be stored through its tensor map
   bool vec_scales;                // the scales of a row can be read four at a time
+  uint64_t wait_ns;               // limit of every wait
+  int withheld_tile;              // test of the timeout: the last block of K of this tile is not loaded; -1
 };
 
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (format 0, K-major),
@@ -249,14 +251,23 @@ __device__ __noinline__ void store_rows(const uint8_t* sb, TY* y, int64_t ldy, i
     }
 }
 
-// mbar_wait by a warp that is in no hurry: one lane looks, now and then.
-__device__ __forceinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+// mbar_wait by a whole warp, with one outcome for all its lanes: each waits by
+// itself, and one may give up just before the phase completes for another,
+// while what follows (tcgen05 loads, warp barriers) wants the warp together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, limit_ns));
+}
+
+// warp_wait by a warp that is in no hurry: one lane looks, now and then.
+__device__ __forceinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                            uint64_t limit_ns) {
   int ok = 1;
   if ((threadIdx.x & 31) == 0) {
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(bar, parity)) {
       __nanosleep(400);
-      if (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs) {
+      if (*abort_flag || global_timer_ns() - t0 > limit_ns) {
         if (!*abort_flag) record_error(err, CONVROT_ERR_TIMEOUT);
         *abort_flag = 1;
         ok = 0;
@@ -265,7 +276,7 @@ __device__ __forceinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, vola
     }
   }
   ok = __shfl_sync(0xffffffffu, ok, 0);
-  return ok != 0 && mbar_try_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok != 0 && mbar_try_wait(bar, parity));
 }
 
 // Adds f times the accumulator at `ta` (COLS columns of the warp's lanes) to acc.
@@ -390,7 +401,8 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
         const int w_row = c.nt * BN + static_cast<int>(rank) * (BN / 2);
         const int x_row = c.mt * 256 + static_cast<int>(rank) * LANES;
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
+          if (t == p.withheld_tile && kb == p.KB - 1) break;
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, p.wait_ns)) { ok = false; break; }
           uint8_t* sx = smem + stage * G::STAGE_BYTES;
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * G::STAGE_BYTES);
           const uint32_t fb = full_leader + stage * 8u;
@@ -403,15 +415,15 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       // no copy may land after the CTAs exit
       if (rank == 0)
         for (uint32_t s = 0; s < G::STAGES; ++s)
-          if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err);
+          if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err, p.wait_ns);
     }
     if (warp == EPI_WARPS + 1 && lane == 0 && rank == 0) {
       uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
       bool ok = true;
       for (int t = unit; ok && t < p.total_tiles; t += n_units) {
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, err) ||
-              !mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err)) { ok = false; break; }
+          if (!mbar_wait(&full[stage], phase, abort_flag, err, p.wait_ns) ||
+              !mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sx = smem_u32(smem + stage * G::STAGE_BYTES);
           mma_block<2>(tmem_base + buf * BN, sx, sx + G::X_BYTES, G::IDESC);
@@ -423,7 +435,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       }
       // all issued MMAs complete before TMEM is released
       mma_commit_pair(done, 0x1u);
-      mbar_wait(done, 0, nullptr, err);
+      mbar_wait(done, 0, nullptr, err, p.wait_ns);
     }
     if (warp == EPI_WARPS + 2) {
       int i = 0;
@@ -434,14 +446,14 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
         float v[BN / 32];
 #pragma unroll
         for (int k = 0; k < BN / 32; ++k) v[k] = b && n0 + 32 * k + lane < N ? __ldg(b + n0 + 32 * k + lane) : 0.0f;
-        if (!wait_slowly(&iempty[i & 1], ((i >> 1) & 1) ^ 1u, abort_flag, err)) break;
+        if (!wait_slowly(&iempty[i & 1], ((i >> 1) & 1) ^ 1u, abort_flag, err, p.wait_ns)) break;
         if (lane == 0) {
           info[i & 1] = TileInfo{c.lin, c.mt * 256 + static_cast<int>(rank) * LANES, n0, N,
                                  p.s_w[c.lin] + static_cast<int64_t>(n0 / QBLOCK) * p.KB};
           mbar_arrive(&ifull[i & 1]);
         }
         __syncwarp();
-        if (!wait_slowly(bempty, (i & 1) ^ 1u, abort_flag, err)) break;
+        if (!wait_slowly(bempty, (i & 1) ^ 1u, abort_flag, err, p.wait_ns)) break;
 #pragma unroll
         for (int k = 0; k < BN / 32; ++k) sbias[32 * k + lane] = v[k];
         __syncwarp();
@@ -463,7 +475,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
     const float *xs = nullptr, *ws = nullptr;
     float nx[4], nw[4];
     auto start = [&](int i) {  // the CTA's tile i
-      if (!mbar_wait(&ifull[i & 1], (i >> 1) & 1u, abort_flag, err)) return false;
+      if (!warp_wait(&ifull[i & 1], (i >> 1) & 1u, abort_flag, err, p.wait_ns)) return false;
       c = info[i & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[i & 1]);
@@ -488,7 +500,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       float f[4];  // the factors of this block and the next three at most
 #pragma unroll 1
       for (int kb = 0; kb < p.KB; ++kb) {
-        if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) { ok = false; break; }
+        if (!warp_wait(&tfull[buf], bphase, abort_flag, err, p.wait_ns)) { ok = false; break; }
         tc_fence_after();
         if ((kb & 3) == 0) {
 #pragma unroll
@@ -510,7 +522,7 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
       if (!ok) break;
       const int lin = c.lin, N = c.N, y_row = c.row, y_col = c.col;
       if (t + n_units < p.total_tiles) ok = start(seq + 1);
-      if (!mbar_wait(bfull, seq & 1u, abort_flag, err)) break;
+      if (!warp_wait(bfull, seq & 1u, abort_flag, err, p.wait_ns)) break;
       // store: PER features of a row at a time
       constexpr int PER = STORE_ROW / sizeof(TY);
       constexpr int E = 16 / sizeof(TY);  // of them in 16 bytes
@@ -686,7 +698,8 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = &g_fp8_error;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const Tile c = decode(p, static_cast<int>(blockIdx.x) / p.split);
+  const int tile = static_cast<int>(blockIdx.x) / p.split;
+  const Tile c = decode(p, tile);
   const int N = p.N[c.lin];
   const int m0 = c.mt * G::TILE_ROWS, n0 = c.nt * QBLOCK;
   const int kb_begin = p.KB * rank / p.split, kb_end = p.KB * (rank + 1) / p.split;
@@ -728,7 +741,8 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
       const uint64_t pol = l2_policy_evict_normal();
       uint32_t stage = 0, phase = 0, n_issued = 0;
       for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) break;
+        if (tile == p.withheld_tile && rank == p.split - 1 && kb == kb_end - 1) break;
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, p.wait_ns)) break;
         uint8_t* sx = smem + stage * G::STAGE_BYTES;
         mbar_arrive_expect_tx(&full[stage], G::STAGE_BYTES);
         tma_load_2d(sx + G::X_BYTES, &p.tmap_w[c.lin], &full[stage], kb * BK, n0, pol);
@@ -738,7 +752,7 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
       }
       // no copy may land once the stages hold partial sums, or after the exit
       for (uint32_t s = 0; s < G::STAGES; ++s)
-        if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err);
+        if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err, p.wait_ns);
     }
     __syncwarp();
   } else if (warp == 5) {
@@ -746,9 +760,9 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
       uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
       bool ok = true;
       for (int kb0 = kb_begin; ok && kb0 < kb_end; kb0 += G::KG) {
-        if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err)) break;
+        if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err, p.wait_ns)) break;
         for (int kb = kb0; kb < min(kb0 + G::KG, kb_end); ++kb) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, err)) { ok = false; break; }
+          if (!mbar_wait(&full[stage], phase, abort_flag, err, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sx = smem_u32(smem + stage * G::STAGE_BYTES), sw = sx + G::X_BYTES;
           mma_block<1>(tmem_base + buf * G::BUF_COLS + (kb - kb0) * BN, SWAP ? sw : sx, SWAP ? sx : sw, G::IDESC);
@@ -760,7 +774,7 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
         if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
       }
       mma_commit(done);
-      mbar_wait(done, 0, nullptr, err);
+      mbar_wait(done, 0, nullptr, err, p.wait_ns);
     }
     __syncwarp();
   } else {
@@ -807,7 +821,7 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
           load_scales(ws, kb + 4, p.KB, vec, nw);
         }
       }
-      if (!mbar_wait(&tfull[buf], bphase, abort_flag, err)) break;
+      if (!warp_wait(&tfull[buf], bphase, abort_flag, err, p.wait_ns)) break;
       tc_fence_after();
       const uint32_t ta = t_addr + buf * G::BUF_COLS;
       if constexpr (SWAP) drain_scaled<BN, G::KG>(acc, ta, sc + (flip * 4 + i) * BN, kb_end - kb);
@@ -1081,9 +1095,8 @@ constexpr int64_t RASTER_L2_BYTES = 48ll << 20;  // activation codes a raster gr
 // Everything of a launch but the tensor maps of Y: tiles of tile_rows
 // activation rows x tile_cols features, operand boxes x_box and w_box rows.
 int fill(GemmParams& p, const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
-         int tile_rows, int tile_cols, int x_box, int w_box) {
-  if (Qx)
-    if (int st = make_tmap_codes(&p.tmap_x, Qx, M, K, x_box)) return st;
+         int tile_rows, int tile_cols, int x_box, int w_box, uint64_t test_wait_ns) {
+  if (int st = make_tmap_codes(&p.tmap_x, Qx, M, K, x_box)) return st;
   int64_t cols = 0;
   const int64_t KB = n_blocks(K);
   p.vec_scales = KB % 4 == 0 && aligned16(s_x);
@@ -1110,15 +1123,17 @@ int fill(GemmParams& p, const uint8_t* Qx, const float* s_x, int64_t M, int64_t 
   p.n_lin = n;
   p.split = 1;
   p.tma_y = false;
+  p.wait_ns = test_wait_ns ? test_wait_ns : kWaitLimitNs;
+  p.withheld_tile = test_wait_ns ? p.total_tiles - 1 : -1;
   return CONVROT_OK;
 }
 
 template <typename TY>
 int launch_pair(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
-                int y_dtype, cudaStream_t stream) {
+                int y_dtype, uint64_t test_wait_ns, cudaStream_t stream) {
   using G = PairGeom;
   GemmParams p;
-  if (int st = fill(p, Qx, s_x, M, K, w, n, 256, G::BN, LANES, G::BN / 2)) return st;
+  if (int st = fill(p, Qx, s_x, M, K, w, n, 256, G::BN, LANES, G::BN / 2, test_wait_ns)) return st;
   p.tma_y = true;
   for (int j = 0; j < n; ++j) {
     const uint64_t pitch = static_cast<uint64_t>(w[j].ldy) * sizeof(TY);
@@ -1139,10 +1154,10 @@ int launch_pair(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const
 
 template <typename TY, int BN, bool SWAP>
 int launch_solo(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
-                int split, cudaStream_t stream) {
+                int split, uint64_t test_wait_ns, cudaStream_t stream) {
   using G = SoloGeom<BN, SWAP>;
   GemmParams p;
-  if (int st = fill(p, Qx, s_x, M, K, w, n, G::TILE_ROWS, QBLOCK, G::X_ROWS, G::W_ROWS)) return st;
+  if (int st = fill(p, Qx, s_x, M, K, w, n, G::TILE_ROWS, QBLOCK, G::X_ROWS, G::W_ROWS, test_wait_ns)) return st;
   p.split = split;
   static std::mutex mu;
   static uint64_t done = 0;
@@ -1218,34 +1233,38 @@ int launch_packing_stream(const void* X, int64_t M, int64_t K, int64_t ldx, cons
 
 template <typename TY>
 int launch_as(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* w, int n,
-              int y_dtype, cudaStream_t stream) {
+              int y_dtype, uint64_t test_wait_ns, cudaStream_t stream) {
   const int sms = device_sm_count();
   const int64_t KB = n_blocks(K);
   int64_t cols = 0;  // tiles of 128 features
   for (int j = 0; j < n; ++j) cols += n_blocks(w[j].N);
-  if (M <= STREAM_ROWS) return launch_stream_as<uint8_t, TY>(stream_params(Qx, s_x, M, K, K, w, n), 0, stream);
+  if (M <= STREAM_ROWS) {
+    if (test_wait_ns) return CONVROT_ERR_UNSUPPORTED;  // a kernel without waits
+    return launch_stream_as<uint8_t, TY>(stream_params(Qx, s_x, M, K, K, w, n), 0, stream);
+  }
   if (M <= 64) {
     const int split = pick_split(cols, KB, 2 * sms, 4);
-    if (M <= 16) return launch_solo<TY, 16, true>(Qx, s_x, M, K, w, n, split, stream);
-    if (M <= 32) return launch_solo<TY, 32, true>(Qx, s_x, M, K, w, n, split, stream);
-    return launch_solo<TY, 64, true>(Qx, s_x, M, K, w, n, split, stream);
+    if (M <= 16) return launch_solo<TY, 16, true>(Qx, s_x, M, K, w, n, split, test_wait_ns, stream);
+    if (M <= 32) return launch_solo<TY, 32, true>(Qx, s_x, M, K, w, n, split, test_wait_ns, stream);
+    return launch_solo<TY, 64, true>(Qx, s_x, M, K, w, n, split, test_wait_ns, stream);
   }
   const int64_t solo = (M + 127) / 128 * cols;
   // Whole waves of single-CTA tiles while one wave holds them all: measured at
   // 65 to 2304 rows on five weight shapes, within 2 % of the faster of the two
   // kernels everywhere (1024 rows, 3072 x 3072: 26 us here, 16 us in pairs;
   // 700 rows: 13.6 us here, 15.2 us in pairs).
-  if (solo <= sms) return launch_solo<TY, 128, false>(Qx, s_x, M, K, w, n, pick_split(solo, KB, sms, 4), stream);
-  return launch_pair<TY>(Qx, s_x, M, K, w, n, y_dtype, stream);
+  if (solo <= sms)
+    return launch_solo<TY, 128, false>(Qx, s_x, M, K, w, n, pick_split(solo, KB, sms, 4), test_wait_ns, stream);
+  return launch_pair<TY>(Qx, s_x, M, K, w, n, y_dtype, test_wait_ns, stream);
 }
 
 }  // namespace
 
 int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
-                    int n_weights, int y_dtype, cudaStream_t stream) {
-  if (y_dtype == CONVROT_F32) return launch_as<float>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
-  if (y_dtype == CONVROT_F16) return launch_as<__half>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
-  return launch_as<__nv_bfloat16>(Qx, s_x, M, K, weights, n_weights, y_dtype, stream);
+                    int n_weights, int y_dtype, cudaStream_t stream, uint64_t test_wait_ns) {
+  if (y_dtype == CONVROT_F32) return launch_as<float>(Qx, s_x, M, K, weights, n_weights, y_dtype, test_wait_ns, stream);
+  if (y_dtype == CONVROT_F16) return launch_as<__half>(Qx, s_x, M, K, weights, n_weights, y_dtype, test_wait_ns, stream);
+  return launch_as<__nv_bfloat16>(Qx, s_x, M, K, weights, n_weights, y_dtype, test_wait_ns, stream);
 }
 
 int launch_fp8_packing(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const convrot_fp8_weight* weights,

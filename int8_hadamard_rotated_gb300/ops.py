@@ -144,6 +144,7 @@ SIGNATURES = {
     "fp8_linear": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I, _I, _VP, _SZ, _VP]),
     "convrot_device_status": (_I, [_VP]),
     "convrot_test_block_norm_timeout": (_I, [_VP, _I64, ctypes.c_uint64, _VP]),
+    "fp8_test_linear_timeout": (_I, [_VP, _VP, _I64, _I64, _VP, _I, _I, ctypes.c_uint64, _VP]),
     "convrot_test_handover_timeout": (_I, [_VP, _VP, _I64, _I64, ctypes.POINTER(convrot_weight), _I, _VP, _SZ,
                                            ctypes.c_uint64, _VP]),
     "convrot_test_unscale_sweep": (_I, [_VP, _I, _I, _VP, _VP, _VP]),

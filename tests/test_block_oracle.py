@@ -225,3 +225,13 @@ def test_norm_timeout_test_checks(L):
     assert f(ctypes.byref(a), -1, 1000, None) == ops.ERR_ARG
     a.U = a.H
     assert f(ctypes.byref(a), 0, 1000, None) == ops.ERR_ALIAS
+
+
+def test_linear_timeout_test_checks(L):
+    from int8_hadamard_rotated_gb300 import ops
+    W = ops.convrot_fp8_weight
+    f = L.fp8_test_linear_timeout
+    w = (W * 1)(W(A[2], A[3], A[4], 64, A[5], 64))
+    assert f(A[0], A[1], 16, 256, w, 1, ops.BF16, 0, None) == ops.ERR_ARG          # no limit
+    assert f(None, A[1], 16, 256, w, 1, ops.BF16, 1000, None) == ops.ERR_ARG
+    assert f(A[0], A[1], 16, 24, w, 1, ops.BF16, 1000, None) == ops.ERR_ALIGN
