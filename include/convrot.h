@@ -740,7 +740,7 @@ int convrot_test_block_norm_timeout(const convrot_block_norm_args* args, int64_t
  * loaded. The waits of the blocks of threads that compute that tile give up: the
  * kernel records CONVROT_ERR_TIMEOUT, waits (bounded) for its copies and
  * multiplications in flight, releases its tensor memory and exits. The other
- * tiles are complete.
+ * tiles are complete, that one is not written.
  * Errors: those of fp8_linear_packed, ERR_ARG (also wait_ns == 0), and
  *         ERR_UNSUPPORTED for M <= 8 (that kernel has no waits).
  */

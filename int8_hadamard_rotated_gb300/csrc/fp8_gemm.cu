@@ -635,33 +635,67 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
+// What a warp leaves in place of its sums where a wait gave up: a NaN that no
+// arithmetic forms (fp32 operations give 0x7fffffff). The CTA that adds the
+// sums up has them in hand anyway, while a flag of each CTA beside them, read
+// through distributed shared memory, costs 0.2 us.
+constexpr uint32_t GAVE_UP = 0x7fc0dead;
+
+// GAVE_UP for what a warp holds of a partial tile: `rows` rows from `part` on,
+// one feature per lane. Out of line, off the path of every tile.
+__device__ __noinline__ void mark_rows(float* part, int rows, int pitch) {
+  for (int r = 0; r < rows; ++r) part[r * pitch + (threadIdx.x & 31)] = __uint_as_float(GAVE_UP);
+}
+
+// Four outputs of a row from feature n on, each rounded once; `vec`: all of them
+// exist and the address is aligned to them.
+template <typename TY>
+__device__ __forceinline__ void store_outputs(TY* yr, bool vec, int n, int N, const float (&v)[4]) {
+  if (vec) {
+    store4(yr, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (n + k < N) yr[k] = from_f32<TY>(v[k]);
+  }
+}
+
 // Sums the partial tiles that the cluster's CTAs hold at `smem` (ROWS
 // activation rows x 128 features, PITCH floats apart) in rank order, adds the
 // bias bv of the lane's four features (from feature n on) and stores: one row
 // per warp at a time, the rows shared out over the CTAs. Every thread of the
-// cluster comes here after a barrier that follows the last write.
+// cluster comes here after a barrier that follows the last write. Nothing is
+// stored where a wait gave up: the abort flag of a CTA alone, outputs whose sums
+// are GAVE_UP in one of several CTAs (four neighbours are one warp's, so the
+// first of them speaks for all).
 template <typename TY, int ROWS, int PITCH>
 __device__ __forceinline__ void finish_tile(const GemmParams& p, const Tile& c, int m0, int n, int rank,
-                                            const uint8_t* smem, const float (&bv)[4]) {
+                                            const uint8_t* smem, volatile int* abort_flag, const float (&bv)[4]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = min(ROWS, p.M - m0), N = p.N[c.lin];
-  TY* Y = static_cast<TY*>(p.out[c.lin]);
+  TY* Y = static_cast<TY*>(p.out[c.lin]) + static_cast<int64_t>(m0) * p.ldy[c.lin] + n;
   const int64_t ldy = p.ldy[c.lin];
   const bool vec_out = n + 4 <= N && ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * sizeof(TY) - 1)) == 0;
+  if (p.split == 1) {
+    if (*abort_flag) return;
+    for (int r = warp; r < rows; r += SOLO_THREADS / 32) {
+      const float4 s = *reinterpret_cast<const float4*>(smem + (r * PITCH + lane * 4) * 4);
+      store_outputs(Y + r * ldy, vec_out, n, N, {s.x + bv[0], s.y + bv[1], s.z + bv[2], s.w + bv[3]});
+    }
+    return;
+  }
   for (int r = warp * p.split + rank; r < rows; r += (SOLO_THREADS / 32) * p.split) {
     const int off = (r * PITCH + lane * 4) * 4;
     float4 s[MAX_SPLIT];
-    if (p.split > 1) {
 #pragma unroll
-      for (int j = 0; j < MAX_SPLIT; ++j)
-        if (j < p.split) s[j] = ld_cluster_v4(mapa_shared(smem_u32(smem) + off, j));
-    } else {
-      s[0] = *reinterpret_cast<const float4*>(smem + off);
-    }
+    for (int j = 0; j < MAX_SPLIT; ++j)
+      if (j < p.split) s[j] = ld_cluster_v4(mapa_shared(smem_u32(smem) + off, j));
     float v[4] = {s[0].x, s[0].y, s[0].z, s[0].w};
+    bool whole = __float_as_uint(s[0].x) != GAVE_UP;
 #pragma unroll
     for (int j = 1; j < MAX_SPLIT; ++j)
       if (j < p.split) {
+        whole = whole && __float_as_uint(s[j].x) != GAVE_UP;
         v[0] += s[j].x;
         v[1] += s[j].y;
         v[2] += s[j].z;
@@ -669,16 +703,9 @@ __device__ __forceinline__ void finish_tile(const GemmParams& p, const Tile& c, 
       }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] += bv[k];
-    TY* yr = Y + (m0 + r) * ldy + n;
-    if (vec_out) {
-      store4(yr, v);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (n + k < N) yr[k] = from_f32<TY>(v[k]);
-    }
+    if (whole) store_outputs(Y + r * ldy, vec_out, n, N, v);
   }
-  if (p.split > 1) cluster_sync();  // the others' reads of this CTA's partial sums
+  cluster_sync();  // the others' reads of this CTA's partial sums
 }
 
 template <typename TY, int BN, bool SWAP>
@@ -801,6 +828,7 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
     load_scales(ws, kb_begin, p.KB, vec, nw);
     float f[4];
     int flip = 1;
+    bool ok = true;
 #pragma unroll 1
     for (int kb = kb_begin, i = 0; kb < kb_end; kb += G::KG, i = (i + G::KG) & 3) {
       if (i == 0) {  // the factors of four blocks; the next four's scales are on their way meanwhile
@@ -821,7 +849,8 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
           load_scales(ws, kb + 4, p.KB, vec, nw);
         }
       }
-      if (!warp_wait(&tfull[buf], bphase, abort_flag, err, p.wait_ns)) break;
+      ok = warp_wait(&tfull[buf], bphase, abort_flag, err, p.wait_ns);
+      if (!ok) break;
       tc_fence_after();
       const uint32_t ta = t_addr + buf * G::BUF_COLS;
       if constexpr (SWAP) drain_scaled<BN, G::KG>(acc, ta, sc + (flip * 4 + i) * BN, kb_end - kb);
@@ -855,6 +884,12 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
         *reinterpret_cast<float4*>(part + (32 * warp + lane) * G::PITCH + 4 * i) = v;
       }
     }
+    if (!ok) {
+      __syncwarp();
+      if (SWAP) mark_rows(part + 32 * warp, BN, G::PITCH);
+      else
+        for (int i = 0; i < 4; ++i) mark_rows(part + 32 * warp * G::PITCH + 32 * i, 32, G::PITCH);
+    }
   }
   tc_fence_before();
   if (p.split > 1) cluster_sync(); else __syncthreads();
@@ -862,7 +897,7 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
     tc_fence_after();
     tmem_dealloc(tmem_base, G::TMEM_COLS);
   }
-  finish_tile<TY, G::TILE_ROWS, G::PITCH>(p, c, m0, n, rank, smem, bv);
+  finish_tile<TY, G::TILE_ROWS, G::PITCH>(p, c, m0, n, rank, smem, abort_flag, bv);
 }
 
 // ---------------------------------------------------------------------------

@@ -2,7 +2,7 @@
 trapping or hanging anything: a test entry point leaves the last block of K of
 the last tile out and shortens the limit of the waits, so that the waits for
 that block run out. The kernel records CONVROT_ERR_TIMEOUT once and exits, the
-other tiles are complete, and the next call is correct."""
+other tiles are complete, that one is not written, and the next call is correct."""
 import pytest
 import torch
 
@@ -61,3 +61,13 @@ def test_streamed_weights_have_no_waits(ops):
     assert call(ops, Qx, sx, [packed(1, 64, 256, 128)[:2]], [y], 1000) == ops.ERR_UNSUPPORTED
     torch.cuda.synchronize()
     assert (y == 123.0).all()
+
+
+@pytest.mark.parametrize("M,Ns,K,rows,cols", SHAPES)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_unfinished_sums_are_not_stored(ops, M, Ns, K, rows, cols, out):
+    """Also where only one of the blocks of threads that share the tile's K
+    waited in vain."""
+    _, got = run_out(ops, M, Ns, K, out)
+    m0, n0 = (M - 1) // rows * rows, (Ns[-1] - 1) // cols * cols
+    assert (got[-1][m0:, n0:] == 123.0).all()
