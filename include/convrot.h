@@ -614,7 +614,8 @@ int convrot_block_norm(const convrot_block_norm_args* args, void* stream);
  * that suit its elements; 16-byte aligned rows are read fastest.
  * Errors: ERR_ARG, ERR_ALIGN (K % 16, Q_x not 16-byte aligned, X or s_x not
  *         aligned to its elements), ERR_ALIAS, ERR_UNSUPPORTED (more than
- *         2^31 - 1 scales or 2^31 - 2^16 rows), ERR_DEVICE, ERR_CUDA.
+ *         2^31 - 1 scales, 2^31 - 2^16 rows or as many features), ERR_DEVICE,
+ *         ERR_CUDA.
  */
 int fp8_pack_activations(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* Q_x,
                          float* s_x, void* stream);
@@ -650,8 +651,10 @@ size_t fp8_linear_workspace_size(int64_t M, int64_t K);
  *   weights  host array of n_weights descriptors (1 <= n_weights <=
  *            CONVROT_MAX_LINEARS); a linear with N = 0 is skipped.
  * Errors: ERR_ARG, ERR_ALIGN (K % 16, codes not 16-byte aligned, other arrays
- *         not aligned to their elements), ERR_ALIAS, ERR_UNSUPPORTED,
- *         ERR_DEVICE, ERR_CUDA; ERR_TIMEOUT from convrot_device_status.
+ *         not aligned to their elements), ERR_ALIAS, ERR_UNSUPPORTED (more than
+ *         2^31 - 1 scales of the activation, more than 2^31 - 2^16 rows, output
+ *         features or K, or too many tiles of outputs), ERR_DEVICE, ERR_CUDA;
+ *         ERR_TIMEOUT from convrot_device_status.
  */
 int fp8_linear_packed(const uint8_t* Q_x, const float* s_x, int64_t M, int64_t K,
                       const convrot_fp8_weight* weights, int n_weights, int y_dtype, void* stream);

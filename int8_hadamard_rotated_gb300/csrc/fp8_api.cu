@@ -33,6 +33,9 @@ bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p
 // Most rows of a matrix: the kernels count them in 32 bits and may look as far
 // as a tile or a ring of staged rows past the last one.
 constexpr int64_t MAX_ROWS = 0x7fff0000;
+// Longest K, for the same reason: a warp's steps over K go up to 8192 features
+// past the last one.
+constexpr int64_t MAX_LENGTH = MAX_ROWS;
 
 // Whether rows * pitch (elements) stays far inside 63 bits.
 bool sane(int64_t rows, int64_t pitch) { return pitch <= (1ll << 40) && rows <= MAX_ROWS; }
@@ -44,7 +47,7 @@ int pack_checks(const void* X, int dtype, int64_t M, int64_t K, int64_t ldx, con
   if (!X || !Q || !s) return CONVROT_ERR_ARG;
   const int64_t size = static_cast<int64_t>(dtype_size(dtype));
   if (K % 16 != 0 || !aligned16(Q) || !aligned_to(X, size) || !aligned_to(s, 4)) return CONVROT_ERR_ALIGN;
-  if (!sane(M, ldx) || K > 0x7fffffff || n_scales > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+  if (!sane(M, ldx) || K > MAX_LENGTH || n_scales > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
   const Region x{X, M, K * size, ldx * size}, q = flat(Q, M * K), sc = flat(s, n_scales * 4);
   if (meet(x, q) || meet(x, sc) || meet(q, sc)) return CONVROT_ERR_ALIAS;
   return CONVROT_OK;
@@ -68,7 +71,7 @@ int linear_checks(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, con
   if (M == 0) return CONVROT_OK;
   if (!Qx || !s_x) return CONVROT_ERR_ARG;
   if (K % 16 != 0 || !aligned16(Qx) || !aligned_to(s_x, 4)) return CONVROT_ERR_ALIGN;
-  if (M > MAX_ROWS || K > 0x7fffffff || M * n_blocks(K) > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+  if (M > MAX_ROWS || K > MAX_LENGTH || M * n_blocks(K) > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
   const Region qx = flat(Qx, M * K), sx = flat(s_x, M * n_blocks(K) * 4);
   for (int j = 0; j < n; ++j) {
     if (weights[j].N == 0) continue;
@@ -222,7 +225,7 @@ int fp8_prepare_weight(const void* W, int w_dtype, int64_t N, int64_t K, uint8_t
 }
 
 size_t fp8_linear_workspace_size(int64_t M, int64_t K) {
-  if (M < 0 || K <= 0 || M > MAX_ROWS || K > 0x7fffffff) return 0;
+  if (M < 0 || K <= 0 || M > MAX_ROWS || K > MAX_LENGTH) return 0;
   return round256(static_cast<size_t>(M) * K) + round256(static_cast<size_t>(M) * n_blocks(K) * 4);
 }
 
@@ -243,7 +246,7 @@ int fp8_linear(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, co
   if (M < 0 || K <= 0 || !known_dtype(x_dtype) || ldx < K || !weights || n_weights < 1 ||
       n_weights > CONVROT_MAX_LINEARS || !known_dtype(y_dtype))
     return CONVROT_ERR_ARG;
-  if (M > MAX_ROWS || K > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+  if (M > MAX_ROWS || K > MAX_LENGTH) return CONVROT_ERR_UNSUPPORTED;
   const size_t need = fp8_linear_workspace_size(M, K);
   uint8_t* q = static_cast<uint8_t*>(workspace);
   if (M > 0) {

@@ -992,7 +992,8 @@ fp8_stream_kernel(const __grid_constant__ StreamParams p) {
   };
   uint4 a[2][2], next[2][2];
   if (warp < p.KB) load_w(warp, a);
-  const int Kp = p.KB * BK;
+  // PACK (whose K is short): the packed rows' length, and where their scales lie
+  const int Kp = PACK ? p.KB * BK : 0;
   float* ssx = reinterpret_cast<float*>(sx + p.M * Kp);
   if constexpr (PACK) {
     // eight lanes per block of 128 features, 16 features per lane; a warp's

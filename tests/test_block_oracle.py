@@ -235,3 +235,19 @@ def test_linear_timeout_test_checks(L):
     assert f(A[0], A[1], 16, 256, w, 1, ops.BF16, 0, None) == ops.ERR_ARG          # no limit
     assert f(None, A[1], 16, 256, w, 1, ops.BF16, 1000, None) == ops.ERR_ARG
     assert f(A[0], A[1], 16, 24, w, 1, ops.BF16, 1000, None) == ops.ERR_ALIGN
+
+
+def test_length_limit(L):
+    """Places of K are counted in 32 bits, with steps of up to 8192 past the last."""
+    from int8_hadamard_rotated_gb300 import ops
+    W = ops.convrot_fp8_weight
+    A = [0x7f0000000000 + i * 0x10000000000 for i in range(8)]  # apart by more than a row of 2^31 features
+    most = 0x7fff0000
+    w = (W * 1)(W(A[2], A[3], None, 1, A[5], 1))
+    for K in (most + 16, (1 << 31) - 16):
+        assert L.fp8_pack_activations(A[0], ops.F32, 1, K, K, A[1], A[4], None) == ops.ERR_UNSUPPORTED
+        assert L.fp8_prepare_weight(A[0], ops.F32, 1, K, A[1], A[4], None) == ops.ERR_UNSUPPORTED
+        assert L.fp8_linear_workspace_size(1, K) == 0
+        assert L.fp8_linear_packed(A[0], A[1], 1, K, w, 1, ops.F32, None) == ops.ERR_UNSUPPORTED
+        assert L.fp8_linear(A[0], ops.F32, 1, K, K, w, 1, ops.F32, A[6], 1 << 33, None) == ops.ERR_UNSUPPORTED
+    assert L.fp8_linear_workspace_size(1, most) == most + (most // 128 * 4)
