@@ -856,6 +856,14 @@ def fp8_linear(X: torch.Tensor, qs: Sequence[torch.Tensor], scales: Sequence[tor
     return Ys
 
 
+def _n_samples(t: torch.Tensor, name: str, M: int) -> int:
+    """The samples that a matrix of gates, scales or shifts is for: its rows.
+    None for some rows of H would have no address, which says "absent"."""
+    if t.dim() != 2 or (M and not t.shape[0]):
+        raise ValueError(f"{name} must be a matrix with a row per sample, got {tuple(t.shape)}")
+    return t.shape[0]
+
+
 def _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_weight, post_bias, gate, pre_norm,
                 pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, U, u_dtype, ldu, Q, s,
                 device, handle):
@@ -868,13 +876,13 @@ def _block_norm(H, Y, residual_scale, block_scale, post_norm, post_eps, post_wei
     vec = (K,)
     samples = ld_gate = ld_mod = 0
     if gate is not None:
-        samples = gate.shape[0]
+        samples = _n_samples(gate, "gate", M)
         ld_gate = _rows(gate, "gate", device, (samples, K), _F32)
     if scale is not None:
-        samples = samples or scale.shape[0]
+        samples = samples or _n_samples(scale, "scale", M)
         ld_mod = _rows(scale, "scale", device, (samples, K), _F32)
     if shift is not None:
-        samples = samples or shift.shape[0]
+        samples = samples or _n_samples(shift, "shift", M)
         ld = _rows(shift, "shift", device, (samples, K), _F32)
         if scale is not None and ld != ld_mod:
             raise ValueError("scale and shift must have the same distance between rows")

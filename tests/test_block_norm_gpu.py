@@ -322,3 +322,19 @@ def test_u_feeds_the_int8_linears(ops, M):
         ref = U.double() @ W.double().t()
         assert float((y.double() - ref).norm() / ref.norm()) < 2 * 6 / (254 * 3 ** 0.5)
     assert ops.convrot_device_status() == ops.OK
+
+
+def test_gates_scales_and_shifts_of_no_sample(ops):
+    """Refused for rows that need one, not taken for absent; and of no rows fine."""
+    x, y = torch.randn(8, 64, device="cuda"), torch.randn(8, 64, device="cuda")
+    none, two = torch.empty(0, 64, device="cuda"), torch.randn(2, 64, device="cuda")
+    for bad in (lambda: ops.convrot_block_norm(x, y, gate=none), lambda: ops.convrot_block_norm(x, scale=none),
+                lambda: ops.convrot_block_norm(x, shift=none), lambda: ops.convrot_block_norm_fp8(x, scale=none),
+                lambda: ops.convrot_block_norm(x, y, gate=none, scale=two, rows_per_sample=4),
+                lambda: ops.convrot_block_norm(x, scale=two, shift=none, rows_per_sample=4),
+                lambda: ops.convrot_block_norm(x, scale=two[0]), lambda: ops.convrot_block_norm(x, scale=two[0, 0])):
+        with pytest.raises(ValueError):
+            bad()
+    H, U = ops.convrot_block_norm(x[:0], y[:0], gate=none, scale=none, shift=none)
+    assert H.shape == U.shape == (0, 64)
+    assert ops.convrot_device_status() == ops.OK
