@@ -3,7 +3,7 @@
 // Each entry point checks its arguments on the host (sizes, group rule,
 // alignment, int32 overflow bound, aliasing, workspace size), then enqueues
 // the kernels on the caller's stream. No entry point allocates device memory.
-#include "common.cuh"
+#include "fp8_common.cuh"
 
 #include <cstring>
 #include <mutex>
@@ -55,13 +55,33 @@ bool device_is_sm103() {
   return d && d->is_sm103 == 1;
 }
 
-int read_and_clear_device_error(cudaStream_t stream);  // gemm.cu: syncs, then the GEMM's word
-int read_and_clear_w4_error();                         // gemm_w4.cu: the S8 x S4 GEMM's word
-int read_and_clear_pack_error();                       // pack.cu: the pack kernels' word
-namespace fp8 {
-int read_and_clear_fp8_error();                        // fp8_gemm.cu: the block-scaled GEMM's word
-int read_and_clear_norm_error();                       // fp8_api.cu: the block norms' words
-}  // namespace fp8
+// The kernels' sticky error words, each in its translation unit.
+cudaError_t gemm_error_word(int** p);  // gemm.cu: the GEMM
+cudaError_t w4_error_word(int** p);    // gemm_w4.cu: the S8 x S4 GEMM
+cudaError_t pack_error_word(int** p);  // pack.cu: the packs
+
+namespace {
+
+constexpr int N_WORDS = 7;
+struct ErrorWords {
+  int* word[N_WORDS];
+};
+__device__ int g_status;
+
+// The first word that is set; all are cleared. One launch and one copy for all
+// of them: a copy from the device for each takes 67 us a call.
+__global__ void collect_errors_kernel(ErrorWords e) {
+  int v[N_WORDS], first = 0;
+#pragma unroll
+  for (int i = 0; i < N_WORDS; ++i) v[i] = atomicExch(e.word[i], 0);
+#pragma unroll
+  for (int i = N_WORDS - 1; i >= 0; --i) first = v[i] ? v[i] : first;
+  g_status = first;
+}
+
+std::mutex g_status_mu;
+
+}  // namespace
 
 }  // namespace convrot
 
@@ -561,14 +581,20 @@ int convrot_weight_chunks(const int8_t* Q_w, int64_t N, int64_t K, int32_t* kchu
 
 int convrot_device_status(void* stream) {
   if (int st = check_device()) return st;
-  const int gemm_st = read_and_clear_device_error(static_cast<cudaStream_t>(stream));
-  const int w4_st = read_and_clear_w4_error();
-  const int pack_st = read_and_clear_pack_error();
-  const int fp8_st = fp8::read_and_clear_fp8_error();
-  const int norm_st = fp8::read_and_clear_norm_error();
-  for (int st : {gemm_st, w4_st, pack_st, fp8_st})
-    if (st != CONVROT_OK) return st;
-  return norm_st;
+  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return set_cuda_error(e);
+  ErrorWords words;
+  cudaError_t (*const address[N_WORDS])(int**) = {
+      gemm_error_word, w4_error_word, pack_error_word, fp8::linear_error_word,
+      fp8::norm_error_word<float>, fp8::norm_error_word<__half>, fp8::norm_error_word<__nv_bfloat16>};
+  for (int i = 0; i < N_WORDS; ++i)
+    if ((e = address[i](&words.word[i])) != cudaSuccess) return set_cuda_error(e);
+  std::lock_guard<std::mutex> lock(g_status_mu);
+  collect_errors_kernel<<<1, 1>>>(words);
+  if (int st = check_launch()) return st;
+  int status = 0;
+  e = cudaMemcpyFromSymbol(&status, g_status, sizeof(int));  // after the kernel, on the same stream
+  return e == cudaSuccess ? status : set_cuda_error(e);
 }
 
 size_t int8_gemm_s32_w4_workspace_size(int64_t M, int64_t K) {

@@ -1180,16 +1180,8 @@ int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream, 
 }
 
 template <typename T>
-int read_and_clear_norm_error_as() {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_error, sizeof(int));
-  if (e != cudaSuccess) return set_cuda_error(e);
-  if (v != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_norm_error, &zero, sizeof(int));
-    if (e != cudaSuccess) return set_cuda_error(e);
-  }
-  return v;
+cudaError_t norm_error_word(int** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_norm_error);
 }
 
 }  // namespace fp8

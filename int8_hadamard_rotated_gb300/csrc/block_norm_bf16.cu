@@ -6,7 +6,7 @@ namespace fp8 {
 
 template int launch_block_norm_as<__nv_bfloat16>(const convrot_block_norm_args& a, cudaStream_t stream,
                                                  NormTimeoutTest test);
-template int read_and_clear_norm_error_as<__nv_bfloat16>();
+template cudaError_t norm_error_word<__nv_bfloat16>(int** p);
 
 }  // namespace fp8
 }  // namespace convrot

@@ -6,7 +6,7 @@ namespace fp8 {
 
 template int launch_block_norm_as<__half>(const convrot_block_norm_args& a, cudaStream_t stream,
                                           NormTimeoutTest test);
-template int read_and_clear_norm_error_as<__half>();
+template cudaError_t norm_error_word<__half>(int** p);
 
 }  // namespace fp8
 }  // namespace convrot

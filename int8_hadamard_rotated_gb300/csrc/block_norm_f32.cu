@@ -6,7 +6,7 @@ namespace fp8 {
 
 template int launch_block_norm_as<float>(const convrot_block_norm_args& a, cudaStream_t stream,
                                          NormTimeoutTest test);
-template int read_and_clear_norm_error_as<float>();
+template cudaError_t norm_error_word<float>(int** p);
 
 }  // namespace fp8
 }  // namespace convrot

@@ -179,18 +179,6 @@ int launch_norm(const convrot_block_norm_args& a, void* stream, NormTimeoutTest 
 
 }  // namespace
 
-namespace convrot {
-namespace fp8 {
-
-int read_and_clear_norm_error() {
-  const int st[] = {read_and_clear_norm_error_as<float>(), read_and_clear_norm_error_as<__half>(),
-                    read_and_clear_norm_error_as<__nv_bfloat16>()};
-  return st[0] ? st[0] : st[1] ? st[1] : st[2];
-}
-
-}  // namespace fp8
-}  // namespace convrot
-
 extern "C" {
 
 int convrot_block_norm(const convrot_block_norm_args* args, void* stream) {

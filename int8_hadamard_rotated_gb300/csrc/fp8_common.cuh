@@ -268,11 +268,11 @@ struct NormTimeoutTest {
 };
 
 // block_norm_*.cu, one per type T of H, Y and H_out: arguments already checked;
-// M > 0. The second reads and clears the kernels' error word.
+// M > 0. The second gives the address of the kernels' error word.
 template <typename T>
 int launch_block_norm_as(const convrot_block_norm_args& a, cudaStream_t stream, NormTimeoutTest test);
 template <typename T>
-int read_and_clear_norm_error_as();
+cudaError_t norm_error_word(int** p);
 
 // fp8_gemm.cu: every linear has N > 0; M > 0. launch_fp8_packing packs X
 // itself, for few rows; *launched says whether the call is of that kind.
@@ -282,6 +282,8 @@ int launch_fp8_packing(const void* X, int x_dtype, int64_t M, int64_t K, int64_t
                        int n_weights, int y_dtype, cudaStream_t stream, bool* launched);
 int launch_fp8_gemm(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const convrot_fp8_weight* weights,
                     int n_weights, int y_dtype, cudaStream_t stream, uint64_t test_wait_ns = 0);
+
+cudaError_t linear_error_word(int** p);  // the address of their error word
 
 }  // namespace fp8
 }  // namespace convrot

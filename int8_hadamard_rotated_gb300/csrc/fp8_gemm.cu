@@ -1312,17 +1312,7 @@ int launch_fp8_packing(const void* X, int x_dtype, int64_t M, int64_t K, int64_t
   return launch_packing_stream<__nv_bfloat16>(X, M, K, ldx, weights, n_weights, y_dtype, stream);
 }
 
-int read_and_clear_fp8_error() {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_fp8_error, sizeof(int));
-  if (e != cudaSuccess) return set_cuda_error(e);
-  if (v != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_fp8_error, &zero, sizeof(int));
-    if (e != cudaSuccess) return set_cuda_error(e);
-  }
-  return v;
-}
+cudaError_t linear_error_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_fp8_error); }
 
 }  // namespace fp8
 }  // namespace convrot

@@ -1033,18 +1033,6 @@ int launch_unscale_sweep(const float* divisors, int n_divisors, int y_exp, unsig
   return check_launch();
 }
 
-int read_and_clear_device_error(cudaStream_t stream) {
-  cudaError_t e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  int v = 0;
-  e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int));
-  if (e != cudaSuccess) return set_cuda_error(e);
-  if (v != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
-    if (e != cudaSuccess) return set_cuda_error(e);
-  }
-  return v;
-}
+cudaError_t gemm_error_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_device_error); }
 
 }  // namespace convrot

@@ -700,16 +700,6 @@ int launch_gemm_w4(const __half* x16, const float* s_x, int64_t M, int64_t K, co
   return launch_w4<256, false>(x16, s_x, M, K, lins, n_lin, raw_s32, pairs, stream, sync);
 }
 
-int read_and_clear_w4_error() {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_w4_error, sizeof(int));
-  if (e != cudaSuccess) return set_cuda_error(e);
-  if (v != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_w4_error, &zero, sizeof(int));
-    if (e != cudaSuccess) return set_cuda_error(e);
-  }
-  return v;
-}
+cudaError_t w4_error_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_w4_error); }
 
 }  // namespace convrot

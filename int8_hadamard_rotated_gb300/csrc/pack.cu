@@ -1238,17 +1238,7 @@ int launch_pack_modulated(const float* X, int64_t M, int64_t K, int G, const flo
              : dispatch_group<float, kPackF16, kProModulate>(X, M, k, G, 1.0f, out_codes, scales, stream, mod);
 }
 
-int read_and_clear_pack_error() {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_pack_error, sizeof(int));
-  if (e != cudaSuccess) return set_cuda_error(e);
-  if (v != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_pack_error, &zero, sizeof(int));
-    if (e != cudaSuccess) return set_cuda_error(e);
-  }
-  return v;
-}
+cudaError_t pack_error_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_pack_error); }
 
 int launch_widen(const int8_t* src, __half* dst, int64_t n, cudaStream_t stream) {
   if (n == 0) return CONVROT_OK;

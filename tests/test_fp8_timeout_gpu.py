@@ -71,3 +71,17 @@ def test_unfinished_sums_are_not_stored(ops, M, Ns, K, rows, cols, out):
     _, got = run_out(ops, M, Ns, K, out)
     m0, n0 = (M - 1) // rows * rows, (Ns[-1] - 1) // cols * cols
     assert (got[-1][m0:, n0:] == 123.0).all()
+
+
+def test_one_status_call_clears_every_word(ops):
+    """A linear's timeout and samples out of range of two types of block norm:
+    the timeout is reported, and all are cleared."""
+    Qx, sx, _, _ = packed(2, 16, 256)
+    y = torch.empty(16, 128, device="cuda")
+    for _ in range(2):
+        for dtype in (torch.bfloat16, torch.float32):
+            ops.convrot_block_norm(torch.ones(2, 64, dtype=dtype, device="cuda"), scale=torch.ones(2, 64, device="cuda"),
+                                   row_sample=torch.tensor([0, 5], dtype=torch.int32, device="cuda"))
+        assert call(ops, Qx, sx, [packed(1, 128, 256, 128)[:2]], [y], 100_000) == ops.OK
+        assert ops.convrot_device_status() == ops.ERR_TIMEOUT
+        assert ops.convrot_device_status() == ops.OK
