@@ -921,6 +921,7 @@ block_norm_scattered_kernel(const __grid_constant__ NormParams p) {
 // with gate and modulation bf16 [512, 32768] 251 us, [512, 24001] 102 us; four
 // loads of each array together need 59 registers, which leaves one CTA per SM:
 // 236 and 173 us.
+constexpr int ANY_THREADS = 1024;
 __device__ float block_sum(float v, float* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
   v = warp_sum(v);
@@ -947,7 +948,7 @@ __device__ Stats row_stats_any(const float* x, int kind, float eps, int K, float
 }
 
 template <typename T, typename TU, bool FP8>
-__global__ void __launch_bounds__(1024, 1)
+__global__ void __launch_bounds__(ANY_THREADS, 1)
 block_norm_any_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ float x[];
   __shared__ float red[32];
@@ -1118,9 +1119,8 @@ int launch_typed(NormParams& p, bool vec, bool test, cudaStream_t stream) {
   static uint64_t done = 0;
   auto kernel = block_norm_any_kernel<T, TU, FP8>;
   if (int st = allow_smem(kernel, done, mu)) return st;
-  const int threads = std::min(1024, (std::max(32, p.K / 4) + 31) / 32 * 32);
-  const unsigned grid = std::min(p.M, device_sm_count() * std::max(1, 2048 / threads));
-  return launch_rows(kernel, p, grid, threads, static_cast<size_t>(p.K) * 4, stream);
+  const unsigned grid = std::min(p.M, 2 * device_sm_count());
+  return launch_rows(kernel, p, grid, ANY_THREADS, static_cast<size_t>(p.K) * 4, stream);
 }
 
 }  // namespace

@@ -137,10 +137,19 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 // The codes of four values that are quotients already.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) { return e4m3x2(a, b) | (e4m3x2(c, d) << 16); }
 
-// RN(x / s) without a division: Markstein's correction step ("IA-64 and
-// Elementary Functions", 2000). With r = RN(1 / s) and q0 = RN(x r), which
-// lies within one ulp of x / s, the remainder x - q0 s is exact in one FMA and
-// RN(q0 + (x - q0 s) r) = RN(x / s), as long as everything stays normal.
+// RN(x / s) without a division: a correction step after Markstein ("IA-64 and
+// Elementary Functions", 2000). With r = RN(1 / s) and q0 = RN(x r), the result
+// is RN(q0 + RN(x - q0 s) r), as long as everything stays normal.
+//
+// Markstein's proof asks for a q0 within one ulp of x / s, whose remainder is
+// exact; here r's rounding and the product's put q0 up to 1.5 ulp away. So the
+// step is not proven to give RN(x / s) for every x, and the codes do not need
+// it: the result is within an ulp, which another code can come of only next to
+// a rounding border of e4m3. There it was compared with the IEEE quotient on
+// the CPU, for every significand of s, every significand of a border (16) and
+// the eleven x around their product: 1.48e9 quotients, all equal (q0 up to
+// 1.467 ulp off). Powers of two change nothing in the normal range. For the
+// scale, s = 448, every significand of x was compared: all equal.
 
 // The scale of a block, RN(amax / 448).
 static __device__ __noinline__ float e4m3_scale_divided(float amax) { return __fdiv_rn(amax, kE4M3Max); }
@@ -234,7 +243,9 @@ inline bool known_dtype(int dtype) { return dtype == CONVROT_F32 || dtype == CON
 inline int64_t n_blocks(int64_t n) { return (n + QBLOCK - 1) / QBLOCK; }
 
 // A launch that may set itself up while the kernel before it in the stream
-// ends (every kernel here waits for that one before it touches global memory).
+// ends. Every kernel here waits for that one before it reads or writes global
+// memory; the one that streams weights (fp8_gemm.cu) asks for them in L2 before,
+// which only moves them: what the kernel before still writes is seen.
 struct Launch {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};

@@ -251,3 +251,62 @@ def test_length_limit(L):
         assert L.fp8_linear_packed(A[0], A[1], 1, K, w, 1, ops.F32, None) == ops.ERR_UNSUPPORTED
         assert L.fp8_linear(A[0], ops.F32, 1, K, K, w, 1, ops.F32, A[6], 1 << 33, None) == ops.ERR_UNSUPPORTED
     assert L.fp8_linear_workspace_size(1, most) == most + (most // 128 * 4)
+
+
+def fma32(a, b, c):
+    """fp32 a b + c, rounded once: the product is exact in 64 bits, the sum is
+    rounded to odd there, and then to fp32."""
+    p, c = a.astype(np.float64) * b.astype(np.float64), c.astype(np.float64)
+    s = p + c
+    t = s - p
+    err = (p - (s - t)) + (c - t)
+    inexact_even = (err != 0) & (s.view(np.int64) & 1 == 0)
+    toward = np.where((err > 0) == (s > 0), 1, -1)
+    return (s.view(np.int64) + np.where(inexact_even, toward, 0)).view(np.float64).astype(np.float32)
+
+
+def corrected_quotient(x, s):
+    """The kernels' division: r = RN(1 / s), q0 = RN(x r), RN(q0 + RN(x - q0 s) r)."""
+    r = np.float32(1) / s
+    q0 = x * r
+    return fma32(fma32(-q0, s, x), r, q0)
+
+
+def test_fma32():
+    from fractions import Fraction
+    rng = np.random.default_rng(0)
+    a, b = (rng.integers(1 << 23, 1 << 24, 300).astype(np.float32) for _ in range(2))
+    c = (-(a * b)).astype(np.float32) * np.float32(1) + rng.integers(-4, 4, 300).astype(np.float32)
+    for x, y, z, f in zip(a, b, c, fma32(a, b, c)):
+        exact = Fraction(float(x)) * Fraction(float(y)) + Fraction(float(z))
+        near = [f, np.nextafter(f, np.float32(np.inf)), np.nextafter(f, np.float32(-np.inf))]
+        assert min(abs(Fraction(float(v)) - exact) for v in near) == abs(Fraction(float(f)) - exact)
+
+
+def test_corrected_scale_is_the_ieee_quotient():
+    """amax / 448 for every significand of amax."""
+    for k in range(4):
+        x = (np.arange(k << 21, (k + 1) << 21, dtype=np.int32) + np.float32(1).view(np.int32)).view(np.float32)
+        s = np.full_like(x, 448)
+        np.testing.assert_array_equal(corrected_quotient(x, s), x / s)
+
+
+def test_corrected_quotients_at_rounding_borders():
+    """x next to every rounding border of e4m3 times s: the last 2^14
+    significands of s, where q0 is furthest from the quotient, and 2^14 others."""
+    v = bo.e4m3_values()[:127]
+    borders = np.unique(np.frexp((v[1:] + v[:-1]) / 2)[0] * 2)
+    assert len(borders) == 16
+    m = np.concatenate([np.arange((1 << 23) - (1 << 14), 1 << 23),
+                        np.random.default_rng(0).integers(0, 1 << 23, 1 << 14)]).astype(np.int32)
+    s = (m + np.float32(1).view(np.int32)).view(np.float32)
+    furthest = 0.0
+    for b in borders:
+        x0 = (b * s.astype(np.float64)).astype(np.float32)
+        for k in range(-5, 6):
+            x = (x0.view(np.int32) + np.int32(k)).view(np.float32)
+            q = x / s
+            np.testing.assert_array_equal(corrected_quotient(x, s), q)
+            off = np.abs((x * (np.float32(1) / s)).astype(np.float64) - x.astype(np.float64) / s) / np.spacing(q)
+            furthest = max(furthest, float(off.max()))
+    assert 1.0 < furthest < 1.5        # beyond what a proof by an exact remainder covers
