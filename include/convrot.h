@@ -580,6 +580,8 @@ typedef struct convrot_block_norm_args {
  * Rows whose arrays all start on 16-byte boundaries, with ld a multiple of 16
  * bytes and K a multiple of 8, take the fast path; any others are accepted.
  * The sums of a row are taken in a fixed order: results repeat bit for bit.
+ * They are fp32, so the squares of an RMS norm or LayerNorm overflow, and u is
+ * 0 or NaN, for magnitudes (of what is summed, from the mean) beyond 2^63 or so.
  * A row_sample outside [0, n_samples) is treated as gate 0 without modulation
  * and reported by convrot_device_status as CONVROT_ERR_ARG.
  * Errors: ERR_ARG (also a sample count that rows_per_sample overruns),

@@ -546,11 +546,11 @@ constexpr int WARPS = 8;  // per CTA of the grouped kernel
 // current sample (norm weights, gate and modulation folded, only those that
 // are not 0 or 1) lie in shared memory and are formed again when it changes.
 //
-// bf16 [4608, 3072] with gate, LayerNorm and modulation, two samples: 24.6 us
-// = 4.61 TB/s (a copy with as many bytes 5.7 TB/s); RMS norms on both sides to
-// codes, seven samples: 34.1 us. What is left is the chain from a row's arrival
+// bf16 [4608, 3072] with gate, LayerNorm and modulation, two samples: 24.8 us
+// = 4.57 TB/s (a copy with as many bytes 5.7 TB/s); RMS norms on both sides to
+// codes, seven samples: 33.9 us. What is left is the chain from a row's arrival
 // over two sums to its last store with 16 warps per SM to cover it (registers
-// and the coefficients take the SM), issuing in 40 % of the cycles.
+// and the coefficients take the SM), issuing in 38 % of the cycles.
 // (One thread block per row with one unit per thread and its coefficients in
 // registers: 49 us, 53 instructions per feature, most of them per row and
 // thread; coefficients read through L1 for every row: 60 us; three CTAs per SM
@@ -681,7 +681,7 @@ block_norm_kernel(const __grid_constant__ NormParams p) {
 // what is added (a bias of the first norm; bias and shift of the second) in
 // shared memory where that fits (p.coef_smem) and else read again for every
 // row. Eight warps with up to six units per thread: fp32 [4608, 12288] between
-// two weighted RMS norms with a gate 161 us = 5.65 TB/s, with 24 warps of two
+// two weighted RMS norms with a gate 161 us = 5.63 TB/s, with 24 warps of two
 // units 214 us.
 template <typename T, typename TU, int V, bool FP8, int NW>
 __global__ void __launch_bounds__(NW * 32, 1)
@@ -1066,10 +1066,12 @@ int launch_wide(NormParams& p, cudaStream_t stream) {
 // Warps per row of the grouped kernel: enough that a lane has at most four
 // units (two CTAs per SM; six with all eight warps) and that two rows of every
 // group fit beside the coefficients, and more while there are fewer rows than
-// groups on the GPU. 0: nothing fits. Measured before the sums went across
-// lanes: bf16 [4608, 3072] to codes 40 us with four warps and three units, 52
-// us with two warps and six; [8192, 1280] 25 us with two warps and three units,
-// 26 with one and five, 29 with four.
+// groups on the GPU. 0: nothing fits. More warps per row cost more than the
+// warps per SM that two units allow (24 instead of 16) give: bf16 with gate,
+// LayerNorm and modulation, [4608, 3072] 24.7 us with four warps and three
+// units, 33.1 us with eight and two (to codes 28.9 and 39.6 us); [4608, 2048]
+// 17.2 us with two and four, 21.1 us with four and two; [8192, 1280] 20.9 us
+// with two and three, 21.2 us with one and five, 27.1 us with four and two.
 int pick_warps(const NormParams& p) {
   const int chunks = (p.K + 255) / 256;
   const int64_t sms = device_sm_count();

@@ -192,9 +192,10 @@ __device__ __forceinline__ Tile decode(const GemmParams& p, int t) {
 // tensor-map stores where the rows of Y are 16-byte aligned, else by
 // coalesced element stores.
 //
-// [4608, 3072] through three [3072, 3072] weights to bf16: 113 us = 2.3
-// PFLOP/s; [4608, 12288] through [3072, 12288] to fp32: 144 us = 2.4 PFLOP/s
-// (154 us under sustained load). Two chains bound it about equally. The MMAs
+// [4608, 3072] through three [3072, 3072] weights to bf16: 112 us = 2.3
+// PFLOP/s; [4608, 12288] through [3072, 12288] to fp32: 138 us = 2.5 PFLOP/s
+// (152 us under sustained load). Two chains bound it about equally. In copies
+// of the kernel with parts left out, taken when the whole took 113 us, the MMAs
 // with no loads and no promotion take 82 us on the first shape; with the loads
 // 116 us, since a pair's operands (64 KB per block of K, all from L2) arrive at
 // some 12 TB/s over the GPU; with the promotion and no loads 117 us: reading
@@ -590,8 +591,11 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
 // workspace, no atomics, the same order every time.
 // Bound by the chain of a CTA's blocks, about 0.3 us each from the last load to
 // the promoted sums, against the time its weights take from HBM: 24 rows
-// through [3072, 12288] take 12.9 us = 2.98 TB/s, 331 rows through [1283,
-// 1280] 8.8 us with their pack. (Asking for the weights in L2 before the wait
+// through [3072, 12288] take 12.9 us = 2.98 TB/s. With few blocks it is the
+// fixed costs that count (setting up tensor memory, the cluster's barriers and
+// sums): 331 rows through [1283, 1280], 33 tiles of ten blocks of K, take 6.3 us
+// with K split in four, 7.4 us in two, 7.5 us unsplit, and 8.6 us with their
+// pack, which alone takes 1.8 us. (Asking for the weights in L2 before the wait
 // for the kernel ahead: 7.1 us instead of 6.6 us for 16 rows through three
 // 3072 x 3072 linears.)
 // Six warps: 0-3 promote (32 lanes each), 4 loads, 5 issues MMAs.
@@ -612,8 +616,10 @@ struct SoloGeom {
   // 6.7 us against 7.7 us with one CTA per SM and K split in two).
   static constexpr int STAGES = ((SWAP ? 96 : 200) * 1024) / STAGE_BYTES;
   // With few columns, KG blocks of K, each in an accumulator of its own, are
-  // handed over together: a hand-over costs the epilogue about 0.3 us whatever
-  // its size (24 CTAs on [1, 12288] x [3072, 12288]: 38 us one block at a time).
+  // handed over together, which saves hand-overs: 12 rows through [3072, 12288]
+  // 11.6 us, one block at a time 12.2 us. At more columns or shorter K it makes
+  // little difference (24 rows 12.9 and 12.6 us, 16 rows through three 3072 x
+  // 3072 linears 6.7 us both ways).
   static constexpr int KG = SWAP ? 64 / BN : 1;
   static constexpr int BUF_COLS = KG * BN;
   static constexpr int BUFS = SWAP ? 4 : 2;
@@ -912,10 +918,13 @@ fp8_solo_kernel(const __grid_constant__ GemmParams p) {
 // as long as both operands agree, so a lane takes 16 consecutive codes of a
 // row and spends them on two instructions. The block's fp32 sums are scaled
 // into the warp's accumulators, and the warps' sums meet in shared memory, in
-// warp order. Several CTAs per SM keep enough bytes in flight, and there is no
-// tensor memory, barrier or cluster to set up. One token through three 3072 x
-// 3072 linears, packed here too: 6.7 us = 4.2 TB/s against 8.8 us on tcgen05 with K split over clusters;
-// from 9 rows on that one is faster (16 rows: 9.4 against 6.7 us).
+// warp order. (The instruction's own sums are fp32: outputs of 1 to 8 rows at
+// K = 3072 and 12288 are 1e-7 of the 64-bit result away, root mean square.)
+// Several CTAs per SM keep enough bytes in flight, and there is no tensor
+// memory, barrier or cluster to set up. One token through three 3072 x 3072
+// linears, packed here too: 6.7 us = 4.2 TB/s against 8.8 us on tcgen05 with K
+// split over clusters; from 9 rows on that one is faster (16 rows: 9.4 against
+// 6.7 us).
 //
 // TX: the activations come as codes and scales (uint8_t), or as they are, up
 // to PACK_ROWS rows; then every CTA packs them all into shared memory (the
@@ -1288,7 +1297,7 @@ int launch_as(const uint8_t* Qx, const float* s_x, int64_t M, int64_t K, const c
   // Whole waves of single-CTA tiles while one wave holds them all: measured at
   // 65 to 2304 rows on five weight shapes, within 2 % of the faster of the two
   // kernels everywhere (1024 rows, 3072 x 3072: 26 us here, 16 us in pairs;
-  // 700 rows: 13.6 us here, 15.2 us in pairs).
+  // 700 rows: 12.6 us here, 15.2 us in pairs).
   if (solo <= sms)
     return launch_solo<TY, 128, false>(Qx, s_x, M, K, w, n, pick_split(solo, KB, sms, 4), test_wait_ns, stream);
   return launch_pair<TY>(Qx, s_x, M, K, w, n, y_dtype, test_wait_ns, stream);

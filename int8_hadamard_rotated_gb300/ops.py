@@ -919,7 +919,8 @@ def convrot_block_norm(H: torch.Tensor, Y: Optional[torch.Tensor] = None, *, res
     gate, scale, shift float32 [samples, K], the row m taking the sample
     row_sample[m] (int32) or m // rows_per_sample. Returns (h', u): H_out and U
     where given (H_out may be H), new tensors where not (u of u_dtype, H's own
-    by default), None for what want_h or want_u leaves out."""
+    by default), None for what want_h or want_u leaves out. The INT8 linears
+    take a u of float16 or float32, the fp8 linears any."""
     device, handle = _start(H, stream)
     shape = _matrix(H, "H")
     if H_out is None and want_h:
