@@ -413,7 +413,12 @@ fp8_pair_kernel(const __grid_constant__ GemmParams p) {
           if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      // no copy may land after the CTAs exit
+      // No copy may land after the CTAs exit. The even CTA's barriers count both
+      // CTAs' bytes; where the odd one's wait gave up, it may have issued copies
+      // that the even one does not wait for, and gives them 1 ms, a thousand
+      // times what a copy takes.
+      if (rank == 1 && !ok)
+        for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 1000000;) __nanosleep(10000);
       if (rank == 0)
         for (uint32_t s = 0; s < G::STAGES; ++s)
           if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err, p.wait_ns);
