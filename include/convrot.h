@@ -672,6 +672,182 @@ int fp8_linear(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx,
                const convrot_fp8_weight* weights, int n_weights, int y_dtype, void* workspace,
                size_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Experts
+ * ---------------------------------------------------------------------------
+ * A block whose MLP is a set of E experts, of which a token uses top_k:
+ * moe_route chooses them, moe_plan sorts the choices by expert, the
+ * fp8_expert_* linears take the rows of every expert through its matrices, and
+ * moe_combine adds a token's rows up; fp8_moe is all but the first in one
+ * call. A choice is numbered token * top_k + slot; the experts of a choice are
+ * in [0, E), and -1 says that the slot holds none (a token that pads a batch,
+ * or one with fewer open experts than top_k).
+ */
+
+/* Most experts, and most per token. */
+#define CONVROT_MOE_MAX_EXPERTS 1024
+#define CONVROT_MOE_MAX_TOP_K 32
+/* Most groups of experts. */
+#define CONVROT_MOE_MAX_GROUPS 32
+
+typedef enum convrot_moe_score {
+  CONVROT_MOE_SOFTMAX = 0, /* over all experts */
+  CONVROT_MOE_SIGMOID = 1  /* of every expert by itself */
+} convrot_moe_score;
+
+/*
+ * Arguments of moe_route. For every token:
+ *   s = softmax(logits) or sigmoid(logits),
+ *   v = s + bias; without a bias the logits themselves, which order the same way;
+ *   with n_groups > 1, experts [g E / n_groups, (g + 1) E / n_groups) are group
+ *     g, its value is the sum of its group_top largest v (without a bias and
+ *     group_top = 2: of its two largest s), and only the experts of the
+ *     top_groups groups of largest value stay open;
+ *   the top_k open experts of largest v are chosen, in descending order, equal
+ *     ones in the order of their index;
+ *   weights = scale * s, or scale * s / (sum of the chosen s) (0 where
+ *     none is chosen).
+ * Which values are larger is decided as in 64 bits; the weights are fp32.
+ */
+typedef struct convrot_moe_route_args {
+  int64_t T;            /* tokens */
+  int n_experts, top_k; /* 1 <= top_k <= top_groups * E / n_groups */
+  int dtype;            /* of logits (convrot_dtype) */
+  int score;            /* convrot_moe_score */
+  const void* logits;   /* [T,E], rows ld elements apart */
+  int64_t ld;
+  const float* bias; /* [E] fp32, or NULL; for the choice only */
+  int n_groups;      /* divides E; 1: no groups */
+  int top_groups;    /* 1 .. n_groups */
+  int group_top;     /* 1 or 2 */
+  int renormalise;   /* nonzero: weights of a token sum to scale */
+  float scale;
+  int32_t* experts; /* [T,top_k] */
+  float* weights;   /* [T,top_k] */
+} convrot_moe_route_args;
+
+/*
+ * moe_route -- see convrot_moe_route_args. An expert whose logit or bias is
+ * -inf is closed: it is not chosen, and where fewer than top_k are open the
+ * slots left over get expert -1 and weight 0. A token with a NaN logit (or a
+ * logit of +inf, whose softmax is NaN; or a NaN bias) gets experts 0 ..
+ * top_k - 1 with NaN weights, so that its output shows it.
+ * Errors: ERR_ARG (also a scale that is not finite, a top_k over the experts
+ *         that can be open), ERR_ALIGN (an array not aligned to its elements),
+ *         ERR_ALIAS, ERR_UNSUPPORTED (more than CONVROT_MOE_MAX_EXPERTS
+ *         experts, CONVROT_MOE_MAX_TOP_K choices or CONVROT_MOE_MAX_GROUPS
+ *         groups, 2^31 - 2^16 choices or more), ERR_DEVICE, ERR_CUDA.
+ */
+int moe_route(const convrot_moe_route_args* args, void* stream);
+
+/*
+ * moe_plan -- n choices to rows sorted by expert, a row per choice, the
+ * choices of one expert in their own order.
+ *   experts  [n] (a [T,top_k] array of moe_route).
+ *   order    [n] the choice of a row; -1 behind the last expert's rows.
+ *   place    [n] the row of a choice; -1 for a choice of no expert.
+ *   offsets  [E+1] an expert's first row; offsets[E] is the number of rows.
+ * A choice outside [-1, E) counts as -1 and is reported by
+ * convrot_device_status as CONVROT_ERR_ARG. Results repeat bit for bit.
+ * Errors: ERR_ARG, ERR_ALIGN, ERR_ALIAS, ERR_UNSUPPORTED (more experts than
+ *         CONVROT_MOE_MAX_EXPERTS, 2^31 - 2^16 choices or more), ERR_DEVICE,
+ *         ERR_CUDA.
+ */
+int moe_plan(const int32_t* experts, int64_t n, int n_experts, int32_t* order, int32_t* place,
+             int32_t* offsets, void* stream);
+
+/* The matrices [N,K] of E experts, each as fp8_prepare_weight leaves it. */
+typedef struct convrot_experts {
+  const uint8_t* q;     /* e4m3 codes; expert e's at q + e * q_stride */
+  const float* scale;   /* [ceil(N/128), ceil(K/128)] each, scale_stride elements apart */
+  const float* bias;    /* [N] fp32 each, bias_stride elements apart, or NULL */
+  int64_t N;            /* output features */
+  int64_t q_stride;     /* >= N * K, a multiple of 16 */
+  int64_t scale_stride; /* >= ceil(N/128) * ceil(K/128) */
+  int64_t bias_stride;  /* >= N */
+} convrot_experts;
+
+/*
+ * fp8_expert_linear -- for every row i < offsets[E] of the plan, e its expert
+ * and m = order[i] / top_k its activation row (m = i where order is NULL):
+ *   Y[i,:] = X[m,:] W_e^T + bias_e,
+ * X as codes Q_x [T,K] and scales s_x [T, ceil(K/128)], summed as by
+ * fp8_linear_packed, one rounding to y_dtype. Rows of Y from offsets[E] on are
+ * left as they are. Results repeat bit for bit.
+ *   order, offsets  of moe_plan for n choices; T >= n where order is NULL.
+ * Errors: those of fp8_linear_packed; ERR_ARG (also n_experts or top_k below
+ *         1), ERR_ALIGN (also q_stride % 16), ERR_UNSUPPORTED (more experts
+ *         than CONVROT_MOE_MAX_EXPERTS).
+ */
+int fp8_expert_linear(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
+                      const int32_t* offsets, int64_t n, int n_experts, int top_k,
+                      const convrot_experts* weight, void* Y, int64_t ldy, int y_dtype, void* stream);
+
+/*
+ * fp8_expert_swiglu -- the same rows through two matrices, gate and up:
+ *   g = X[m,:] G_e^T + b, u = X[m,:] U_e^T + b', h = silu(g) * u (fp32),
+ * quantized from the fp32 h as fp8_pack_activations does to Q_h [n,N] (dense)
+ * and s_h [n, ceil(N/128)], where an fp8_expert_linear without order reads
+ * them. Rows from offsets[E] on are left as they are.
+ *   gate, up  the same N, N % 16 == 0.
+ * Errors: as fp8_expert_linear.
+ */
+int fp8_expert_swiglu(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
+                      const int32_t* offsets, int64_t n, int n_experts, int top_k,
+                      const convrot_experts* gate, const convrot_experts* up, uint8_t* Q_h, float* s_h,
+                      void* stream);
+
+/*
+ * moe_combine -- Y[t,:] = residual[t,:] + sum_j weights[t,j] rows[place[t,j],:],
+ * fp32, in the order of j, one rounding at the end; a choice whose place is -1
+ * adds nothing, whatever its weight.
+ *   rows      [n,N] of r_dtype, rows ldr elements apart.
+ *   place, weights  [T,top_k].
+ *   residual  [T,N] of y_dtype (rows ld_res apart), or NULL; may be Y itself.
+ * Rows that all start on 16-byte boundaries, with N % 8 == 0, are read fastest.
+ * Errors: ERR_ARG, ERR_ALIGN (an array not aligned to its elements), ERR_ALIAS,
+ *         ERR_UNSUPPORTED (too many outputs for one launch), ERR_DEVICE,
+ *         ERR_CUDA.
+ */
+int moe_combine(const void* rows, int r_dtype, int64_t ldr, int64_t n, const int32_t* place,
+                const float* weights, int64_t T, int top_k, int64_t N, const void* residual, int64_t ld_res,
+                void* Y, int64_t ldy, int y_dtype, void* stream);
+
+/* Arguments of fp8_moe. */
+typedef struct convrot_moe_args {
+  const void* X; /* [T,K] of x_dtype, rows ldx elements apart */
+  int x_dtype;
+  int64_t T, K, ldx;
+  const int32_t* experts; /* [T,top_k] */
+  const float* weights;   /* [T,top_k] */
+  int top_k, n_experts;
+  const convrot_experts* gate; /* [I,K] each, I % 16 == 0 */
+  const convrot_experts* up;   /* [I,K] each */
+  const convrot_experts* down; /* [N,I] each */
+  const void* residual;        /* [T,N] of y_dtype, rows ld_res apart, or NULL */
+  int64_t ld_res;
+  void* Y; /* [T,N] of y_dtype, rows ldy apart; may be residual itself */
+  int64_t ldy;
+  int y_dtype;
+} convrot_moe_args;
+
+/* Device bytes fp8_moe needs for T tokens; 0 for invalid sizes. */
+size_t fp8_moe_workspace_size(int64_t T, int64_t K, int64_t I, int64_t N, int top_k, int n_experts,
+                              int y_dtype);
+
+/*
+ * fp8_moe -- the experts' part of a block:
+ *   Y[t] = residual[t] + sum_j weights[t,j] D_e(silu(G_e(x_t)) * U_e(x_t)), e = experts[t,j],
+ * X and the hidden rows quantized as by fp8_pack_activations, sums in fp32, one
+ * rounding to y_dtype. Choices of -1 add nothing. A choice outside [-1, E)
+ * counts as -1 and is reported as by moe_plan.
+ *   workspace  at least fp8_moe_workspace_size(...) bytes, 16-byte aligned, not
+ *              used by another call that may run at the same time.
+ * Errors: those of the operators above, and ERR_WORKSPACE.
+ */
+int fp8_moe(const convrot_moe_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Size of the fixed device array that convrot_linear_noalloc uses (32 MiB). */
 #define CONVROT_NOALLOC_SCRATCH_BYTES (32u << 20)
 
@@ -778,7 +954,8 @@ int convrot_test_unscale_sweep(const float* divisors, int n_divisors, int y_exp,
  * device's sticky error word: CONVROT_OK, or CONVROT_ERR_TIMEOUT when a
  * kernel's bounded wait on a TMA or tensor-core completion barrier gave up
  * (the kernel then skipped its remaining work and released its resources), or
- * CONVROT_ERR_ARG when convrot_block_norm met a row_sample out of range.
+ * CONVROT_ERR_ARG when convrot_block_norm met a row_sample out of range, or
+ * moe_plan or fp8_moe an expert out of range.
  */
 int convrot_device_status(void* stream);
 

@@ -4,6 +4,7 @@
 // alignment, int32 overflow bound, aliasing, workspace size), then enqueues
 // the kernels on the caller's stream. No entry point allocates device memory.
 #include "fp8_common.cuh"
+#include "moe_common.cuh"
 
 #include <cstring>
 #include <mutex>
@@ -62,7 +63,7 @@ cudaError_t pack_error_word(int** p);  // pack.cu: the packs
 
 namespace {
 
-constexpr int N_WORDS = 7;
+constexpr int N_WORDS = 9;
 struct ErrorWords {
   int* word[N_WORDS];
 };
@@ -586,7 +587,8 @@ int convrot_device_status(void* stream) {
   ErrorWords words;
   cudaError_t (*const address[N_WORDS])(int**) = {
       gemm_error_word, w4_error_word, pack_error_word, fp8::linear_error_word,
-      fp8::norm_error_word<float>, fp8::norm_error_word<__half>, fp8::norm_error_word<__nv_bfloat16>};
+      fp8::norm_error_word<float>, fp8::norm_error_word<__half>, fp8::norm_error_word<__nv_bfloat16>,
+      moe::route_error_word, moe::expert_error_word};
   for (int i = 0; i < N_WORDS; ++i)
     if ((e = address[i](&words.word[i])) != cudaSuccess) return set_cuda_error(e);
   std::lock_guard<std::mutex> lock(g_status_mu);

@@ -6,6 +6,8 @@
 
 #include <cuda_bf16.h>
 
+#include <mutex>
+
 #include "common.cuh"
 
 namespace convrot {
@@ -264,6 +266,27 @@ struct Launch {
     cfg.numAttrs = cluster > 1 ? 2 : 1;
   }
 };
+
+// Raises the kernel's shared-memory limit, once per device. `regs`: the
+// registers a thread that the kernel's own redistribution counts on (it would
+// wait forever for more than the launch has).
+template <typename F>
+int allow_smem(F* kernel, int bytes, uint64_t& done, std::mutex& mu, int regs = 0) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 64 || !((done >> dev) & 1u)) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    if (attr.numRegs < regs) return CONVROT_ERR_UNSUPPORTED;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    if (dev < 64) done |= 1ull << dev;
+  }
+  return CONVROT_OK;
+}
 
 // fp8_pack.cu
 int launch_fp8_pack(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* Q, float* s,

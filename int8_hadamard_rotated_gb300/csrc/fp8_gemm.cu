@@ -17,7 +17,6 @@
 #include "fp8_common.cuh"
 
 #include <algorithm>
-#include <mutex>
 
 namespace convrot {
 namespace fp8 {
@@ -1117,27 +1116,6 @@ int make_tmap_out(CUtensorMap* m, void* base, int y_dtype, int64_t rows, int64_t
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? CONVROT_OK : set_cuda_error(cudaErrorInvalidValue);
-}
-
-// Raises the kernel's shared-memory limit, once per device. `regs`: the
-// registers a thread that the kernel's own redistribution counts on (it would
-// wait forever for more than the launch has).
-template <typename F>
-int allow_smem(F* kernel, int bytes, uint64_t& done, std::mutex& mu, int regs = 0) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  std::lock_guard<std::mutex> lock(mu);
-  if (dev >= 64 || !((done >> dev) & 1u)) {
-    cudaFuncAttributes attr;
-    e = cudaFuncGetAttributes(&attr, kernel);
-    if (e != cudaSuccess) return set_cuda_error(e);
-    if (attr.numRegs < regs) return CONVROT_ERR_UNSUPPORTED;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return set_cuda_error(e);
-    if (dev < 64) done |= 1ull << dev;
-  }
-  return CONVROT_OK;
 }
 
 constexpr int64_t RASTER_L2_BYTES = 48ll << 20;  // activation codes a raster group keeps in L2

@@ -1,0 +1,52 @@
+// moe_common.cuh -- what the experts' operators share: the launchers behind
+// their entry points (moe_api.cu) and the limits that the kernels count on.
+#pragma once
+
+#include "fp8_common.cuh"
+
+namespace convrot {
+namespace moe {
+
+constexpr int MAX_EXPERTS = CONVROT_MOE_MAX_EXPERTS;
+constexpr int MAX_TOP_K = CONVROT_MOE_MAX_TOP_K;
+
+// Rows sorted by expert, as moe_plan leaves them.
+struct Rows {
+  const int32_t* order;    // [n] the choice (token * top_k + slot) of a row, or null: row i of the activation
+  const int32_t* offsets;  // [E + 1] an expert's first row
+  int64_t n, T;            // rows; rows of the activation
+  int E, top_k;
+};
+
+// moe_route.cu: arguments already checked; T > 0 (n > 0).
+int launch_route(const convrot_moe_route_args& a, cudaStream_t stream);
+int launch_plan(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
+                cudaStream_t stream);
+struct CombineArgs {
+  const void* rows;  // [n,N] of r_dtype
+  int r_dtype;
+  int64_t ldr, n;
+  const int32_t* place;  // [T,top_k]
+  const float* weights;  // [T,top_k]
+  int64_t T;
+  int top_k;
+  int64_t N;
+  const void* residual;  // [T,N] of y_dtype, or null
+  int64_t ld_res;
+  void* Y;
+  int64_t ldy;
+  int y_dtype;
+};
+int launch_combine(const CombineArgs& a, cudaStream_t stream);
+cudaError_t route_error_word(int** p);
+
+// expert_gemm.cu: n, T > 0, every width > 0.
+int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& gate,
+                         const convrot_experts& up, uint8_t* Q_h, float* s_h, cudaStream_t stream,
+                         uint64_t test_wait_ns = 0);
+int launch_expert_linear(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& w, void* Y,
+                         int64_t ldy, int y_dtype, cudaStream_t stream, uint64_t test_wait_ns = 0);
+cudaError_t expert_error_word(int** p);
+
+}  // namespace moe
+}  // namespace convrot

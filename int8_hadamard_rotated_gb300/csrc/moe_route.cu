@@ -1,0 +1,572 @@
+// moe_route.cu -- what stands around the experts' linears: the router's choice
+// of experts, the plan that sorts the choices by expert, and the weighted sum
+// of the experts' rows.
+#include "moe_common.cuh"
+
+#include <climits>
+
+namespace convrot {
+namespace moe {
+
+using fp8::from_f32;
+using fp8::Launch;
+using fp8::to_f32;
+
+// Sticky device error word of these kernels (experts out of range).
+__device__ int g_moe_error = 0;
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// the router
+// ---------------------------------------------------------------------------
+//
+//   s = softmax(l) or 1 / (1 + exp(-l)),   v = s + bias (l itself without one),
+// the top_k largest v of the best groups, ties to the lowest index.
+//
+// One token per warp, its logits read once; expert i is on lane i % 32. The
+// work is a chain of warp-wide maxima over order-preserving 32-bit keys
+// (redux), so a token costs latency, not bandwidth, and many warps hide it.
+//
+// Which of two values is larger must not hang on the rounding of exp: values
+// are formed in fp32 with a bound on their error, and where more than one is
+// within twice the bound of the largest (about one token in a few hundred),
+// those alone are formed again in 64 bits and compared there. So the choice is
+// that of 64-bit arithmetic at the price of fp32. (All values in 64 bits would
+// take some 50 us for 4096 x 256 logits at this GPU's fp64 rate.)
+
+constexpr int ROUTE_WARPS = 4;
+
+struct RouteParams {
+  const void* logits;
+  int64_t ld, T;
+  const float* bias;
+  int32_t* experts;
+  float* weights;
+  float scale;
+  int E, top_k, n_groups, per_group, top_groups, group_top, lanes_per_group;
+  bool sigmoid, renormalise;
+};
+
+// Order-preserving keys: a < b as floats <=> key(a) < key(b); 0 is below every
+// value's key and says "not to be chosen".
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 to +0: they are equal
+  return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+// The index (any lane's `i`) of the largest `v`, the lowest among equal ones;
+// lanes without a candidate give i = INT_MAX.
+__device__ __forceinline__ int warp_argmax(double v, int i) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    const double w = __shfl_xor_sync(0xffffffffu, v, d);
+    const int j = __shfl_xor_sync(0xffffffffu, i, d);
+    if (j != INT_MAX && (i == INT_MAX || w > v || (w == v && j < i))) {
+      v = w;
+      i = j;
+    }
+  }
+  return i;
+}
+
+// exp(-c) / (1 + exp(-l)) for c = 0, or l <= c < 0: without underflow in the
+// latter case where l is near c.
+__device__ __forceinline__ float sigmoid_from(float l, float c) {
+  const float e = expf(-fabsf(l));
+  return __fdiv_rn(l >= 0.0f ? 1.0f : c == 0.0f ? e : expf(l - c), 1.0f + e);
+}
+
+template <typename T, int EPL>
+__global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __grid_constant__ RouteParams p) {
+  extern __shared__ float route_smem[];  // grouped: [warp][E + padding] logits, then values
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  constexpr uint32_t ALL = 0xffffffffu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * ROUTE_WARPS + warp;
+  if (token >= p.T) return;
+  const T* row = static_cast<const T*>(p.logits) + token * p.ld;
+  const bool biased = p.bias != nullptr;
+
+  float l[EPL], s[EPL];
+  bool bad = false;  // the row has no scores
+  float m = -INFINITY;
+#pragma unroll
+  for (int r = 0; r < EPL; ++r) {
+    const int e = lane + 32 * r;
+    l[r] = e < p.E ? to_f32(row[e]) : -INFINITY;
+    bad |= l[r] != l[r] || (!p.sigmoid && l[r] == INFINITY);
+    m = fmaxf(m, l[r]);
+  }
+  float total = 1.0f;
+  if (p.sigmoid) {
+#pragma unroll
+    for (int r = 0; r < EPL; ++r) s[r] = sigmoid_from(l[r], 0.0f);
+  } else {
+    m = value_of(__reduce_max_sync(ALL, key_of(m)));
+    float sum = 0.0f;
+#pragma unroll
+    for (int r = 0; r < EPL; ++r) {
+      s[r] = l[r] == -INFINITY ? 0.0f : expf(l[r] - m);
+      sum += s[r];
+    }
+    total = warp_sum(sum);
+#pragma unroll
+    for (int r = 0; r < EPL; ++r) s[r] = total > 0.0f ? __fdiv_rn(s[r], total) : 0.0f;
+  }
+  // what is compared; an expert whose logit or bias is -inf is not chosen
+  uint32_t key[EPL];
+#pragma unroll
+  for (int r = 0; r < EPL; ++r) {
+    const int e = lane + 32 * r;
+    const float b = biased && e < p.E ? __ldg(p.bias + e) : 0.0f;
+    bad |= b != b;
+    const float v = biased ? s[r] + b : l[r];
+    key[r] = l[r] == -INFINITY || v == -INFINITY ? 0u : key_of(v);
+  }
+  if (__any_sync(ALL, bad)) {  // a NaN stays visible: in the weights
+    if (lane < p.top_k) {
+      p.experts[token * p.top_k + lane] = lane;
+      p.weights[token * p.top_k + lane] = __uint_as_float(0x7fffffffu);
+    }
+    return;
+  }
+
+  // Bound on the error of an fp32 value against its 64-bit one. Sigmoid: exp
+  // within 2 ulp and two more roundings, 3.6e-7 s, s <= 1. Softmax: exp within
+  // 2 ulp, the rounding of its argument (x exp(-x) 2^-24 <= 2^-25), a sum of
+  // at most EPL + 5 steps and a division, 44 x 2^-24 s at most, s <= 1 / total.
+  // The bias adds 2^-24 |v|.
+  const float score_error = p.sigmoid ? 0x1p-21f : 0x1p-18f * __fdiv_rn(1.0f, fmaxf(total, 1.0f));
+  auto error_at = [&](float v) { return score_error + 0x1p-23f * fabsf(v); };
+  double total64 = 0.0;  // softmax: formed when first needed
+  auto need_total64 = [&]() {  // by the whole warp
+    if (p.sigmoid || total64 != 0.0) return;
+#pragma unroll
+    for (int r = 0; r < EPL; ++r)
+      total64 += l[r] == -INFINITY ? 0.0 : exp(static_cast<double>(l[r]) - static_cast<double>(m));
+    total64 = warp_sum(total64);
+  };
+  auto value64 = [&](float logit, int e) {
+    const double sc = p.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(logit)))
+                                : exp(static_cast<double>(logit) - static_cast<double>(m)) / total64;
+    return biased ? sc + static_cast<double>(__ldg(p.bias + e)) : sc;
+  };
+
+  if (p.n_groups > 1) {
+    // The groups' values: lanes_per_group lanes look through a group each, from
+    // shared memory, where a group starts lanes_per_group words further than
+    // the one before it ends (another bank for each).
+    const int P = p.lanes_per_group, pitch = p.per_group + P;
+    float* sl = route_smem + warp * 2 * p.n_groups * pitch;
+    float* sv = sl + p.n_groups * pitch;
+    const bool exact = p.group_top == 1 && !biased;
+#pragma unroll
+    for (int r = 0; r < EPL; ++r) {
+      const int e = lane + 32 * r;
+      if (e < p.E) {
+        const int at = e + e / p.per_group * P;
+        sl[at] = l[r];
+        sv[at] = key[r] == 0u ? -INFINITY : exact ? l[r] : biased ? value_of(key[r]) : s[r];
+      }
+    }
+    __syncwarp();
+    const int g = lane / P, sub = lane - g * P;
+    const bool mine = g < p.n_groups;
+    float a = -INFINITY, b = -INFINITY;  // the two largest
+    if (mine)
+      for (int i = sub; i < p.per_group; i += P) {
+        const float v = sv[g * pitch + i];
+        b = fmaxf(b, fminf(a, v));
+        a = fmaxf(a, v);
+      }
+    for (int d = 1; d < P; d *= 2) {
+      const float oa = __shfl_xor_sync(ALL, a, d), ob = __shfl_xor_sync(ALL, b, d);
+      b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+      a = fmaxf(a, oa);
+    }
+    const bool two = p.group_top == 2 && b > -INFINITY;
+    const float value = two ? a + b : a;
+    uint32_t gkey = mine && value > -INFINITY ? key_of(value) : 0u;
+    uint32_t open = 0;  // the chosen groups
+    for (int j = 0; j < p.top_groups; ++j) {
+      const uint32_t top = __reduce_max_sync(ALL, gkey);
+      if (top == 0u) break;
+      int best = static_cast<int>(__reduce_min_sync(ALL, gkey == top ? static_cast<uint32_t>(g) : 0xffffu));
+      if (!exact) {
+        const float v = value_of(top), lo = v - 5.0f * error_at(v);
+        const bool near = gkey != 0u && (gkey == top || value >= lo);
+        if (__popc(__ballot_sync(ALL, near && sub == 0)) > 1) {
+          need_total64();
+          double a64 = -INFINITY, b64 = -INFINITY;
+          if (near) {
+            const float least = two ? b : a;
+            const float from = least - 2.5f * error_at(least);
+            for (int i = sub; i < p.per_group; i += P) {
+              const float w = sv[g * pitch + i];
+              if (w == -INFINITY || !(w >= from || w == a)) continue;
+              const double x = value64(sl[g * pitch + i], g * p.per_group + i);
+              b64 = fmax(b64, fmin(a64, x));
+              a64 = fmax(a64, x);
+            }
+          }
+          for (int d = 1; d < P; d *= 2) {
+            const double oa = __shfl_xor_sync(ALL, a64, d), ob = __shfl_xor_sync(ALL, b64, d);
+            b64 = fmax(fmax(b64, ob), fmin(a64, oa));
+            a64 = fmax(a64, oa);
+          }
+          best = warp_argmax(two ? a64 + b64 : a64, near ? g : INT_MAX);
+        }
+      }
+      open |= 1u << best;
+      if (g == best) gkey = 0u;
+    }
+#pragma unroll
+    for (int r = 0; r < EPL; ++r) {
+      const int e = lane + 32 * r;
+      if (e < p.E && !(open >> (e / p.per_group) & 1u)) key[r] = 0u;
+    }
+  }
+
+  int chosen = -1;  // lane j: the j-th expert and its logit
+  float logit = -INFINITY;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int r = 0; r < EPL; ++r) top = max(top, key[r]);
+    top = __reduce_max_sync(ALL, top);
+    if (top == 0u) break;
+    uint32_t e = 0xffffu;
+#pragma unroll
+    for (int r = EPL - 1; r >= 0; --r)
+      if (key[r] == top) e = lane + 32 * r;
+    e = __reduce_min_sync(ALL, e);
+    if (biased) {
+      const float v = value_of(top), lo = v - 2.5f * error_at(v);
+      int count = 0;
+#pragma unroll
+      for (int r = 0; r < EPL; ++r) count += key[r] != 0u && (key[r] == top || value_of(key[r]) >= lo);
+      if (__reduce_add_sync(ALL, count) > 1) {
+        need_total64();
+        double best = -INFINITY;
+        int at = INT_MAX;
+#pragma unroll
+        for (int r = 0; r < EPL; ++r)
+          if (key[r] != 0u && (key[r] == top || value_of(key[r]) >= lo)) {
+            const double x = value64(l[r], lane + 32 * r);
+            if (at == INT_MAX || x > best) {
+              best = x;
+              at = lane + 32 * r;
+            }
+          }
+        e = warp_argmax(best, at);
+      }
+    }
+    float of = 0.0f;
+#pragma unroll
+    for (int r = 0; r < EPL; ++r)
+      if (e == lane + 32 * r) {
+        of = l[r];
+        key[r] = 0u;
+      }
+    of = __shfl_sync(ALL, of, e & 31);
+    if (lane == j) {
+      chosen = static_cast<int>(e);
+      logit = of;
+    }
+  }
+  // The weights from the logits: where they are renormalised, relative to the
+  // largest chosen one, so that scores too small for fp32 keep their ratios.
+  const float most = p.renormalise ? value_of(__reduce_max_sync(ALL, key_of(logit))) : 0.0f;
+  float weight = 0.0f;
+  if (chosen >= 0)
+    weight = p.sigmoid         ? sigmoid_from(logit, fminf(most, 0.0f))
+             : p.renormalise ? expf(logit - most)
+                             : __fdiv_rn(expf(logit - m), total);
+  if (p.renormalise) {
+    const float sum = warp_sum(weight);
+    weight = sum > 0.0f ? __fdiv_rn(weight, sum) : 0.0f;
+  }
+  if (lane < p.top_k) {
+    p.experts[token * p.top_k + lane] = chosen;
+    p.weights[token * p.top_k + lane] = weight * p.scale;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the plan
+// ---------------------------------------------------------------------------
+//
+// A stable counting sort of n choices by expert, by one cluster: every warp
+// takes a contiguous part of the choices and counts them per expert in its own
+// row of shared memory (32 at a time; the lanes that hold the same expert find
+// each other by match, and one of them adds their number), the rows' prefix
+// sums give every warp its first place in every expert, and a second turn over
+// the choices, which are in L1 by then, hands the places out. The CTAs' counts
+// meet through distributed shared memory. No atomics: the order is the
+// choices' own. Choices outside [0, E) count as expert E, behind all others.
+
+constexpr int PLAN_WARPS = 32;
+constexpr int PLAN_MAX_CLUSTER = 8;
+
+__device__ __forceinline__ int ld_cluster_i32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(PLAN_WARPS * 32)
+moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int n_ctas, int32_t* __restrict__ order,
+                int32_t* __restrict__ place, int32_t* __restrict__ offsets) {
+  extern __shared__ int plan_smem[];  // counts [PLAN_WARPS][E + 1], totals [E + 1], first [E + 1]
+  __shared__ int warp_sums[PLAN_WARPS];
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  constexpr uint32_t ALL = 0xffffffffu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = E + 1;
+  const int rank = n_ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  int* counts = plan_smem + warp * B;
+  int* totals = plan_smem + PLAN_WARPS * B;
+  int* first = totals + B;
+  for (int i = lane; i < B; i += 32) counts[i] = 0;
+  // this warp's choices: whole groups of 32, shared out evenly
+  const int64_t groups = (n + 31) / 32, parts = static_cast<int64_t>(n_ctas) * PLAN_WARPS;
+  const int64_t part = static_cast<int64_t>(rank) * PLAN_WARPS + warp;
+  const int64_t g0 = groups * part / parts, g1 = groups * (part + 1) / parts;
+  auto bucket_at = [&](int64_t i) {
+    if (i >= n) return -1;
+    const int e = __ldg(experts + i);
+    return e >= 0 && e < E ? e : E;
+  };
+  __syncwarp();
+  int next = g0 < g1 ? bucket_at(g0 * 32 + lane) : -1;
+  for (int64_t g = g0; g < g1; ++g) {
+    const int b = next;
+    if (g + 1 < g1) next = bucket_at((g + 1) * 32 + lane);
+    if (b == E && __ldg(experts + g * 32 + lane) != -1) record_error(&g_moe_error, CONVROT_ERR_ARG);
+    const uint32_t same = __match_any_sync(ALL, b);
+    if (b >= 0 && (same >> lane) == 1u) counts[b] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < B; e += PLAN_WARPS * 32) {
+    int sum = 0;
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+      const int c = plan_smem[w * B + e];
+      plan_smem[w * B + e] = sum;
+      sum += c;
+    }
+    totals[e] = sum;
+  }
+  if (n_ctas > 1) cluster_sync(); else __syncthreads();
+  // an expert's choices in the CTAs before this one, and in all; a prefix sum
+  // over the experts, E + 1 <= 1025 of them: two threads' turns at most
+  int carry = 0;
+  for (int e0 = 0; e0 < B; e0 += PLAN_WARPS * 32) {
+    const int e = e0 + threadIdx.x;
+    int before = 0, all = 0;
+    if (e < B)
+      for (int c = 0; c < n_ctas; ++c) {
+        const int v = n_ctas > 1 ? ld_cluster_i32(mapa_shared(smem_u32(totals + e), c)) : totals[e];
+        if (c < rank) before += v;
+        all += v;
+      }
+    int scan = all;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(ALL, scan, d);
+      if (lane >= d) scan += v;
+    }
+    if (lane == 31) warp_sums[warp] = scan;
+    __syncthreads();
+    int ahead = carry;
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+      if (w < warp) ahead += warp_sums[w];
+      carry += warp_sums[w];
+    }
+    if (e < B) {
+      first[e] = ahead + scan - all + before;
+      if (rank == 0) offsets[e] = ahead + scan - all;  // offsets[E]: where the choices of no expert begin
+    }
+    __syncthreads();
+  }
+  for (int64_t g = g0; g < g1; ++g) {
+    const int64_t i = g * 32 + lane;
+    const int b = bucket_at(i);
+    const uint32_t same = __match_any_sync(ALL, b);
+    int at = 0;
+    if (b >= 0) at = first[b] + counts[b] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (b >= 0 && (same >> lane) == 1u) counts[b] += __popc(same);
+    __syncwarp();
+    if (b >= 0) {
+      order[at] = b < E ? static_cast<int32_t>(i) : -1;
+      place[i] = b < E ? at : -1;
+    }
+  }
+  if (n_ctas > 1) cluster_sync();  // the others' reads of this CTA's totals
+}
+
+// ---------------------------------------------------------------------------
+// the weighted sum
+// ---------------------------------------------------------------------------
+//
+//   Y[t] = residual[t] + sum_j weights[t,j] rows[place[t,j]], summed in fp32 in
+// the order of j, one rounding at the end. Reads every row once: bound by HBM.
+
+constexpr int COMBINE_THREADS = 256;
+
+template <typename T>
+__device__ __forceinline__ void add8(float (&acc)[8], const T* p, float w) {
+  fp8::Pair x[4];
+  fp8::load8(p, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f32x2_unpack(x[i], a, b);
+    acc[2 * i] = fmaf(w, a, acc[2 * i]);
+    acc[2 * i + 1] = fmaf(w, b, acc[2 * i + 1]);
+  }
+}
+
+template <typename TR, typename TY, bool VEC>
+__global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const __grid_constant__ CombineArgs a) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  constexpr int E = VEC ? 8 : 1;  // features per thread
+  const int64_t per_row = (a.N + E - 1) / E;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * COMBINE_THREADS + threadIdx.x;
+  const int64_t t = i / per_row, col = (i - t * per_row) * E;
+  if (t >= a.T) return;
+  float acc[E];
+#pragma unroll
+  for (int k = 0; k < E; ++k) acc[k] = 0.0f;
+  const TR* rows = static_cast<const TR*>(a.rows) + col;
+  for (int j = 0; j < a.top_k; ++j) {
+    const int64_t r = __ldg(a.place + t * a.top_k + j);
+    if (r < 0 || r >= a.n) continue;
+    const float w = __ldg(a.weights + t * a.top_k + j);
+    if constexpr (VEC) add8(acc, rows + r * a.ldr, w);
+    else acc[0] = fmaf(w, to_f32(rows[r * a.ldr]), acc[0]);
+  }
+  TY* y = static_cast<TY*>(a.Y) + t * a.ldy + col;
+  const TY* res = a.residual ? static_cast<const TY*>(a.residual) + t * a.ld_res + col : nullptr;
+  if constexpr (VEC) {
+    if (res) add8(acc, res, 1.0f);
+    fp8::Pair x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = f32x2_pack(acc[2 * k], acc[2 * k + 1]);
+    fp8::store8(y, x);
+  } else {
+    *y = from_f32<TY>(res ? acc[0] + to_f32(*res) : acc[0]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+template <typename T, int EPL>
+int route_launch(const RouteParams& p, cudaStream_t stream) {
+  const size_t smem =
+      p.n_groups > 1 ? sizeof(float) * ROUTE_WARPS * 2 * p.n_groups * (p.per_group + p.lanes_per_group) : 0;
+  Launch l(static_cast<unsigned>((p.T + ROUTE_WARPS - 1) / ROUTE_WARPS), ROUTE_WARPS * 32, smem, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, moe_route_kernel<T, EPL>, p);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+template <typename T>
+int route_as(const RouteParams& p, cudaStream_t stream) {
+  if (p.E <= 64) return route_launch<T, 2>(p, stream);
+  if (p.E <= 128) return route_launch<T, 4>(p, stream);
+  if (p.E <= 256) return route_launch<T, 8>(p, stream);
+  if (p.E <= 512) return route_launch<T, 16>(p, stream);
+  return route_launch<T, 32>(p, stream);
+}
+
+template <typename TR, typename TY>
+int combine_as(const CombineArgs& a, cudaStream_t stream) {
+  auto fits = [&](const void* p, int64_t ld, size_t size) { return aligned16(p) && (ld * size) % 16 == 0; };
+  const bool vec = a.N % 8 == 0 && fits(a.rows, a.ldr, sizeof(TR)) && fits(a.Y, a.ldy, sizeof(TY)) &&
+                   (!a.residual || fits(a.residual, a.ld_res, sizeof(TY)));
+  const int64_t items = a.T * (vec ? a.N / 8 : a.N);
+  const int64_t blocks = (items + COMBINE_THREADS - 1) / COMBINE_THREADS;
+  if (blocks > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+  Launch l(static_cast<unsigned>(blocks), COMBINE_THREADS, 0, stream);
+  const cudaError_t e = vec ? cudaLaunchKernelEx(&l.cfg, moe_combine_kernel<TR, TY, true>, a)
+                            : cudaLaunchKernelEx(&l.cfg, moe_combine_kernel<TR, TY, false>, a);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+template <typename TR>
+int combine_rows(const CombineArgs& a, cudaStream_t stream) {
+  if (a.y_dtype == CONVROT_F32) return combine_as<TR, float>(a, stream);
+  if (a.y_dtype == CONVROT_F16) return combine_as<TR, __half>(a, stream);
+  return combine_as<TR, __nv_bfloat16>(a, stream);
+}
+
+}  // namespace
+
+int launch_route(const convrot_moe_route_args& a, cudaStream_t stream) {
+  RouteParams p{};
+  p.logits = a.logits;
+  p.ld = a.ld;
+  p.T = a.T;
+  p.bias = a.bias;
+  p.experts = a.experts;
+  p.weights = a.weights;
+  p.scale = a.scale;
+  p.E = a.n_experts;
+  p.top_k = a.top_k;
+  p.n_groups = a.n_groups;
+  p.per_group = a.n_experts / a.n_groups;
+  p.top_groups = a.top_groups;
+  p.group_top = a.group_top;
+  p.lanes_per_group = 1;
+  while (2 * p.lanes_per_group * a.n_groups <= 32) p.lanes_per_group *= 2;
+  p.sigmoid = a.score == CONVROT_MOE_SIGMOID;
+  p.renormalise = a.renormalise != 0;
+  if (a.dtype == CONVROT_F32) return route_as<float>(p, stream);
+  if (a.dtype == CONVROT_F16) return route_as<__half>(p, stream);
+  return route_as<__nv_bfloat16>(p, stream);
+}
+
+int launch_plan(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
+                cudaStream_t stream) {
+  // one CTA while its warps have a few turns each
+  int ctas = 1;
+  while (ctas < PLAN_MAX_CLUSTER && n > ctas * PLAN_WARPS * 64) ctas *= 2;
+  const size_t smem = sizeof(int) * (PLAN_WARPS + 2) * (E + 1);
+  static_assert(sizeof(int) * (PLAN_WARPS + 2) * (MAX_EXPERTS + 1) <= 227 * 1024, "shared memory");
+  static std::mutex mu;
+  static uint64_t done = 0;
+  if (int st = fp8::allow_smem(moe_plan_kernel, sizeof(int) * (PLAN_WARPS + 2) * (MAX_EXPERTS + 1), done, mu)) return st;
+  Launch l(ctas, PLAN_WARPS * 32, smem, stream, ctas);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, moe_plan_kernel, experts, n, E, ctas, order, place, offsets);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+int launch_combine(const CombineArgs& a, cudaStream_t stream) {
+  if (a.r_dtype == CONVROT_F32) return combine_rows<float>(a, stream);
+  if (a.r_dtype == CONVROT_F16) return combine_rows<__half>(a, stream);
+  return combine_rows<__nv_bfloat16>(a, stream);
+}
+
+cudaError_t route_error_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_moe_error); }
+
+}  // namespace moe
+}  // namespace convrot

@@ -54,6 +54,12 @@ GEMM_SYNC_BYTES = 4096
 NORM_MAX_K = 32768
 FP8_BLOCK = 128
 
+MOE_SOFTMAX = 0
+MOE_SIGMOID = 1
+MOE_MAX_EXPERTS = 1024
+MOE_MAX_TOP_K = 32
+MOE_MAX_GROUPS = 32
+
 
 class ConvrotError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -95,6 +101,28 @@ class convrot_block_norm_args(ctypes.Structure):
 class convrot_fp8_weight(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
+
+
+class convrot_moe_route_args(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("n_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("score", ctypes.c_int), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("n_groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_top", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float),
+                ("experts", ctypes.c_void_p), ("weights", ctypes.c_void_p)]
+
+
+class convrot_experts(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("N", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64), ("bias_stride", ctypes.c_int64)]
+
+
+class convrot_moe_args(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("x_dtype", ctypes.c_int), ("T", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("experts", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("top_k", ctypes.c_int), ("n_experts", ctypes.c_int), ("gate", ctypes.c_void_p),
+                ("up", ctypes.c_void_p), ("down", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ld_res", ctypes.c_int64), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("y_dtype", ctypes.c_int)]
 
 
 _LIB = None
@@ -142,6 +170,13 @@ SIGNATURES = {
     "fp8_linear_workspace_size": (_SZ, [_I64, _I64]),
     "fp8_linear_packed": (_I, [_VP, _VP, _I64, _I64, _VP, _I, _I, _VP]),
     "fp8_linear": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I, _I, _VP, _SZ, _VP]),
+    "moe_route": (_I, [_VP, _VP]),
+    "moe_plan": (_I, [_VP, _I64, _I, _VP, _VP, _VP, _VP]),
+    "fp8_expert_linear": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I, _I, _VP, _VP, _I64, _I, _VP]),
+    "fp8_expert_swiglu": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I, _I, _VP, _VP, _VP, _VP, _VP]),
+    "moe_combine": (_I, [_VP, _I, _I64, _I64, _VP, _VP, _I64, _I, _I64, _VP, _I64, _VP, _I64, _I, _VP]),
+    "fp8_moe_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I, _I, _I]),
+    "fp8_moe": (_I, [_VP, _VP, _SZ, _VP]),
     "convrot_device_status": (_I, [_VP]),
     "convrot_test_block_norm_timeout": (_I, [_VP, _I64, ctypes.c_uint64, _VP]),
     "fp8_test_linear_timeout": (_I, [_VP, _VP, _I64, _I64, _VP, _I, _I, ctypes.c_uint64, _VP]),
@@ -957,3 +992,222 @@ def convrot_block_norm_fp8(H: torch.Tensor, Y: Optional[torch.Tensor] = None, *,
                 pre_eps, pre_weight, pre_bias, scale, shift, row_sample, rows_per_sample, H_out, 0, 0, 0,
                 _dense(Q, "Q", device, shape, _E4M3), _dense(s, "s", device, kb, _F32), device, handle)
     return H_out, Q, s
+
+
+# ---------------------------------------------------------------------------
+# experts
+# ---------------------------------------------------------------------------
+
+_ROUTE_ARGS = struct.Struct("@qiiiiPqPiiiifPP")
+_EXPERTS = struct.Struct("@PPPqqqq")
+assert _ROUTE_ARGS.size == ctypes.sizeof(convrot_moe_route_args)
+assert _EXPERTS.size == ctypes.sizeof(convrot_experts)
+
+
+def moe_route(logits: torch.Tensor, top_k: int, *, score: int = MOE_SOFTMAX, bias: Optional[torch.Tensor] = None,
+              n_groups: int = 1, top_groups: int = 1, group_top: int = 2, renormalise: bool = True,
+              scale: float = 1.0, experts: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+              stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Router logits [T,E] (float32, float16 or bfloat16, rows contiguous) ->
+    (experts int32 [T,top_k], weights float32 [T,top_k]): the top_k largest of
+    score(logits) + bias in the best top_groups of n_groups groups of experts,
+    equal ones in the order of their index, weighted by their scores (without
+    the bias). Logits of -inf close an expert; slots that no open expert fills
+    get expert -1 and weight 0."""
+    device, handle = _start(logits, stream)
+    T, E = shape = _matrix(logits, "logits")
+    ld = _rows(logits, "logits", device, shape)
+    out = (T, top_k)
+    if experts is None:
+        experts = _empty(out, torch.int32, device, stream)
+    if weights is None:
+        weights = _empty(out, _F32, device, stream)
+    args = _ROUTE_ARGS.pack(T, E, top_k, _DTYPES[logits.dtype], score, logits.data_ptr(), ld,
+                            0 if bias is None else _dense(bias, "bias", device, (E,), _F32), n_groups, top_groups,
+                            group_top, 1 if renormalise else 0, scale,
+                            _dense(experts, "experts", device, out, torch.int32),
+                            _dense(weights, "weights", device, out, _F32))
+    _check(lib().moe_route(args, handle), "moe_route")
+    return experts, weights
+
+
+def moe_plan(experts: torch.Tensor, n_experts: int, order: Optional[torch.Tensor] = None,
+             place: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None, stream=None):
+    """The choices (int32, of any shape) sorted by expert: (order, place,
+    offsets), int32. order[i] is the choice of row i (-1 behind the last one),
+    place[c] the row of choice c (-1 for none), and expert e has the rows from
+    offsets[e] to offsets[e + 1]."""
+    device, handle = _start(experts, stream)
+    n, i32 = experts.numel(), torch.int32
+    if order is None:
+        order = _empty((n,), i32, device, stream)
+    if place is None:
+        place = _empty((n,), i32, device, stream)
+    if offsets is None:
+        offsets = _empty((n_experts + 1,), i32, device, stream)
+    _check(lib().moe_plan(_dense(experts, "experts", device, experts.shape, i32), n, n_experts,
+                          _dense(order, "order", device, (n,), i32), _dense(place, "place", device, (n,), i32),
+                          _dense(offsets, "offsets", device, (n_experts + 1,), i32), handle), "moe_plan")
+    return order, place, offsets
+
+
+def fp8_prepare_experts(W: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """fp8_prepare_weight of every expert's matrix W[e], W [E,N,K]: (Q
+    float8_e4m3fn [E,N,K], s float32 [E, ceil(N/128), ceil(K/128)])."""
+    device, handle = _start(W, stream)
+    if W.dim() != 3 or W.dtype not in _DTYPES or not W.is_contiguous():
+        raise ValueError("W must be a contiguous float32, float16 or bfloat16 tensor [experts, N, K]")
+    E, N, K = W.shape
+    Q = _empty((E, N, K), _E4M3, device, stream)
+    s = _empty((E, _n_blocks(N), _n_blocks(K)), _F32, device, stream)
+    for e in range(E):
+        _check(lib().fp8_prepare_weight(W[e].data_ptr(), _DTYPES[W.dtype], N, K, Q[e].data_ptr(), s[e].data_ptr(),
+                                        handle), "fp8_prepare_weight")
+    return Q, s
+
+
+def _experts(w, name: str, device: int, K: int, E: Optional[int] = None):
+    """(descriptor, E, N) of a set of experts' matrices: a tuple of codes
+    [E,N,K], scales [E, ceil(N/128), ceil(K/128)] and, or None, biases [E,N].
+    An expert's own part is dense; the experts may be further apart."""
+    q, s, b = w if len(w) == 3 else (*w, None)
+    if q.dim() != 3:
+        raise ValueError(f"{name}: the codes must have the shape (experts, N, K)")
+    n, N = q.shape[:2]
+
+    def part(t, what, shape, dtype):
+        dense, step = True, 1
+        for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:] if t.dim() == len(shape) else ())):
+            dense = dense and (size == 1 or stride == step)
+            step *= size
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not dense:
+            raise ValueError(f"{name}: {what} must be {dtype} of shape {tuple(shape)} on the device of the other "
+                             f"tensors, dense for every expert, got {t.dtype} {tuple(t.shape)}")
+        return t.data_ptr(), t.stride(0) if n > 1 else step
+
+    if E is not None and n != E:
+        raise ValueError(f"{name}: {n} experts, and {E} elsewhere in the call")
+    q_ptr, q_stride = part(q, "codes", (n, N, K), _E4M3)
+    s_ptr, s_stride = part(s, "scales", (n, _n_blocks(N), _n_blocks(K)), _F32)
+    b_ptr, b_stride = (0, N) if b is None else part(b, "biases", (n, N), _F32)
+    return _EXPERTS.pack(q_ptr, s_ptr, b_ptr, N, q_stride, s_stride, b_stride), n, N
+
+
+def _plan_of(Q_x, s_x, order, offsets, E: int, device: int):
+    """(T, K, n, addresses of Q_x, s_x, order and offsets) of an expert linear."""
+    T, K = shape = _matrix(Q_x, "Q_x")
+    n = T if order is None else order.numel()
+    return (T, K, n, _dense(Q_x, "Q_x", device, shape, _E4M3), _dense(s_x, "s_x", device, (T, _n_blocks(K)), _F32),
+            0 if order is None else _dense(order, "order", device, (n,), torch.int32),
+            _dense(offsets, "offsets", device, (E + 1,), torch.int32))
+
+
+def fp8_expert_linear(Q_x: torch.Tensor, s_x: torch.Tensor, offsets: torch.Tensor, weight,
+                      order: Optional[torch.Tensor] = None, top_k: int = 1, Y: Optional[torch.Tensor] = None,
+                      out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """Rows in the order of a moe_plan, each through its expert's matrix:
+    Y[i] = X[m] W_e^T + b_e, with m = i, or, given the plan's order,
+    m = order[i] // top_k. weight: (codes [E,N,K], scales, biases or None) as
+    fp8_prepare_experts gives them. Rows from offsets[E] on are left as they
+    are (in a new Y: uninitialised)."""
+    device, handle = _start(Q_x, stream)
+    w, E, N = _experts(weight, "weight", device, _matrix(Q_x, "Q_x")[1])
+    T, K, n, q, s, o, f = _plan_of(Q_x, s_x, order, offsets, E, device)
+    if Y is None:
+        Y = _empty((n, N), out_dtype, device, stream)
+    ldy = _rows(Y, "Y", device, (n, N))
+    _check(lib().fp8_expert_linear(q, s, T, K, o, f, n, E, top_k, w, Y.data_ptr(), ldy, _DTYPES[Y.dtype], handle),
+           "fp8_expert_linear")
+    return Y
+
+
+def fp8_expert_swiglu(Q_x: torch.Tensor, s_x: torch.Tensor, order: Optional[torch.Tensor], offsets: torch.Tensor,
+                      top_k: int, gate, up, Q_h: Optional[torch.Tensor] = None, s_h: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The rows of a moe_plan through their expert's gate and up matrices (as
+    fp8_expert_linear, order and top_k included): h = silu(gate) * up, quantized
+    as it leaves to (Q_h float8_e4m3fn [n,N], s_h float32 [n, ceil(N/128)]),
+    which an fp8_expert_linear without order reads."""
+    device, handle = _start(Q_x, stream)
+    K = _matrix(Q_x, "Q_x")[1]
+    g, E, N = _experts(gate, "gate", device, K)
+    u, _, N_up = _experts(up, "up", device, K, E)
+    if N_up != N:
+        raise ValueError("gate and up must have the same output features")
+    T, K, n, q, s, o, f = _plan_of(Q_x, s_x, order, offsets, E, device)
+    if Q_h is None:
+        Q_h = _empty((n, N), _E4M3, device, stream)
+    if s_h is None:
+        s_h = _empty((n, _n_blocks(N)), _F32, device, stream)
+    _check(lib().fp8_expert_swiglu(q, s, T, K, o, f, n, E, top_k, g, u, _dense(Q_h, "Q_h", device, (n, N), _E4M3),
+                                   _dense(s_h, "s_h", device, (n, _n_blocks(N)), _F32), handle), "fp8_expert_swiglu")
+    return Q_h, s_h
+
+
+def moe_combine(rows: torch.Tensor, place: torch.Tensor, weights: torch.Tensor,
+                residual: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+                out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """Y[t] = residual[t] + sum_j weights[t,j] rows[place[t,j]]: rows [n,N],
+    place int32 and weights float32 [T,top_k] (place of any shape with as many
+    elements). New outputs are of out_dtype (rows' own by default; a residual
+    has the type of Y, and may be Y)."""
+    device, handle = _start(rows, stream)
+    n, N = shape = _matrix(rows, "rows")
+    T, top_k = _matrix(weights, "weights")
+    if place.numel() != T * top_k:
+        raise ValueError(f"place must have {T * top_k} elements, got {place.numel()}")
+    if Y is None:
+        Y = _empty((T, N), out_dtype or (rows.dtype if residual is None else residual.dtype), device, stream)
+    ldr = _rows(rows, "rows", device, shape)
+    ldy = _rows(Y, "Y", device, (T, N))
+    res, ld_res = (0, N) if residual is None else (residual.data_ptr(),
+                                                   _rows(residual, "residual", device, (T, N), Y.dtype))
+    _check(lib().moe_combine(rows.data_ptr(), _DTYPES[rows.dtype], ldr, n,
+                             _dense(place, "place", device, place.shape, torch.int32),
+                             _dense(weights, "weights", device, (T, top_k), _F32), T, top_k, N, res, ld_res,
+                             Y.data_ptr(), ldy, _DTYPES[Y.dtype], handle), "moe_combine")
+    return Y
+
+
+def fp8_moe_workspace_size(T: int, K: int, inner: int, N: int, top_k: int, n_experts: int,
+                           out_dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(lib().fp8_moe_workspace_size(T, K, inner, N, top_k, n_experts, _DTYPES[out_dtype]))
+
+
+def fp8_moe(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, gate, up, down,
+            residual: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+            out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None,
+            stream=None) -> torch.Tensor:
+    """Y[t] = residual[t] + sum_j weights[t,j] down_e(silu(gate_e(x_t)) * up_e(x_t)),
+    e = experts[t,j] (moe_route's results; -1 adds nothing): X [T,K] (float32,
+    float16 or bfloat16, rows contiguous) is packed, the choices are sorted by
+    expert, and the experts' linears, SwiGLU and the weighted sum follow. gate,
+    up, down: (codes, scales, biases or None) as fp8_prepare_experts gives them,
+    of matrices [I,K], [I,K] and [N,I]. New outputs are of out_dtype (X's own by
+    default); a residual has the type of Y, and may be Y."""
+    device, handle = _start(X, stream)
+    T, K = shape = _matrix(X, "X")
+    ldx = _rows(X, "X", device, shape)
+    g, E, inner = _experts(gate, "gate", device, K)
+    u, _, inner_up = _experts(up, "up", device, K, E)
+    if inner_up != inner:
+        raise ValueError("gate and up must have the same output features")
+    d, _, N = _experts(down, "down", device, inner, E)
+    top_k = _matrix(experts, "experts")[1]
+    if Y is None:
+        Y = _empty((T, N), out_dtype or (X.dtype if residual is None else residual.dtype), device, stream)
+    ldy = _rows(Y, "Y", device, (T, N))
+    res, ld_res = (0, N) if residual is None else (residual.data_ptr(),
+                                                   _rows(residual, "residual", device, (T, N), Y.dtype))
+    ws = workspace
+    if ws is None:
+        ws = _empty((max(fp8_moe_workspace_size(T, K, inner, N, top_k, E, Y.dtype), 1),), torch.uint8, device, stream)
+    elif ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of the other tensors")
+    at = lambda b: ctypes.cast(b, _VP).value  # noqa: E731
+    args = convrot_moe_args(X.data_ptr(), _DTYPES[X.dtype], T, K, ldx,
+                            _dense(experts, "experts", device, (T, top_k), torch.int32),
+                            _dense(weights, "weights", device, (T, top_k), _F32), top_k, E, at(g), at(u), at(d),
+                            res, ld_res, Y.data_ptr(), ldy, _DTYPES[Y.dtype])
+    _check(lib().fp8_moe(ctypes.byref(args), ws.data_ptr(), ws.numel() * ws.element_size(), handle), "fp8_moe")
+    return Y

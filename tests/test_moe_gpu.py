@@ -1,0 +1,341 @@
+"""The experts' operators on the GPU against their 64-bit statements
+(oracle/moe_oracle.py)."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import host
+from oracle import block_oracle as bo
+from oracle import moe_oracle as mo
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+U24 = 2.0 ** -24  # half a step of fp32
+INF = float("inf")
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def codes(t):
+    return host(t.view(torch.uint8))
+
+
+def dev_codes(Q):
+    return torch.from_numpy(Q).cuda().view(torch.float8_e4m3fn)
+
+
+def activations(seed, M, K, dtype="f32"):
+    g = gen(seed)
+    X = torch.randn(M, K, generator=g) * (1 + 29 * (torch.rand(K, generator=g) < 0.02))
+    return X.to(DT[dtype])
+
+
+def matrices(seed, E, N, K, bias):
+    """The experts' matrices on the device, and as the statement has them."""
+    r = np.random.default_rng(seed)
+    W = r.normal(size=(E, N, K)).astype(np.float32) * np.float32(K ** -0.5)
+    both = [bo.fp8_pack(w, 128) for w in W]
+    q, s = np.stack([b[0] for b in both]), np.stack([b[1] for b in both])
+    b = r.normal(size=(E, N)).astype(np.float32) * np.float32(0.1) if bias else None
+    return (dev_codes(q), torch.from_numpy(s).cuda(), None if b is None else torch.from_numpy(b).cuda()), (q, s, b)
+
+
+def choices(seed, T, E, k, dropped=0.0, only=None):
+    """int32 [T,k] distinct experts per token (of `only`, where given), some -1."""
+    r = np.random.default_rng(seed)
+    pool = np.arange(E) if only is None else np.asarray(only)
+    e = np.stack([r.permutation(pool)[:k] for _ in range(T)]).astype(np.int32)
+    e[r.random((T, k)) < dropped] = -1
+    w = r.random((T, k)).astype(np.float32)
+    return e, w
+
+
+def assert_within(y, ref, bound):
+    """y off by half a step of its type and `bound`."""
+    half = torch.finfo(y.dtype).eps / 2
+    got = host(y.float()).astype(np.float64)
+    bound = half * np.abs(ref) * (1 + half) + bound * (1 + half)
+    if y.dtype == torch.float16:
+        bound = bound + 2.0 ** -25  # half a subnormal step
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), f"{bad.sum()} of {bad.size} off, first {np.argwhere(bad)[0]}: {got[bad][0]} against {ref[bad][0]}"
+
+
+# ---------------------------------------------------------------------------
+# the router
+# ---------------------------------------------------------------------------
+
+def check_route(ops, logits, k, bias=None, **kw):
+    score = {"softmax": ops.MOE_SOFTMAX, "sigmoid": ops.MOE_SIGMOID}
+    e, w = ops.moe_route(logits, k, bias=None if bias is None else bias.cuda(),
+                         **{n: score[v] if n == "score" else v for n, v in kw.items()})
+    eo, wo = mo.route(host(logits.float()), k, bias=None if bias is None else bias.numpy(), **kw)
+    np.testing.assert_array_equal(host(e), eo)
+    # exp within 2 ulp, sums of up to 1024 scores (37 steps) and up to 32
+    # weights, two divisions, the factor
+    got = host(w)
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(wo))
+    np.testing.assert_allclose(got, wo, rtol=64 * U24, atol=1e-38)
+    return host(e), got
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (2, 2), (7, 3), (60, 4), (64, 8), (65, 8), (160, 6), (256, 8), (511, 9), (1024, 32)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_route(ops, E, k, score, dtype):
+    for T in (1, 5, 130):
+        L = (2 * torch.randn(T, E, generator=gen(E + T))).to(DT[dtype]).cuda()  # 16-bit logits are full of ties
+        check_route(ops, L, k, score=score, renormalise=E % 2 == 0, scale=1.0 if E < 100 else 2.5)
+        check_route(ops, L, k, bias=0.1 * torch.randn(E, generator=gen(E)), score=score)
+
+
+@pytest.mark.parametrize("E,groups,top,k", [(8, 4, 2, 3), (64, 2, 1, 8), (160, 8, 3, 6), (256, 8, 4, 8), (96, 32, 7, 5),
+                                            (1024, 16, 5, 8), (60, 5, 5, 4), (12, 12, 3, 3)])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_route_groups(ops, E, groups, top, k, group_top):
+    for score, biased, dtype in (("sigmoid", True, "f32"), ("softmax", False, "bf16"), ("softmax", True, "f16"),
+                                 ("sigmoid", False, "f32")):
+        L = (2 * torch.randn(77, E, generator=gen(E))).to(DT[dtype]).cuda()
+        check_route(ops, L, k, bias=0.1 * torch.randn(E, generator=gen(1)) if biased else None, score=score,
+                    n_groups=groups, top_groups=top, group_top=group_top)
+
+
+def test_route_near_ties(ops):
+    """Values that fp32 cannot tell apart: saturated sigmoids, scores that the
+    bias makes nearly equal, scores that underflow."""
+    E = 128
+    L = torch.zeros(40, E)
+    L[:20] = 18.0 + torch.rand(20, E, generator=gen(0))              # 1 - 1e-8: equal in fp32, not in 64 bits
+    L[20:30] = -90.0 - 10 * torch.rand(10, E, generator=gen(1))      # exp(-l) overflows fp32
+    L[30:] = 1e-4 * torch.randn(10, E, generator=gen(2))
+    for score in ("sigmoid", "softmax"):
+        for bias in (torch.zeros(E), -torch.sigmoid(L[35]), 1e-7 * torch.randn(E, generator=gen(3))):
+            check_route(ops, L.cuda(), 8, bias=bias, score=score)
+            check_route(ops, L.cuda(), 8, bias=bias, score=score, n_groups=8, top_groups=3)
+        check_route(ops, L.cuda(), 8, score=score)
+        check_route(ops, L.cuda(), 8, score=score, n_groups=4, top_groups=2, group_top=2)
+
+
+def test_route_closed_and_bad(ops):
+    E = 24
+    L = torch.randn(12, E, generator=gen(4))
+    L[0] = -INF                     # nothing open
+    L[1, 1:] = -INF                 # one
+    L[2, 5:] = -INF                 # fewer than k
+    L[3, 2] = float("nan")
+    L[4, 3] = INF                   # softmax: no scores; sigmoid: 1
+    L[5] = -3.0e38                  # finite, far from 0
+    L[6, 0] = 3.0e38
+    L[7, :12] = -INF                # whole groups
+    L[8] = 0.0                      # all equal
+    L[9, ::2] = -0.0
+    L[9, 1::2] = 0.0
+    bias = 0.2 * torch.randn(E, generator=gen(5))
+    closing = bias.clone()
+    closing[3] = -INF
+    pushing = bias.clone()
+    pushing[4] = INF
+    for score in ("softmax", "sigmoid"):
+        for b in (None, bias, closing, pushing):
+            for groups in (dict(), dict(n_groups=4, top_groups=2, group_top=2), dict(n_groups=4, top_groups=2, group_top=1)):
+                for r in (False, True):
+                    e, w = check_route(ops, L.cuda(), 8, bias=b, score=score, renormalise=r, **groups)
+        assert (e[0] == -1).all() and (w[0] == 0).all()
+        assert np.isnan(w[3]).all() and (e[3] == np.arange(8)).all()
+    nan = bias.clone()
+    nan[7] = float("nan")
+    e, w = check_route(ops, L.cuda(), 8, bias=nan)
+    assert np.isnan(w).all()
+
+
+def test_route_rows_apart(ops):
+    base = torch.randn(33, 300, generator=gen(6)).cuda()
+    for off, E in ((0, 64), (1, 65), (37, 256)):
+        check_route(ops, base[:, off:off + E], 8)
+    e, w = ops.moe_route(torch.empty(0, 16, device="cuda"), 4)
+    assert e.shape == w.shape == (0, 4)
+
+
+# ---------------------------------------------------------------------------
+# the plan
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,E", [(0, 5), (1, 1), (1, 1024), (31, 3), (32, 8), (33, 8), (1000, 60), (2049, 128),
+                                 (4097, 256), (20000, 7), (65536, 256), (70001, 1024)])
+def test_plan(ops, n, E):
+    r = np.random.default_rng(n)
+    e = r.integers(-1, E, size=n).astype(np.int32)
+    if n > 100:
+        e[10:90] = E - 1            # a run of one expert
+        e[e == E // 2] = -1         # and an expert without rows
+    order, place, offsets = (host(t) for t in ops.moe_plan(torch.from_numpy(e).cuda(), E))
+    flat = np.where(e < 0, E, e)
+    sort = np.argsort(flat, kind="stable").astype(np.int32)
+    assert (offsets == np.searchsorted(flat[sort], np.arange(E + 1))).all()
+    assert (order == np.where(np.arange(n) < offsets[E], sort, -1)).all()
+    back = np.empty(n, np.int32)
+    back[sort] = np.arange(n)
+    assert (place == np.where(e < 0, -1, back)).all()
+    if n <= 5000:
+        for got, want in zip((order, place, offsets), mo.plan(e, E)):
+            np.testing.assert_array_equal(got, want)
+    assert ops.convrot_device_status() == ops.OK
+
+
+def test_plan_out_of_range(ops):
+    """Experts outside [-1, E) are dropped and reported."""
+    for bad in (-2, 4, 2 ** 31 - 1, -2 ** 31):
+        e = np.int32([0, 3, bad, 1, -1, 3])
+        order, place, offsets = (host(t) for t in ops.moe_plan(torch.from_numpy(e).cuda(), 4))
+        np.testing.assert_array_equal(order, [0, 3, 1, 5, -1, -1])
+        np.testing.assert_array_equal(place, [0, 2, -1, 1, -1, 3])
+        np.testing.assert_array_equal(offsets, [0, 1, 2, 2, 4])
+        assert ops.convrot_device_status() == ops.ERR_ARG
+        assert ops.convrot_device_status() == ops.OK
+
+
+# ---------------------------------------------------------------------------
+# the experts' linears
+# ---------------------------------------------------------------------------
+
+# (T, E, k, only): rows per expert from none to many, one expert that has all
+SPREADS = [(1, 8, 1, None), (1, 8, 8, None), (3, 16, 2, None), (9, 4, 2, None), (40, 5, 3, None), (150, 6, 2, [1, 4]),
+           (200, 3, 1, [1]), (700, 4, 2, None)]
+
+
+def planned(seed, T, E, k, only, dropped):
+    e, w = choices(seed, T, E, k, dropped, only)
+    order, place, offsets = mo.plan(e, E)
+    t = [torch.from_numpy(a).cuda() for a in (order, place, offsets)]
+    return e, w, (order, place, offsets), t
+
+
+@pytest.mark.parametrize("T,E,k,only", SPREADS)
+@pytest.mark.parametrize("N,K", [(16, 16), (128, 128), (131, 656), (640, 1040)])
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+def test_expert_linear(ops, T, E, k, only, N, K, out):
+    bias = N != 128
+    _, _, (order, _, offsets), (d_order, _, d_offsets) = planned(T + N, T, E, k, only, 0.1 if T > 1 else 0.0)
+    n, rows = T * k, int(offsets[E])
+    dw, hw = matrices(N, E, N, K, bias)
+    for gather in (False, True):
+        Q, s = bo.fp8_pack(activations(T, T if gather else n, K).numpy())
+        ref, mag = mo.expert_linear(Q, s, order[:rows] // k if gather else np.arange(rows), offsets, *hw)
+        y = torch.full((n, N), 7.0, dtype=DT[out], device="cuda")
+        ops.fp8_expert_linear(dev_codes(Q), torch.from_numpy(s).cuda(), d_offsets, dw,
+                              order=d_order if gather else None, top_k=k, Y=y)
+        assert_within(y[:rows], ref, mo.linear_error(mag, K))
+        assert (host(y[rows:].float()) == 7.0).all()  # rows behind the last one stay as they were
+    assert ops.convrot_device_status() == ops.OK
+
+
+@pytest.mark.parametrize("T,E,k,only", SPREADS)
+@pytest.mark.parametrize("I,K", [(16, 16), (128, 128), (144, 656), (656, 400)])
+def test_expert_swiglu(ops, T, E, k, only, I, K):  # noqa: E741
+    bias = I != 128
+    _, _, (order, _, offsets), (d_order, _, d_offsets) = planned(T + I, T, E, k, only, 0.1 if T > 1 else 0.0)
+    n, rows = T * k, int(offsets[E])
+    dg, hg = matrices(I, E, I, K, bias)
+    du, hu = matrices(I + 1, E, I, K, bias)
+    for gather in (False, True):
+        Q, s = bo.fp8_pack(activations(T, T if gather else n, K).numpy())
+        src = order[:rows] // k if gather else np.arange(rows)
+        g, ga = mo.expert_linear(Q, s, src, offsets, *hg)
+        u, ua = mo.expert_linear(Q, s, src, offsets, *hu)
+        h, dh = mo.swiglu(g, u, mo.linear_error(ga, K), mo.linear_error(ua, K))
+        Qh = torch.full((n, I), 0x55, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        sh = torch.full((n, bo.n_blocks(I)), 7.0, device="cuda")
+        ops.fp8_expert_swiglu(dev_codes(Q), torch.from_numpy(s).cuda(), d_order if gather else None, d_offsets, k, dg,
+                              du, Q_h=Qh, s_h=sh)
+        got, sc = codes(Qh), host(sh)
+        assert (got[rows:] == 0x55).all() and (sc[rows:] == 7.0).all()
+        S = bo.widen(sc[:rows], rows, I)
+        value = bo.e4m3_values()[got[:rows]] * S
+        # the scale: the largest magnitude over 448; the codes: nearest
+        for j in range(bo.n_blocks(I)):
+            b = slice(128 * j, 128 * (j + 1))
+            top, off = np.abs(h[:, b]).max(1), dh[:, b].max(1)
+            assert (np.abs(sc[:rows, j] * 448.0 - top) <= off + top * 2 * U24).all()
+        half = np.maximum(2.0 ** -4 * np.maximum(np.abs(value), np.abs(h)), 2.0 ** -10 * S)
+        assert (np.abs(value - h) <= half * (1 + 1e-6) + dh + np.abs(h) * 4 * U24).all()
+    assert ops.convrot_device_status() == ops.OK
+
+
+def test_expert_strides(ops):
+    """Gate and up as halves of one array, experts apart; a Y with rows apart and at odd offsets."""
+    E, I, K, T, k = 5, 144, 272, 70, 2  # noqa: E741
+    _, _, (order, _, offsets), (d_order, _, d_offsets) = planned(3, T, E, k, None, 0.0)
+    dg, _ = matrices(1, E, I, K, True)
+    du, _ = matrices(2, E, I, K, True)
+    q = torch.cat([dg[0].view(torch.uint8), du[0].view(torch.uint8)], 1).view(torch.float8_e4m3fn)
+    s = torch.cat([dg[1], du[1]], 1)
+    b = torch.cat([dg[2], du[2]], 1)
+    nb = bo.n_blocks(I)
+    Q, sx = ops.fp8_pack_activations(activations(4, T, K).cuda())
+    want = ops.fp8_expert_swiglu(Q, sx, d_order, d_offsets, k, dg, du)
+    got = ops.fp8_expert_swiglu(Q, sx, d_order, d_offsets, k, (q[:, :I], s[:, :nb], b[:, :I]),
+                                (q[:, I:], s[:, nb:], b[:, I:]))
+    assert (codes(got[0]) == codes(want[0])).all() and (host(got[1]) == host(want[1])).all()
+    y = ops.fp8_expert_linear(Q, sx, d_offsets, dg, order=d_order, top_k=k)
+    for off in (0, 1, 8):
+        base = torch.zeros(T * k, I + 24, dtype=torch.bfloat16, device="cuda")
+        ops.fp8_expert_linear(Q, sx, d_offsets, dg, order=d_order, top_k=k, Y=base[:, off:off + I])
+        assert (host(base[:, off:off + I].float()) == host(y.float())).all()
+        assert (host(base[:, :off].float()) == 0).all() and (host(base[:, off + I:].float()) == 0).all()
+
+
+def test_prepare_experts(ops):
+    W = torch.randn(3, 130, 272, generator=gen(1)).cuda()
+    Q, s = ops.fp8_prepare_experts(W)
+    for e in range(3):
+        q, t = ops.fp8_prepare_weight(W[e])
+        assert (codes(Q[e]) == codes(q)).all() and (host(s[e]) == host(t)).all()
+
+
+# ---------------------------------------------------------------------------
+# the weighted sum, and all of it
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,k,N", [(1, 1, 1), (1, 8, 4096), (7, 3, 131), (33, 8, 640), (300, 32, 24)])
+@pytest.mark.parametrize("rows,out", [("bf16", "bf16"), ("f32", "f16"), ("f16", "f32")])
+def test_combine(ops, T, k, N, rows, out):
+    r = np.random.default_rng(T + N)
+    n = T * k
+    R = torch.from_numpy(r.normal(size=(n, N)).astype(np.float32)).to(DT[rows]).cuda()
+    place = r.permutation(n).astype(np.int32).reshape(T, k)
+    place[r.random((T, k)) < 0.2] = -1
+    w = r.normal(size=(T, k)).astype(np.float32)
+    w[place < 0] = np.nan  # a choice without a row adds nothing, whatever its weight
+    res = torch.from_numpy(r.normal(size=(T, N)).astype(np.float32)).to(DT[out]).cuda()
+    for residual in (None, res):
+        ref, mag = mo.combine(host(R.float()).astype(np.float64), place, w,
+                              None if residual is None else host(res.float()))
+        y = ops.moe_combine(R, torch.from_numpy(place).cuda(), torch.from_numpy(w).cuda(), residual=residual,
+                            Y=torch.full((T, N), 9.0, dtype=DT[out], device="cuda"))
+        assert_within(y, ref, (k + 1) * U24 * mag)
+    z = res.clone()
+    ops.moe_combine(R, torch.from_numpy(place).cuda(), torch.from_numpy(w).cuda(), residual=z, Y=z)
+    assert (host(z.float()) == host(y.float())).all()
+
+
+@pytest.mark.parametrize("T,E,k,only", SPREADS + [(2, 8, 4, None), (4, 8, 2, [2, 5]), (8, 16, 3, None), (9, 16, 3, None),
+                                                  (64, 32, 4, None)])
+@pytest.mark.parametrize("K,I,N,dtype,out", [(256, 128, 256, "bf16", "bf16"), (400, 144, 264, "f16", "f16"),
+                                             (1040, 656, 133, "f32", "f32")])
+def test_moe(ops, T, E, k, only, K, I, N, dtype, out):  # noqa: E741
+    e, w = choices(T + K, T, E, k, 0.1 if T > 2 else 0.0, only)
+    bias = K != 256
+    dg, hg = matrices(1, E, I, K, bias)
+    du, hu = matrices(2, E, I, K, bias)
+    dd, hd = matrices(3, E, N, I, bias)
+    X = activations(T, T, K, dtype)
+    res = torch.randn(T, N, generator=gen(T)).to(DT[out]) if N != 264 else None
+    ref, bound = mo.moe(X.float().numpy(), e, w, hg, hu, hd, None if res is None else res.float().numpy())
+    y = ops.fp8_moe(X.cuda(), torch.from_numpy(e).cuda(), torch.from_numpy(w).cuda(), dg, du, dd,
+                    residual=None if res is None else res.cuda(),
+                    Y=torch.full((T, N), float("nan"), dtype=DT[out], device="cuda"))
+    assert_within(y, ref, bound)
+    assert ops.convrot_device_status() == ops.OK
