@@ -63,7 +63,7 @@ cudaError_t pack_error_word(int** p);  // pack.cu: the packs
 
 namespace {
 
-constexpr int N_WORDS = 9;
+constexpr int N_WORDS = 10;
 struct ErrorWords {
   int* word[N_WORDS];
 };
@@ -588,7 +588,7 @@ int convrot_device_status(void* stream) {
   cudaError_t (*const address[N_WORDS])(int**) = {
       gemm_error_word, w4_error_word, pack_error_word, fp8::linear_error_word,
       fp8::norm_error_word<float>, fp8::norm_error_word<__half>, fp8::norm_error_word<__nv_bfloat16>,
-      moe::route_error_word, moe::expert_error_word};
+      moe::route_error_word, moe::pair_error_word, moe::few_error_word};
   for (int i = 0; i < N_WORDS; ++i)
     if ((e = address[i](&words.word[i])) != cudaSuccess) return set_cuda_error(e);
   std::lock_guard<std::mutex> lock(g_status_mu);

@@ -6,33 +6,15 @@
 //
 // and, for a gate and an up matrix, h = silu(g) u, quantized over 128 features
 // as it leaves.
-#include "moe_common.cuh"
+#include "expert_common.cuh"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace convrot {
 namespace moe {
 
-using namespace fp8;
-
-__device__ int g_expert_error = 0;
-
 namespace {
-
-constexpr int BK = QBLOCK;
-
-// One expert's first and last row, within [0, n] whatever the plan says.
-__device__ __forceinline__ int2 rows_of(const Rows& r, int e) {
-  const int n = static_cast<int>(r.n);
-  const int a = min(max(__ldg(r.offsets + e), 0), n), b = min(max(__ldg(r.offsets + e + 1), a), n);
-  return make_int2(a, b);
-}
-// The activation row of sorted row i.
-__device__ __forceinline__ int64_t source_row(const Rows& r, int i) {
-  if (!r.order) return i;
-  const int64_t t = __ldg(r.order + i) / r.top_k;
-  return min(max(t, int64_t{0}), r.T - 1);
-}
 
 // ---------------------------------------------------------------------------
 // few rows per expert: weights streamed to registers
@@ -50,18 +32,6 @@ constexpr int CHUNK = 8;  // rows at a time
 constexpr int STREAM_WARPS = 8;
 constexpr int BLOCK_CTAS = QBLOCK / FEATURES;  // CTAs that share a block's scale
 
-__device__ __forceinline__ void mma_sync_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -133,9 +103,9 @@ __global__ void __launch_bounds__(STREAM_WARPS * 32) expert_stream_kernel(const 
     if (warp < p.KB) load_w(warp, a);
     // the row whose codes this lane holds and the two whose results it has
     // (past the last one: the last one again, not stored)
-    const uint8_t* xr = p.X + source_row(p.rows, min(i0 + g, last)) * p.K;
-    const float* s0 = p.s_x + source_row(p.rows, min(i0 + 2 * t, last)) * p.KB;
-    const float* s1 = p.s_x + source_row(p.rows, min(i0 + 2 * t + 1, last)) * p.KB;
+    const uint8_t* xr = p.X + static_cast<int64_t>(source_row(p.rows, min(i0 + g, last))) * p.K;
+    const float* s0 = p.s_x + static_cast<int64_t>(source_row(p.rows, min(i0 + 2 * t, last))) * p.KB;
+    const float* s1 = p.s_x + static_cast<int64_t>(source_row(p.rows, min(i0 + 2 * t + 1, last))) * p.KB;
     float acc[W][4] = {};
     for (int kb = warp; kb < p.KB; kb += NW) {
       if (kb + NW < p.KB) load_w(kb + NW, next);
@@ -236,12 +206,20 @@ int launch_stream(StreamParams& p, cudaStream_t stream) {
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
+int pick(const Rows& r) {
+  if (const char* v = getenv("EXPERT_KERNEL")) return atoi(v);
+  return r.n / r.E > 64 ? 2 : 1;
+}
+
 }  // namespace
 
 int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& gate,
                          const convrot_experts& up, uint8_t* Q_h, float* s_h, cudaStream_t stream,
                          uint64_t test_wait_ns) {
-  (void)test_wait_ns;
+  const ExpertCall c{Q, s, K, r, &gate, &up, Q_h, s_h, gate.N, 0, test_wait_ns};
+  const int which = pick(r);
+  if (which == 2) return launch_expert_pair(c, stream);
+  if (which == 1) return launch_expert_few(c, stream);
   StreamParams p = stream_params(Q, s, K, r, gate.N);
   p.w[0] = gate;
   p.w[1] = up;
@@ -253,7 +231,10 @@ int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows
 
 int launch_expert_linear(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& w, void* Y,
                          int64_t ldy, int y_dtype, cudaStream_t stream, uint64_t test_wait_ns) {
-  (void)test_wait_ns;
+  const ExpertCall c{Q, s, K, r, &w, nullptr, Y, nullptr, ldy, y_dtype, test_wait_ns};
+  const int which = pick(r);
+  if (which == 2) return launch_expert_pair(c, stream);
+  if (which == 1) return launch_expert_few(c, stream);
   StreamParams p = stream_params(Q, s, K, r, w.N);
   p.w[0] = w;
   p.out = Y;
@@ -262,8 +243,6 @@ int launch_expert_linear(const uint8_t* Q, const float* s, int64_t K, const Rows
   if (y_dtype == CONVROT_F16) return launch_stream<false, __half>(p, stream);
   return launch_stream<false, __nv_bfloat16>(p, stream);
 }
-
-cudaError_t expert_error_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_expert_error); }
 
 }  // namespace moe
 }  // namespace convrot

@@ -46,7 +46,9 @@ int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows
                          uint64_t test_wait_ns = 0);
 int launch_expert_linear(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& w, void* Y,
                          int64_t ldy, int y_dtype, cudaStream_t stream, uint64_t test_wait_ns = 0);
-cudaError_t expert_error_word(int** p);
+// expert_pair.cu, expert_few.cu
+cudaError_t pair_error_word(int** p);
+cudaError_t few_error_word(int** p);
 
 }  // namespace moe
 }  // namespace convrot

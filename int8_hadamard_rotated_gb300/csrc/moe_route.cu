@@ -45,6 +45,7 @@ struct RouteParams {
   float* weights;
   float scale;
   int E, top_k, n_groups, per_group, top_groups, group_top, lanes_per_group;
+  uint32_t group_factor;  // e / per_group = e * group_factor >> 20 for e < 1024
   bool sigmoid, renormalise;
 };
 
@@ -81,6 +82,13 @@ __device__ __forceinline__ int warp_argmax(double v, int i) {
     }
   }
   return i;
+}
+
+// Scores in 64 bits. Out of line: inlined, the compiler moves them out of the
+// loops that rarely need them (160 us for 4096 x 256 logits).
+__device__ __noinline__ double exp64(float l, float m) { return exp(static_cast<double>(l) - static_cast<double>(m)); }
+__device__ __noinline__ double score64(float l, float m, double total, bool sigmoid) {
+  return sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : exp64(l, m) / total;
 }
 
 // exp(-c) / (1 + exp(-l)) for c = 0, or l <= c < 0: without underflow in the
@@ -156,15 +164,18 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
   double total64 = 0.0;  // softmax: formed when first needed
   auto need_total64 = [&]() {  // by the whole warp
     if (p.sigmoid || total64 != 0.0) return;
+#pragma unroll 1
+    for (int r = 0; r < EPL; ++r) {
+      float x = -INFINITY;
 #pragma unroll
-    for (int r = 0; r < EPL; ++r)
-      total64 += l[r] == -INFINITY ? 0.0 : exp(static_cast<double>(l[r]) - static_cast<double>(m));
+      for (int i = 0; i < EPL; ++i)
+        if (i == r) x = l[i];
+      total64 += x == -INFINITY ? 0.0 : exp64(x, m);
+    }
     total64 = warp_sum(total64);
   };
   auto value64 = [&](float logit, int e) {
-    const double sc = p.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(logit)))
-                                : exp(static_cast<double>(logit) - static_cast<double>(m)) / total64;
-    return biased ? sc + static_cast<double>(__ldg(p.bias + e)) : sc;
+    return score64(logit, m, total64, p.sigmoid) + (biased ? static_cast<double>(__ldg(p.bias + e)) : 0.0);
   };
 
   if (p.n_groups > 1) {
@@ -179,7 +190,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     for (int r = 0; r < EPL; ++r) {
       const int e = lane + 32 * r;
       if (e < p.E) {
-        const int at = e + e / p.per_group * P;
+        const int at = e + static_cast<int>(e * p.group_factor >> 20) * P;
         sl[at] = l[r];
         sv[at] = key[r] == 0u ? -INFINITY : exact ? l[r] : biased ? value_of(key[r]) : s[r];
       }
@@ -238,57 +249,81 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
 #pragma unroll
     for (int r = 0; r < EPL; ++r) {
       const int e = lane + 32 * r;
-      if (e < p.E && !(open >> (e / p.per_group) & 1u)) key[r] = 0u;
+      if (e < p.E && !(open >> (e * p.group_factor >> 20) & 1u)) key[r] = 0u;
     }
   }
 
-  int chosen = -1;  // lane j: the j-th expert and its logit
-  float logit = -INFINITY;
-  for (int j = 0; j < p.top_k; ++j) {
-    uint32_t top = 0u;
+  // The choice. A first turn goes by the fp32 values and takes one more than
+  // top_k; where two neighbours of that list are near, a second one compares
+  // what is near the largest in 64 bits.
+  int chosen;  // lane j: the j-th expert, its logit and its value's key
+  float logit;
+  uint32_t taken, place_key;
+  auto choose = [&](bool exact, int count) {
+    chosen = -1;
+    logit = -INFINITY;
+    taken = place_key = 0u;
+    for (int j = 0; j < count; ++j) {
+      uint32_t top = 0u;
 #pragma unroll
-    for (int r = 0; r < EPL; ++r) top = max(top, key[r]);
-    top = __reduce_max_sync(ALL, top);
-    if (top == 0u) break;
-    uint32_t e = 0xffffu;
+      for (int r = 0; r < EPL; ++r) top = max(top, taken >> r & 1u ? 0u : key[r]);
+      top = __reduce_max_sync(ALL, top);
+      if (top == 0u) break;
+      uint32_t e = 0xffffu;
 #pragma unroll
-    for (int r = EPL - 1; r >= 0; --r)
-      if (key[r] == top) e = lane + 32 * r;
-    e = __reduce_min_sync(ALL, e);
-    if (biased) {
-      const float v = value_of(top), lo = v - 2.5f * error_at(v);
-      int count = 0;
-#pragma unroll
-      for (int r = 0; r < EPL; ++r) count += key[r] != 0u && (key[r] == top || value_of(key[r]) >= lo);
-      if (__reduce_add_sync(ALL, count) > 1) {
-        need_total64();
-        double best = -INFINITY;
-        int at = INT_MAX;
+      for (int r = EPL - 1; r >= 0; --r)
+        if (key[r] == top && !(taken >> r & 1u)) e = lane + 32 * r;
+      e = __reduce_min_sync(ALL, e);
+      if (exact) {
+        const float v = value_of(top), lo = v - 2.5f * error_at(v);
+        uint32_t near = 0u;
 #pragma unroll
         for (int r = 0; r < EPL; ++r)
-          if (key[r] != 0u && (key[r] == top || value_of(key[r]) >= lo)) {
-            const double x = value64(l[r], lane + 32 * r);
-            if (at == INT_MAX || x > best) {
-              best = x;
+          if (key[r] != 0u && !(taken >> r & 1u) && (key[r] == top || value_of(key[r]) >= lo)) near |= 1u << r;
+        if (__reduce_add_sync(ALL, __popc(near)) > 1) {
+          need_total64();
+          double best = -INFINITY;
+          int at = INT_MAX;
+          for (; near; near &= near - 1) {
+            const int r = __ffs(near) - 1;
+            float x = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+              if (i == r) x = l[i];
+            const double y = value64(x, lane + 32 * r);
+            if (at == INT_MAX || y > best) {
+              best = y;
               at = lane + 32 * r;
             }
           }
-        e = warp_argmax(best, at);
+          e = warp_argmax(best, at);
+        }
       }
-    }
-    float of = 0.0f;
+      float of = 0.0f;
 #pragma unroll
-    for (int r = 0; r < EPL; ++r)
-      if (e == lane + 32 * r) {
-        of = l[r];
-        key[r] = 0u;
+      for (int r = 0; r < EPL; ++r)
+        if (e == lane + 32 * r) {
+          of = l[r];
+          taken |= 1u << r;
+        }
+      of = __shfl_sync(ALL, of, e & 31);
+      if (lane == j) {
+        chosen = static_cast<int>(e);
+        logit = of;
+        place_key = top;
       }
-    of = __shfl_sync(ALL, of, e & 31);
-    if (lane == j) {
-      chosen = static_cast<int>(e);
-      logit = of;
     }
+  };
+  // (of 32 choices the 33rd has no lane to compare with)
+  choose(biased && p.top_k == 32, min(p.top_k + (biased ? 1 : 0), 32));
+  if (biased && p.top_k < 32) {
+    const uint32_t next = __shfl_down_sync(ALL, place_key, 1);
+    const float v = value_of(place_key);
+    const bool near = lane < p.top_k && next != 0u && !(value_of(next) < v - 2.5f * error_at(v));
+    if (__any_sync(ALL, near)) choose(true, p.top_k);
+    if (lane >= p.top_k) chosen = -1;
   }
+  if (chosen < 0) logit = -INFINITY;
   // The weights from the logits: where they are renormalised, relative to the
   // largest chosen one, so that scores too small for fp32 keep their ratios.
   const float most = p.renormalise ? value_of(__reduce_max_sync(ALL, key_of(logit))) : 0.0f;
@@ -311,114 +346,98 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
 // the plan
 // ---------------------------------------------------------------------------
 //
-// A stable counting sort of n choices by expert, by one cluster: every warp
-// takes a contiguous part of the choices and counts them per expert in its own
-// row of shared memory (32 at a time; the lanes that hold the same expert find
-// each other by match, and one of them adds their number), the rows' prefix
-// sums give every warp its first place in every expert, and a second turn over
-// the choices, which are in L1 by then, hands the places out. The CTAs' counts
-// meet through distributed shared memory. No atomics: the order is the
-// choices' own. Choices outside [0, E) count as expert E, behind all others.
+// A stable counting sort of n choices by expert in one launch: every CTA places
+// the choices of W experts and looks through all choices for them, twice. Every
+// warp has a contiguous part: the first turn counts its choices of each of the
+// CTA's experts and those of lower ones, the second hands the places out, by
+// ballots. Nothing passes between CTAs and there are no atomics: the order is
+// the choices' own. Choices outside [0, E) count as expert E, behind all others.
+// 65536 choices are read (E + 1) / W times over, from L2 and then L1; a sort in
+// one cluster of eight CTAs, each choice ranked in its warp by match, took 22 us.
 
 constexpr int PLAN_WARPS = 32;
-constexpr int PLAN_MAX_CLUSTER = 8;
+constexpr int PLAN_STEP = 4;  // choices per lane and turn
 
-__device__ __forceinline__ int ld_cluster_i32(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
+template <int W>
 __global__ void __launch_bounds__(PLAN_WARPS * 32)
-moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int n_ctas, int32_t* __restrict__ order,
+moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* __restrict__ order,
                 int32_t* __restrict__ place, int32_t* __restrict__ offsets) {
-  extern __shared__ int plan_smem[];  // counts [PLAN_WARPS][E + 1], totals [E + 1], first [E + 1]
-  __shared__ int warp_sums[PLAN_WARPS];
+  __shared__ int counts[PLAN_WARPS][W + 1];  // of the CTA's experts; of lower ones
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   constexpr uint32_t ALL = 0xffffffffu;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = E + 1;
-  const int rank = n_ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  int* counts = plan_smem + warp * B;
-  int* totals = plan_smem + PLAN_WARPS * B;
-  int* first = totals + B;
-  for (int i = lane; i < B; i += 32) counts[i] = 0;
-  // this warp's choices: whole groups of 32, shared out evenly
-  const int64_t groups = (n + 31) / 32, parts = static_cast<int64_t>(n_ctas) * PLAN_WARPS;
-  const int64_t part = static_cast<int64_t>(rank) * PLAN_WARPS + warp;
-  const int64_t g0 = groups * part / parts, g1 = groups * (part + 1) / parts;
-  auto bucket_at = [&](int64_t i) {
-    if (i >= n) return -1;
-    const int e = __ldg(experts + i);
-    return e >= 0 && e < E ? e : E;
-  };
-  __syncwarp();
-  int next = g0 < g1 ? bucket_at(g0 * 32 + lane) : -1;
-  for (int64_t g = g0; g < g1; ++g) {
-    const int b = next;
-    if (g + 1 < g1) next = bucket_at((g + 1) * 32 + lane);
-    if (b == E && __ldg(experts + g * 32 + lane) != -1) record_error(&g_moe_error, CONVROT_ERR_ARG);
-    const uint32_t same = __match_any_sync(ALL, b);
-    if (b >= 0 && (same >> lane) == 1u) counts[b] += __popc(same);
-    __syncwarp();
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < B; e += PLAN_WARPS * 32) {
-    int sum = 0;
-    for (int w = 0; w < PLAN_WARPS; ++w) {
-      const int c = plan_smem[w * B + e];
-      plan_smem[w * B + e] = sum;
-      sum += c;
-    }
-    totals[e] = sum;
-  }
-  if (n_ctas > 1) cluster_sync(); else __syncthreads();
-  // an expert's choices in the CTAs before this one, and in all; a prefix sum
-  // over the experts, E + 1 <= 1025 of them: two threads' turns at most
-  int carry = 0;
-  for (int e0 = 0; e0 < B; e0 += PLAN_WARPS * 32) {
-    const int e = e0 + threadIdx.x;
-    int before = 0, all = 0;
-    if (e < B)
-      for (int c = 0; c < n_ctas; ++c) {
-        const int v = n_ctas > 1 ? ld_cluster_i32(mapa_shared(smem_u32(totals + e), c)) : totals[e];
-        if (c < rank) before += v;
-        all += v;
-      }
-    int scan = all;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = static_cast<int>(blockIdx.x) * W;
+  constexpr int TURN = 32 * PLAN_STEP;
+  const int64_t turns = (n + TURN - 1) / TURN;
+  const int64_t t0 = turns * warp / PLAN_WARPS, t1 = turns * (warp + 1) / PLAN_WARPS;
+  // a turn's choices, as places among the CTA's experts: negative for lower ones
+  auto load = [&](int64_t t, int (&b)[PLAN_STEP]) {
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int v = __shfl_up_sync(ALL, scan, d);
-      if (lane >= d) scan += v;
+    for (int j = 0; j < PLAN_STEP; ++j) {
+      const int64_t i = t * TURN + 32 * j + lane;
+      int e = INT_MAX;
+      if (i < n) {
+        e = __ldg(experts + i);
+        if (e < 0 || e >= E) {
+          if (e != -1) record_error(&g_moe_error, CONVROT_ERR_ARG);
+          e = E;
+        }
+        e -= e0;
+      }
+      b[j] = e;
     }
-    if (lane == 31) warp_sums[warp] = scan;
-    __syncthreads();
-    int ahead = carry;
-    for (int w = 0; w < PLAN_WARPS; ++w) {
-      if (w < warp) ahead += warp_sums[w];
-      carry += warp_sums[w];
-    }
-    if (e < B) {
-      first[e] = ahead + scan - all + before;
-      if (rank == 0) offsets[e] = ahead + scan - all;  // offsets[E]: where the choices of no expert begin
-    }
-    __syncthreads();
-  }
-  for (int64_t g = g0; g < g1; ++g) {
-    const int64_t i = g * 32 + lane;
-    const int b = bucket_at(i);
-    const uint32_t same = __match_any_sync(ALL, b);
-    int at = 0;
-    if (b >= 0) at = first[b] + counts[b] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (b >= 0 && (same >> lane) == 1u) counts[b] += __popc(same);
-    __syncwarp();
-    if (b >= 0) {
-      order[at] = b < E ? static_cast<int32_t>(i) : -1;
-      place[i] = b < E ? at : -1;
+  };
+  int mine[W] = {}, lower = 0;
+  for (int64_t t = t0; t < t1; ++t) {
+    int b[PLAN_STEP];
+    load(t, b);
+#pragma unroll
+    for (int j = 0; j < PLAN_STEP; ++j) {
+      lower += b[j] < 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) mine[w] += b[j] == w;
     }
   }
-  if (n_ctas > 1) cluster_sync();  // the others' reads of this CTA's totals
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const int c = __reduce_add_sync(ALL, mine[w]);
+    if (lane == 0) counts[warp][w] = c;
+  }
+  lower = __reduce_add_sync(ALL, lower);
+  if (lane == 0) counts[warp][W] = lower;
+  __syncthreads();
+  // lane v has warp v's counts
+  int at[W], first = __reduce_add_sync(ALL, counts[lane][W]);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const int c = counts[lane][w];
+    at[w] = first + __reduce_add_sync(ALL, lane < warp ? c : 0);
+    if (threadIdx.x == 0 && e0 + w <= E) offsets[e0 + w] = first;
+    first += __reduce_add_sync(ALL, c);
+  }
+  const uint32_t before = (1u << lane) - 1u;
+  for (int64_t t = t0; t < t1; ++t) {
+    int b[PLAN_STEP];
+    load(t, b);
+#pragma unroll
+    for (int j = 0; j < PLAN_STEP; ++j) {
+      const bool here = b[j] >= 0 && b[j] < W;
+      if (!__any_sync(ALL, here)) continue;
+      int to = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint32_t same = __ballot_sync(ALL, b[j] == w);
+        if (b[j] == w) to = at[w] + __popc(same & before);
+        at[w] += __popc(same);
+      }
+      if (here) {
+        const int64_t i = t * TURN + 32 * j + lane;
+        const bool some = e0 + b[j] < E;
+        order[to] = some ? static_cast<int32_t>(i) : -1;
+        place[i] = some ? to : -1;
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -534,6 +553,7 @@ int launch_route(const convrot_moe_route_args& a, cudaStream_t stream) {
   p.top_k = a.top_k;
   p.n_groups = a.n_groups;
   p.per_group = a.n_experts / a.n_groups;
+  p.group_factor = ((1u << 20) + p.per_group - 1) / p.per_group;
   p.top_groups = a.top_groups;
   p.group_top = a.group_top;
   p.lanes_per_group = 1;
@@ -545,19 +565,21 @@ int launch_route(const convrot_moe_route_args& a, cudaStream_t stream) {
   return route_as<__nv_bfloat16>(p, stream);
 }
 
+template <int W>
+static int plan_as(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
+                   cudaStream_t stream) {
+  Launch l(static_cast<unsigned>((E + W) / W), PLAN_WARPS * 32, 0, stream);  // E + 1 buckets
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, moe_plan_kernel<W>, experts, n, E, order, place, offsets);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+// As many experts per CTA as give every SM one CTA.
 int launch_plan(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
                 cudaStream_t stream) {
-  // one CTA while its warps have a few turns each
-  int ctas = 1;
-  while (ctas < PLAN_MAX_CLUSTER && n > ctas * PLAN_WARPS * 64) ctas *= 2;
-  const size_t smem = sizeof(int) * (PLAN_WARPS + 2) * (E + 1);
-  static_assert(sizeof(int) * (PLAN_WARPS + 2) * (MAX_EXPERTS + 1) <= 227 * 1024, "shared memory");
-  static std::mutex mu;
-  static uint64_t done = 0;
-  if (int st = fp8::allow_smem(moe_plan_kernel, sizeof(int) * (PLAN_WARPS + 2) * (MAX_EXPERTS + 1), done, mu)) return st;
-  Launch l(ctas, PLAN_WARPS * 32, smem, stream, ctas);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, moe_plan_kernel, experts, n, E, ctas, order, place, offsets);
-  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+  if (E < 152) return plan_as<1>(experts, n, E, order, place, offsets, stream);
+  if (E < 304) return plan_as<2>(experts, n, E, order, place, offsets, stream);
+  if (E < 608) return plan_as<4>(experts, n, E, order, place, offsets, stream);
+  return plan_as<8>(experts, n, E, order, place, offsets, stream);
 }
 
 int launch_combine(const CombineArgs& a, cudaStream_t stream) {
