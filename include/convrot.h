@@ -768,6 +768,10 @@ typedef struct convrot_experts {
   int64_t bias_stride;  /* >= N */
 } convrot_experts;
 
+/* Device bytes that the two expert linears need for n rows taken by an order;
+ * 0 for invalid sizes, and where they need none. */
+size_t fp8_expert_workspace_size(int64_t n, int64_t K, int n_experts);
+
 /*
  * fp8_expert_linear -- for every row i < offsets[E] of the plan, e its expert
  * and m = order[i] / top_k its activation row (m = i where order is NULL):
@@ -776,13 +780,17 @@ typedef struct convrot_experts {
  * fp8_linear_packed, one rounding to y_dtype. Rows of Y from offsets[E] on are
  * left as they are. Results repeat bit for bit.
  *   order, offsets  of moe_plan for n choices; T >= n where order is NULL.
- * Errors: those of fp8_linear_packed; ERR_ARG (also n_experts or top_k below
+ *   workspace  with order: at least fp8_expert_workspace_size(n, K, n_experts)
+ *              bytes, 16-byte aligned (NULL where that is 0): many rows per
+ *              expert are sorted there first.
+ * Errors: those of fp8_linear_packed; ERR_WORKSPACE; ERR_ARG (also n_experts or top_k below
  *         1), ERR_ALIGN (also q_stride % 16), ERR_UNSUPPORTED (more experts
  *         than CONVROT_MOE_MAX_EXPERTS).
  */
 int fp8_expert_linear(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
                       const int32_t* offsets, int64_t n, int n_experts, int top_k,
-                      const convrot_experts* weight, void* Y, int64_t ldy, int y_dtype, void* stream);
+                      const convrot_experts* weight, void* Y, int64_t ldy, int y_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /*
  * fp8_expert_swiglu -- the same rows through two matrices, gate and up:
@@ -796,7 +804,7 @@ int fp8_expert_linear(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K
 int fp8_expert_swiglu(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
                       const int32_t* offsets, int64_t n, int n_experts, int top_k,
                       const convrot_experts* gate, const convrot_experts* up, uint8_t* Q_h, float* s_h,
-                      void* stream);
+                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * moe_combine -- Y[t,:] = residual[t,:] + sum_j weights[t,j] rows[place[t,j],:],

@@ -134,17 +134,8 @@ __device__ __forceinline__ void tma_gather4(void* smem_dst, const void* tmap, ui
       "r"(smem_u32(bar)), "l"(cache_hint)
       : "memory");
 }
-// The same, counted on an mbarrier of either CTA of the pair.
-__device__ __forceinline__ void tma_gather4_pair(void* smem_dst, const void* tmap, uint32_t bar_cluster_addr, int32_t x,
-                                                 int4 rows, uint64_t cache_hint) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;"
-      ::"r"(smem_u32(smem_dst)), "l"(tmap), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w),
-      "r"(bar_cluster_addr), "l"(cache_hint)
-      : "memory");
-}
-// A box of a three-dimensional map (an expert's matrix), likewise.
+// A box of a three-dimensional map (an expert's matrix), counted on an mbarrier
+// of either CTA of the pair.
 __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t bar_cluster_addr, int32_t x,
                                                  int32_t y, int32_t z, uint64_t cache_hint) {
   asm volatile(

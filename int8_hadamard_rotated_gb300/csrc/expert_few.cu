@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 namespace convrot {
 namespace moe {
@@ -420,7 +421,8 @@ int launch_as(const ExpertCall& c, cudaStream_t stream) {
   const double items = std::max(reached, static_cast<double>(n) / BN) * static_cast<double>(cols);
   const int sms = device_sm_count();
   int split = 1;
-  while (split < MAX_SPLIT && items * split < 4 * sms && 2 * split <= KB) split *= 2;
+  while (split < MAX_SPLIT && items * split < 0.5 * sms && 2 * split <= KB) split *= 2;
+  if (const char* v = getenv("EXPERT_SPLIT")) { split = atoi(v); while (split > KB) split /= 2; }
   static std::mutex units_mu;
   static int units_of[64][MAX_SPLIT + 1] = {};
   int dev = 0;

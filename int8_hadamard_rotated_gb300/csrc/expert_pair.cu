@@ -6,9 +6,8 @@
 // weights, M = 256 MMAs of the even CTA, one TMEM accumulator per block of K,
 // promoted with the block's scales into fp32 registers that stay for the tile.
 // What differs: which tiles there are is known on the device alone (every CTA
-// sums the experts' row tiles up when it starts); the activation rows are
-// gathered by the plan (32 gather copies of four rows, one per lane of the
-// loading warp) or lie together; and with SwiGLU a tile's weight rows are 128
+// sums the experts' row tiles up when it starts); a tile's last rows may be the
+// next expert's, and are not stored; and with SwiGLU a tile's weight rows are 128
 // of the gate and the same 128 of the up matrix, dealt out in runs of 64 so
 // that every epilogue thread has gate and up of the same 64 features of its
 // row. It forms h there; the two threads of a row exchange their maxima through
@@ -34,12 +33,12 @@ constexpr int STORE_BYTES = 2 * STORE_BLOCK;  // one warp's two store buffers
 constexpr int ROWS = 256;                     // of a tile
 
 struct PairParams {
-  CUtensorMap tmap_x;     // codes [T,K], box one row (gathered) or LANES rows
+  CUtensorMap tmap_x;     // codes [n,K] in the plan's order
   CUtensorMap tmap_w[2];  // codes [E][N,K]: the matrix, or gate and up
   CUtensorMap tmap_y;     // Y [n,N], where tma_y
   Rows rows;
   convrot_experts w[2];
-  const float* s_x;  // [T,KB]
+  const float* s_x;  // [n,KB]
   void* out;         // Y, or the codes of h
   float* s_out;      // their scales
   int64_t ldy;
@@ -160,21 +159,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) expert_pair_kernel(const __gr
     if (warp == EPI_WARPS) {
       const uint64_t pol = l2_policy_evict_normal();
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
-      const bool gather = p.rows.order != nullptr;
       uint32_t stage = 0, phase = 0, n_issued = 0;
       bool ok = true;
       for (int t = unit; ok && t < total; t += n_units) {
         int2 range;
         const Item c = find_item_grouped(p.rows, ROWS, first, p.n_cols, t, range);
         const int row = range.x + c.tile * ROWS + static_cast<int>(rank) * LANES;
-        int4 rows;  // this lane's four rows of the tile (past the expert's last: that one again)
-        if (gather) {
-          const int i = row + 4 * lane, last = range.y - 1;
-          rows.x = source_row(p.rows, min(i, last));
-          rows.y = source_row(p.rows, min(i + 1, last));
-          rows.z = source_row(p.rows, min(i + 2, last));
-          rows.w = source_row(p.rows, min(i + 3, last));
-        }
         for (int kb = 0; kb < p.KB; ++kb) {
           if (p.withhold && t == total - 1 && kb == p.KB - 1) break;
           ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, err, p.wait_ns);
@@ -191,10 +181,9 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) expert_pair_kernel(const __gr
             } else {
               tma_load_3d_pair(sw, &p.tmap_w[0], fb, kb * BK, c.col * FEATURES + static_cast<int>(rank) * LANES, c.expert, pol);
             }
-            if (!gather) tma_load_2d_pair(sx, &p.tmap_x, fb, kb * BK, row, pol);
+            tma_load_2d_pair(sx, &p.tmap_x, fb, kb * BK, row, pol);
           }
           __syncwarp();
-          if (gather) tma_gather4_pair(sx + lane * 4 * BK, &p.tmap_x, fb, kb * BK, rows, pol);
           ++n_issued;
           if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -287,7 +276,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) expert_pair_kernel(const __gr
       c.row += 32 * quarter;  // the warp's first row
       // rows past the expert's last read the last one's scales; their outputs
       // are not stored
-      xs = p.s_x + static_cast<int64_t>(source_row(p.rows, min(c.row + lane, c.end - 1))) * p.KB;
+      xs = p.s_x + static_cast<int64_t>(min(c.row + lane, c.end - 1)) * p.KB;
       ws0 = SWIGLU || half == 0 ? c.ws[0] : c.ws[1];
       ws1 = c.ws[1];
       load_scales(xs, 0, p.KB, p.vec_scales, nx);
@@ -433,7 +422,7 @@ int launch_as(const ExpertCall& c, cudaStream_t stream) {
   using G = Geom;
   const int64_t N = c.w->N, KB = n_blocks(c.K);
   PairParams p;
-  if (int st = make_tmap_codes(&p.tmap_x, c.Q, c.rows.T, c.K, c.rows.order ? 1 : LANES)) return st;
+  if (int st = make_tmap_codes(&p.tmap_x, c.Q, c.rows.n, c.K, LANES)) return st;
   for (int j = 0; j < (SWIGLU ? 2 : 1); ++j) {
     p.w[j] = j ? *c.up : *c.w;
     if (int st = make_tmap_experts(&p.tmap_w[j], p.w[j], c.rows.E, c.K, SWIGLU ? 64 : LANES)) return st;

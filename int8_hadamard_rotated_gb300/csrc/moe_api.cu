@@ -79,6 +79,33 @@ bool meets_inputs(const Region& out, const uint8_t* Q_x, const float* s_x, int64
          meet(out, flat(offsets, (E + 1) * 4));
 }
 
+size_t sorted_bytes(int64_t n, int64_t K) {
+  return round256(static_cast<size_t>(n) * K) + round256(static_cast<size_t>(n) * n_blocks(K) * 4);
+}
+// Where the linear wants its rows in the plan's order and they come by token,
+// they are sorted into the workspace first: its checks (ws: the part in use) ...
+int workspace_checks(void* workspace, size_t bytes, const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K,
+                     const int32_t* order, const int32_t* offsets, int64_t n, int E, Region& ws) {
+  ws = flat(nullptr, 0);
+  if (!order || !many_rows(n, E)) return CONVROT_OK;
+  if (!workspace || bytes < sorted_bytes(n, K)) return CONVROT_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return CONVROT_ERR_ALIGN;
+  if (n > 0x7fffffff / n_blocks(K)) return CONVROT_ERR_UNSUPPORTED;
+  ws = flat(workspace, static_cast<int64_t>(sorted_bytes(n, K)));
+  return meets_inputs(ws, Q_x, s_x, T, K, order, offsets, n, E) ? CONVROT_ERR_ALIAS : CONVROT_OK;
+}
+// ... and the sort; Q_x, s_x and rows are the sorted ones from then on.
+int sort_rows(const uint8_t*& Q_x, const float*& s_x, int64_t K, Rows& rows, const Region& ws, cudaStream_t stream) {
+  if (!ws.p) return CONVROT_OK;
+  uint8_t* q = static_cast<uint8_t*>(const_cast<void*>(ws.p));
+  float* s = reinterpret_cast<float*>(q + round256(static_cast<size_t>(rows.n) * K));
+  if (int st = launch_gather(Q_x, s_x, K, rows, q, s, stream)) return st;
+  Q_x = q;
+  s_x = s;
+  rows = Rows{nullptr, rows.offsets, rows.n, rows.n, rows.E, 1};
+  return CONVROT_OK;
+}
+
 int combine_checks(const CombineArgs& a) {
   if (a.T < 0 || a.n < 0 || a.N < 0 || a.top_k < 1 || !known_dtype(a.r_dtype) || !known_dtype(a.y_dtype) ||
       a.ldr < a.N || a.ldy < a.N || (a.residual && a.ld_res < a.N))
@@ -111,8 +138,9 @@ struct Workspace {
       at += round256(b);
       return here;
     };
-    q_x = take(static_cast<size_t>(T) * K);
-    s_x = take(static_cast<size_t>(T) * n_blocks(K) * 4);
+    const size_t m = static_cast<size_t>(many_rows(n, E) ? n : T);  // rows sorted by expert, or tokens
+    q_x = take(m * K);
+    s_x = take(m * n_blocks(K) * 4);
     order = take(static_cast<size_t>(n) * 4);
     place = take(static_cast<size_t>(n) * 4);
     offsets = take(static_cast<size_t>(E + 1) * 4);
@@ -145,7 +173,7 @@ int moe_checks(const convrot_moe_args& a, void* workspace, size_t workspace_byte
   for (const auto& [w, K] : {std::pair{a.gate, a.K}, std::pair{a.up, a.K}, std::pair{a.down, I}})
     if (int st = experts_checks(*w, a.n_experts, K)) return st;
   if (!sane(a.T, a.ldx) || !sane(a.T, a.ldy) || (a.residual && !sane(a.T, a.ld_res)) ||
-      a.T > 0x7fffffff / n_blocks(a.K) || n > 0x7fffffff / n_blocks(I))
+      n > 0x7fffffff / n_blocks(a.K) || n > 0x7fffffff / n_blocks(I))
     return CONVROT_ERR_UNSUPPORTED;
   const Region y{a.Y, a.T, N * ys, a.ldy * ys}, work = flat(workspace, static_cast<int64_t>(ws.bytes));
   const Region in[] = {{a.X, a.T, a.K * xs, a.ldx * xs}, flat(a.experts, n * 4), flat(a.weights, n * 4)};
@@ -189,7 +217,7 @@ int moe_plan(const int32_t* experts, int64_t n, int n_experts, int32_t* order, i
 
 int fp8_expert_linear(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
                       const int32_t* offsets, int64_t n, int n_experts, int top_k, const convrot_experts* weight, void* Y,
-                      int64_t ldy, int y_dtype, void* stream) {
+                      int64_t ldy, int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
   if (!known_dtype(y_dtype)) return CONVROT_ERR_ARG;
   if (int st = expert_checks(Q_x, s_x, T, K, order, offsets, n, n_experts, top_k, weight)) return st;
   if (n == 0 || weight->N == 0) return CONVROT_OK;
@@ -200,14 +228,19 @@ int fp8_expert_linear(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K
   const Region y{Y, n, weight->N * size, ldy * size};
   if (meets_inputs(y, Q_x, s_x, T, K, order, offsets, n, n_experts) || meets(y, spans(*weight, n_experts, K)))
     return CONVROT_ERR_ALIAS;
+  Region ws;
+  if (int st = workspace_checks(workspace, workspace_bytes, Q_x, s_x, T, K, order, offsets, n, n_experts, ws)) return st;
+  if (meet(ws, y) || meets(ws, spans(*weight, n_experts, K))) return CONVROT_ERR_ALIAS;
   if (int st = check_device()) return st;
-  return launch_expert_linear(Q_x, s_x, K, Rows{order, offsets, n, T, n_experts, top_k}, *weight, Y, ldy, y_dtype,
-                              static_cast<cudaStream_t>(stream));
+  Rows rows{order, offsets, n, T, n_experts, top_k};
+  if (int st = sort_rows(Q_x, s_x, K, rows, ws, static_cast<cudaStream_t>(stream))) return st;
+  return launch_expert_linear(Q_x, s_x, K, rows, *weight, Y, ldy, y_dtype, static_cast<cudaStream_t>(stream));
 }
 
 int fp8_expert_swiglu(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
                       const int32_t* offsets, int64_t n, int n_experts, int top_k, const convrot_experts* gate,
-                      const convrot_experts* up, uint8_t* Q_h, float* s_h, void* stream) {
+                      const convrot_experts* up, uint8_t* Q_h, float* s_h, void* workspace, size_t workspace_bytes,
+                      void* stream) {
   for (const convrot_experts* w : {gate, up})
     if (int st = expert_checks(Q_x, s_x, T, K, order, offsets, n, n_experts, top_k, w)) return st;
   const int64_t N = gate->N;
@@ -222,19 +255,30 @@ int fp8_expert_swiglu(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K
     if (meets_inputs(out, Q_x, s_x, T, K, order, offsets, n, n_experts)) return CONVROT_ERR_ALIAS;
     if (meets(out, spans(*gate, n_experts, K)) || meets(out, spans(*up, n_experts, K))) return CONVROT_ERR_ALIAS;
   }
+  Region ws;
+  if (int st = workspace_checks(workspace, workspace_bytes, Q_x, s_x, T, K, order, offsets, n, n_experts, ws)) return st;
+  if (meet(ws, q) || meet(ws, s) || meets(ws, spans(*gate, n_experts, K)) || meets(ws, spans(*up, n_experts, K)))
+    return CONVROT_ERR_ALIAS;
   if (int st = check_device()) return st;
-  return launch_expert_swiglu(Q_x, s_x, K, Rows{order, offsets, n, T, n_experts, top_k}, *gate, *up, Q_h, s_h,
-                              static_cast<cudaStream_t>(stream));
+  Rows rows{order, offsets, n, T, n_experts, top_k};
+  if (int st = sort_rows(Q_x, s_x, K, rows, ws, static_cast<cudaStream_t>(stream))) return st;
+  return launch_expert_swiglu(Q_x, s_x, K, rows, *gate, *up, Q_h, s_h, static_cast<cudaStream_t>(stream));
 }
 
 int moe_combine(const void* rows, int r_dtype, int64_t ldr, int64_t n, const int32_t* place, const float* weights,
                 int64_t T, int top_k, int64_t N, const void* residual, int64_t ld_res, void* Y, int64_t ldy,
                 int y_dtype, void* stream) {
-  const CombineArgs a{rows, r_dtype, ldr, n, place, weights, T, top_k, N, residual, ld_res, Y, ldy, y_dtype};
+  const CombineArgs a{rows, r_dtype, ldr, n, place, weights, T, top_k, N, residual, ld_res, Y, ldy, y_dtype,
+                      nullptr, 0};
   if (int st = combine_checks(a)) return st;
   if (T == 0 || N == 0) return CONVROT_OK;
   if (int st = check_device()) return st;
   return launch_combine(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t fp8_expert_workspace_size(int64_t n, int64_t K, int n_experts) {
+  if (n < 0 || K <= 0 || n > MAX_ROWS || K > MAX_LENGTH || n_experts < 1 || n_experts > MAX_EXPERTS) return 0;
+  return many_rows(n, n_experts) ? sorted_bytes(n, K) : 0;
 }
 
 size_t fp8_moe_workspace_size(int64_t T, int64_t K, int64_t I, int64_t N, int top_k, int n_experts, int y_dtype) {
@@ -257,12 +301,15 @@ int fp8_moe(const convrot_moe_args* args, void* workspace, size_t workspace_byte
   int32_t *order = reinterpret_cast<int32_t*>(ws + at.order), *place = reinterpret_cast<int32_t*>(ws + at.place);
   int32_t* offsets = reinterpret_cast<int32_t*>(ws + at.offsets);
   if (int st = launch_plan(a.experts, n, a.n_experts, order, place, offsets, s)) return st;
-  if (int st = launch_fp8_pack(a.X, a.x_dtype, a.T, a.K, a.ldx, q_x, s_x, s)) return st;
   const Rows by_token{order, offsets, n, a.T, a.n_experts, a.top_k}, sorted{nullptr, offsets, n, n, a.n_experts, 1};
-  if (int st = launch_expert_swiglu(q_x, s_x, a.K, by_token, *a.gate, *a.up, q_h, s_h, s)) return st;
+  const bool many = many_rows(n, a.n_experts);
+  if (int st = many ? launch_pack_sorted(a.X, a.x_dtype, a.T, a.K, a.ldx, place, a.top_k, q_x, s_x, s)
+                    : launch_fp8_pack(a.X, a.x_dtype, a.T, a.K, a.ldx, q_x, s_x, s))
+    return st;
+  if (int st = launch_expert_swiglu(q_x, s_x, a.K, many ? sorted : by_token, *a.gate, *a.up, q_h, s_h, s)) return st;
   if (int st = launch_expert_linear(q_h, s_h, I, sorted, *a.down, ws + at.rows, N, CONVROT_F32, s)) return st;
   return launch_combine(CombineArgs{ws + at.rows, CONVROT_F32, N, n, place, a.weights, a.T, a.top_k, N, a.residual,
-                                    a.ld_res, a.Y, a.ldy, a.y_dtype}, s);
+                                    a.ld_res, a.Y, a.ldy, a.y_dtype, nullptr, 0}, s);
 }
 
 }  // extern "C"

@@ -36,10 +36,21 @@ struct CombineArgs {
   void* Y;
   int64_t ldy;
   int y_dtype;
+  const float* r_scale;  // [n, r_blocks] a factor per row and 128 features of rows, or null
+  int64_t r_blocks;
 };
 int launch_combine(const CombineArgs& a, cudaStream_t stream);
 cudaError_t route_error_word(int** p);
 
+// Codes and scales by token, or X itself, to codes and scales in the plan's order.
+int launch_gather(const uint8_t* Q, const float* s, int64_t K, const Rows& r, uint8_t* Q_out, float* s_out,
+                  cudaStream_t stream);
+int launch_pack_sorted(const void* X, int x_dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* place, int top_k,
+                       uint8_t* Q, float* s, cudaStream_t stream);
+
+// Whether n rows of E experts are taken by the kernel for many rows per expert,
+// which wants them in the plan's order (r.order null).
+bool many_rows(int64_t n, int E);
 // expert_gemm.cu: n, T > 0, every width > 0.
 int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& gate,
                          const convrot_experts& up, uint8_t* Q_h, float* s_h, cudaStream_t stream,

@@ -4,6 +4,7 @@
 #include "moe_common.cuh"
 
 #include <climits>
+#include <type_traits>
 
 namespace convrot {
 namespace moe {
@@ -356,9 +357,9 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
 // one cluster of eight CTAs, each choice ranked in its warp by match, took 22 us.
 
 constexpr int PLAN_WARPS = 32;
-constexpr int PLAN_STEP = 4;  // choices per lane and turn
 
-template <int W>
+// STEP: choices per lane and turn, loaded together.
+template <int W, int STEP>
 __global__ void __launch_bounds__(PLAN_WARPS * 32)
 moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* __restrict__ order,
                 int32_t* __restrict__ place, int32_t* __restrict__ offsets) {
@@ -367,32 +368,31 @@ moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* 
   pdl_launch_dependents();
   constexpr uint32_t ALL = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = static_cast<int>(blockIdx.x) * W;
-  constexpr int TURN = 32 * PLAN_STEP;
+  constexpr int TURN = 32 * STEP;
   const int64_t turns = (n + TURN - 1) / TURN;
   const int64_t t0 = turns * warp / PLAN_WARPS, t1 = turns * (warp + 1) / PLAN_WARPS;
   // a turn's choices, as places among the CTA's experts: negative for lower ones
-  auto load = [&](int64_t t, int (&b)[PLAN_STEP]) {
+  auto load = [&](int64_t t, int (&b)[STEP]) {
+    bool bad = false;
 #pragma unroll
-    for (int j = 0; j < PLAN_STEP; ++j) {
+    for (int j = 0; j < STEP; ++j) {
       const int64_t i = t * TURN + 32 * j + lane;
-      int e = INT_MAX;
-      if (i < n) {
-        e = __ldg(experts + i);
-        if (e < 0 || e >= E) {
-          if (e != -1) record_error(&g_moe_error, CONVROT_ERR_ARG);
-          e = E;
-        }
-        e -= e0;
-      }
-      b[j] = e;
+      b[j] = i < n ? __ldg(experts + i) : INT_MIN;
     }
+#pragma unroll
+    for (int j = 0; j < STEP; ++j) {
+      const bool some = t * TURN + 32 * j + lane < n, in = b[j] >= 0 && b[j] < E;
+      bad |= some && !in && b[j] != -1;
+      b[j] = !some ? INT_MAX : (in ? b[j] : E) - e0;
+    }
+    if (bad) record_error(&g_moe_error, CONVROT_ERR_ARG);
   };
   int mine[W] = {}, lower = 0;
   for (int64_t t = t0; t < t1; ++t) {
-    int b[PLAN_STEP];
+    int b[STEP];
     load(t, b);
 #pragma unroll
-    for (int j = 0; j < PLAN_STEP; ++j) {
+    for (int j = 0; j < STEP; ++j) {
       lower += b[j] < 0;
 #pragma unroll
       for (int w = 0; w < W; ++w) mine[w] += b[j] == w;
@@ -417,10 +417,10 @@ moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* 
   }
   const uint32_t before = (1u << lane) - 1u;
   for (int64_t t = t0; t < t1; ++t) {
-    int b[PLAN_STEP];
+    int b[STEP];
     load(t, b);
 #pragma unroll
-    for (int j = 0; j < PLAN_STEP; ++j) {
+    for (int j = 0; j < STEP; ++j) {
       const bool here = b[j] >= 0 && b[j] < W;
       if (!__any_sync(ALL, here)) continue;
       int to = 0;
@@ -441,24 +441,97 @@ moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* 
 }
 
 // ---------------------------------------------------------------------------
+// rows in the plan's order
+// ---------------------------------------------------------------------------
+//
+// The many-row kernel reads the rows of a tile once for every column of tiles,
+// and gathering them each time costs it more than this one pass (bound by
+// writing n K bytes): copies of four rows by index take the copy engine 43 ns
+// each, 1.1 ms for 4096 tokens' 32768 rows of 4096 codes against 0.5 ms.
+
+constexpr int ROW_THREADS = 256;
+
+// Codes and scales of X by token to rows in the plan's order: a warp per row.
+__global__ void __launch_bounds__(ROW_THREADS)
+moe_gather_kernel(const uint8_t* __restrict__ Q, const float* __restrict__ s, int64_t K, int KB, const __grid_constant__ Rows r,
+                  uint8_t* __restrict__ Q_out, float* __restrict__ s_out) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+  if (i >= r.n || i >= __ldg(r.offsets + r.E)) return;
+  const int64_t m = min(max(static_cast<int64_t>(__ldg(r.order + i)) / r.top_k, int64_t{0}), r.T - 1);
+  const uint4* from = reinterpret_cast<const uint4*>(Q + m * K);
+  uint4* to = reinterpret_cast<uint4*>(Q_out + i * K);
+  const int64_t pieces = K / 16;
+  for (int64_t c0 = lane; c0 < pieces; c0 += 4 * 32) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c0 + 32 * j < pieces) v[j] = __ldg(from + c0 + 32 * j);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c0 + 32 * j < pieces) to[c0 + 32 * j] = v[j];
+  }
+  for (int b = lane; b < KB; b += 32) s_out[i * KB + b] = __ldg(s + m * KB + b);
+}
+
+// fp8_pack_kernel with the codes and scales of a token stored to every row that
+// the plan gives it.
+template <typename T>
+__global__ void __launch_bounds__(ROW_THREADS, sizeof(T) == 2 ? 8 : 6)
+moe_pack_kernel(const T* __restrict__ X, int64_t ldx, uint32_t n_qblocks, uint32_t KB, uint32_t K, bool vec,
+                const int32_t* __restrict__ place, int top_k, int64_t n, uint8_t* __restrict__ Q, float* __restrict__ s) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const uint32_t sub = threadIdx.x & 7, b = blockIdx.x * (ROW_THREADS / 8) + (threadIdx.x >> 3);
+  const uint32_t row = b / KB, kb = b - row * KB, col = kb * fp8::QBLOCK + sub * 16;
+  const bool on = b < n_qblocks && col < K;
+  fp8::Pair x[8];
+  if (on) {
+    fp8::load16(X + row * ldx + col, vec, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0ull;
+  }
+  float m = fp8::max_magnitude(x);
+#pragma unroll
+  for (int d = 1; d < 8; d *= 2) m = fp8::max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float sc = fp8::e4m3_scale(m);
+  uint32_t c[4];
+  fp8::e4m3_codes(x, sc, fp8::e4m3_factor(sc), c);
+  if (!on) return;
+  const uint4 codes = make_uint4(c[0], c[1], c[2], c[3]);
+  for (int j = 0; j < top_k; ++j) {
+    const int64_t p = __ldg(place + static_cast<int64_t>(row) * top_k + j);
+    if (p < 0 || p >= n) continue;
+    *reinterpret_cast<uint4*>(Q + p * K + col) = codes;
+    if (sub == 0) s[p * KB + kb] = sc;
+  }
+}
+
+// ---------------------------------------------------------------------------
 // the weighted sum
 // ---------------------------------------------------------------------------
 //
 //   Y[t] = residual[t] + sum_j weights[t,j] rows[place[t,j]], summed in fp32 in
 // the order of j, one rounding at the end. Reads every row once: bound by HBM.
 
-constexpr int COMBINE_THREADS = 256;
+// A token's rows are loaded several at a time: one after the other, their
+// latencies add up (bf16 [32, 2048] of eight rows 7.5 us).
 
-template <typename T>
-__device__ __forceinline__ void add8(float (&acc)[8], const T* p, float w) {
-  fp8::Pair x[4];
-  fp8::load8(p, x);
+constexpr int COMBINE_THREADS = 128;
+constexpr int COMBINE_BATCH = 8;
+
+template <int E, typename T>
+__device__ __forceinline__ void load_row(const T* p, float (&x)[E]) {
+  if constexpr (E == 8) {
+    fp8::Pair v[4];
+    fp8::load8(p, v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b;
-    f32x2_unpack(x[i], a, b);
-    acc[2 * i] = fmaf(w, a, acc[2 * i]);
-    acc[2 * i + 1] = fmaf(w, b, acc[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) f32x2_unpack(v[i], x[2 * i], x[2 * i + 1]);
+  } else {
+    x[0] = to_f32(*p);
   }
 }
 
@@ -475,23 +548,41 @@ __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const __gr
 #pragma unroll
   for (int k = 0; k < E; ++k) acc[k] = 0.0f;
   const TR* rows = static_cast<const TR*>(a.rows) + col;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t r = __ldg(a.place + t * a.top_k + j);
-    if (r < 0 || r >= a.n) continue;
-    const float w = __ldg(a.weights + t * a.top_k + j);
-    if constexpr (VEC) add8(acc, rows + r * a.ldr, w);
-    else acc[0] = fmaf(w, to_f32(rows[r * a.ldr]), acc[0]);
+  for (int j0 = 0; j0 < a.top_k; j0 += COMBINE_BATCH) {
+    float x[COMBINE_BATCH][E], w[COMBINE_BATCH];
+    int64_t r[COMBINE_BATCH];
+#pragma unroll
+    for (int j = 0; j < COMBINE_BATCH; ++j) {
+      const bool on = j0 + j < a.top_k;
+      r[j] = on ? __ldg(a.place + t * a.top_k + j0 + j) : -1;
+      w[j] = on ? __ldg(a.weights + t * a.top_k + j0 + j) : 0.0f;
+      if (r[j] >= a.n) r[j] = -1;
+    }
+#pragma unroll
+    for (int j = 0; j < COMBINE_BATCH; ++j)
+      if (r[j] >= 0) load_row<E>(rows + r[j] * a.ldr, x[j]);
+#pragma unroll
+    for (int j = 0; j < COMBINE_BATCH; ++j)
+      if (r[j] >= 0) {
+        if (a.r_scale) w[j] *= __ldg(a.r_scale + r[j] * a.r_blocks + col / fp8::QBLOCK);
+#pragma unroll
+        for (int k = 0; k < E; ++k) acc[k] = fmaf(w[j], x[j][k], acc[k]);
+      }
   }
   TY* y = static_cast<TY*>(a.Y) + t * a.ldy + col;
-  const TY* res = a.residual ? static_cast<const TY*>(a.residual) + t * a.ld_res + col : nullptr;
+  if (a.residual) {
+    float x[E];
+    load_row<E>(static_cast<const TY*>(a.residual) + t * a.ld_res + col, x);
+#pragma unroll
+    for (int k = 0; k < E; ++k) acc[k] += x[k];
+  }
   if constexpr (VEC) {
-    if (res) add8(acc, res, 1.0f);
     fp8::Pair x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = f32x2_pack(acc[2 * k], acc[2 * k + 1]);
     fp8::store8(y, x);
   } else {
-    *y = from_f32<TY>(res ? acc[0] + to_f32(*res) : acc[0]);
+    *y = from_f32<TY>(acc[0]);
   }
 }
 
@@ -569,7 +660,9 @@ template <int W>
 static int plan_as(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
                    cudaStream_t stream) {
   Launch l(static_cast<unsigned>((E + W) / W), PLAN_WARPS * 32, 0, stream);  // E + 1 buckets
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, moe_plan_kernel<W>, experts, n, E, order, place, offsets);
+  const cudaError_t e = n > PLAN_WARPS * 32 * 8
+                            ? cudaLaunchKernelEx(&l.cfg, moe_plan_kernel<W, 16>, experts, n, E, order, place, offsets)
+                            : cudaLaunchKernelEx(&l.cfg, moe_plan_kernel<W, 4>, experts, n, E, order, place, offsets);
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
@@ -580,6 +673,33 @@ int launch_plan(const int32_t* experts, int64_t n, int E, int32_t* order, int32_
   if (E < 304) return plan_as<2>(experts, n, E, order, place, offsets, stream);
   if (E < 608) return plan_as<4>(experts, n, E, order, place, offsets, stream);
   return plan_as<8>(experts, n, E, order, place, offsets, stream);
+}
+
+int launch_gather(const uint8_t* Q, const float* s, int64_t K, const Rows& r, uint8_t* Q_out, float* s_out,
+                  cudaStream_t stream) {
+  const int64_t per = ROW_THREADS / 32;
+  Launch l(static_cast<unsigned>((r.n + per - 1) / per), ROW_THREADS, 0, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, moe_gather_kernel, Q, s, K, static_cast<int>(fp8::n_blocks(K)), r, Q_out, s_out);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+template <typename T>
+static int pack_as(const void* X, int64_t T_, int64_t K, int64_t ldx, const int32_t* place, int top_k, uint8_t* Q, float* s,
+                   cudaStream_t stream) {
+  const int64_t KB = fp8::n_blocks(K), blocks = T_ * KB, per = ROW_THREADS / 8;
+  const bool vec = aligned16(X) && (ldx * sizeof(T)) % 16 == 0;
+  Launch l(static_cast<unsigned>((blocks + per - 1) / per), ROW_THREADS, 0, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, moe_pack_kernel<T>, static_cast<const T*>(X), ldx,
+                                           static_cast<uint32_t>(blocks), static_cast<uint32_t>(KB),
+                                           static_cast<uint32_t>(K), vec, place, top_k, T_ * top_k, Q, s);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+int launch_pack_sorted(const void* X, int x_dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* place, int top_k,
+                       uint8_t* Q, float* s, cudaStream_t stream) {
+  if (x_dtype == CONVROT_F32) return pack_as<float>(X, T, K, ldx, place, top_k, Q, s, stream);
+  if (x_dtype == CONVROT_F16) return pack_as<__half>(X, T, K, ldx, place, top_k, Q, s, stream);
+  return pack_as<__nv_bfloat16>(X, T, K, ldx, place, top_k, Q, s, stream);
 }
 
 int launch_combine(const CombineArgs& a, cudaStream_t stream) {

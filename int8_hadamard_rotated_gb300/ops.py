@@ -172,8 +172,10 @@ SIGNATURES = {
     "fp8_linear": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I, _I, _VP, _SZ, _VP]),
     "moe_route": (_I, [_VP, _VP]),
     "moe_plan": (_I, [_VP, _I64, _I, _VP, _VP, _VP, _VP]),
-    "fp8_expert_linear": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I, _I, _VP, _VP, _I64, _I, _VP]),
-    "fp8_expert_swiglu": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I, _I, _VP, _VP, _VP, _VP, _VP]),
+    "fp8_expert_linear": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I, _I, _VP, _VP, _I64, _I, _VP, _SZ,
+                               _VP]),
+    "fp8_expert_swiglu": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I, _I, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "fp8_expert_workspace_size": (_SZ, [_I64, _I64, _I]),
     "moe_combine": (_I, [_VP, _I, _I64, _I64, _VP, _VP, _I64, _I, _I64, _VP, _I64, _VP, _I64, _I, _VP]),
     "fp8_moe_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I, _I, _I]),
     "fp8_moe": (_I, [_VP, _VP, _SZ, _VP]),
@@ -1102,9 +1104,27 @@ def _plan_of(Q_x, s_x, order, offsets, E: int, device: int):
             _dense(offsets, "offsets", device, (E + 1,), torch.int32))
 
 
+def fp8_expert_workspace_size(n: int, K: int, n_experts: int) -> int:
+    return int(lib().fp8_expert_workspace_size(n, K, n_experts))
+
+
+def _bytes(workspace, size: int, device: int, stream):
+    """(address, size) of a workspace of at least `size` bytes: the given one, or
+    a new one where some is needed (returned third, to be kept for the call)."""
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the device of the other tensors")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if size == 0:
+        return 0, 0, None
+    ws = _empty((size,), torch.uint8, device, stream)
+    return ws.data_ptr(), size, ws
+
+
 def fp8_expert_linear(Q_x: torch.Tensor, s_x: torch.Tensor, offsets: torch.Tensor, weight,
                       order: Optional[torch.Tensor] = None, top_k: int = 1, Y: Optional[torch.Tensor] = None,
-                      out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+                      out_dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
     """Rows in the order of a moe_plan, each through its expert's matrix:
     Y[i] = X[m] W_e^T + b_e, with m = i, or, given the plan's order,
     m = order[i] // top_k. weight: (codes [E,N,K], scales, biases or None) as
@@ -1116,14 +1136,15 @@ def fp8_expert_linear(Q_x: torch.Tensor, s_x: torch.Tensor, offsets: torch.Tenso
     if Y is None:
         Y = _empty((n, N), out_dtype, device, stream)
     ldy = _rows(Y, "Y", device, (n, N))
-    _check(lib().fp8_expert_linear(q, s, T, K, o, f, n, E, top_k, w, Y.data_ptr(), ldy, _DTYPES[Y.dtype], handle),
-           "fp8_expert_linear")
+    ws, size, keep = _bytes(workspace, 0 if order is None else fp8_expert_workspace_size(n, K, E), device, stream)
+    _check(lib().fp8_expert_linear(q, s, T, K, o, f, n, E, top_k, w, Y.data_ptr(), ldy, _DTYPES[Y.dtype], ws, size,
+                                   handle), "fp8_expert_linear")
     return Y
 
 
 def fp8_expert_swiglu(Q_x: torch.Tensor, s_x: torch.Tensor, order: Optional[torch.Tensor], offsets: torch.Tensor,
                       top_k: int, gate, up, Q_h: Optional[torch.Tensor] = None, s_h: Optional[torch.Tensor] = None,
-                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The rows of a moe_plan through their expert's gate and up matrices (as
     fp8_expert_linear, order and top_k included): h = silu(gate) * up, quantized
     as it leaves to (Q_h float8_e4m3fn [n,N], s_h float32 [n, ceil(N/128)]),
@@ -1139,8 +1160,10 @@ def fp8_expert_swiglu(Q_x: torch.Tensor, s_x: torch.Tensor, order: Optional[torc
         Q_h = _empty((n, N), _E4M3, device, stream)
     if s_h is None:
         s_h = _empty((n, _n_blocks(N)), _F32, device, stream)
+    ws, size, keep = _bytes(workspace, 0 if order is None else fp8_expert_workspace_size(n, K, E), device, stream)
     _check(lib().fp8_expert_swiglu(q, s, T, K, o, f, n, E, top_k, g, u, _dense(Q_h, "Q_h", device, (n, N), _E4M3),
-                                   _dense(s_h, "s_h", device, (n, _n_blocks(N)), _F32), handle), "fp8_expert_swiglu")
+                                   _dense(s_h, "s_h", device, (n, _n_blocks(N)), _F32), ws, size, handle),
+           "fp8_expert_swiglu")
     return Q_h, s_h
 
 
@@ -1199,15 +1222,11 @@ def fp8_moe(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, gate,
     ldy = _rows(Y, "Y", device, (T, N))
     res, ld_res = (0, N) if residual is None else (residual.data_ptr(),
                                                    _rows(residual, "residual", device, (T, N), Y.dtype))
-    ws = workspace
-    if ws is None:
-        ws = _empty((max(fp8_moe_workspace_size(T, K, inner, N, top_k, E, Y.dtype), 1),), torch.uint8, device, stream)
-    elif ws.get_device() != device or not ws.is_contiguous():
-        raise ValueError("workspace must be contiguous and on the device of the other tensors")
+    ws, size, keep = _bytes(workspace, fp8_moe_workspace_size(T, K, inner, N, top_k, E, Y.dtype), device, stream)
     at = lambda b: ctypes.cast(b, _VP).value  # noqa: E731
     args = convrot_moe_args(X.data_ptr(), _DTYPES[X.dtype], T, K, ldx,
                             _dense(experts, "experts", device, (T, top_k), torch.int32),
                             _dense(weights, "weights", device, (T, top_k), _F32), top_k, E, at(g), at(u), at(d),
                             res, ld_res, Y.data_ptr(), ldy, _DTYPES[Y.dtype])
-    _check(lib().fp8_moe(ctypes.byref(args), ws.data_ptr(), ws.numel() * ws.element_size(), handle), "fp8_moe")
+    _check(lib().fp8_moe(ctypes.byref(args), ws, size, handle), "fp8_moe")
     return Y
