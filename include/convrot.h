@@ -737,9 +737,12 @@ typedef struct convrot_moe_route_args {
  *         that can be open), ERR_ALIGN (an array not aligned to its elements),
  *         ERR_ALIAS, ERR_UNSUPPORTED (more than CONVROT_MOE_MAX_EXPERTS
  *         experts, CONVROT_MOE_MAX_TOP_K choices or CONVROT_MOE_MAX_GROUPS
- *         groups, 2^31 - 2^16 choices or more), ERR_DEVICE, ERR_CUDA.
+ *         groups, over 2^31 - 2^16 choices), ERR_DEVICE, ERR_CUDA.
  */
 int moe_route(const convrot_moe_route_args* args, void* stream);
+
+/* Device bytes moe_plan needs (0 for few choices, and for invalid sizes). */
+size_t moe_plan_workspace_size(int64_t n, int n_experts);
 
 /*
  * moe_plan -- n choices to rows sorted by expert, a row per choice, the
@@ -748,14 +751,16 @@ int moe_route(const convrot_moe_route_args* args, void* stream);
  *   order    [n] the choice of a row; -1 behind the last expert's rows.
  *   place    [n] the row of a choice; -1 for a choice of no expert.
  *   offsets  [E+1] an expert's first row; offsets[E] is the number of rows.
+ *   workspace  at least moe_plan_workspace_size(n, n_experts) bytes, 4-byte
+ *              aligned (NULL where that is 0).
  * A choice outside [-1, E) counts as -1 and is reported by
  * convrot_device_status as CONVROT_ERR_ARG. Results repeat bit for bit.
- * Errors: ERR_ARG, ERR_ALIGN, ERR_ALIAS, ERR_UNSUPPORTED (more experts than
- *         CONVROT_MOE_MAX_EXPERTS, 2^31 - 2^16 choices or more), ERR_DEVICE,
+ * Errors: ERR_ARG, ERR_ALIGN, ERR_ALIAS, ERR_WORKSPACE, ERR_UNSUPPORTED (more
+ *         experts than CONVROT_MOE_MAX_EXPERTS, over 2^31 - 2^16 choices), ERR_DEVICE,
  *         ERR_CUDA.
  */
 int moe_plan(const int32_t* experts, int64_t n, int n_experts, int32_t* order, int32_t* place,
-             int32_t* offsets, void* stream);
+             int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream);
 
 /* The matrices [N,K] of E experts, each as fp8_prepare_weight leaves it. */
 typedef struct convrot_experts {
@@ -848,7 +853,9 @@ size_t fp8_moe_workspace_size(int64_t T, int64_t K, int64_t I, int64_t N, int to
  * fp8_moe -- the experts' part of a block:
  *   Y[t] = residual[t] + sum_j weights[t,j] D_e(silu(G_e(x_t)) * U_e(x_t)), e = experts[t,j],
  * X and the hidden rows quantized as by fp8_pack_activations, sums in fp32, one
- * rounding to y_dtype. Choices of -1 add nothing. A choice outside [-1, E)
+ * rounding to y_dtype. With a bf16 Y the rows that D_e gives pass to the sum in
+ * binary16 with a power of two per 128 features: a relative error of 2^-11 each
+ * at most, an eighth of a rounding to bf16, for half the bytes. Choices of -1 add nothing. A choice outside [-1, E)
  * counts as -1 and is reported as by moe_plan.
  *   workspace  at least fp8_moe_workspace_size(...) bytes, 16-byte aligned, not
  *              used by another call that may run at the same time.

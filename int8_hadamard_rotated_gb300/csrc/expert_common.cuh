@@ -124,6 +124,41 @@ __device__ __forceinline__ Item find_item_grouped(const Rows& r, int tile, const
   return i;
 }
 
+__device__ __forceinline__ unsigned long long f32x2_add(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// silu(g) u = g u / (1 + exp(-g)), with exp(-g) and the reciprocal from the
+// hardware's approximations (ex2.approx, rcp.approx, within 2^-22 each): the
+// relative error is a few 1e-7 and |g| 2^-24 from the exponent's rounding.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * g));
+  return g * rcp_approx(1.0f + e) * u;
+}
+
+// Rows that only moe_combine reads, on the way to a bf16 output: binary16
+// with a power of two per row and 128 features that brings the largest
+// magnitude just below 2^15, so that every value within 2^-29 of it keeps 11
+// bits (a row's rounding is an eighth of bf16's) and none overflows.
+struct ScaledHalf {};
+template <typename TY> constexpr bool SCALED = false;
+template <> inline constexpr bool SCALED<ScaledHalf> = true;
+template <typename TY> struct StoredAs { using type = TY; };
+template <> struct StoredAs<ScaledHalf> { using type = __half; };
+template <typename TY> using Stored = typename StoredAs<TY>::type;
+
+// What a value has to do with the choice of the power: infinities and NaN stay
+// what they are under any, and must not push their finite neighbours out.
+__device__ __forceinline__ float finite_magnitude(float v) { return fabsf(v) <= 3.402823466e38f ? fabsf(v) : 0.0f; }
+// 2^-14 of the power of two at or below a finite `top` >= 0, at least 2^-126.
+__device__ __forceinline__ float power_of(float top) {
+  const uint32_t e = __float_as_uint(top) >> 23;
+  return e < 15u ? 0x1p-126f : __uint_as_float((e - 14u) << 23);
+}
+
 // Four rows of a matrix (box one row high) to four consecutive rows of a tile.
 __device__ __forceinline__ void tma_gather4(void* smem_dst, const void* tmap, uint64_t* bar, int32_t x, int4 rows,
                                             uint64_t cache_hint) {
@@ -176,6 +211,7 @@ struct ExpertCall {
   int y_dtype;
   uint64_t test_wait_ns;
 };
+// A linear with s_out stores ScaledHalf rows, s_out [n, ceil(N/128)] their powers.
 int launch_expert_pair(const ExpertCall& c, cudaStream_t stream);
 // expert_few.cu: few rows per expert.
 int launch_expert_few(const ExpertCall& c, cudaStream_t stream);

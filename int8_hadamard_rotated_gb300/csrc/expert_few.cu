@@ -9,11 +9,15 @@
 // shares of K and add their partial tiles up through distributed shared memory,
 // in rank order.
 //
-// Ten warps: 0-3 promote the first matrix' accumulators (32 lanes each), 4-7
-// the second's, 8 loads (activation rows gathered by the plan, four to a copy),
-// 9 issues MMAs. The promoted sums meet in shared memory as [row][weight row],
-// where a warp takes a row at a time: a lane has four features, and the row's
-// largest magnitude of 128 is a warp's.
+// The MMAs' width is the item's rows, rounded up to 16, so that a tile that an
+// expert does not fill costs no more than its rows.
+//
+// Twelve warps: 0-3 promote the first matrix' accumulators (32 lanes each), 4-7
+// the second's, 8 loads (activation rows in the plan's order, or gathered by
+// the plan, four to a copy), 9 issues MMAs, 10 and 11 only complete their
+// warpgroup. The promoted sums meet in shared
+// memory as [row][weight row], 32 rows at a time, where a warp takes a row: a
+// lane has four features, and the largest magnitude of 128 is a warp's.
 #include "expert_common.cuh"
 
 #include <algorithm>
@@ -29,12 +33,15 @@ __device__ int g_few_error = 0;
 namespace {
 
 constexpr int EPI_WARPS = 8;
-constexpr int FEW_THREADS = (EPI_WARPS + 2) * 32;
+constexpr int FEW_THREADS = (EPI_WARPS + 4) * 32;  // three warpgroups
+// The control warpgroup gives up registers for the epilogue's accumulators.
+constexpr int LAUNCH_REGS = 168, CONTROL_REGS = 56, EPI_REGS = 224;
+static_assert(2 * EPI_REGS + CONTROL_REGS <= 3 * LAUNCH_REGS, "within what the block was launched with");
 constexpr int MAX_SPLIT = 4;
 constexpr int W_ROWS = 2 * QBLOCK;  // weight rows of an item
 
 struct FewParams {
-  CUtensorMap tmap_x;     // codes [T,K], box one row (gathered) or BN rows
+  CUtensorMap tmap_x;     // codes [T,K], box one row (gathered) or 16 rows
   CUtensorMap tmap_w[2];  // codes [E][N,K]: the matrix, or gate and up; box 128 rows
   Rows rows;
   convrot_experts w[2];
@@ -53,37 +60,38 @@ struct FewGeom {
   static constexpr int W_BYTES = QBLOCK * BK;  // of one matrix
   static constexpr int X_BYTES = BN * BK;
   static constexpr int STAGE_BYTES = 2 * W_BYTES + X_BYTES;
-  static constexpr int STAGES = BN == 64 ? 3 : 5;
-  static constexpr int KG = 64 / BN;            // blocks of K handed over together
-  static constexpr int BUF_COLS = 2 * KG * BN;  // 128
-  static constexpr int BUFS = 4;
-  static constexpr int TMEM_COLS = BUFS * BUF_COLS;
-  static constexpr uint32_t IDESC = idesc_e4m3_f32(LANES, BN);
-  static constexpr int SMEM_PART = STAGES * STAGE_BYTES;           // [BN][W_ROWS] fp32
-  static constexpr int SMEM_SCALES = SMEM_PART + BN * W_ROWS * 4;  // [warp][2][4 blocks][BN] fp32
+  static constexpr int STAGES = BN == 128 ? 3 : BN == 64 ? 4 : 5;
+  static constexpr int KG = BN < 64 ? 64 / BN : 1;  // blocks of K handed over together
+  static constexpr int BUF_COLS = 2 * KG * BN;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int BUFS = TMEM_COLS / BUF_COLS;
+  static constexpr int PART_ROWS = BN < 32 ? BN : 32;
+  static constexpr int SMEM_PART = STAGES * STAGE_BYTES;                  // [PART_ROWS][W_ROWS] fp32
+  static constexpr int SMEM_SCALES = SMEM_PART + PART_ROWS * W_ROWS * 4;  // [warp][2][4 blocks][BN] fp32
   static constexpr int SMEM_BARS = SMEM_SCALES + EPI_WARPS * 2 * 4 * BN * 4;
-  static constexpr int SMEM_FIRST = SMEM_BARS + (2 * STAGES + 2 * BUFS + 3) * 8 + 16;  // [E + 1]
+  static constexpr int SMEM_WIDTH = SMEM_BARS + (2 * STAGES + 2 * BUFS + 3) * 8 + 16;  // [STAGES] columns of a stage
+  static constexpr int SMEM_FIRST = SMEM_WIDTH + STAGES * 4;                           // [E + 1]
   static constexpr int smem(int E) { return SMEM_FIRST + (E + 1) * 4 + 1024; }
   static_assert(smem(MAX_EXPERTS) <= 227 * 1024, "shared memory");
-  static_assert(BN % 16 == 0 && 64 % BN == 0, "columns");
+  static_assert(BN % 16 == 0 && (64 % BN == 0 || BN == 128), "columns");
 };
 
-// Adds n <= KG accumulators of BN columns (W_MATRICES * BN apart), each with a
-// factor per column at f + its index * BN, to acc. One wait for all of them.
+// Adds n <= KG accumulators of `width` <= BN columns (2 * BN apart), each with a
+// factor per column at f + its index * BN, to acc; 16 columns at a time, the
+// next ones on their way.
 template <int BN, int KG>
-__device__ __forceinline__ void drain_columns(unsigned long long (&acc)[BN / 2], uint32_t ta, const float* f, int n) {
+__device__ __forceinline__ void drain_columns(unsigned long long (&acc)[BN / 2], uint32_t ta, const float* f, int n, int width) {
   constexpr int PER = BN / 16;
-  uint32_t r[KG * PER][16];
+  uint32_t r[2][16];
+  tmem_ld16(ta, r[0]);
 #pragma unroll
-  for (int q = 0; q < KG * PER; ++q) tmem_ld16(ta + (q / PER) * 2 * BN + (q % PER) * 16, r[q]);
-#pragma unroll
-  for (int q = 0; q < KG * PER; ++q) tmem_wait16(r[q]);
-#pragma unroll
-  for (int g = 0; g < KG; ++g) {
-    if (g >= n) break;
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const uint32_t(&v)[16] = r[g * PER + q];
+  for (int i = 0; i < KG * PER; ++i) {
+    const int g = i / PER, q = i % PER;
+    if (g < n && (KG > 1 || 16 * q < width)) {
+      tmem_wait16(r[i & 1]);
+      const int h = (i + 1) / PER, p = (i + 1) % PER;
+      if (i + 1 < KG * PER) tmem_ld16(ta + h * 2 * BN + p * 16, r[(i + 1) & 1]);
+      const uint32_t(&v)[16] = r[i & 1];
 #pragma unroll
       for (int k = 0; k < 8; k += 2) {
         const float4 s = *reinterpret_cast<const float4*>(f + g * BN + q * 16 + 2 * k);
@@ -93,6 +101,7 @@ __device__ __forceinline__ void drain_columns(unsigned long long (&acc)[BN / 2],
       }
     }
   }
+  tmem_ld_wait();  // a load past the width may still be on its way
 }
 
 // warp_wait for what the CTAs of a cluster have handed over: what they wrote
@@ -120,6 +129,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
   uint64_t* pempty = pfull + 1;  // and have been read
   uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(pempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
+  volatile int* stage_width = reinterpret_cast<volatile int*>(smem + G::SMEM_WIDTH);
   int* first = reinterpret_cast<int*>(smem + G::SMEM_FIRST);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = &g_few_error;
@@ -158,83 +168,91 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
   const uint32_t tmem_base = *tmem_base_smem;
   const int total = first[p.rows.E] * p.n_cols;
 
-  if (warp == EPI_WARPS) {
-    const uint64_t pol = l2_policy_evict_normal();
-    const bool gather = p.rows.order != nullptr;
-    uint32_t stage = 0, phase = 0, n_issued = 0;
-    bool ok = true;
-    for (int t = unit; ok && t < total; t += n_units) {
-      const Item c = find_item(first, p.rows.E, p.n_cols, t);
-      const int2 range = rows_of(p.rows, c.expert);
-      const int row = range.x + c.tile * BN;
-      int4 rows;  // the four rows that this lane's copy takes (past the expert's last: that one again)
-      if (gather && lane < BN / 4) {
-        const int i = row + 4 * lane, last = range.y - 1;
-        rows.x = source_row(p.rows, min(i, last));
-        rows.y = source_row(p.rows, min(i + 1, last));
-        rows.z = source_row(p.rows, min(i + 2, last));
-        rows.w = source_row(p.rows, min(i + 3, last));
-      }
-      for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (p.withhold && t == total - 1 && rank == split - 1 && kb == kb_end - 1) break;
-        ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, err, p.wait_ns);
-        if (!ok) break;
-        uint8_t* sw = smem + stage * G::STAGE_BYTES;
-        uint8_t* sx = sw + 2 * G::W_BYTES;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[stage], G::STAGE_BYTES);
-          const int f = c.col * FEATURES;
-          tma_load_3d(sw, &p.tmap_w[0], &full[stage], kb * BK, f, c.expert, pol);
-          if (SWIGLU) tma_load_3d(sw + G::W_BYTES, &p.tmap_w[1], &full[stage], kb * BK, f, c.expert, pol);
-          else tma_load_3d(sw + G::W_BYTES, &p.tmap_w[0], &full[stage], kb * BK, f + QBLOCK, c.expert, pol);
-          if (!gather) tma_load_2d(sx, &p.tmap_x, &full[stage], kb * BK, row, pol);
-        }
-        __syncwarp();
-        if (gather && lane < BN / 4) tma_gather4(sx + lane * 4 * BK, &p.tmap_x, &full[stage], kb * BK, rows, pol);
-        ++n_issued;
-        if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
-      }
-    }
-    // no copy may land after the exit
-    if (lane == 0)
-      for (uint32_t s = 0; s < G::STAGES; ++s)
-        if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err, p.wait_ns);
-    __syncwarp();
-  } else if (warp == EPI_WARPS + 1) {
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
+  if (warp >= EPI_WARPS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONTROL_REGS));
+    if (warp == EPI_WARPS) {
+      const uint64_t pol = l2_policy_evict_normal();
+      const bool gather = p.rows.order != nullptr;
+      uint32_t stage = 0, phase = 0, n_issued = 0;
       bool ok = true;
       for (int t = unit; ok && t < total; t += n_units) {
-        for (int kb0 = kb_begin; ok && kb0 < kb_end; kb0 += G::KG) {
-          ok = mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err, p.wait_ns);
-          for (int kb = kb0; ok && kb < min(kb0 + G::KG, kb_end); ++kb) {
-            ok = mbar_wait(&full[stage], phase, abort_flag, err, p.wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t sw = smem_u32(smem + stage * G::STAGE_BYTES), sx = sw + 2 * G::W_BYTES;
-            const uint32_t d = tmem_base + buf * G::BUF_COLS + (kb - kb0) * 2 * BN;
-            mma_block<1>(d, sw, sx, G::IDESC);
-            mma_block<1>(d + BN, sw + G::W_BYTES, sx, G::IDESC);
-            mma_commit(&empty[stage]);
-            if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
-          }
+        const Item c = find_item(first, p.rows.E, p.n_cols, t);
+        const int2 range = rows_of(p.rows, c.expert);
+        const int row = range.x + c.tile * BN, width = (min(BN, range.y - row) + 15) & ~15;
+        int4 rows;  // the four rows that this lane's copy takes (past the expert's last: that one again)
+        if (gather && lane < BN / 4) {
+          const int i = row + 4 * lane, last = range.y - 1;
+          rows.x = source_row(p.rows, min(i, last));
+          rows.y = source_row(p.rows, min(i + 1, last));
+          rows.z = source_row(p.rows, min(i + 2, last));
+          rows.w = source_row(p.rows, min(i + 3, last));
+        }
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
+          if (p.withhold && t == total - 1 && rank == split - 1 && kb == kb_end - 1) break;
+          ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, err, p.wait_ns);
           if (!ok) break;
-          mma_commit(&tfull[buf]);
-          if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
+          uint8_t* sw = smem + stage * G::STAGE_BYTES;
+          uint8_t* sx = sw + 2 * G::W_BYTES;
+          if (lane == 0) {
+            stage_width[stage] = width;
+            mbar_arrive_expect_tx(&full[stage], 2 * G::W_BYTES + width * BK);
+            const int f = c.col * FEATURES;
+            tma_load_3d(sw, &p.tmap_w[0], &full[stage], kb * BK, f, c.expert, pol);
+            if (SWIGLU) tma_load_3d(sw + G::W_BYTES, &p.tmap_w[1], &full[stage], kb * BK, f, c.expert, pol);
+            else tma_load_3d(sw + G::W_BYTES, &p.tmap_w[0], &full[stage], kb * BK, f + QBLOCK, c.expert, pol);
+            if (!gather)
+              for (int r = 0; r < width; r += 16) tma_load_2d(sx + r * BK, &p.tmap_x, &full[stage], kb * BK, row + r, pol);
+          }
+          __syncwarp();
+          if (gather && 4 * lane < width) tma_gather4(sx + lane * 4 * BK, &p.tmap_x, &full[stage], kb * BK, rows, pol);
+          ++n_issued;
+          if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      mma_commit(done);
-      mbar_wait(done, 0, nullptr, err, p.wait_ns);
+      // no copy may land after the exit
+      if (lane == 0)
+        for (uint32_t s = 0; s < G::STAGES; ++s)
+          if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err, p.wait_ns);
+      __syncwarp();
+    } else if (warp == EPI_WARPS + 1) {
+      if (lane == 0) {
+        uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
+        bool ok = true;
+        for (int t = unit; ok && t < total; t += n_units) {
+          for (int kb0 = kb_begin; ok && kb0 < kb_end; kb0 += G::KG) {
+            ok = mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err, p.wait_ns);
+            for (int kb = kb0; ok && kb < min(kb0 + G::KG, kb_end); ++kb) {
+              ok = mbar_wait(&full[stage], phase, abort_flag, err, p.wait_ns);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t sw = smem_u32(smem + stage * G::STAGE_BYTES), sx = sw + 2 * G::W_BYTES;
+              const uint32_t idesc = idesc_e4m3_f32(LANES, stage_width[stage]);
+              const uint32_t d = tmem_base + buf * G::BUF_COLS + (kb - kb0) * 2 * BN;
+              mma_block<1>(d, sw, sx, idesc);
+              mma_block<1>(d + BN, sw + G::W_BYTES, sx, idesc);
+              mma_commit(&empty[stage]);
+              if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) break;
+            mma_commit(&tfull[buf]);
+            if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
+          }
+        }
+        mma_commit(done);
+        mbar_wait(done, 0, nullptr, err, p.wait_ns);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     const int quarter = warp & 3, m = warp >> 2;  // of the lanes; the matrix, or half of the features
     const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + m * BN;
     float* sc = reinterpret_cast<float*>(smem + G::SMEM_SCALES) + warp * (2 * 4 * BN);
     float* part = reinterpret_cast<float*>(smem + G::SMEM_PART);
     constexpr int XR = (BN + 31) / 32;  // columns whose scales this lane fetches
     uint32_t buf = 0, bphase = 0;
-    int flip = 1, seq = 0;
+    int flip = 1;
+    uint32_t seq = 0;  // partial tiles that have been handed over
     const bool vec = p.vec_scales && kb_begin % 4 == 0;
     const int N = p.N;
     auto arrive_everywhere = [&](uint64_t* bar) {
@@ -245,18 +263,43 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
         mbar_arrive_cluster(mapa_shared(smem_u32(bar), lane));
       }
     };
-    for (int t = unit; t < total; t += n_units, ++seq) {
+    // An item's place is looked up, and its first scales are loaded, while the
+    // one before it is finished.
+    struct Info {
+      int row, valid, col, expert;
+      const float* xs[XR];
+      const float* ws;
+    };
+    auto look_up = [&](int t) {
       const Item c = find_item(first, p.rows.E, p.n_cols, t);
       const int2 range = rows_of(p.rows, c.expert);
-      const int row = range.x + c.tile * BN, valid = min(BN, range.y - row), n0 = c.col * FEATURES;
-      const float* xs[XR];
+      Info i;
+      i.row = range.x + c.tile * BN;
+      i.valid = min(BN, range.y - i.row);
+      i.col = c.col;
+      i.expert = c.expert;
 #pragma unroll
-      for (int i = 0; i < XR; ++i)
-        xs[i] = p.s_x + static_cast<int64_t>(source_row(p.rows, min(row + (32 * i + lane) % BN, range.y - 1))) * p.KB;
+      for (int k = 0; k < XR; ++k)
+        i.xs[k] = p.s_x + static_cast<int64_t>(source_row(p.rows, min(i.row + (32 * k + lane) % BN, range.y - 1))) * p.KB;
       // (a half past the features reads the first one's scales; it is not stored)
       const convrot_experts& w = p.w[SWIGLU ? m : 0];
-      const int block = n0 / QBLOCK + (!SWIGLU && m && n0 + QBLOCK < N ? 1 : 0);
-      const float* ws = w.scale + c.expert * w.scale_stride + static_cast<int64_t>(block) * p.KB;
+      const int n0 = c.col * FEATURES, block = n0 / QBLOCK + (!SWIGLU && m && n0 + QBLOCK < N ? 1 : 0);
+      i.ws = w.scale + c.expert * w.scale_stride + static_cast<int64_t>(block) * p.KB;
+      return i;
+    };
+    float nx[XR][4], nw[4];
+    auto load_factors = [&](const Info& i, int kb) {
+#pragma unroll
+      for (int k = 0; k < XR; ++k) load_scales(i.xs[k], kb, p.KB, vec, nx[k]);
+      load_scales(i.ws, kb, p.KB, vec, nw);
+    };
+    Info info{};
+    if (unit < total) {
+      info = look_up(unit);
+      load_factors(info, kb_begin);
+    }
+    for (int t = unit; t < total; t += n_units) {
+      const int row = info.row, valid = info.valid, width = (valid + 15) & ~15, n0 = info.col * FEATURES;
       float bv[2][4];  // of this lane's four features of either half
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -264,16 +307,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int n = n0 + (SWIGLU ? 0 : j * QBLOCK) + 4 * lane + k;
-          bv[j][k] = wj.bias && n < N ? __ldg(wj.bias + c.expert * wj.bias_stride + n) : 0.0f;
+          bv[j][k] = wj.bias && n < N ? __ldg(wj.bias + info.expert * wj.bias_stride + n) : 0.0f;
         }
       }
       unsigned long long acc[BN / 2];
 #pragma unroll
       for (int i = 0; i < BN / 2; ++i) acc[i] = 0ull;
-      float nx[XR][4], nw[4];
-#pragma unroll
-      for (int i = 0; i < XR; ++i) load_scales(xs[i], kb_begin, p.KB, vec, nx[i]);
-      load_scales(ws, kb_begin, p.KB, vec, nw);
       bool ok = true;
 #pragma unroll 1
       for (int kb = kb_begin, i = 0; kb < kb_end; kb += G::KG, i = (i + G::KG) & 3) {
@@ -285,84 +324,108 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
             for (int k = 0; k < XR; ++k)
               if (BN >= 32 || lane < BN) sc[(flip * 4 + j) * BN + 32 * k + lane] = nx[k][j] * nw[j];
           __syncwarp();
-          if (kb + 4 < kb_end) {
-#pragma unroll
-            for (int k = 0; k < XR; ++k) load_scales(xs[k], kb + 4, p.KB, vec, nx[k]);
-            load_scales(ws, kb + 4, p.KB, vec, nw);
-          }
+          if (kb + 4 < kb_end) load_factors(info, kb + 4);
         }
         ok = warp_wait(&tfull[buf], bphase, abort_flag, err, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
-        drain_columns<BN, G::KG>(acc, t_addr + buf * G::BUF_COLS, sc + (flip * 4 + i) * BN, kb_end - kb);
+        drain_columns<BN, G::KG>(acc, t_addr + buf * G::BUF_COLS, sc + (flip * 4 + i) * BN, kb_end - kb, width);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[buf]);
         if (++buf == G::BUFS) { buf = 0; bphase ^= 1u; }
       }
-      // the partial tile, once the one before it has been read everywhere
-      if (!ok || !cluster_wait(pempty, (seq & 1u) ^ 1u, abort_flag, err, p.wait_ns)) break;
-#pragma unroll
-      for (int i = 0; i < BN / 2; ++i) {
-        float a, b;
-        f32x2_unpack(acc[i], a, b);
-        part[2 * i * W_ROWS + 32 * warp + lane] = a;
-        part[(2 * i + 1) * W_ROWS + 32 * warp + lane] = b;
+      if (!ok) break;
+      const int col = info.col;
+      if (t + n_units < total) {
+        info = look_up(t + n_units);
+        load_factors(info, kb_begin);
       }
-      arrive_everywhere(pfull);
-      if (!cluster_wait(pfull, seq & 1u, abort_flag, err, p.wait_ns)) break;
-      for (int r = warp * split + rank; r < valid; r += EPI_WARPS * split) {
-        float v[2][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float* at = part + r * W_ROWS + j * QBLOCK + 4 * lane;
-          if (split == 1) {
-            const float4 s = *reinterpret_cast<const float4*>(at);
-            v[j][0] = s.x; v[j][1] = s.y; v[j][2] = s.z; v[j][3] = s.w;
-          } else {
-            float4 s[MAX_SPLIT];
+      for (int part_row = 0; part_row < BN; part_row += G::PART_ROWS) {
+        if (part_row >= valid) break;
+        // the partial tile, once the one before it has been read everywhere
+        ok = cluster_wait(pempty, (seq & 1u) ^ 1u, abort_flag, err, p.wait_ns);
+        if (!ok) break;
 #pragma unroll
-            for (int k = 0; k < MAX_SPLIT; ++k)
-              if (k < split) s[k] = ld_cluster_v4(mapa_shared(smem_u32(at), k));
-            v[j][0] = s[0].x; v[j][1] = s[0].y; v[j][2] = s[0].z; v[j][3] = s[0].w;
-#pragma unroll
-            for (int k = 1; k < MAX_SPLIT; ++k)
-              if (k < split) {
-                v[j][0] += s[k].x;
-                v[j][1] += s[k].y;
-                v[j][2] += s[k].z;
-                v[j][3] += s[k].w;
-              }
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[j][k] += bv[j][k];
+        for (int i = 0; i < G::PART_ROWS / 2; ++i) {
+          float a, b;
+          f32x2_unpack(acc[part_row / 2 + i], a, b);
+          part[2 * i * W_ROWS + 32 * warp + lane] = a;
+          part[(2 * i + 1) * W_ROWS + 32 * warp + lane] = b;
         }
-        const int64_t i = row + r;
-        if constexpr (SWIGLU) {
-          Pair h[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            h[k] = f32x2_pack(silu_mul_fast(v[0][2 * k], v[1][2 * k]), silu_mul_fast(v[0][2 * k + 1], v[1][2 * k + 1]));
-          float top = max_magnitude(h);
-#pragma unroll
-          for (int d = 1; d < 32; d *= 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const float scale = e4m3_scale(top);
-          uint32_t q[1];
-          e4m3_codes(h, scale, e4m3_factor(scale), q);
-          const int n = n0 + 4 * lane;
-          if (n < N) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + i * p.ldy + n) = q[0];
-          if (lane == 0) p.s_out[i * ((N + QBLOCK - 1) / QBLOCK) + c.col] = scale;
-        } else {
+        arrive_everywhere(pfull);
+        ok = cluster_wait(pfull, seq & 1u, abort_flag, err, p.wait_ns);
+        if (!ok) break;
+        ++seq;
+        const int rows = min(G::PART_ROWS, valid - part_row);
+        for (int r = warp * split + rank; r < rows; r += EPI_WARPS * split) {
+          float v[2][4];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int n = n0 + j * QBLOCK + 4 * lane;
-            TY* y = static_cast<TY*>(p.out) + i * p.ldy + n;
-            const bool whole = n + 4 <= N && (reinterpret_cast<uintptr_t>(y) & (4 * sizeof(TY) - 1)) == 0;
-            store_outputs(y, whole, n, N, v[j]);
+            const float* at = part + r * W_ROWS + j * QBLOCK + 4 * lane;
+            if (split == 1) {
+              const float4 s = *reinterpret_cast<const float4*>(at);
+              v[j][0] = s.x; v[j][1] = s.y; v[j][2] = s.z; v[j][3] = s.w;
+            } else {
+              float4 s[MAX_SPLIT];
+#pragma unroll
+              for (int k = 0; k < MAX_SPLIT; ++k)
+                if (k < split) s[k] = ld_cluster_v4(mapa_shared(smem_u32(at), k));
+              v[j][0] = s[0].x; v[j][1] = s[0].y; v[j][2] = s[0].z; v[j][3] = s[0].w;
+#pragma unroll
+              for (int k = 1; k < MAX_SPLIT; ++k)
+                if (k < split) {
+                  v[j][0] += s[k].x;
+                  v[j][1] += s[k].y;
+                  v[j][2] += s[k].z;
+                  v[j][3] += s[k].w;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[j][k] += bv[j][k];
+          }
+          const int64_t i = row + part_row + r;
+          if constexpr (SWIGLU) {
+            Pair h[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              h[k] = f32x2_pack(silu_mul(v[0][2 * k], v[1][2 * k]), silu_mul(v[0][2 * k + 1], v[1][2 * k + 1]));
+            float top = max_magnitude(h);
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float scale = e4m3_scale(top);
+            uint32_t q[1];
+            e4m3_codes(h, scale, e4m3_factor(scale), q);
+            const int n = n0 + 4 * lane;
+            if (n < N) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + i * p.ldy + n) = q[0];
+            if (lane == 0) p.s_out[i * ((N + QBLOCK - 1) / QBLOCK) + col] = scale;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int n = n0 + j * QBLOCK + 4 * lane;
+              if constexpr (SCALED<TY>) {
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = fmaxf(top, finite_magnitude(v[j][k]));
+                // (bits of positive floats order as integers)
+                top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                const float factor = power_of(top);
+                if (lane == 0 && n0 + j * QBLOCK < N) p.s_out[i * ((N + QBLOCK - 1) / QBLOCK) + 2 * col + j] = factor;
+                const float inv = __frcp_rn(factor);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[j][k] *= inv;
+              }
+              using TS = Stored<TY>;
+              TS* y = static_cast<TS*>(p.out) + i * p.ldy + n;
+              const bool whole = n + 4 <= N && (reinterpret_cast<uintptr_t>(y) & (4 * sizeof(TS) - 1)) == 0;
+              store_outputs(y, whole, n, N, v[j]);
+            }
           }
         }
+        arrive_everywhere(pempty);
       }
-      arrive_everywhere(pempty);
+      if (!ok) break;
     }
   }
   tc_fence_before();
@@ -390,7 +453,7 @@ int launch_as(const ExpertCall& c, cudaStream_t stream) {
   using G = FewGeom<BN>;
   const int64_t N = c.w->N, KB = n_blocks(c.K), E = c.rows.E, n = c.rows.n;
   FewParams p;
-  if (int st = make_tmap_codes(&p.tmap_x, c.Q, c.rows.T, c.K, c.rows.order ? 1 : BN)) return st;
+  if (int st = make_tmap_codes(&p.tmap_x, c.Q, c.rows.T, c.K, c.rows.order ? 1 : 16)) return st;
   for (int j = 0; j < (SWIGLU ? 2 : 1); ++j) {
     p.w[j] = j ? *c.up : *c.w;
     if (int st = make_tmap_experts(&p.tmap_w[j], p.w[j], E, c.K, QBLOCK)) return st;
@@ -414,7 +477,7 @@ int launch_as(const ExpertCall& c, cudaStream_t stream) {
   static std::mutex mu;
   static uint64_t done = 0;
   auto kernel = expert_few_kernel<BN, SWIGLU, TY>;
-  if (int st = allow_smem(kernel, G::smem(MAX_EXPERTS), done, mu)) return st;
+  if (int st = allow_smem(kernel, G::smem(MAX_EXPERTS), done, mu, LAUNCH_REGS)) return st;
   // The items that choices spread evenly would give; K is split while they
   // leave CTAs without one.
   const double reached = static_cast<double>(E) * (1.0 - std::pow(1.0 - 1.0 / static_cast<double>(E), static_cast<double>(n)));
@@ -449,6 +512,7 @@ int launch_as(const ExpertCall& c, cudaStream_t stream) {
 template <int BN>
 int launch_columns(const ExpertCall& c, cudaStream_t stream) {
   if (c.up) return launch_as<BN, true, uint8_t>(c, stream);
+  if (c.s_out) return launch_as<BN, false, ScaledHalf>(c, stream);
   if (c.y_dtype == CONVROT_F32) return launch_as<BN, false, float>(c, stream);
   if (c.y_dtype == CONVROT_F16) return launch_as<BN, false, __half>(c, stream);
   return launch_as<BN, false, __nv_bfloat16>(c, stream);
@@ -458,9 +522,14 @@ int launch_columns(const ExpertCall& c, cudaStream_t stream) {
 
 int launch_expert_few(const ExpertCall& c, cudaStream_t stream) {
   const int64_t per = c.rows.n / c.rows.E;
+  if (const char* v = getenv("EXPERT_BN")) {
+    const int bn = atoi(v);
+    return bn == 16 ? launch_columns<16>(c, stream) : bn == 32 ? launch_columns<32>(c, stream) : bn == 64 ? launch_columns<64>(c, stream) : launch_columns<128>(c, stream);
+  }
   if (per <= 12) return launch_columns<16>(c, stream);
   if (per <= 24) return launch_columns<32>(c, stream);
-  return launch_columns<64>(c, stream);
+  if (per <= 56) return launch_columns<64>(c, stream);
+  return launch_columns<128>(c, stream);
 }
 
 cudaError_t few_error_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_few_error); }

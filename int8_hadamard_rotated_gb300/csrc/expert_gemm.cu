@@ -14,7 +14,7 @@ namespace convrot {
 namespace moe {
 
 bool many_rows(int64_t n, int E) {
-  if (const char* v = getenv("EXPERT_KERNEL")) return atoi(v) == 2;
+  if (const char* v = getenv("EXPERT_KERNEL")) return atoi(v) >= 2;
   return n / E > 64;
 }
 
@@ -22,13 +22,17 @@ int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows
                          const convrot_experts& up, uint8_t* Q_h, float* s_h, cudaStream_t stream,
                          uint64_t test_wait_ns) {
   const ExpertCall c{Q, s, K, r, &gate, &up, Q_h, s_h, gate.N, 0, test_wait_ns};
-  return many_rows(r.n, r.E) ? launch_expert_pair(c, stream) : launch_expert_few(c, stream);
+  const char* v = getenv("EXPERT_KERNEL");
+  const bool pair = v ? atoi(v) == 2 : many_rows(r.n, r.E);
+  return pair ? launch_expert_pair(c, stream) : launch_expert_few(c, stream);
 }
 
 int launch_expert_linear(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& w, void* Y,
-                         int64_t ldy, int y_dtype, cudaStream_t stream, uint64_t test_wait_ns) {
-  const ExpertCall c{Q, s, K, r, &w, nullptr, Y, nullptr, ldy, y_dtype, test_wait_ns};
-  return many_rows(r.n, r.E) ? launch_expert_pair(c, stream) : launch_expert_few(c, stream);
+                         int64_t ldy, int y_dtype, float* powers, cudaStream_t stream, uint64_t test_wait_ns) {
+  const ExpertCall c{Q, s, K, r, &w, nullptr, Y, powers, ldy, y_dtype, test_wait_ns};
+  const char* v = getenv("EXPERT_KERNEL");
+  const bool pair = v ? atoi(v) == 2 : many_rows(r.n, r.E);
+  return pair ? launch_expert_pair(c, stream) : launch_expert_few(c, stream);
 }
 
 }  // namespace moe

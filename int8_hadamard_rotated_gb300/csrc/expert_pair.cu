@@ -90,6 +90,25 @@ __device__ __forceinline__ void drain2(unsigned long long (&acc)[64], uint32_t t
   }
 }
 
+// The first `rows` rows of a staged block, 16 bytes per lane: rows of Y start on
+// 16-byte boundaries.
+template <typename TS>
+static __device__ __noinline__ void store_part(const uint8_t* sb, TS* y, int64_t ldy, int rows, int cols) {
+  const int lane = threadIdx.x & 31, ch = lane & 7;
+  constexpr int E = 16 / sizeof(TS);
+#pragma unroll 1
+  for (int r = lane >> 3; r < min(rows, 32); r += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(sb + r * STORE_ROW + (swizzled(ch, r) << 4));
+    TS* to = y + r * ldy + ch * E;
+    if ((ch + 1) * E <= cols) {
+      *reinterpret_cast<uint4*>(to) = v;
+    } else {
+      const TS* from = reinterpret_cast<const TS*>(&v);
+      for (int k = 0; ch * E + k < cols; ++k) to[k] = from[k];
+    }
+  }
+}
+
 template <typename TY, bool SWIGLU>
 __global__ void __launch_bounds__(PAIR_THREADS, 1) expert_pair_kernel(const __grid_constant__ PairParams p) {
   using G = Geom;
@@ -332,8 +351,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) expert_pair_kernel(const __gr
           f32x2_unpack(acc[COLS / 4 + k], u0, u1);
           const float2 bg = *reinterpret_cast<const float2*>(bias + 2 * k);
           const float2 bu = *reinterpret_cast<const float2*>(bias + COLS / 2 + 2 * k);
-          g0 = silu_mul_fast(g0 + bg.x, u0 + bu.x);
-          g1 = silu_mul_fast(g1 + bg.y, u1 + bu.y);
+          g0 = silu_mul(g0 + bg.x, u0 + bu.x);
+          g1 = silu_mul(g1 + bg.y, u1 + bu.y);
           asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(top), "f"(g0), "f"(g1));
           acc[k] = f32x2_pack(g0, g1);
         }
@@ -361,9 +380,34 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) expert_pair_kernel(const __gr
           if (half == 0) p.s_out[static_cast<int64_t>(i) * ((p.N + QBLOCK - 1) / QBLOCK) + col / QBLOCK] = sc;
         }
       } else {
+        using TS = Stored<TY>;
+        const unsigned long long* add = reinterpret_cast<const unsigned long long*>(bias);
+#pragma unroll
+        for (int k = 0; k < COLS / 2; k += 2) {
+          const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(add + k);
+          acc[k] = f32x2_add(acc[k], bb.x);
+          acc[k + 1] = f32x2_add(acc[k + 1], bb.y);
+        }
+        if constexpr (SCALED<TY>) {
+          // a thread's columns are the 128 features of one power
+          float top = 0.0f;
+#pragma unroll
+          for (int k = 0; k < COLS / 2; ++k) {
+            float a, b;
+            f32x2_unpack(acc[k], a, b);
+            top = fmaxf(top, fmaxf(finite_magnitude(a), finite_magnitude(b)));
+          }
+          const float power = power_of(top), inv = __frcp_rn(power);
+          const unsigned long long inv2 = f32x2_pack(inv, inv);
+#pragma unroll
+          for (int k = 0; k < COLS / 2; ++k) acc[k] = f32x2_mul(acc[k], inv2);
+          const int n = col + half * COLS;
+          if (row + lane < end && n < p.N)
+            p.s_out[static_cast<int64_t>(row + lane) * ((p.N + QBLOCK - 1) / QBLOCK) + n / QBLOCK] = power;
+        }
         // store: PER features of a row at a time
-        constexpr int PER = STORE_ROW / sizeof(TY);
-        constexpr int E = 16 / sizeof(TY);  // of them in 16 bytes
+        constexpr int PER = STORE_ROW / sizeof(TS);
+        constexpr int E = 16 / sizeof(TS);  // of them in 16 bytes
         static_assert((COLS / PER) % 2 == 0, "both store buffers equally often");
         const bool whole = p.tma_y && row + 32 <= end;  // else the next expert's rows are in the block
 #pragma unroll
@@ -376,15 +420,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) expert_pair_kernel(const __gr
             float v[E];
 #pragma unroll
             for (int k = 0; k < E; k += 2) f32x2_unpack(acc[(b * PER + ch * E + k) / 2], v[k], v[k + 1]);
-#pragma unroll
-            for (int k = 0; k < E; k += 4) {
-              const float4 bb = *reinterpret_cast<const float4*>(bias + b * PER + ch * E + k);
-              v[k] += bb.x;
-              v[k + 1] += bb.y;
-              v[k + 2] += bb.z;
-              v[k + 3] += bb.w;
-            }
-            *reinterpret_cast<uint4*>(sb + lane * STORE_ROW + (swizzled(ch, lane) << 4)) = pack16<TY>(v);
+            *reinterpret_cast<uint4*>(sb + lane * STORE_ROW + (swizzled(ch, lane) << 4)) = pack16<TS>(v);
           }
           const int n = col + half * COLS + b * PER;
           if (whole) {
@@ -396,7 +432,9 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) expert_pair_kernel(const __gr
             }
           } else {
             __syncwarp();
-            store_rows<TY>(sb, static_cast<TY*>(p.out) + row * p.ldy + n, p.ldy, min(32, end - row), p.N - n);
+            TS* y = static_cast<TS*>(p.out) + row * p.ldy + n;
+            if (p.tma_y) store_part<TS>(sb, y, p.ldy, end - row, p.N - n);
+            else store_rows<TS>(sb, y, p.ldy, min(32, end - row), p.N - n);
             // (an empty group, so that the next store into this buffer waits
             // for the right one)
             if (lane == 0) bulk_commit();
@@ -441,7 +479,7 @@ int launch_as(const ExpertCall& c, cudaStream_t stream) {
   p.vec_scales = KB % 4 == 0 && aligned16(c.s);
   for (int j = 0; j < (SWIGLU ? 2 : 1); ++j)
     p.vec_scales = p.vec_scales && aligned16(p.w[j].scale) && p.w[j].scale_stride % 4 == 0;
-  const uint64_t pitch = static_cast<uint64_t>(c.ldy) * sizeof(TY);
+  const uint64_t pitch = static_cast<uint64_t>(c.ldy) * sizeof(Stored<TY>);
   p.tma_y = !SWIGLU && aligned16(c.out) && pitch % 16 == 0 && pitch < (1ull << 40);
   if (p.tma_y)
     if (int st = make_tmap_out(&p.tmap_y, c.out, c.y_dtype, c.rows.n, N, c.ldy)) return st;
@@ -461,6 +499,7 @@ int launch_as(const ExpertCall& c, cudaStream_t stream) {
 
 int launch_expert_pair(const ExpertCall& c, cudaStream_t stream) {
   if (c.up) return launch_as<uint8_t, true>(c, stream);
+  if (c.s_out) return launch_as<ScaledHalf, false>(c, stream);
   if (c.y_dtype == CONVROT_F32) return launch_as<float, false>(c, stream);
   if (c.y_dtype == CONVROT_F16) return launch_as<__half, false>(c, stream);
   return launch_as<__nv_bfloat16, false>(c, stream);

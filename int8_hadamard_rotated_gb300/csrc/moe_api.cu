@@ -130,8 +130,9 @@ int combine_checks(const CombineArgs& a) {
 
 // Where fp8_moe keeps what passes between its steps.
 struct Workspace {
-  size_t q_x, s_x, order, place, offsets, q_h, s_h, rows, bytes;
-  Workspace(int64_t T, int64_t K, int64_t I, int64_t N, int64_t n, int E) {
+  size_t q_x, s_x, order, place, offsets, plan, q_h, s_h, rows, powers, bytes;
+  int64_t ld;  // of the rows, elements
+  Workspace(int64_t T, int64_t K, int64_t I, int64_t N, int64_t n, int E, int y_dtype) {
     size_t at = 0;
     auto take = [&](size_t b) {
       const size_t here = at;
@@ -144,9 +145,14 @@ struct Workspace {
     order = take(static_cast<size_t>(n) * 4);
     place = take(static_cast<size_t>(n) * 4);
     offsets = take(static_cast<size_t>(E + 1) * 4);
+    plan = take(plan_workspace(n, E));
     q_h = take(static_cast<size_t>(n) * I);
     s_h = take(static_cast<size_t>(n) * n_blocks(I) * 4);
-    rows = take(static_cast<size_t>(n) * N * 4);
+    // rows that start on 16-byte boundaries: fp32, or binary16 with their powers of two
+    const bool half = y_dtype == CONVROT_BF16;
+    ld = half ? (N + 7) / 8 * 8 : (N + 3) / 4 * 4;
+    rows = take(static_cast<size_t>(n) * ld * (half ? 2 : 4));
+    powers = take(half ? static_cast<size_t>(n) * n_blocks(N) * 4 : 0);
     bytes = at;
   }
 };
@@ -165,7 +171,7 @@ int moe_checks(const convrot_moe_args& a, void* workspace, size_t workspace_byte
   if (a.T == 0 || N == 0) return CONVROT_OK;
   const int64_t n = a.T * a.top_k, xs = size_of(a.x_dtype), ys = size_of(a.y_dtype);
   if (!a.X || !a.experts || !a.weights || !a.Y) return CONVROT_ERR_ARG;
-  const Workspace ws(a.T, a.K, I, N, n, a.n_experts);
+  const Workspace ws(a.T, a.K, I, N, n, a.n_experts, a.y_dtype);
   if (!workspace || workspace_bytes < ws.bytes) return CONVROT_ERR_WORKSPACE;
   if (a.K % 16 != 0 || I % 16 != 0 || !aligned16(workspace) || !aligned_to(a.X, xs) || !aligned_to(a.experts, 4) ||
       !aligned_to(a.weights, 4) || !aligned_to(a.Y, ys) || !aligned_to(a.residual, ys))
@@ -201,18 +207,21 @@ int moe_route(const convrot_moe_route_args* args, void* stream) {
 }
 
 int moe_plan(const int32_t* experts, int64_t n, int n_experts, int32_t* order, int32_t* place, int32_t* offsets,
-             void* stream) {
+             void* workspace, size_t workspace_bytes, void* stream) {
   if (n < 0 || n_experts < 1) return CONVROT_ERR_ARG;
   if (n_experts > MAX_EXPERTS || n > MAX_ROWS) return CONVROT_ERR_UNSUPPORTED;
   if (!offsets || (n > 0 && (!experts || !order || !place))) return CONVROT_ERR_ARG;
-  const Region arrays[] = {flat(experts, n * 4), flat(order, n * 4), flat(place, n * 4), flat(offsets, (n_experts + 1) * 4)};
-  for (int i = 0; i < 4; ++i) {
+  const size_t need = plan_workspace(n, n_experts);
+  if (need && (!workspace || workspace_bytes < need)) return CONVROT_ERR_WORKSPACE;
+  const Region arrays[] = {flat(experts, n * 4), flat(order, n * 4), flat(place, n * 4),
+                           flat(offsets, (n_experts + 1) * 4), flat(need ? workspace : nullptr, static_cast<int64_t>(need))};
+  for (int i = 0; i < 5; ++i) {
     if (!aligned_to(arrays[i].p, 4)) return CONVROT_ERR_ALIGN;
     for (int j = 0; j < i; ++j)
       if (meet(arrays[i], arrays[j])) return CONVROT_ERR_ALIAS;
   }
   if (int st = check_device()) return st;
-  return launch_plan(experts, n, n_experts, order, place, offsets, static_cast<cudaStream_t>(stream));
+  return launch_plan(experts, n, n_experts, order, place, offsets, workspace, static_cast<cudaStream_t>(stream));
 }
 
 int fp8_expert_linear(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
@@ -234,7 +243,8 @@ int fp8_expert_linear(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K
   if (int st = check_device()) return st;
   Rows rows{order, offsets, n, T, n_experts, top_k};
   if (int st = sort_rows(Q_x, s_x, K, rows, ws, static_cast<cudaStream_t>(stream))) return st;
-  return launch_expert_linear(Q_x, s_x, K, rows, *weight, Y, ldy, y_dtype, static_cast<cudaStream_t>(stream));
+  return launch_expert_linear(Q_x, s_x, K, rows, *weight, Y, ldy, y_dtype, nullptr,
+                              static_cast<cudaStream_t>(stream));
 }
 
 int fp8_expert_swiglu(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
@@ -276,6 +286,11 @@ int moe_combine(const void* rows, int r_dtype, int64_t ldr, int64_t n, const int
   return launch_combine(a, static_cast<cudaStream_t>(stream));
 }
 
+size_t moe_plan_workspace_size(int64_t n, int n_experts) {
+  if (n < 0 || n > MAX_ROWS || n_experts < 1 || n_experts > MAX_EXPERTS) return 0;
+  return plan_workspace(n, n_experts);
+}
+
 size_t fp8_expert_workspace_size(int64_t n, int64_t K, int n_experts) {
   if (n < 0 || K <= 0 || n > MAX_ROWS || K > MAX_LENGTH || n_experts < 1 || n_experts > MAX_EXPERTS) return 0;
   return many_rows(n, n_experts) ? sorted_bytes(n, K) : 0;
@@ -283,7 +298,7 @@ size_t fp8_expert_workspace_size(int64_t n, int64_t K, int n_experts) {
 
 size_t fp8_moe_workspace_size(int64_t T, int64_t K, int64_t I, int64_t N, int top_k, int n_experts, int y_dtype) {
   if (!workspace_sizes(T, K, I, N, top_k, n_experts, y_dtype)) return 0;
-  return Workspace(T, K, I, N, T * top_k, n_experts).bytes;
+  return Workspace(T, K, I, N, T * top_k, n_experts, y_dtype).bytes;
 }
 
 int fp8_moe(const convrot_moe_args* args, void* workspace, size_t workspace_bytes, void* stream) {
@@ -294,22 +309,25 @@ int fp8_moe(const convrot_moe_args* args, void* workspace, size_t workspace_byte
   if (a.T == 0 || N == 0) return CONVROT_OK;
   if (int st = check_device()) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Workspace at(a.T, a.K, I, N, n, a.n_experts);
+  const Workspace at(a.T, a.K, I, N, n, a.n_experts, a.y_dtype);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint8_t *q_x = ws + at.q_x, *q_h = ws + at.q_h;
   float *s_x = reinterpret_cast<float*>(ws + at.s_x), *s_h = reinterpret_cast<float*>(ws + at.s_h);
   int32_t *order = reinterpret_cast<int32_t*>(ws + at.order), *place = reinterpret_cast<int32_t*>(ws + at.place);
   int32_t* offsets = reinterpret_cast<int32_t*>(ws + at.offsets);
-  if (int st = launch_plan(a.experts, n, a.n_experts, order, place, offsets, s)) return st;
+  if (int st = launch_plan(a.experts, n, a.n_experts, order, place, offsets, ws + at.plan, s)) return st;
   const Rows by_token{order, offsets, n, a.T, a.n_experts, a.top_k}, sorted{nullptr, offsets, n, n, a.n_experts, 1};
   const bool many = many_rows(n, a.n_experts);
   if (int st = many ? launch_pack_sorted(a.X, a.x_dtype, a.T, a.K, a.ldx, place, a.top_k, q_x, s_x, s)
                     : launch_fp8_pack(a.X, a.x_dtype, a.T, a.K, a.ldx, q_x, s_x, s))
     return st;
   if (int st = launch_expert_swiglu(q_x, s_x, a.K, many ? sorted : by_token, *a.gate, *a.up, q_h, s_h, s)) return st;
-  if (int st = launch_expert_linear(q_h, s_h, I, sorted, *a.down, ws + at.rows, N, CONVROT_F32, s)) return st;
-  return launch_combine(CombineArgs{ws + at.rows, CONVROT_F32, N, n, place, a.weights, a.T, a.top_k, N, a.residual,
-                                    a.ld_res, a.Y, a.ldy, a.y_dtype, nullptr, 0}, s);
+  const bool half = a.y_dtype == CONVROT_BF16;
+  float* powers = half ? reinterpret_cast<float*>(ws + at.powers) : nullptr;
+  const int rows = half ? CONVROT_F16 : CONVROT_F32;
+  if (int st = launch_expert_linear(q_h, s_h, I, sorted, *a.down, ws + at.rows, at.ld, rows, powers, s)) return st;
+  return launch_combine(CombineArgs{ws + at.rows, rows, at.ld, n, place, a.weights, a.T, a.top_k, N, a.residual,
+                                    a.ld_res, a.Y, a.ldy, a.y_dtype, powers, n_blocks(N)}, s);
 }
 
 }  // extern "C"

@@ -20,7 +20,8 @@ struct Rows {
 
 // moe_route.cu: arguments already checked; T > 0 (n > 0).
 int launch_route(const convrot_moe_route_args& a, cudaStream_t stream);
-int launch_plan(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
+size_t plan_workspace(int64_t n, int E);
+int launch_plan(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets, void* workspace,
                 cudaStream_t stream);
 struct CombineArgs {
   const void* rows;  // [n,N] of r_dtype
@@ -51,12 +52,14 @@ int launch_pack_sorted(const void* X, int x_dtype, int64_t T, int64_t K, int64_t
 // Whether n rows of E experts are taken by the kernel for many rows per expert,
 // which wants them in the plan's order (r.order null).
 bool many_rows(int64_t n, int E);
-// expert_gemm.cu: n, T > 0, every width > 0.
+// expert_gemm.cu: n, T > 0, every width > 0. With `powers` [n, ceil(N/128)], Y
+// (binary16) is stored divided by a power of two per row and 128 features, to
+// be read with it by launch_combine (its r_scale).
 int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& gate,
                          const convrot_experts& up, uint8_t* Q_h, float* s_h, cudaStream_t stream,
                          uint64_t test_wait_ns = 0);
 int launch_expert_linear(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& w, void* Y,
-                         int64_t ldy, int y_dtype, cudaStream_t stream, uint64_t test_wait_ns = 0);
+                         int64_t ldy, int y_dtype, float* powers, cudaStream_t stream, uint64_t test_wait_ns = 0);
 // expert_pair.cu, expert_few.cu
 cudaError_t pair_error_word(int** p);
 cudaError_t few_error_word(int** p);

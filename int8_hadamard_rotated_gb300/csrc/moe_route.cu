@@ -3,8 +3,8 @@
 // of the experts' rows.
 #include "moe_common.cuh"
 
+#include <algorithm>
 #include <climits>
-#include <type_traits>
 
 namespace convrot {
 namespace moe {
@@ -347,19 +347,36 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
 // the plan
 // ---------------------------------------------------------------------------
 //
-// A stable counting sort of n choices by expert in one launch: every CTA places
-// the choices of W experts and looks through all choices for them, twice. Every
-// warp has a contiguous part: the first turn counts its choices of each of the
-// CTA's experts and those of lower ones, the second hands the places out, by
-// ballots. Nothing passes between CTAs and there are no atomics: the order is
-// the choices' own. Choices outside [0, E) count as expert E, behind all others.
-// 65536 choices are read (E + 1) / W times over, from L2 and then L1; a sort in
-// one cluster of eight CTAs, each choice ranked in its warp by match, took 22 us.
+// A stable counting sort of n choices by expert. No atomics decide an order:
+// it is the choices' own. Choices outside [0, E) count as expert E, behind all
+// others.
+//
+// Few choices: one launch. Every CTA places the choices of W experts and looks
+// through all choices for them, twice: every warp has a contiguous part; the
+// first turn counts its choices of each of the CTA's experts and those of lower
+// ones, the second hands the places out, by ballots. Nothing passes between
+// CTAs, but every SM looks at every choice: 512 of 128 experts take 2.7 us,
+// 65536 of 256 experts 32 us.
+//
+// Many: two launches. The choices are dealt out in contiguous parts; the first
+// launch counts a part's choices of every expert, the second sums the parts
+// before its own up and ranks its choices (32 at a time: the lanes that hold the
+// same expert find each other by match).
 
 constexpr int PLAN_WARPS = 32;
+constexpr int PLAN_STEP = 4;          // choices per lane and turn
+constexpr int64_t PLAN_ONE = 4096;    // most choices of the one launch
+constexpr int PART_WARPS = 8;         // the two launches: warps of a CTA
+constexpr int64_t PLAN_PARTS = 64;    // most parts
+constexpr int64_t PART_LEAST = 1024;  // fewest choices of a part
 
-// STEP: choices per lane and turn, loaded together.
-template <int W, int STEP>
+__device__ __forceinline__ int bucket_of(int e, int E, bool& bad) {
+  if (e >= 0 && e < E) return e;
+  bad |= e != -1;
+  return E;
+}
+
+template <int W>
 __global__ void __launch_bounds__(PLAN_WARPS * 32)
 moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* __restrict__ order,
                 int32_t* __restrict__ place, int32_t* __restrict__ offsets) {
@@ -368,31 +385,25 @@ moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* 
   pdl_launch_dependents();
   constexpr uint32_t ALL = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = static_cast<int>(blockIdx.x) * W;
-  constexpr int TURN = 32 * STEP;
+  constexpr int TURN = 32 * PLAN_STEP;
   const int64_t turns = (n + TURN - 1) / TURN;
   const int64_t t0 = turns * warp / PLAN_WARPS, t1 = turns * (warp + 1) / PLAN_WARPS;
   // a turn's choices, as places among the CTA's experts: negative for lower ones
-  auto load = [&](int64_t t, int (&b)[STEP]) {
+  auto load = [&](int64_t t, int (&b)[PLAN_STEP]) {
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < STEP; ++j) {
+    for (int j = 0; j < PLAN_STEP; ++j) {
       const int64_t i = t * TURN + 32 * j + lane;
-      b[j] = i < n ? __ldg(experts + i) : INT_MIN;
-    }
-#pragma unroll
-    for (int j = 0; j < STEP; ++j) {
-      const bool some = t * TURN + 32 * j + lane < n, in = b[j] >= 0 && b[j] < E;
-      bad |= some && !in && b[j] != -1;
-      b[j] = !some ? INT_MAX : (in ? b[j] : E) - e0;
+      b[j] = i < n ? bucket_of(__ldg(experts + i), E, bad) - e0 : INT_MAX;
     }
     if (bad) record_error(&g_moe_error, CONVROT_ERR_ARG);
   };
   int mine[W] = {}, lower = 0;
   for (int64_t t = t0; t < t1; ++t) {
-    int b[STEP];
+    int b[PLAN_STEP];
     load(t, b);
 #pragma unroll
-    for (int j = 0; j < STEP; ++j) {
+    for (int j = 0; j < PLAN_STEP; ++j) {
       lower += b[j] < 0;
 #pragma unroll
       for (int w = 0; w < W; ++w) mine[w] += b[j] == w;
@@ -417,10 +428,10 @@ moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* 
   }
   const uint32_t before = (1u << lane) - 1u;
   for (int64_t t = t0; t < t1; ++t) {
-    int b[STEP];
+    int b[PLAN_STEP];
     load(t, b);
 #pragma unroll
-    for (int j = 0; j < STEP; ++j) {
+    for (int j = 0; j < PLAN_STEP; ++j) {
       const bool here = b[j] >= 0 && b[j] < W;
       if (!__any_sync(ALL, here)) continue;
       int to = 0;
@@ -436,6 +447,107 @@ moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* 
         order[to] = some ? static_cast<int32_t>(i) : -1;
         place[i] = some ? to : -1;
       }
+    }
+  }
+}
+
+// Part p of `parts`: choices [part_start(p), part_start(p + 1)), whole groups of 32.
+__device__ __forceinline__ int64_t part_start(int64_t n, int64_t parts, int64_t p) {
+  const int64_t at = (n + 31) / 32 * p / parts * 32;
+  return at < n ? at : n;
+}
+
+// counts [part][E + 1]
+__global__ void __launch_bounds__(PART_WARPS * 32)
+moe_count_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* __restrict__ counts) {
+  __shared__ int count[MAX_EXPERTS + 1];
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  for (int e = threadIdx.x; e <= E; e += PART_WARPS * 32) count[e] = 0;
+  __syncthreads();
+  const int64_t i0 = part_start(n, gridDim.x, blockIdx.x), i1 = part_start(n, gridDim.x, blockIdx.x + 1);
+  bool bad = false;
+#pragma unroll 4
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += PART_WARPS * 32)
+    atomicAdd(&count[bucket_of(__ldg(experts + i), E, bad)], 1);  // a sum: any order gives the same
+  if (bad) record_error(&g_moe_error, CONVROT_ERR_ARG);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += PART_WARPS * 32) counts[static_cast<int64_t>(blockIdx.x) * (E + 1) + e] = count[e];
+}
+
+__global__ void __launch_bounds__(PART_WARPS * 32)
+moe_place_kernel(const int32_t* __restrict__ experts, int64_t n, int E, const int32_t* __restrict__ counts,
+                 int32_t* __restrict__ order, int32_t* __restrict__ place, int32_t* __restrict__ offsets) {
+  extern __shared__ int place_smem[];  // next place [PART_WARPS][E + 1]
+  __shared__ int warp_sums[PART_WARPS];
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  constexpr uint32_t ALL = 0xffffffffu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = E + 1;
+  const int part = static_cast<int>(blockIdx.x), parts = static_cast<int>(gridDim.x);
+  int* next = place_smem + warp * B;
+  for (int e = lane; e < B; e += 32) next[e] = 0;
+  __syncwarp();
+  const int64_t i0 = part_start(n, parts, part), i1 = part_start(n, parts, part + 1);
+  const int64_t groups = (i1 - i0 + 31) / 32, g0 = groups * warp / PART_WARPS, g1 = groups * (warp + 1) / PART_WARPS;
+  bool bad = false;
+  auto bucket_at = [&](int64_t i) { return i < i1 ? bucket_of(__ldg(experts + i), E, bad) : -1; };
+  for (int64_t g = g0; g < g1; ++g) {
+    const int b = bucket_at(i0 + g * 32 + lane);
+    const uint32_t same = __match_any_sync(ALL, b);
+    if (b >= 0 && (same >> lane) == 1u) next[b] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  int carry = 0;  // choices of the experts before this turn's
+  for (int e0 = 0; e0 < B; e0 += PART_WARPS * 32) {
+    const int e = e0 + threadIdx.x;
+    int before = 0, all = 0;
+    if (e < B) {
+#pragma unroll 16
+      for (int c = 0; c < parts; ++c) {
+        const int v = __ldg(counts + static_cast<int64_t>(c) * B + e);
+        before += c < part ? v : 0;
+        all += v;
+      }
+    }
+    int scan = all;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(ALL, scan, d);
+      if (lane >= d) scan += v;
+    }
+    if (lane == 31) warp_sums[warp] = scan;
+    __syncthreads();
+    int first = carry + scan - all;
+#pragma unroll
+    for (int w = 0; w < PART_WARPS; ++w) {
+      if (w < warp) first += warp_sums[w];
+      carry += warp_sums[w];
+    }
+    if (e < B) {
+      if (part == 0) offsets[e] = first;
+      int at = first + before;
+#pragma unroll
+      for (int w = 0; w < PART_WARPS; ++w) {
+        const int c = place_smem[w * B + e];
+        place_smem[w * B + e] = at;
+        at += c;
+      }
+    }
+    __syncthreads();
+  }
+  for (int64_t g = g0; g < g1; ++g) {
+    const int64_t i = i0 + g * 32 + lane;
+    const int b = bucket_at(i);
+    const uint32_t same = __match_any_sync(ALL, b);
+    const int to = b >= 0 ? next[b] + __popc(same & ((1u << lane) - 1u)) : 0;
+    __syncwarp();
+    if (b >= 0 && (same >> lane) == 1u) next[b] += __popc(same);
+    __syncwarp();
+    if (b >= 0) {
+      order[to] = b < E ? static_cast<int32_t>(i) : -1;
+      place[i] = b < E ? to : -1;
     }
   }
 }
@@ -521,66 +633,117 @@ moe_pack_kernel(const T* __restrict__ X, int64_t ldx, uint32_t n_qblocks, uint32
 // latencies add up (bf16 [32, 2048] of eight rows 7.5 us).
 
 constexpr int COMBINE_THREADS = 128;
-constexpr int COMBINE_BATCH = 8;
 
-template <int E, typename T>
-__device__ __forceinline__ void load_row(const T* p, float (&x)[E]) {
-  if constexpr (E == 8) {
-    fp8::Pair v[4];
-    fp8::load8(p, v);
+// Eight values of a row (one, without VEC) as they are in memory: loads that
+// stay where they are written, before the first use of any of them.
+template <typename T, bool VEC>
+struct Raw {
+  static constexpr int PIECES = VEC ? sizeof(T) / 2 : 1;
+  uint4 v[PIECES];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f32x2_unpack(v[i], x[2 * i], x[2 * i + 1]);
-  } else {
-    x[0] = to_f32(*p);
+      for (int i = 0; i < PIECES; ++i)
+        asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                     : "l"(reinterpret_cast<const uint4*>(p) + i));
+    } else if constexpr (sizeof(T) == 4) {
+      asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v[0].x) : "l"(p));
+    } else {
+      uint16_t h;
+      asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h) : "l"(p));
+      v[0].x = h;
+    }
   }
-}
+  __device__ __forceinline__ void unpack(float (&x)[VEC ? 8 : 1]) const {
+    if constexpr (!VEC && sizeof(T) == 4) {
+      x[0] = __uint_as_float(v[0].x);
+    } else if constexpr (!VEC) {
+      float none;
+      fp8::unpack2<T>(v[0].x, x[0], none);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[4 * i] = __uint_as_float(v[i].x);
+        x[4 * i + 1] = __uint_as_float(v[i].y);
+        x[4 * i + 2] = __uint_as_float(v[i].z);
+        x[4 * i + 3] = __uint_as_float(v[i].w);
+      }
+    } else {
+      fp8::unpack2<T>(v[0].x, x[0], x[1]);
+      fp8::unpack2<T>(v[0].y, x[2], x[3]);
+      fp8::unpack2<T>(v[0].z, x[4], x[5]);
+      fp8::unpack2<T>(v[0].w, x[6], x[7]);
+    }
+  }
+};
 
 template <typename TR, typename TY, bool VEC>
-__global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const __grid_constant__ CombineArgs a) {
+__global__ void __launch_bounds__(COMBINE_THREADS, 8) moe_combine_kernel(const __grid_constant__ CombineArgs a) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
-  constexpr int E = VEC ? 8 : 1;  // features per thread
+  constexpr int E = VEC ? 8 : 1;                 // features per thread
+  constexpr int BATCH = sizeof(TR) == 4 ? 4 : 8;  // rows loaded together
   const int64_t per_row = (a.N + E - 1) / E;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * COMBINE_THREADS + threadIdx.x;
   const int64_t t = i / per_row, col = (i - t * per_row) * E;
   if (t >= a.T) return;
+  const int32_t* place = a.place + t * a.top_k;
+  const float* weights = a.weights + t * a.top_k;
+  const TR* rows = static_cast<const TR*>(a.rows) + col;
+  const int n = static_cast<int>(a.n);
   float acc[E];
 #pragma unroll
   for (int k = 0; k < E; ++k) acc[k] = 0.0f;
-  const TR* rows = static_cast<const TR*>(a.rows) + col;
-  for (int j0 = 0; j0 < a.top_k; j0 += COMBINE_BATCH) {
-    float x[COMBINE_BATCH][E], w[COMBINE_BATCH];
-    int64_t r[COMBINE_BATCH];
+  for (int j0 = 0; j0 < a.top_k; j0 += BATCH) {
+    Raw<TR, VEC> x[BATCH];
+    float w[BATCH], s[BATCH];
+    uint32_t on = 0;
+    int r[BATCH];
 #pragma unroll
-    for (int j = 0; j < COMBINE_BATCH; ++j) {
-      const bool on = j0 + j < a.top_k;
-      r[j] = on ? __ldg(a.place + t * a.top_k + j0 + j) : -1;
-      w[j] = on ? __ldg(a.weights + t * a.top_k + j0 + j) : 0.0f;
-      if (r[j] >= a.n) r[j] = -1;
+    for (int j = 0; j < BATCH; ++j) {
+      r[j] = j0 + j < a.top_k ? __ldg(place + j0 + j) : -1;
+      w[j] = j0 + j < a.top_k ? __ldg(weights + j0 + j) : 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < COMBINE_BATCH; ++j)
-      if (r[j] >= 0) load_row<E>(rows + r[j] * a.ldr, x[j]);
+    for (int j = 0; j < BATCH; ++j) {
+      s[j] = 1.0f;
+      if (r[j] >= 0 && r[j] < n) {
+        on |= 1u << j;
+        x[j].load(rows + r[j] * a.ldr);
+        if (a.r_scale) s[j] = __ldg(a.r_scale + r[j] * a.r_blocks + col / fp8::QBLOCK);
+      }
+    }
 #pragma unroll
-    for (int j = 0; j < COMBINE_BATCH; ++j)
-      if (r[j] >= 0) {
-        if (a.r_scale) w[j] *= __ldg(a.r_scale + r[j] * a.r_blocks + col / fp8::QBLOCK);
+    for (int j = 0; j < BATCH; ++j)
+      if (on >> j & 1u) {
+        float v[E];
+        x[j].unpack(v);
+        const float f = w[j] * s[j];
 #pragma unroll
-        for (int k = 0; k < E; ++k) acc[k] = fmaf(w[j], x[j][k], acc[k]);
+        for (int k = 0; k < E; ++k) acc[k] = fmaf(f, v[k], acc[k]);
       }
   }
   TY* y = static_cast<TY*>(a.Y) + t * a.ldy + col;
   if (a.residual) {
-    float x[E];
-    load_row<E>(static_cast<const TY*>(a.residual) + t * a.ld_res + col, x);
+    const TY* res = static_cast<const TY*>(a.residual) + t * a.ld_res + col;
+    float v[E];
+    if constexpr (VEC) {
+      fp8::Pair q[4];
+      fp8::load8(res, q);
 #pragma unroll
-    for (int k = 0; k < E; ++k) acc[k] += x[k];
+      for (int k = 0; k < 4; ++k) f32x2_unpack(q[k], v[2 * k], v[2 * k + 1]);
+    } else {
+      v[0] = to_f32(*res);
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) acc[k] += v[k];
   }
   if constexpr (VEC) {
-    fp8::Pair x[4];
+    fp8::Pair q[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = f32x2_pack(acc[2 * k], acc[2 * k + 1]);
-    fp8::store8(y, x);
+    for (int k = 0; k < 4; ++k) q[k] = f32x2_pack(acc[2 * k], acc[2 * k + 1]);
+    fp8::store8(y, q);
   } else {
     *y = from_f32<TY>(acc[0]);
   }
@@ -660,19 +823,30 @@ template <int W>
 static int plan_as(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
                    cudaStream_t stream) {
   Launch l(static_cast<unsigned>((E + W) / W), PLAN_WARPS * 32, 0, stream);  // E + 1 buckets
-  const cudaError_t e = n > PLAN_WARPS * 32 * 8
-                            ? cudaLaunchKernelEx(&l.cfg, moe_plan_kernel<W, 16>, experts, n, E, order, place, offsets)
-                            : cudaLaunchKernelEx(&l.cfg, moe_plan_kernel<W, 4>, experts, n, E, order, place, offsets);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, moe_plan_kernel<W>, experts, n, E, order, place, offsets);
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
-// As many experts per CTA as give every SM one CTA.
-int launch_plan(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
+static int64_t plan_parts(int64_t n) { return n <= PLAN_ONE ? 0 : std::min(PLAN_PARTS, (n + PART_LEAST - 1) / PART_LEAST); }
+size_t plan_workspace(int64_t n, int E) { return static_cast<size_t>(plan_parts(n)) * (E + 1) * sizeof(int32_t); }
+
+int launch_plan(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets, void* workspace,
                 cudaStream_t stream) {
-  if (E < 152) return plan_as<1>(experts, n, E, order, place, offsets, stream);
-  if (E < 304) return plan_as<2>(experts, n, E, order, place, offsets, stream);
-  if (E < 608) return plan_as<4>(experts, n, E, order, place, offsets, stream);
-  return plan_as<8>(experts, n, E, order, place, offsets, stream);
+  const int64_t parts = plan_parts(n);
+  if (parts == 0) {  // as many experts per CTA as leave every SM about one CTA
+    if (E < 152) return plan_as<1>(experts, n, E, order, place, offsets, stream);
+    if (E < 304) return plan_as<2>(experts, n, E, order, place, offsets, stream);
+    if (E < 608) return plan_as<4>(experts, n, E, order, place, offsets, stream);
+    return plan_as<8>(experts, n, E, order, place, offsets, stream);
+  }
+  int32_t* counts = static_cast<int32_t*>(workspace);
+  static_assert(PART_WARPS * (MAX_EXPERTS + 1) * 4 <= 48 * 1024, "shared memory");
+  Launch count(static_cast<unsigned>(parts), PART_WARPS * 32, 0, stream);
+  cudaError_t e = cudaLaunchKernelEx(&count.cfg, moe_count_kernel, experts, n, E, counts);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  Launch put(static_cast<unsigned>(parts), PART_WARPS * 32, sizeof(int) * PART_WARPS * (E + 1), stream);
+  e = cudaLaunchKernelEx(&put.cfg, moe_place_kernel, experts, n, E, static_cast<const int32_t*>(counts), order, place, offsets);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
 int launch_gather(const uint8_t* Q, const float* s, int64_t K, const Rows& r, uint8_t* Q_out, float* s_out,

@@ -171,7 +171,8 @@ SIGNATURES = {
     "fp8_linear_packed": (_I, [_VP, _VP, _I64, _I64, _VP, _I, _I, _VP]),
     "fp8_linear": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I, _I, _VP, _SZ, _VP]),
     "moe_route": (_I, [_VP, _VP]),
-    "moe_plan": (_I, [_VP, _I64, _I, _VP, _VP, _VP, _VP]),
+    "moe_plan_workspace_size": (_SZ, [_I64, _I]),
+    "moe_plan": (_I, [_VP, _I64, _I, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "fp8_expert_linear": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I, _I, _VP, _VP, _I64, _I, _VP, _SZ,
                                _VP]),
     "fp8_expert_swiglu": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I, _I, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
@@ -1033,8 +1034,26 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: int = MOE_SOFTMAX, bia
     return experts, weights
 
 
+def moe_plan_workspace_size(n: int, n_experts: int) -> int:
+    return int(lib().moe_plan_workspace_size(n, n_experts))
+
+
+def _bytes(workspace, size: int, device: int, stream):
+    """(address, size) of a workspace of at least `size` bytes: the given one, or
+    a new one where some is needed (returned third, to be kept for the call)."""
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the device of the other tensors")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if size == 0:
+        return 0, 0, None
+    ws = _empty((size,), torch.uint8, device, stream)
+    return ws.data_ptr(), size, ws
+
+
 def moe_plan(experts: torch.Tensor, n_experts: int, order: Optional[torch.Tensor] = None,
-             place: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None, stream=None):
+             place: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None, stream=None):
     """The choices (int32, of any shape) sorted by expert: (order, place,
     offsets), int32. order[i] is the choice of row i (-1 behind the last one),
     place[c] the row of choice c (-1 for none), and expert e has the rows from
@@ -1047,9 +1066,10 @@ def moe_plan(experts: torch.Tensor, n_experts: int, order: Optional[torch.Tensor
         place = _empty((n,), i32, device, stream)
     if offsets is None:
         offsets = _empty((n_experts + 1,), i32, device, stream)
+    ws, size, keep = _bytes(workspace, moe_plan_workspace_size(n, n_experts), device, stream)
     _check(lib().moe_plan(_dense(experts, "experts", device, experts.shape, i32), n, n_experts,
                           _dense(order, "order", device, (n,), i32), _dense(place, "place", device, (n,), i32),
-                          _dense(offsets, "offsets", device, (n_experts + 1,), i32), handle), "moe_plan")
+                          _dense(offsets, "offsets", device, (n_experts + 1,), i32), ws, size, handle), "moe_plan")
     return order, place, offsets
 
 
@@ -1106,19 +1126,6 @@ def _plan_of(Q_x, s_x, order, offsets, E: int, device: int):
 
 def fp8_expert_workspace_size(n: int, K: int, n_experts: int) -> int:
     return int(lib().fp8_expert_workspace_size(n, K, n_experts))
-
-
-def _bytes(workspace, size: int, device: int, stream):
-    """(address, size) of a workspace of at least `size` bytes: the given one, or
-    a new one where some is needed (returned third, to be kept for the call)."""
-    if workspace is not None:
-        if workspace.get_device() != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous and on the device of the other tensors")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    if size == 0:
-        return 0, 0, None
-    ws = _empty((size,), torch.uint8, device, stream)
-    return ws.data_ptr(), size, ws
 
 
 def fp8_expert_linear(Q_x: torch.Tensor, s_x: torch.Tensor, offsets: torch.Tensor, weight,

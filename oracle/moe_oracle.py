@@ -130,8 +130,9 @@ def combine(rows, place, weights, residual=None):
     return Y, A
 
 
-def moe(X, experts, weights, gate, up, down, residual=None):
-    """(Y, what fp32 arithmetic and the codes it may choose can move it by)."""
+def moe(X, experts, weights, gate, up, down, residual=None, rows_error=0.0):
+    """(Y, what fp32 arithmetic and the codes it may choose can move it by);
+    rows_error: the relative rounding of the rows that are summed up."""
     T, k = experts.shape
     Qx, sx = bo.fp8_pack(np.asarray(X, np.float32))
     E = gate[0].shape[0]
@@ -151,5 +152,5 @@ def moe(X, experts, weights, gate, up, down, residual=None):
         if i.start < i.stop:
             dy[i] += slack[i] @ np.abs(val[down[0][e]] * bo.widen(down[1][e], *down[0][e].shape, bo.BLOCK)).T
     Y, A = combine(y, place, weights, residual)
-    D, _ = combine(dy, place, np.abs(weights))
+    D, _ = combine(dy + rows_error * np.abs(y) * (1 + 2.0 ** -10), place, np.abs(weights))
     return Y, D + (k + 3) * U24 * A
