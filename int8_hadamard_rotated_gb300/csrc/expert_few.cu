@@ -60,8 +60,8 @@ struct FewGeom {
   static constexpr int W_BYTES = QBLOCK * BK;  // of one matrix
   static constexpr int X_BYTES = BN * BK;
   static constexpr int STAGE_BYTES = 2 * W_BYTES + X_BYTES;
-  static constexpr int STAGES = BN == 128 ? 3 : BN == 64 ? 4 : 5;
-  static constexpr int KG = BN < 64 ? 64 / BN : 1;  // blocks of K handed over together
+  static constexpr int STAGES = BN == 64 ? 4 : 5;
+  static constexpr int KG = 64 / BN;  // blocks of K handed over together
   static constexpr int BUF_COLS = 2 * KG * BN;
   static constexpr int TMEM_COLS = 512;
   static constexpr int BUFS = TMEM_COLS / BUF_COLS;
@@ -73,7 +73,7 @@ struct FewGeom {
   static constexpr int SMEM_FIRST = SMEM_WIDTH + STAGES * 4;                           // [E + 1]
   static constexpr int smem(int E) { return SMEM_FIRST + (E + 1) * 4 + 1024; }
   static_assert(smem(MAX_EXPERTS) <= 227 * 1024, "shared memory");
-  static_assert(BN % 16 == 0 && (64 % BN == 0 || BN == 128), "columns");
+  static_assert(BN % 16 == 0 && 64 % BN == 0, "columns");
 };
 
 // Adds n <= KG accumulators of `width` <= BN columns (2 * BN apart), each with a
@@ -102,6 +102,17 @@ __device__ __forceinline__ void drain_columns(unsigned long long (&acc)[BN / 2],
     }
   }
   tmem_ld_wait();  // a load past the width may still be on its way
+}
+
+// Where an item's walk over the blocks of K starts: not at the first one for
+// all. Rows of K = 4096 codes lie 4 KB apart, and CTAs that read the same block
+// of their rows at the same time meet in a few of the memory's channels: 144
+// items, one per CTA, were read at 3.7 TB/s. A multiple of four where the
+// scales are read four at a time. By the matrix' place alone, so that an
+// output's sum has the same order in every call.
+__device__ __forceinline__ int first_block(int expert, int col, int n_cols, int blocks, bool vec) {
+  const int at = expert * n_cols + col;
+  return vec ? at % (blocks / 4) * 4 : at * 5 % blocks;
 }
 
 // warp_wait for what the CTAs of a cluster have handed over: what they wrote
@@ -135,7 +146,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
   int* err = &g_few_error;
   const int split = p.split, rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int unit = static_cast<int>(blockIdx.x) / split, n_units = static_cast<int>(gridDim.x) / split;
-  const int kb_begin = p.KB * rank / split, kb_end = p.KB * (rank + 1) / split;
+  const int kb_begin = p.KB * rank / split, kb_end = p.KB * (rank + 1) / split;  // this CTA's blocks of K
+  const int blocks = kb_end - kb_begin;
+  const bool vec = p.vec_scales && kb_begin % 4 == 0 && blocks % 4 == 0;
 
   if (threadIdx.x == EPI_WARPS * 32) {
     for (int s = 0; s < G::STAGES; ++s) {
@@ -187,8 +200,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
           rows.z = source_row(p.rows, min(i + 2, last));
           rows.w = source_row(p.rows, min(i + 3, last));
         }
-        for (int kb = kb_begin; kb < kb_end; ++kb) {
-          if (p.withhold && t == total - 1 && rank == split - 1 && kb == kb_end - 1) break;
+        int kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, vec);
+        for (int i = 0; i < blocks; ++i) {
+          if (p.withhold && t == total - 1 && rank == split - 1 && i == blocks - 1) break;
           ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, err, p.wait_ns);
           if (!ok) break;
           uint8_t* sw = smem + stage * G::STAGE_BYTES;
@@ -206,6 +220,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
           __syncwarp();
           if (gather && 4 * lane < width) tma_gather4(sx + lane * 4 * BK, &p.tmap_x, &full[stage], kb * BK, rows, pol);
           ++n_issued;
+          if (++kb == kb_end) kb = kb_begin;
           if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
         }
       }
@@ -219,15 +234,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
         uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
         bool ok = true;
         for (int t = unit; ok && t < total; t += n_units) {
-          for (int kb0 = kb_begin; ok && kb0 < kb_end; kb0 += G::KG) {
+          for (int i0 = 0; ok && i0 < blocks; i0 += G::KG) {
             ok = mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err, p.wait_ns);
-            for (int kb = kb0; ok && kb < min(kb0 + G::KG, kb_end); ++kb) {
+            for (int i = i0; ok && i < min(i0 + G::KG, blocks); ++i) {
               ok = mbar_wait(&full[stage], phase, abort_flag, err, p.wait_ns);
               if (!ok) break;
               tc_fence_after();
               const uint32_t sw = smem_u32(smem + stage * G::STAGE_BYTES), sx = sw + 2 * G::W_BYTES;
               const uint32_t idesc = idesc_e4m3_f32(LANES, stage_width[stage]);
-              const uint32_t d = tmem_base + buf * G::BUF_COLS + (kb - kb0) * 2 * BN;
+              const uint32_t d = tmem_base + buf * G::BUF_COLS + (i - i0) * 2 * BN;
               mma_block<1>(d, sw, sx, idesc);
               mma_block<1>(d + BN, sw + G::W_BYTES, sx, idesc);
               mma_commit(&empty[stage]);
@@ -253,7 +268,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
     uint32_t buf = 0, bphase = 0;
     int flip = 1;
     uint32_t seq = 0;  // partial tiles that have been handed over
-    const bool vec = p.vec_scales && kb_begin % 4 == 0;
     const int N = p.N;
     auto arrive_everywhere = [&](uint64_t* bar) {
       __syncwarp();
@@ -266,7 +280,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
     // An item's place is looked up, and its first scales are loaded, while the
     // one before it is finished.
     struct Info {
-      int row, valid, col, expert;
+      int row, valid, col, expert, kb;  // kb: the first block of K
       const float* xs[XR];
       const float* ws;
     };
@@ -278,6 +292,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
       i.valid = min(BN, range.y - i.row);
       i.col = c.col;
       i.expert = c.expert;
+      i.kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, vec);
 #pragma unroll
       for (int k = 0; k < XR; ++k)
         i.xs[k] = p.s_x + static_cast<int64_t>(source_row(p.rows, min(i.row + (32 * k + lane) % BN, range.y - 1))) * p.KB;
@@ -288,15 +303,26 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
       return i;
     };
     float nx[XR][4], nw[4];
-    auto load_factors = [&](const Info& i, int kb) {
+    // Four blocks' scales from kb on (past the CTA's last one: its first ones),
+    // `count` of them in use.
+    auto load_four = [&](const float* s, int kb, int count, float (&v)[4]) {
+      if (vec) {
+        const float4 f = ldg_now4(s + kb);
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+      } else {
 #pragma unroll
-      for (int k = 0; k < XR; ++k) load_scales(i.xs[k], kb, p.KB, vec, nx[k]);
-      load_scales(i.ws, kb, p.KB, vec, nw);
+        for (int i = 0; i < 4; ++i) v[i] = i < count ? ldg_now(s + (kb + i < kb_end ? kb + i : kb + i - blocks)) : 0.0f;
+      }
+    };
+    auto load_factors = [&](const Info& i, int kb, int count) {
+#pragma unroll
+      for (int k = 0; k < XR; ++k) load_four(i.xs[k], kb, count, nx[k]);
+      load_four(i.ws, kb, count, nw);
     };
     Info info{};
     if (unit < total) {
       info = look_up(unit);
-      load_factors(info, kb_begin);
+      load_factors(info, info.kb, blocks);
     }
     for (int t = unit; t < total; t += n_units) {
       const int row = info.row, valid = info.valid, width = (valid + 15) & ~15, n0 = info.col * FEATURES;
@@ -315,7 +341,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
       for (int i = 0; i < BN / 2; ++i) acc[i] = 0ull;
       bool ok = true;
 #pragma unroll 1
-      for (int kb = kb_begin, i = 0; kb < kb_end; kb += G::KG, i = (i + G::KG) & 3) {
+      for (int done_blocks = 0, kb = info.kb, i = 0; done_blocks < blocks; done_blocks += G::KG, i = (i + G::KG) & 3) {
         if (i == 0) {  // the factors of four blocks; the next four's scales are on their way meanwhile
           flip ^= 1;
 #pragma unroll
@@ -324,12 +350,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
             for (int k = 0; k < XR; ++k)
               if (BN >= 32 || lane < BN) sc[(flip * 4 + j) * BN + 32 * k + lane] = nx[k][j] * nw[j];
           __syncwarp();
-          if (kb + 4 < kb_end) load_factors(info, kb + 4);
+          kb = kb + 4 < kb_end ? kb + 4 : kb + 4 - blocks;
+          if (done_blocks + 4 < blocks) load_factors(info, kb, blocks - done_blocks - 4);
         }
         ok = warp_wait(&tfull[buf], bphase, abort_flag, err, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
-        drain_columns<BN, G::KG>(acc, t_addr + buf * G::BUF_COLS, sc + (flip * 4 + i) * BN, kb_end - kb, width);
+        drain_columns<BN, G::KG>(acc, t_addr + buf * G::BUF_COLS, sc + (flip * 4 + i) * BN, blocks - done_blocks, width);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[buf]);
@@ -339,7 +366,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
       const int col = info.col;
       if (t + n_units < total) {
         info = look_up(t + n_units);
-        load_factors(info, kb_begin);
+        load_factors(info, info.kb, blocks);
       }
 #pragma unroll
       for (int part_row = 0; part_row < BN; part_row += G::PART_ROWS) {
@@ -524,12 +551,11 @@ int launch_expert_few(const ExpertCall& c, cudaStream_t stream) {
   const int64_t per = c.rows.n / c.rows.E;
   if (const char* v = getenv("EXPERT_BN")) {
     const int bn = atoi(v);
-    return bn == 16 ? launch_columns<16>(c, stream) : bn == 32 ? launch_columns<32>(c, stream) : bn == 64 ? launch_columns<64>(c, stream) : launch_columns<128>(c, stream);
+    return bn == 16 ? launch_columns<16>(c, stream) : bn == 32 ? launch_columns<32>(c, stream) : launch_columns<64>(c, stream);
   }
   if (per <= 12) return launch_columns<16>(c, stream);
   if (per <= 24) return launch_columns<32>(c, stream);
-  if (per <= 56) return launch_columns<64>(c, stream);
-  return launch_columns<128>(c, stream);
+  return launch_columns<64>(c, stream);
 }
 
 cudaError_t few_error_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_few_error); }

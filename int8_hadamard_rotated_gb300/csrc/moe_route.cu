@@ -679,15 +679,14 @@ struct Raw {
 };
 
 template <typename TR, typename TY, bool VEC>
-__global__ void __launch_bounds__(COMBINE_THREADS, 8) moe_combine_kernel(const __grid_constant__ CombineArgs a) {
+__global__ void __launch_bounds__(COMBINE_THREADS, 8) moe_combine_kernel(const __grid_constant__ CombineArgs a, uint32_t chunks) {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
   constexpr int E = VEC ? 8 : 1;                 // features per thread
   constexpr int BATCH = sizeof(TR) == 4 ? 4 : 8;  // rows loaded together
-  const int64_t per_row = (a.N + E - 1) / E;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * COMBINE_THREADS + threadIdx.x;
-  const int64_t t = i / per_row, col = (i - t * per_row) * E;
-  if (t >= a.T) return;
+  const uint32_t token = blockIdx.x / chunks;
+  const int64_t t = token, col = ((blockIdx.x - token * chunks) * blockDim.x + threadIdx.x) * static_cast<int64_t>(E);
+  if (col >= a.N) return;
   const int32_t* place = a.place + t * a.top_k;
   const float* weights = a.weights + t * a.top_k;
   const TR* rows = static_cast<const TR*>(a.rows) + col;
@@ -720,8 +719,14 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 8) moe_combine_kernel(const _
         float v[E];
         x[j].unpack(v);
         const float f = w[j] * s[j];
+        if constexpr (VEC) {
+          const unsigned long long f2 = f32x2_pack(f, f);
 #pragma unroll
-        for (int k = 0; k < E; ++k) acc[k] = fmaf(f, v[k], acc[k]);
+          for (int k = 0; k < E; k += 2)
+            f32x2_unpack(f32x2_fma(f2, f32x2_pack(v[k], v[k + 1]), f32x2_pack(acc[k], acc[k + 1])), acc[k], acc[k + 1]);
+        } else {
+          acc[0] = fmaf(f, v[0], acc[0]);
+        }
       }
   }
   TY* y = static_cast<TY*>(a.Y) + t * a.ldy + col;
@@ -776,12 +781,14 @@ int combine_as(const CombineArgs& a, cudaStream_t stream) {
   auto fits = [&](const void* p, int64_t ld, size_t size) { return aligned16(p) && (ld * size) % 16 == 0; };
   const bool vec = a.N % 8 == 0 && fits(a.rows, a.ldr, sizeof(TR)) && fits(a.Y, a.ldy, sizeof(TY)) &&
                    (!a.residual || fits(a.residual, a.ld_res, sizeof(TY)));
-  const int64_t items = a.T * (vec ? a.N / 8 : a.N);
-  const int64_t blocks = (items + COMBINE_THREADS - 1) / COMBINE_THREADS;
-  if (blocks > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
-  Launch l(static_cast<unsigned>(blocks), COMBINE_THREADS, 0, stream);
-  const cudaError_t e = vec ? cudaLaunchKernelEx(&l.cfg, moe_combine_kernel<TR, TY, true>, a)
-                            : cudaLaunchKernelEx(&l.cfg, moe_combine_kernel<TR, TY, false>, a);
+  const int64_t items = vec ? a.N / 8 : a.N;  // of a token
+  const int64_t threads = std::min<int64_t>(COMBINE_THREADS, (items + 31) / 32 * 32);
+  const int64_t chunks = (items + threads - 1) / threads;
+  if (chunks * a.T > 0x7fffffff) return CONVROT_ERR_UNSUPPORTED;
+  Launch l(static_cast<unsigned>(chunks * a.T), static_cast<unsigned>(threads), 0, stream);
+  const uint32_t c = static_cast<uint32_t>(chunks);
+  const cudaError_t e = vec ? cudaLaunchKernelEx(&l.cfg, moe_combine_kernel<TR, TY, true>, a, c)
+                            : cudaLaunchKernelEx(&l.cfg, moe_combine_kernel<TR, TY, false>, a, c);
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
