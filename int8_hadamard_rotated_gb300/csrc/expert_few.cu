@@ -22,7 +22,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 
 namespace convrot {
 namespace moe {
@@ -463,16 +462,24 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
   }
 }
 
-// Clusters of `split` CTAs that run at the same time, or 0.
+// Clusters of `split` CTAs that run at the same time: looked up once per device
+// (every instance of the kernel takes an SM to itself).
 template <typename F>
-int resident_clusters(F* kernel, int smem, int split) {
-  Launch l(split, FEW_THREADS, smem, nullptr, split);
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
+int resident_clusters(F* kernel, int smem, int split, int& n) {
+  static std::mutex mu;
+  static int known[64][MAX_SPLIT + 1] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  std::lock_guard<std::mutex> lock(mu);
+  n = dev < 64 ? known[dev][split] : 0;
+  if (n == 0) {
+    Launch l(split, FEW_THREADS, smem, nullptr, split);
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    if (dev < 64) known[dev][split] = n;
   }
-  return n;
+  return CONVROT_OK;
 }
 
 template <int BN, bool SWIGLU, typename TY>
@@ -505,34 +512,30 @@ int launch_as(const ExpertCall& c, cudaStream_t stream) {
   static uint64_t done = 0;
   auto kernel = expert_few_kernel<BN, SWIGLU, TY>;
   if (int st = allow_smem(kernel, G::smem(MAX_EXPERTS), done, mu, LAUNCH_REGS)) return st;
-  // The items that choices spread evenly would give; K is split while they
-  // leave CTAs without one.
+  // K is split over as many CTAs as give each item of evenly spread choices a
+  // cluster of its own at the same time: one CTA streams some 60 GB/s a
+  // microsecond at most, but a second round of a cluster's exchange costs more
+  // than it gains. SwiGLU of 2 x 1536 x 4096 matrices: 36 items (three experts)
+  // take 22.2, 15.7 and 14.1 us unsplit, in two and in four, 72 items 22.6, 19.7
+  // and 20.5 us, 96 items 23.5, 28.2 and 27.5 us.
   const double reached = static_cast<double>(E) * (1.0 - std::pow(1.0 - 1.0 / static_cast<double>(E), static_cast<double>(n)));
   const double items = std::max(reached, static_cast<double>(n) / BN) * static_cast<double>(cols);
   const int sms = device_sm_count();
-  int split = 1;
-  while (split < MAX_SPLIT && items * split < 0.5 * sms && 2 * split <= KB) split *= 2;
-  if (const char* v = getenv("EXPERT_SPLIT")) { split = atoi(v); while (split > KB) split /= 2; }
-  static std::mutex units_mu;
-  static int units_of[64][MAX_SPLIT + 1] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  int units = 0;
-  {
-    std::lock_guard<std::mutex> lock(units_mu);
-    int* known = dev < 64 ? &units_of[dev][split] : nullptr;
-    if (known && *known) units = *known;
-    else {
-      units = split == 1 ? sms : resident_clusters(kernel, G::smem(MAX_EXPERTS), split);
-      if (units <= 0) units = sms / split;
-      if (known) *known = units;
+  int split = 1, units = sms;
+  for (int s : {4, 2}) {
+    if (items > sms / s || KB < s) continue;
+    int n = 0;
+    if (int st = resident_clusters(kernel, G::smem(MAX_EXPERTS), s, n)) return st;
+    if (items <= n) {
+      split = s;
+      units = n;
+      break;
     }
   }
   units = static_cast<int>(std::min<int64_t>(units, cols * tiles));
   p.split = split;
   Launch l(static_cast<unsigned>(units * split), FEW_THREADS, G::smem(c.rows.E), stream, split);
-  e = cudaLaunchKernelEx(&l.cfg, kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, p);
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
@@ -548,12 +551,14 @@ int launch_columns(const ExpertCall& c, cudaStream_t stream) {
 }  // namespace
 
 int launch_expert_few(const ExpertCall& c, cudaStream_t stream) {
+  // Items of the rows that an expert has on average: narrower ones cost less
+  // while the expert's rows are one item, and read its weights once more for
+  // every further item. 64 experts of 3 x 1024 x 2048 (16 of 3 x 1536 x 4096),
+  // gate and up: 16 rows each 54, 59 and 63 us (41, 50 and 58) with 16, 32 and 64
+  // columns; 24 rows 64, 68 and 67 us (54, 48 and 57); 32 rows 80, 74 and 71 us
+  // (69, 64 and 59).
   const int64_t per = c.rows.n / c.rows.E;
-  if (const char* v = getenv("EXPERT_BN")) {
-    const int bn = atoi(v);
-    return bn == 16 ? launch_columns<16>(c, stream) : bn == 32 ? launch_columns<32>(c, stream) : launch_columns<64>(c, stream);
-  }
-  if (per <= 12) return launch_columns<16>(c, stream);
+  if (per <= 16) return launch_columns<16>(c, stream);
   if (per <= 24) return launch_columns<32>(c, stream);
   return launch_columns<64>(c, stream);
 }

@@ -8,31 +8,26 @@
 // as it leaves. Which kernel takes them.
 #include "expert_common.cuh"
 
-#include <cstdlib>
-
 namespace convrot {
 namespace moe {
 
-bool many_rows(int64_t n, int E) {
-  if (const char* v = getenv("EXPERT_KERNEL")) return atoi(v) >= 2;
-  return n / E > 64;
-}
+// By the rows that an expert has on average. 64 experts of 3 x 1024 x 2048 (16 of
+// 3 x 1536 x 4096), gate and up plus down: 48 rows each take 140 us (91) with
+// the few-row kernel and 130 us (100) with the other, 64 rows 143 us (103) and 132
+// us (100), 128 rows 247 us (175) and 148 us (103).
+bool many_rows(int64_t n, int E) { return n / E > 56; }
 
 int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& gate,
                          const convrot_experts& up, uint8_t* Q_h, float* s_h, cudaStream_t stream,
                          uint64_t test_wait_ns) {
   const ExpertCall c{Q, s, K, r, &gate, &up, Q_h, s_h, gate.N, 0, test_wait_ns};
-  const char* v = getenv("EXPERT_KERNEL");
-  const bool pair = v ? atoi(v) == 2 : many_rows(r.n, r.E);
-  return pair ? launch_expert_pair(c, stream) : launch_expert_few(c, stream);
+  return many_rows(r.n, r.E) ? launch_expert_pair(c, stream) : launch_expert_few(c, stream);
 }
 
 int launch_expert_linear(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& w, void* Y,
                          int64_t ldy, int y_dtype, float* powers, cudaStream_t stream, uint64_t test_wait_ns) {
   const ExpertCall c{Q, s, K, r, &w, nullptr, Y, powers, ldy, y_dtype, test_wait_ns};
-  const char* v = getenv("EXPERT_KERNEL");
-  const bool pair = v ? atoi(v) == 2 : many_rows(r.n, r.E);
-  return pair ? launch_expert_pair(c, stream) : launch_expert_few(c, stream);
+  return many_rows(r.n, r.E) ? launch_expert_pair(c, stream) : launch_expert_few(c, stream);
 }
 
 }  // namespace moe

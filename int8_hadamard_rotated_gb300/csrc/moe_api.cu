@@ -315,12 +315,15 @@ int fp8_moe(const convrot_moe_args* args, void* workspace, size_t workspace_byte
   float *s_x = reinterpret_cast<float*>(ws + at.s_x), *s_h = reinterpret_cast<float*>(ws + at.s_h);
   int32_t *order = reinterpret_cast<int32_t*>(ws + at.order), *place = reinterpret_cast<int32_t*>(ws + at.place);
   int32_t* offsets = reinterpret_cast<int32_t*>(ws + at.offsets);
-  if (int st = launch_plan(a.experts, n, a.n_experts, order, place, offsets, ws + at.plan, s)) return st;
   const Rows by_token{order, offsets, n, a.T, a.n_experts, a.top_k}, sorted{nullptr, offsets, n, n, a.n_experts, 1};
   const bool many = many_rows(n, a.n_experts);
-  if (int st = many ? launch_pack_sorted(a.X, a.x_dtype, a.T, a.K, a.ldx, place, a.top_k, q_x, s_x, s)
-                    : launch_fp8_pack(a.X, a.x_dtype, a.T, a.K, a.ldx, q_x, s_x, s))
+  if (many) {
+    if (int st = launch_plan(a.experts, n, a.n_experts, order, place, offsets, ws + at.plan, s)) return st;
+    if (int st = launch_pack_sorted(a.X, a.x_dtype, a.T, a.K, a.ldx, place, a.top_k, q_x, s_x, s)) return st;
+  } else if (int st = launch_plan_pack(a.experts, n, a.n_experts, order, place, offsets, ws + at.plan, a.X, a.x_dtype, a.T,
+                                       a.K, a.ldx, a.top_k, q_x, s_x, s)) {
     return st;
+  }
   if (int st = launch_expert_swiglu(q_x, s_x, a.K, many ? sorted : by_token, *a.gate, *a.up, q_h, s_h, s)) return st;
   const bool half = a.y_dtype == CONVROT_BF16;
   float* powers = half ? reinterpret_cast<float*>(ws + at.powers) : nullptr;

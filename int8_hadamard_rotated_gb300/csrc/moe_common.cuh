@@ -49,6 +49,11 @@ int launch_gather(const uint8_t* Q, const float* s, int64_t K, const Rows& r, ui
 int launch_pack_sorted(const void* X, int x_dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* place, int top_k,
                        uint8_t* Q, float* s, cudaStream_t stream);
 
+// launch_plan, and X packed by token; in one launch where the choices are few.
+int launch_plan_pack(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
+                     void* workspace, const void* X, int x_dtype, int64_t T, int64_t K, int64_t ldx, int top_k, uint8_t* Q,
+                     float* s, cudaStream_t stream);
+
 // Whether n rows of E experts are taken by the kernel for many rows per expert,
 // which wants them in the plan's order (r.order null).
 bool many_rows(int64_t n, int E);

@@ -92,6 +92,14 @@ __device__ __noinline__ double score64(float l, float m, double total, bool sigm
   return sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : exp64(l, m) / total;
 }
 
+// The sigmoid to choose by: the hardware's base-2 exponential and reciprocal,
+// within the bound on the values' error below.
+__device__ __forceinline__ float sigmoid_fast(float l) {
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * fabsf(l)));
+  return rcp_approx(1.0f + e) * (l >= 0.0f ? 1.0f : e);
+}
+
 // exp(-c) / (1 + exp(-l)) for c = 0, or l <= c < 0: without underflow in the
 // latter case where l is near c.
 __device__ __forceinline__ float sigmoid_from(float l, float c) {
@@ -100,7 +108,7 @@ __device__ __forceinline__ float sigmoid_from(float l, float c) {
 }
 
 template <typename T, int EPL>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 8 : 1) moe_route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ float route_smem[];  // grouped: [warp][E + padding] logits, then values
   pdl_wait_prerequisites();
   pdl_launch_dependents();
@@ -124,7 +132,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
   float total = 1.0f;
   if (p.sigmoid) {
 #pragma unroll
-    for (int r = 0; r < EPL; ++r) s[r] = sigmoid_from(l[r], 0.0f);
+    for (int r = 0; r < EPL; ++r) s[r] = sigmoid_fast(l[r]);
   } else {
     m = value_of(__reduce_max_sync(ALL, key_of(m)));
     float sum = 0.0f;
@@ -134,8 +142,9 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
       sum += s[r];
     }
     total = warp_sum(sum);
+    const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
 #pragma unroll
-    for (int r = 0; r < EPL; ++r) s[r] = total > 0.0f ? __fdiv_rn(s[r], total) : 0.0f;
+    for (int r = 0; r < EPL; ++r) s[r] *= inv;
   }
   // what is compared; an expert whose logit or bias is -inf is not chosen
   uint32_t key[EPL];
@@ -155,10 +164,12 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     return;
   }
 
-  // Bound on the error of an fp32 value against its 64-bit one. Sigmoid: exp
-  // within 2 ulp and two more roundings, 3.6e-7 s, s <= 1. Softmax: exp within
-  // 2 ulp, the rounding of its argument (x exp(-x) 2^-24 <= 2^-25), a sum of
-  // at most EPL + 5 steps and a division, 44 x 2^-24 s at most, s <= 1 / total.
+  // Bound on the error of an fp32 value against its 64-bit one. Sigmoid: the
+  // exponential is within 2^-22 and, from its argument's rounding, |x| 2^-23,
+  // both times s (1 - s) (|x| s (1 - s) <= 0.23); the sum, the reciprocal (one
+  // ulp) and the product make 4 x 2^-24 s: 3.3e-7 in all. Softmax: exp within 2
+  // ulp, the rounding of its argument (x exp(-x) 2^-24 <= 2^-25), a sum of at
+  // most EPL + 5 steps, a division and a product: 44 x 2^-24 / total at most.
   // The bias adds 2^-24 |v|.
   const float score_error = p.sigmoid ? 0x1p-21f : 0x1p-18f * __fdiv_rn(1.0f, fmaxf(total, 1.0f));
   auto error_at = [&](float v) { return score_error + 0x1p-23f * fabsf(v); };
@@ -264,17 +275,26 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
     chosen = -1;
     logit = -INFINITY;
     taken = place_key = 0u;
+    // each lane's largest key that is left, and the first place that has it
+    uint32_t best_key;
+    int best_r;
+    auto look = [&]() {
+      best_key = 0u;
+      best_r = 0;
+#pragma unroll
+      for (int r = EPL - 1; r >= 0; --r) {
+        const uint32_t k = taken >> r & 1u ? 0u : key[r];
+        if (k >= best_key) {
+          best_key = k;
+          best_r = r;
+        }
+      }
+    };
+    look();
     for (int j = 0; j < count; ++j) {
-      uint32_t top = 0u;
-#pragma unroll
-      for (int r = 0; r < EPL; ++r) top = max(top, taken >> r & 1u ? 0u : key[r]);
-      top = __reduce_max_sync(ALL, top);
+      const uint32_t top = __reduce_max_sync(ALL, best_key);
       if (top == 0u) break;
-      uint32_t e = 0xffffu;
-#pragma unroll
-      for (int r = EPL - 1; r >= 0; --r)
-        if (key[r] == top && !(taken >> r & 1u)) e = lane + 32 * r;
-      e = __reduce_min_sync(ALL, e);
+      uint32_t e = __reduce_min_sync(ALL, best_key == top ? static_cast<uint32_t>(lane + 32 * best_r) : 0xffffu);
       if (exact) {
         const float v = value_of(top), lo = v - 2.5f * error_at(v);
         uint32_t near = 0u;
@@ -301,12 +321,13 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
         }
       }
       float of = 0.0f;
+      if ((e & 31u) == static_cast<uint32_t>(lane)) {
 #pragma unroll
-      for (int r = 0; r < EPL; ++r)
-        if (e == lane + 32 * r) {
-          of = l[r];
-          taken |= 1u << r;
-        }
+        for (int r = 0; r < EPL; ++r)
+          if (e >> 5 == static_cast<uint32_t>(r)) of = l[r];
+        taken |= 1u << (e >> 5);
+        look();
+      }
       of = __shfl_sync(ALL, of, e & 31);
       if (lane == j) {
         chosen = static_cast<int>(e);
@@ -366,8 +387,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) moe_route_kernel(const __gri
 constexpr int PLAN_WARPS = 32;
 constexpr int PLAN_STEP = 4;          // choices per lane and turn
 constexpr int64_t PLAN_ONE = 4096;    // most choices of the one launch
-constexpr int PART_WARPS = 8;         // the two launches: warps of a CTA
-constexpr int64_t PLAN_PARTS = 64;    // most parts
+constexpr int PART_WARPS = 16;        // the two launches: warps of a CTA
+constexpr int64_t PLAN_PARTS = 32;    // most parts
 constexpr int64_t PART_LEAST = 1024;  // fewest choices of a part
 
 __device__ __forceinline__ int bucket_of(int e, int E, bool& bad) {
@@ -377,12 +398,10 @@ __device__ __forceinline__ int bucket_of(int e, int E, bool& bad) {
 }
 
 template <int W>
-__global__ void __launch_bounds__(PLAN_WARPS * 32)
-moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* __restrict__ order,
-                int32_t* __restrict__ place, int32_t* __restrict__ offsets) {
+__device__ __forceinline__ void plan_experts(const int32_t* __restrict__ experts, int64_t n, int E,
+                                             int32_t* __restrict__ order, int32_t* __restrict__ place,
+                                             int32_t* __restrict__ offsets) {
   __shared__ int counts[PLAN_WARPS][W + 1];  // of the CTA's experts; of lower ones
-  pdl_wait_prerequisites();
-  pdl_launch_dependents();
   constexpr uint32_t ALL = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = static_cast<int>(blockIdx.x) * W;
   constexpr int TURN = 32 * PLAN_STEP;
@@ -451,6 +470,15 @@ moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* 
   }
 }
 
+template <int W>
+__global__ void __launch_bounds__(PLAN_WARPS * 32)
+moe_plan_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* __restrict__ order,
+                int32_t* __restrict__ place, int32_t* __restrict__ offsets) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  plan_experts<W>(experts, n, E, order, place, offsets);
+}
+
 // Part p of `parts`: choices [part_start(p), part_start(p + 1)), whole groups of 32.
 __device__ __forceinline__ int64_t part_start(int64_t n, int64_t parts, int64_t p) {
   const int64_t at = (n + 31) / 32 * p / parts * 32;
@@ -504,11 +532,13 @@ moe_place_kernel(const int32_t* __restrict__ experts, int64_t n, int E, const in
     const int e = e0 + threadIdx.x;
     int before = 0, all = 0;
     if (e < B) {
-#pragma unroll 16
-      for (int c = 0; c < parts; ++c) {
-        const int v = __ldg(counts + static_cast<int64_t>(c) * B + e);
-        before += c < part ? v : 0;
-        all += v;
+      int v[PLAN_PARTS];  // on their way together
+#pragma unroll
+      for (int c = 0; c < PLAN_PARTS; ++c) v[c] = c < parts ? __ldg(counts + static_cast<int64_t>(c) * B + e) : 0;
+#pragma unroll
+      for (int c = 0; c < PLAN_PARTS; ++c) {
+        before += c < part ? v[c] : 0;
+        all += v[c];
       }
     }
     int scan = all;
@@ -588,20 +618,26 @@ moe_gather_kernel(const uint8_t* __restrict__ Q, const float* __restrict__ s, in
   for (int b = lane; b < KB; b += 32) s_out[i * KB + b] = __ldg(s + m * KB + b);
 }
 
-// fp8_pack_kernel with the codes and scales of a token stored to every row that
-// the plan gives it.
+struct PackArgs {
+  const void* X;
+  int64_t ldx;
+  uint32_t n_qblocks, KB, K;
+  bool vec;
+  const int32_t* place;  // null: rows by token
+  int top_k;
+  int64_t n;
+  uint8_t* Q;
+  float* s;
+};
+// The codes and scale of the 128 features of a token that eight lanes share
+// (fp8_pack_kernel's), to the token's row or to every row that the plan gives it.
 template <typename T>
-__global__ void __launch_bounds__(ROW_THREADS, sizeof(T) == 2 ? 8 : 6)
-moe_pack_kernel(const T* __restrict__ X, int64_t ldx, uint32_t n_qblocks, uint32_t KB, uint32_t K, bool vec,
-                const int32_t* __restrict__ place, int top_k, int64_t n, uint8_t* __restrict__ Q, float* __restrict__ s) {
-  pdl_wait_prerequisites();
-  pdl_launch_dependents();
-  const uint32_t sub = threadIdx.x & 7, b = blockIdx.x * (ROW_THREADS / 8) + (threadIdx.x >> 3);
-  const uint32_t row = b / KB, kb = b - row * KB, col = kb * fp8::QBLOCK + sub * 16;
-  const bool on = b < n_qblocks && col < K;
+__device__ __forceinline__ void pack_block(const PackArgs& a, uint32_t b) {
+  const uint32_t sub = threadIdx.x & 7, row = b / a.KB, kb = b - row * a.KB, col = kb * fp8::QBLOCK + sub * 16;
+  const bool on = b < a.n_qblocks && col < a.K;
   fp8::Pair x[8];
   if (on) {
-    fp8::load16(X + row * ldx + col, vec, x);
+    fp8::load16(static_cast<const T*>(a.X) + row * a.ldx + col, a.vec, x);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0ull;
@@ -614,12 +650,37 @@ moe_pack_kernel(const T* __restrict__ X, int64_t ldx, uint32_t n_qblocks, uint32
   fp8::e4m3_codes(x, sc, fp8::e4m3_factor(sc), c);
   if (!on) return;
   const uint4 codes = make_uint4(c[0], c[1], c[2], c[3]);
-  for (int j = 0; j < top_k; ++j) {
-    const int64_t p = __ldg(place + static_cast<int64_t>(row) * top_k + j);
-    if (p < 0 || p >= n) continue;
-    *reinterpret_cast<uint4*>(Q + p * K + col) = codes;
-    if (sub == 0) s[p * KB + kb] = sc;
+  if (!a.place) {
+    *reinterpret_cast<uint4*>(a.Q + static_cast<int64_t>(row) * a.K + col) = codes;
+    if (sub == 0) a.s[static_cast<int64_t>(row) * a.KB + kb] = sc;
+    return;
   }
+  for (int j = 0; j < a.top_k; ++j) {
+    const int64_t p = __ldg(a.place + static_cast<int64_t>(row) * a.top_k + j);
+    if (p < 0 || p >= a.n) continue;
+    *reinterpret_cast<uint4*>(a.Q + p * a.K + col) = codes;
+    if (sub == 0) a.s[p * a.KB + kb] = sc;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(ROW_THREADS, sizeof(T) == 2 ? 8 : 6) moe_pack_kernel(const __grid_constant__ PackArgs a) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  pack_block<T>(a, blockIdx.x * (ROW_THREADS / 8) + (threadIdx.x >> 3));
+}
+
+// A plan of few choices and the pack by token, which need nothing of each
+// other, in one launch: the first `plan_ctas` CTAs plan.
+template <typename T, int W>
+__global__ void __launch_bounds__(PLAN_WARPS * 32)
+moe_plan_pack_kernel(const int32_t* __restrict__ experts, int64_t n, int E, int32_t* __restrict__ order,
+                     int32_t* __restrict__ place, int32_t* __restrict__ offsets, uint32_t plan_ctas,
+                     const __grid_constant__ PackArgs a) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  if (blockIdx.x < plan_ctas) plan_experts<W>(experts, n, E, order, place, offsets);
+  else pack_block<T>(a, (blockIdx.x - plan_ctas) * (PLAN_WARPS * 4) + (threadIdx.x >> 3));
 }
 
 // ---------------------------------------------------------------------------
@@ -686,49 +747,51 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 8) moe_combine_kernel(const _
   constexpr int BATCH = sizeof(TR) == 4 ? 4 : 8;  // rows loaded together
   const uint32_t token = blockIdx.x / chunks;
   const int64_t t = token, col = ((blockIdx.x - token * chunks) * blockDim.x + threadIdx.x) * static_cast<int64_t>(E);
-  if (col >= a.N) return;
-  const int32_t* place = a.place + t * a.top_k;
-  const float* weights = a.weights + t * a.top_k;
+  // lane j has the token's choice j (top_k <= 32)
+  const int lane = threadIdx.x & 31;
+  int mine = -1;
+  float weight = 0.0f;
+  if (lane < a.top_k) {
+    mine = __ldg(a.place + t * a.top_k + lane);
+    weight = __ldg(a.weights + t * a.top_k + lane);
+    if (mine >= a.n) mine = -1;
+  }
   const TR* rows = static_cast<const TR*>(a.rows) + col;
-  const int n = static_cast<int>(a.n);
   float acc[E];
 #pragma unroll
   for (int k = 0; k < E; ++k) acc[k] = 0.0f;
+#pragma unroll 1
   for (int j0 = 0; j0 < a.top_k; j0 += BATCH) {
     Raw<TR, VEC> x[BATCH];
-    float w[BATCH], s[BATCH];
-    uint32_t on = 0;
+    float s[BATCH];
     int r[BATCH];
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      r[j] = j0 + j < a.top_k ? __ldg(place + j0 + j) : -1;
-      w[j] = j0 + j < a.top_k ? __ldg(weights + j0 + j) : 0.0f;
+      if (j0 + j >= a.top_k) break;
+      r[j] = __shfl_sync(0xffffffffu, mine, j0 + j);
+      if (r[j] < 0 || col >= a.N) continue;
+      x[j].load(rows + r[j] * a.ldr);
+      if (a.r_scale) s[j] = __ldg(a.r_scale + r[j] * a.r_blocks + col / fp8::QBLOCK);
     }
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      s[j] = 1.0f;
-      if (r[j] >= 0 && r[j] < n) {
-        on |= 1u << j;
-        x[j].load(rows + r[j] * a.ldr);
-        if (a.r_scale) s[j] = __ldg(a.r_scale + r[j] * a.r_blocks + col / fp8::QBLOCK);
+      if (j0 + j >= a.top_k) break;
+      float f = __shfl_sync(0xffffffffu, weight, j0 + j);
+      if (r[j] < 0) continue;
+      float v[E];
+      x[j].unpack(v);
+      if (a.r_scale) f *= s[j];
+      if constexpr (VEC) {
+        const unsigned long long f2 = f32x2_pack(f, f);
+#pragma unroll
+        for (int k = 0; k < E; k += 2)
+          f32x2_unpack(f32x2_fma(f2, f32x2_pack(v[k], v[k + 1]), f32x2_pack(acc[k], acc[k + 1])), acc[k], acc[k + 1]);
+      } else {
+        acc[0] = fmaf(f, v[0], acc[0]);
       }
     }
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j)
-      if (on >> j & 1u) {
-        float v[E];
-        x[j].unpack(v);
-        const float f = w[j] * s[j];
-        if constexpr (VEC) {
-          const unsigned long long f2 = f32x2_pack(f, f);
-#pragma unroll
-          for (int k = 0; k < E; k += 2)
-            f32x2_unpack(f32x2_fma(f2, f32x2_pack(v[k], v[k + 1]), f32x2_pack(acc[k], acc[k + 1])), acc[k], acc[k + 1]);
-        } else {
-          acc[0] = fmaf(f, v[0], acc[0]);
-        }
-      }
   }
+  if (col >= a.N) return;
   TY* y = static_cast<TY*>(a.Y) + t * a.ldy + col;
   if (a.residual) {
     const TY* res = static_cast<const TY*>(a.residual) + t * a.ld_res + col;
@@ -847,7 +910,11 @@ int launch_plan(const int32_t* experts, int64_t n, int E, int32_t* order, int32_
     return plan_as<8>(experts, n, E, order, place, offsets, stream);
   }
   int32_t* counts = static_cast<int32_t*>(workspace);
-  static_assert(PART_WARPS * (MAX_EXPERTS + 1) * 4 <= 48 * 1024, "shared memory");
+  static std::mutex mu;
+  static uint64_t done = 0;
+  constexpr int most = PART_WARPS * (MAX_EXPERTS + 1) * 4;
+  static_assert(most <= 100 * 1024, "shared memory");
+  if (int st = fp8::allow_smem(moe_place_kernel, most, done, mu)) return st;
   Launch count(static_cast<unsigned>(parts), PART_WARPS * 32, 0, stream);
   cudaError_t e = cudaLaunchKernelEx(&count.cfg, moe_count_kernel, experts, n, E, counts);
   if (e != cudaSuccess) return set_cuda_error(e);
@@ -864,23 +931,52 @@ int launch_gather(const uint8_t* Q, const float* s, int64_t K, const Rows& r, ui
   return e == cudaSuccess ? check_launch() : set_cuda_error(e);
 }
 
-template <typename T>
-static int pack_as(const void* X, int64_t T_, int64_t K, int64_t ldx, const int32_t* place, int top_k, uint8_t* Q, float* s,
-                   cudaStream_t stream) {
-  const int64_t KB = fp8::n_blocks(K), blocks = T_ * KB, per = ROW_THREADS / 8;
-  const bool vec = aligned16(X) && (ldx * sizeof(T)) % 16 == 0;
-  Launch l(static_cast<unsigned>((blocks + per - 1) / per), ROW_THREADS, 0, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, moe_pack_kernel<T>, static_cast<const T*>(X), ldx,
-                                           static_cast<uint32_t>(blocks), static_cast<uint32_t>(KB),
-                                           static_cast<uint32_t>(K), vec, place, top_k, T_ * top_k, Q, s);
-  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+static PackArgs pack_args(const void* X, int x_dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* place, int top_k,
+                          uint8_t* Q, float* s) {
+  const int64_t KB = fp8::n_blocks(K);
+  return PackArgs{X, ldx, static_cast<uint32_t>(T * KB), static_cast<uint32_t>(KB), static_cast<uint32_t>(K),
+                  aligned16(X) && (ldx * fp8::dtype_size(x_dtype)) % 16 == 0, place, top_k, T * top_k, Q, s};
 }
 
 int launch_pack_sorted(const void* X, int x_dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* place, int top_k,
                        uint8_t* Q, float* s, cudaStream_t stream) {
-  if (x_dtype == CONVROT_F32) return pack_as<float>(X, T, K, ldx, place, top_k, Q, s, stream);
-  if (x_dtype == CONVROT_F16) return pack_as<__half>(X, T, K, ldx, place, top_k, Q, s, stream);
-  return pack_as<__nv_bfloat16>(X, T, K, ldx, place, top_k, Q, s, stream);
+  const PackArgs a = pack_args(X, x_dtype, T, K, ldx, place, top_k, Q, s);
+  const uint32_t per = ROW_THREADS / 8;
+  Launch l((a.n_qblocks + per - 1) / per, ROW_THREADS, 0, stream);
+  const cudaError_t e = x_dtype == CONVROT_F32   ? cudaLaunchKernelEx(&l.cfg, moe_pack_kernel<float>, a)
+                        : x_dtype == CONVROT_F16 ? cudaLaunchKernelEx(&l.cfg, moe_pack_kernel<__half>, a)
+                                                 : cudaLaunchKernelEx(&l.cfg, moe_pack_kernel<__nv_bfloat16>, a);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+
+template <typename T, int W>
+static int plan_pack_as(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
+                        const PackArgs& a, cudaStream_t stream) {
+  const uint32_t plan_ctas = static_cast<uint32_t>((E + W) / W), per = PLAN_WARPS * 4;
+  Launch l(plan_ctas + (a.n_qblocks + per - 1) / per, PLAN_WARPS * 32, 0, stream);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&l.cfg, moe_plan_pack_kernel<T, W>, experts, n, E, order, place, offsets, plan_ctas, a);
+  return e == cudaSuccess ? check_launch() : set_cuda_error(e);
+}
+template <typename T>
+static int plan_pack_of(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
+                        const PackArgs& a, cudaStream_t stream) {
+  if (E < 152) return plan_pack_as<T, 1>(experts, n, E, order, place, offsets, a, stream);
+  if (E < 304) return plan_pack_as<T, 2>(experts, n, E, order, place, offsets, a, stream);
+  return plan_pack_as<T, 8>(experts, n, E, order, place, offsets, a, stream);
+}
+
+int launch_plan_pack(const int32_t* experts, int64_t n, int E, int32_t* order, int32_t* place, int32_t* offsets,
+                     void* workspace, const void* X, int x_dtype, int64_t T, int64_t K, int64_t ldx, int top_k, uint8_t* Q,
+                     float* s, cudaStream_t stream) {
+  if (plan_parts(n) > 0) {
+    if (int st = launch_plan(experts, n, E, order, place, offsets, workspace, stream)) return st;
+    return fp8::launch_fp8_pack(X, x_dtype, T, K, ldx, Q, s, stream);
+  }
+  const PackArgs a = pack_args(X, x_dtype, T, K, ldx, nullptr, top_k, Q, s);
+  if (x_dtype == CONVROT_F32) return plan_pack_of<float>(experts, n, E, order, place, offsets, a, stream);
+  if (x_dtype == CONVROT_F16) return plan_pack_of<__half>(experts, n, E, order, place, offsets, a, stream);
+  return plan_pack_of<__nv_bfloat16>(experts, n, E, order, place, offsets, a, stream);
 }
 
 int launch_combine(const CombineArgs& a, cudaStream_t stream) {
