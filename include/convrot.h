@@ -945,6 +945,23 @@ int fp8_test_linear_timeout(const uint8_t* Q_x, const float* s_x, int64_t M, int
                             void* stream);
 
 /*
+ * fp8_test_expert_timeout -- a test of the expert linears' timeout path, not
+ * part of the method: fp8_expert_linear (fp8_expert_swiglu with `weight` the gate,
+ * where `up` is given; then out are codes, ld = N, and s_out their scales) on n
+ * rows in the plan's order, with every bounded device wait of the launch limited
+ * to wait_ns nanoseconds and the last block of K of the last tile not loaded.
+ * The waits of the blocks of threads that compute that tile give up: the kernel
+ * records CONVROT_ERR_TIMEOUT, waits (bounded) for its copies and
+ * multiplications in flight, releases its tensor memory and exits. The other
+ * tiles are complete, that one is not written.
+ * Errors: those of the two calls, ERR_ARG (also wait_ns == 0 or n == 0).
+ */
+int fp8_test_expert_timeout(const uint8_t* Q_x, const float* s_x, int64_t n, int64_t K,
+                            const int32_t* offsets, int n_experts, const convrot_experts* weight,
+                            const convrot_experts* up, void* out, float* s_out, int64_t ld, int y_dtype,
+                            uint64_t wait_ns, void* stream);
+
+/*
  * convrot_test_unscale_sweep -- a test of the GEMM epilogue's unscaling step,
  * not part of the method. The epilogue divides by a linear's input scale a
  * without a division per element (Markstein's correction step: r = RN(1/a),

@@ -275,6 +275,23 @@ int fp8_expert_swiglu(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K
   return launch_expert_swiglu(Q_x, s_x, K, rows, *gate, *up, Q_h, s_h, static_cast<cudaStream_t>(stream));
 }
 
+int fp8_test_expert_timeout(const uint8_t* Q_x, const float* s_x, int64_t n, int64_t K, const int32_t* offsets,
+                            int n_experts, const convrot_experts* weight, const convrot_experts* up, void* out,
+                            float* s_out, int64_t ld, int y_dtype, uint64_t wait_ns, void* stream) {
+  if (wait_ns == 0 || n < 1 || !weight || !out || !known_dtype(y_dtype) || ld < weight->N || weight->N < 1 ||
+      (up && (up->N != weight->N || !s_out)))
+    return CONVROT_ERR_ARG;
+  if (up && (ld != weight->N || ld % 16 != 0 || !aligned16(out))) return CONVROT_ERR_ALIGN;
+  for (const convrot_experts* w : {weight, up})
+    if (w)
+      if (int st = expert_checks(Q_x, s_x, n, K, nullptr, offsets, n, n_experts, 1, w)) return st;
+  if (int st = check_device()) return st;
+  const Rows rows{nullptr, offsets, n, n, n_experts, 1};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (up) return launch_expert_swiglu(Q_x, s_x, K, rows, *weight, *up, static_cast<uint8_t*>(out), s_out, s, wait_ns);
+  return launch_expert_linear(Q_x, s_x, K, rows, *weight, out, ld, y_dtype, nullptr, s, wait_ns);
+}
+
 int moe_combine(const void* rows, int r_dtype, int64_t ldr, int64_t n, const int32_t* place, const float* weights,
                 int64_t T, int top_k, int64_t N, const void* residual, int64_t ld_res, void* Y, int64_t ldy,
                 int y_dtype, void* stream) {

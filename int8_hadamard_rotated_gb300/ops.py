@@ -183,6 +183,8 @@ SIGNATURES = {
     "convrot_device_status": (_I, [_VP]),
     "convrot_test_block_norm_timeout": (_I, [_VP, _I64, ctypes.c_uint64, _VP]),
     "fp8_test_linear_timeout": (_I, [_VP, _VP, _I64, _I64, _VP, _I, _I, ctypes.c_uint64, _VP]),
+    "fp8_test_expert_timeout": (_I, [_VP, _VP, _I64, _I64, _VP, _I, _VP, _VP, _VP, _VP, _I64, _I, ctypes.c_uint64,
+                                     _VP]),
     "convrot_test_handover_timeout": (_I, [_VP, _VP, _I64, _I64, ctypes.POINTER(convrot_weight), _I, _VP, _SZ,
                                            ctypes.c_uint64, _VP]),
     "convrot_test_unscale_sweep": (_I, [_VP, _I, _I, _VP, _VP, _VP]),
@@ -1172,6 +1174,24 @@ def fp8_expert_swiglu(Q_x: torch.Tensor, s_x: torch.Tensor, order: Optional[torc
                                    _dense(s_h, "s_h", device, (n, _n_blocks(N)), _F32), ws, size, handle),
            "fp8_expert_swiglu")
     return Q_h, s_h
+
+
+def fp8_test_expert_timeout(Q_x: torch.Tensor, s_x: torch.Tensor, offsets: torch.Tensor, weight, wait_ns: int,
+                            Y: torch.Tensor, up=None, s_h: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Test-only launch of an expert linear (SwiGLU with `up`: Y are codes, s_h
+    their scales) on rows in the plan's order, whose last tile is not loaded to its
+    end: the kernel's waits give up after wait_ns, it records ERR_TIMEOUT (read it
+    with convrot_device_status) and leaves that tile unwritten."""
+    device, handle = _start(Q_x, stream)
+    w, E, N = _experts(weight, "weight", device, _matrix(Q_x, "Q_x")[1])
+    n, K, _, q, s, _, f = _plan_of(Q_x, s_x, None, offsets, E, device)
+    u = None if up is None else _experts(up, "up", device, K, E)[0]
+    y = _dense(Y, "Y", device, (n, N), Y.dtype if up is None else _E4M3)
+    _check(lib().fp8_test_expert_timeout(q, s, n, K, f, E, w, u, y,
+                                         0 if s_h is None else _dense(s_h, "s_h", device, (n, _n_blocks(N)), _F32), N,
+                                         F32 if up is not None else _DTYPES[Y.dtype], int(wait_ns), handle),
+           "fp8_test_expert_timeout")
+    return Y
 
 
 def moe_combine(rows: torch.Tensor, place: torch.Tensor, weights: torch.Tensor,

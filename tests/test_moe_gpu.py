@@ -340,3 +340,193 @@ def test_moe(ops, T, E, k, only, K, I, N, dtype, out):  # noqa: E741
                     Y=torch.full((T, N), float("nan"), dtype=DT[out], device="cuda"))
     assert_within(y, ref, bound)
     assert ops.convrot_device_status() == ops.OK
+
+
+# ---------------------------------------------------------------------------
+# the operators together
+# ---------------------------------------------------------------------------
+
+def block(ops, T, E, k, K, I, N, seed=0):  # noqa: E741
+    """(X, experts, weights, gate, up, down) on the device, of random matrices packed there."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    mats = [(*ops.fp8_prepare_experts(r(E, n, m) * m ** -0.5), 0.1 * r(E, n)) for n, m in ((I, K), (I, K), (N, I))]
+    e, w = ops.moe_route(r(T, E), k)
+    return (r(T, K).to(torch.bfloat16), e, w, *mats)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 16, 4), (5, 8, 2), (100, 16, 4), (300, 6, 2), (2000, 8, 4)])
+def test_moe_is_its_parts(ops, T, E, k):
+    """fp8_moe gives what the pack, the plan, the linears and the sum give one by one."""
+    X, e, w, gate, up, down = block(ops, T, E, k, 400, 272, 384, T)
+    e[T // 3] = -1
+    res = torch.randn(T, 384, generator=gen(T)).cuda()
+    got = ops.fp8_moe(X, e, w, gate, up, down, residual=res)
+    assert got.dtype == torch.float32
+    order, place, offsets = ops.moe_plan(e, E)
+    h = ops.fp8_expert_swiglu(*ops.fp8_pack_activations(X), order, offsets, k, gate, up)
+    rows = ops.fp8_expert_linear(*h, offsets, down, out_dtype=torch.float32)
+    want = ops.moe_combine(rows, place, w, residual=res)
+    assert torch.equal(got, want)
+    assert ops.convrot_device_status() == ops.OK
+
+
+def test_block_with_experts(ops):
+    """A transformer block's MLP: norm, router, experts, residual; against 64 bits."""
+    T, E, k, K, I = 90, 12, 3, 256, 144  # noqa: E741
+    X, _, _, gate, up, down = block(ops, T, E, k, K, I, K, 7)
+    router = torch.randn(E, K, generator=gen(8)).cuda() * K ** -0.5
+    h, u = ops.convrot_block_norm(X, want_h=True)
+    logits = u.float() @ router.t()
+    e, w = ops.moe_route(logits, k, score=ops.MOE_SIGMOID, bias=0.05 * torch.randn(E, generator=gen(9)).cuda(), n_groups=4,
+                         top_groups=2, scale=2.0)
+    y = ops.fp8_moe(u, e, w, gate, up, down, residual=h)
+    sets = [(codes(q), host(s), host(b)) for q, s, b in (gate, up, down)]
+    ref, bound = mo.moe(host(u.float()), host(e), host(w), *sets, host(h.float()), rows_error=2.0 ** -11)
+    assert_within(y, ref, bound)
+
+
+def test_results_repeat(ops):
+    """Bit for bit, also next to another call on another stream."""
+    for T in (1, 40, 700):
+        args = block(ops, T, 16, 4, 512, 256, 384, T)
+        other = block(ops, 600, 16, 4, 512, 256, 384, T + 1)
+        first = ops.fp8_moe(*args)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(5):
+            z = ops.fp8_moe(*other, stream=side)
+            assert torch.equal(ops.fp8_moe(*args), first)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(ops.fp8_moe(*other), z)
+    assert ops.convrot_device_status() == ops.OK
+
+
+@pytest.mark.parametrize("T", [1, 30, 500])
+def test_captured_and_replayed(ops, T):
+    """One graph of router, experts and sum, replayed on new inputs whose tokens
+    choose other experts."""
+    E, k, K, I, N = 8, 2, 256, 128, 200  # noqa: E741
+    X, _, _, gate, up, down = block(ops, T, E, k, K, I, N)
+    logits = torch.zeros(T, E, device="cuda")
+    ws = torch.empty(ops.fp8_moe_workspace_size(T, K, I, N, k, E), dtype=torch.uint8, device="cuda")
+    Y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+
+    def run():
+        e, w = ops.moe_route(logits, k)
+        ops.fp8_moe(X, e, w, gate, up, down, Y=Y, workspace=ws)
+        return e
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i in range(4):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        X.copy_(torch.randn(T, K, generator=g, device="cuda"))
+        logits.copy_(torch.randn(T, E, generator=g, device="cuda") * 3)
+        if i == 3:
+            logits.fill_(-INF)  # no expert open: nothing is added
+        Y.fill_(9.0)
+        graph.replay()
+        got = Y.clone()
+        run()
+        assert torch.equal(Y, got)
+    assert (got == 0).all()
+
+
+@pytest.mark.parametrize("counts", [[3, 5, 2], [40, 50, 30], [300, 20, 90]])
+def test_non_finite_rows_stay_in_their_rows(ops, counts):
+    """Infinities and NaN in some rows, next to others in the same tiles; rows
+    behind the last one full of NaN codes."""
+    E, K, I = len(counts), 272, 144  # noqa: E741
+    n, total = sum(counts), sum(counts) + 37
+    X = activations(3, total, K)
+    clean = X.clone()
+    bad = [0, counts[0], n - 1]
+    X[0, 5], X[counts[0], 9], X[n - 1, 200] = INF, float("nan"), -INF
+    X[n:] = float("nan")
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    gate, up = matrices(1, E, I, K, True)[0], matrices(2, E, I, K, True)[0]
+    down = matrices(3, E, 200, I, True)[0]
+    out = []
+    for x in (X, clean):
+        Qh = torch.zeros(total, I, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        h = ops.fp8_expert_swiglu(*ops.fp8_pack_activations(x.cuda()), None, offsets, 1, gate, up, Q_h=Qh,
+                                  s_h=torch.zeros(total, 2, device="cuda"))
+        y = ops.fp8_expert_linear(*h, offsets, down, Y=torch.zeros(total, 200, device="cuda"))
+        out.append((codes(h[0]), host(h[1]), host(y)))
+    good = [i for i in range(total) if i not in bad]
+    for a, b in zip(*out):
+        assert (a[good] == b[good]).all()
+    assert not np.isfinite(out[0][2][bad]).any() and np.isfinite(out[0][2][good]).all()
+
+
+def test_bf16_rows_keep_their_precision(ops):
+    """fp8_moe's bf16 output, whose rows pass in binary16 with a power of two:
+    large, small and zero rows, and outputs of an odd width."""
+    T, E, k, K, I, N = 70, 4, 2, 128, 128, 133  # noqa: E741
+    X, e, w, gate, up, down = block(ops, T, E, k, K, I, N, 5)
+    for factor in (1.0, 1e30, 1e-30, 0.0):
+        d = (down[0], down[1] * factor, down[2] * factor)
+        want = ops.fp8_moe(X, e, w, gate, up, d, out_dtype=torch.float32)
+        got = ops.fp8_moe(X, e, w, gate, up, d)
+        order, place, offsets = ops.moe_plan(e, E)
+        rows = ops.fp8_expert_linear(*ops.fp8_expert_swiglu(*ops.fp8_pack_activations(X), order, offsets, k, gate, up),
+                                     offsets, d, out_dtype=torch.float32)
+        mag = host(ops.moe_combine(rows.abs(), place, w)).astype(np.float64)
+        # half a step of bf16, and half one of binary16 for every row
+        bound = 2.0 ** -8 * np.abs(host(want)) + 2.0 ** -11 * mag * 1.01 + 8 * U24 * mag
+        assert (np.abs(host(got.float()).astype(np.float64) - host(want)) <= bound).all(), factor
+
+
+def test_rows_past_31_bits(ops):
+    """Sorted codes, outputs and rows of more than 2^31 bytes and elements."""
+    T, k, E, K, N = 37500, 8, 4, 8192, 16
+    n = T * k
+    g = torch.Generator(device="cuda").manual_seed(1)
+    e = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    X = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+    Q, s = ops.fp8_pack_activations(X)
+    W = (*ops.fp8_prepare_experts(torch.randn(E, N, K, generator=g, device="cuda")), None)
+    order, place, offsets = ops.moe_plan(e, E)
+    wide = torch.empty(n, 8192, dtype=torch.bfloat16, device="cuda")  # 2.5e9 elements
+    y = ops.fp8_expert_linear(Q, s, offsets, W, order=order, top_k=k, Y=wide[:, 8176:])
+    few = torch.arange(n - 40, n, device="cuda")
+    t = order[few] // k
+    x = ops.fp8_expert_linear(Q[t.long()].contiguous(), s[t.long()].contiguous(),
+                              torch.tensor([0, 0, 0, 0, 40], dtype=torch.int32, device="cuda"), W)
+    assert torch.allclose(y[few].float(), x.float(), rtol=2.0 ** -7, atol=1e-3 * float(x.float().abs().max()))
+    w = torch.rand(T, k, generator=g, device="cuda")
+    z = ops.moe_combine(wide[:, 8176:], place, w, out_dtype=torch.float32)
+    last = place[-8:].long()
+    want = (w[-1].double()[:, None] * wide[last][:, 8176:].double()).sum(0)
+    assert torch.allclose(z[-1].double(), want, rtol=1e-5, atol=1e-5 * float(want.abs().max()))
+
+
+def test_binding_refuses(ops):
+    X, e, w, gate, up, down = block(ops, 6, 4, 2, 64, 32, 48)
+    Q, s = ops.fp8_pack_activations(X)
+    order, place, offsets = ops.moe_plan(e, 4)
+    bad = [
+        lambda: ops.moe_route(X[0], 2), lambda: ops.moe_route(X, 2, bias=torch.zeros(5, device="cuda")),
+        lambda: ops.moe_route(X, 2, experts=torch.empty(6, 3, dtype=torch.int32, device="cuda")),
+        lambda: ops.moe_plan(e.long(), 4), lambda: ops.moe_plan(e, 4, order=order[:-1]),
+        lambda: ops.fp8_expert_linear(Q, s, offsets[:-1], gate), lambda: ops.fp8_expert_linear(Q, s[:, :0], offsets, gate),
+        lambda: ops.fp8_expert_linear(Q, s, offsets, (gate[0].transpose(1, 2), gate[1])),
+        lambda: ops.fp8_expert_linear(Q, s, offsets, (gate[0][0], gate[1])),
+        lambda: ops.fp8_expert_swiglu(Q, s, order, offsets, 2, gate, down),
+        lambda: ops.fp8_expert_swiglu(Q, s, order, offsets, 2, gate, tuple(x[:3] for x in up)),
+        lambda: ops.moe_combine(X, place[:-1], w), lambda: ops.moe_combine(X, place, w, residual=X[:-1]),
+        lambda: ops.fp8_moe(X, e, w[:, :1], gate, up, down), lambda: ops.fp8_moe(X, e, w, gate, up, gate),
+        lambda: ops.fp8_moe(X, e, w, gate, up, down, residual=X),
+        lambda: ops.fp8_prepare_experts(torch.zeros(4, 16, device="cuda"))]
+    for i, f in enumerate(bad):
+        with pytest.raises((ValueError, KeyError)):
+            f()
+            pytest.fail(f"call {i} was taken")
+    for f in (lambda: ops.moe_route(X, 33), lambda: ops.moe_route(X, 2, n_groups=3),
+              lambda: ops.fp8_moe(X, e, w, gate, up, down, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ops.ConvrotError):
+            f()
+    torch.cuda.synchronize()
