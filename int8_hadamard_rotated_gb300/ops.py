@@ -1005,8 +1005,10 @@ def convrot_block_norm_fp8(H: torch.Tensor, Y: Optional[torch.Tensor] = None, *,
 
 _ROUTE_ARGS = struct.Struct("@qiiiiPqPiiiifPP")
 _EXPERTS = struct.Struct("@PPPqqqq")
+_MOE_ARGS = struct.Struct("@PiqqqPPiiPPPPqPqi0q")
 assert _ROUTE_ARGS.size == ctypes.sizeof(convrot_moe_route_args)
 assert _EXPERTS.size == ctypes.sizeof(convrot_experts)
+assert _MOE_ARGS.size == ctypes.sizeof(convrot_moe_args)
 
 
 def moe_route(logits: torch.Tensor, top_k: int, *, score: int = MOE_SOFTMAX, bias: Optional[torch.Tensor] = None,
@@ -1049,7 +1051,7 @@ def _bytes(workspace, size: int, device: int, stream):
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if size == 0:
         return 0, 0, None
-    ws = _empty((size,), torch.uint8, device, stream)
+    ws = _empty(size, torch.uint8, device, stream)
     return ws.data_ptr(), size, ws
 
 
@@ -1090,6 +1092,21 @@ def fp8_prepare_experts(W: torch.Tensor, stream=None) -> Tuple[torch.Tensor, tor
     return Q, s
 
 
+def _per_expert(t: torch.Tensor, name: str, what: str, device: int, shape, dtype) -> Tuple[int, int]:
+    """(address, distance between experts) of an array whose part of every
+    expert is dense."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device:
+        step = 1
+        for s in shape[1:]:
+            step *= s
+        if t.is_contiguous():
+            return t.data_ptr(), step
+        if shape[0] == 0 or t[0].is_contiguous():
+            return t.data_ptr(), t.stride(0) if shape[0] > 1 else step
+    raise ValueError(f"{name}: {what} must be {dtype} of shape {tuple(shape)} on the device of the other tensors, dense "
+                     f"for every expert, got {t.dtype} {tuple(t.shape)}")
+
+
 def _experts(w, name: str, device: int, K: int, E: Optional[int] = None):
     """(descriptor, E, N) of a set of experts' matrices: a tuple of codes
     [E,N,K], scales [E, ceil(N/128), ceil(K/128)] and, or None, biases [E,N].
@@ -1097,23 +1114,12 @@ def _experts(w, name: str, device: int, K: int, E: Optional[int] = None):
     q, s, b = w if len(w) == 3 else (*w, None)
     if q.dim() != 3:
         raise ValueError(f"{name}: the codes must have the shape (experts, N, K)")
-    n, N = q.shape[:2]
-
-    def part(t, what, shape, dtype):
-        dense, step = True, 1
-        for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:] if t.dim() == len(shape) else ())):
-            dense = dense and (size == 1 or stride == step)
-            step *= size
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not dense:
-            raise ValueError(f"{name}: {what} must be {dtype} of shape {tuple(shape)} on the device of the other "
-                             f"tensors, dense for every expert, got {t.dtype} {tuple(t.shape)}")
-        return t.data_ptr(), t.stride(0) if n > 1 else step
-
+    n, N, _ = q.shape
     if E is not None and n != E:
         raise ValueError(f"{name}: {n} experts, and {E} elsewhere in the call")
-    q_ptr, q_stride = part(q, "codes", (n, N, K), _E4M3)
-    s_ptr, s_stride = part(s, "scales", (n, _n_blocks(N), _n_blocks(K)), _F32)
-    b_ptr, b_stride = (0, N) if b is None else part(b, "biases", (n, N), _F32)
+    q_ptr, q_stride = _per_expert(q, name, "codes", device, (n, N, K), _E4M3)
+    s_ptr, s_stride = _per_expert(s, name, "scales", device, (n, _n_blocks(N), _n_blocks(K)), _F32)
+    b_ptr, b_stride = (0, N) if b is None else _per_expert(b, name, "biases", device, (n, N), _F32)
     return _EXPERTS.pack(q_ptr, s_ptr, b_ptr, N, q_stride, s_stride, b_stride), n, N
 
 
@@ -1250,10 +1256,11 @@ def fp8_moe(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, gate,
     res, ld_res = (0, N) if residual is None else (residual.data_ptr(),
                                                    _rows(residual, "residual", device, (T, N), Y.dtype))
     ws, size, keep = _bytes(workspace, fp8_moe_workspace_size(T, K, inner, N, top_k, E, Y.dtype), device, stream)
-    at = lambda b: ctypes.cast(b, _VP).value  # noqa: E731
-    args = convrot_moe_args(X.data_ptr(), _DTYPES[X.dtype], T, K, ldx,
-                            _dense(experts, "experts", device, (T, top_k), torch.int32),
-                            _dense(weights, "weights", device, (T, top_k), _F32), top_k, E, at(g), at(u), at(d),
-                            res, ld_res, Y.data_ptr(), ldy, _DTYPES[Y.dtype])
-    _check(lib().fp8_moe(ctypes.byref(args), ws, size, handle), "fp8_moe")
+    sets = ctypes.create_string_buffer(g + u + d)
+    at = ctypes.addressof(sets)
+    args = _MOE_ARGS.pack(X.data_ptr(), _DTYPES[X.dtype], T, K, ldx,
+                          _dense(experts, "experts", device, (T, top_k), torch.int32),
+                          _dense(weights, "weights", device, (T, top_k), _F32), top_k, E, at, at + _EXPERTS.size,
+                          at + 2 * _EXPERTS.size, res, ld_res, Y.data_ptr(), ldy, _DTYPES[Y.dtype])
+    _check(lib().fp8_moe(args, ws, size, handle), "fp8_moe")
     return Y
