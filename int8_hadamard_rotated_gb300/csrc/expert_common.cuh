@@ -169,6 +169,17 @@ __device__ __forceinline__ void tma_gather4(void* smem_dst, const void* tmap, ui
       "r"(smem_u32(bar)), "l"(cache_hint)
       : "memory");
 }
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 // A box of a three-dimensional map (an expert's matrix), counted on an mbarrier
 // of either CTA of the pair.
 __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t bar_cluster_addr, int32_t x,

@@ -13,8 +13,8 @@
 // expert does not fill costs no more than its rows.
 //
 // Twelve warps: 0-3 promote the first matrix' accumulators (32 lanes each), 4-7
-// the second's, 8 loads (activation rows in the plan's order, or gathered by
-// the plan, four to a copy), 9 issues MMAs, 10 and 11 only complete their
+// the second's, 8 loads weights and 10 activation rows (in the plan's order, or
+// gathered by the plan, four to a copy), 9 issues MMAs, 11 only completes the
 // warpgroup. The promoted sums meet in shared
 // memory as [row][weight row], 32 rows at a time, where a warp takes a row: a
 // lane has four features, and the largest magnitude of 128 is a warp's.
@@ -182,70 +182,120 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
 
   if (warp >= EPI_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONTROL_REGS));
+    const uint64_t pol = l2_policy_evict_normal();
     if (warp == EPI_WARPS) {
-      const uint64_t pol = l2_policy_evict_normal();
-      const bool gather = p.rows.order != nullptr;
-      uint32_t stage = 0, phase = 0, n_issued = 0;
-      bool ok = true;
-      for (int t = unit; ok && t < total; t += n_units) {
-        const Item c = find_item(first, p.rows.E, p.n_cols, t);
-        const int2 range = rows_of(p.rows, c.expert);
-        const int row = range.x + c.tile * BN, width = (min(BN, range.y - row) + 15) & ~15;
-        int4 rows;  // the four rows that this lane's copy takes (past the expert's last: that one again)
-        if (gather && lane < BN / 4) {
-          const int i = row + 4 * lane, last = range.y - 1;
-          rows.x = source_row(p.rows, min(i, last));
-          rows.y = source_row(p.rows, min(i + 1, last));
-          rows.z = source_row(p.rows, min(i + 2, last));
-          rows.w = source_row(p.rows, min(i + 3, last));
-        }
-        int kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, vec);
-        for (int i = 0; i < blocks; ++i) {
-          if (p.withhold && t == total - 1 && rank == split - 1 && i == blocks - 1) break;
-          ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, err, p.wait_ns);
-          if (!ok) break;
-          uint8_t* sw = smem + stage * G::STAGE_BYTES;
-          uint8_t* sx = sw + 2 * G::W_BYTES;
-          if (lane == 0) {
-            stage_width[stage] = width;
-            mbar_arrive_expect_tx(&full[stage], 2 * G::W_BYTES + width * BK);
-            const int f = c.col * FEATURES;
+      if (lane == 0) {
+        uint32_t stage = 0, phase = 0, n_issued = 0;
+        bool ok = true;
+        // an item is looked up while the one before it is loaded
+        struct Source {
+          int col, expert, width;
+        };
+        auto look_up = [&](int t) {
+          const Item c = find_item(first, p.rows.E, p.n_cols, t);
+          const int2 range = rows_of(p.rows, c.expert);
+          return Source{c.col, c.expert, (min(BN, range.y - range.x - c.tile * BN) + 15) & ~15};
+        };
+        Source next{};
+        if (unit < total) next = look_up(unit);
+        for (int t = unit; ok && t < total; t += n_units) {
+          const Source c = next;
+          const int f = c.col * FEATURES;
+          int kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, vec);
+          for (int i = 0; i < blocks; ++i) {
+            if (i == min(blocks, G::STAGES) - 1 && t + n_units < total) next = look_up(t + n_units);
+            if (p.withhold && t == total - 1 && rank == split - 1 && i == blocks - 1) break;
+            ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, p.wait_ns);
+            if (!ok) break;
+            uint8_t* sw = smem + stage * G::STAGE_BYTES;
+            stage_width[stage] = c.width;
+            mbar_arrive_expect_tx(&full[stage], 2 * G::W_BYTES + c.width * BK);
             tma_load_3d(sw, &p.tmap_w[0], &full[stage], kb * BK, f, c.expert, pol);
             if (SWIGLU) tma_load_3d(sw + G::W_BYTES, &p.tmap_w[1], &full[stage], kb * BK, f, c.expert, pol);
             else tma_load_3d(sw + G::W_BYTES, &p.tmap_w[0], &full[stage], kb * BK, f + QBLOCK, c.expert, pol);
-            if (!gather)
-              for (int r = 0; r < width; r += 16) tma_load_2d(sx + r * BK, &p.tmap_x, &full[stage], kb * BK, row + r, pol);
+            ++n_issued;
+            if (++kb == kb_end) kb = kb_begin;
+            if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
+          }
+        }
+        // no copy may land after the exit
+        for (uint32_t s = 0; s < G::STAGES; ++s)
+          if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err, p.wait_ns);
+      }
+      __syncwarp();
+    } else if (warp == EPI_WARPS + 2) {
+      const bool gather = p.rows.order != nullptr;
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      struct Source {
+        int row, width, kb;
+        int4 rows;  // gathered: the four rows that this lane's copy takes (past the expert's last: that one again)
+      };
+      auto look_up = [&](int t) {
+        const Item c = find_item(first, p.rows.E, p.n_cols, t);
+        const int2 range = rows_of(p.rows, c.expert);
+        Source s;
+        s.row = range.x + c.tile * BN;
+        s.width = (min(BN, range.y - s.row) + 15) & ~15;
+        s.kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, vec);
+        s.rows = make_int4(0, 0, 0, 0);
+        if (gather && lane < BN / 4) {
+          const int i = s.row + 4 * lane, last = range.y - 1;
+          s.rows.x = source_row(p.rows, min(i, last));
+          s.rows.y = source_row(p.rows, min(i + 1, last));
+          s.rows.z = source_row(p.rows, min(i + 2, last));
+          s.rows.w = source_row(p.rows, min(i + 3, last));
+        }
+        return s;
+      };
+      Source next{};
+      if (unit < total) next = look_up(unit);
+      for (int t = unit; ok && t < total; t += n_units) {
+        const Source c = next;
+        int kb = c.kb;
+        for (int i = 0; i < blocks; ++i) {
+          if (i == min(blocks, G::STAGES) - 1 && t + n_units < total) next = look_up(t + n_units);
+          if (p.withhold && t == total - 1 && rank == split - 1 && i == blocks - 1) break;
+          ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, err, p.wait_ns);
+          if (!ok) break;
+          uint8_t* sx = smem + stage * G::STAGE_BYTES + 2 * G::W_BYTES;
+          if (gather) {
+            if (4 * lane < c.width) tma_gather4(sx + lane * 4 * BK, &p.tmap_x, &full[stage], kb * BK, c.rows, pol);
+          } else if (16 * lane < c.width) {
+            tma_load_2d(sx + lane * 16 * BK, &p.tmap_x, &full[stage], kb * BK, c.row + 16 * lane, pol);
           }
           __syncwarp();
-          if (gather && 4 * lane < width) tma_gather4(sx + lane * 4 * BK, &p.tmap_x, &full[stage], kb * BK, rows, pol);
-          ++n_issued;
           if (++kb == kb_end) kb = kb_begin;
           if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      // no copy may land after the exit
-      if (lane == 0)
-        for (uint32_t s = 0; s < G::STAGES; ++s)
-          if (n_issued > s) mbar_wait(&full[s], ((n_issued - 1 - s) / G::STAGES) & 1u, nullptr, err, p.wait_ns);
+      // Copies that the other loading warp, whose wait gave up first, does not
+      // wait for have 1 ms to land, a thousand times what a copy takes.
+      if (!ok && lane == 0)
+        for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 1000000;) __nanosleep(10000);
       __syncwarp();
     } else if (warp == EPI_WARPS + 1) {
       if (lane == 0) {
         uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
-        bool ok = true;
+        bool ok = true, there = false;  // there: the stage has been seen to be full
         for (int t = unit; ok && t < total; t += n_units) {
           for (int i0 = 0; ok && i0 < blocks; i0 += G::KG) {
             ok = mbar_wait(&tempty[buf], bphase ^ 1u, abort_flag, err, p.wait_ns);
             for (int i = i0; ok && i < min(i0 + G::KG, blocks); ++i) {
-              ok = mbar_wait(&full[stage], phase, abort_flag, err, p.wait_ns);
+              ok = there || mbar_wait(&full[stage], phase, abort_flag, err, p.wait_ns);
               if (!ok) break;
               tc_fence_after();
               const uint32_t sw = smem_u32(smem + stage * G::STAGE_BYTES), sx = sw + 2 * G::W_BYTES;
               const uint32_t idesc = idesc_e4m3_f32(LANES, stage_width[stage]);
               const uint32_t d = tmem_base + buf * G::BUF_COLS + (i - i0) * 2 * BN;
               mma_block<1>(d, sw, sx, idesc);
+              // a look at the next stage while the tensor cores are busy
+              const uint32_t after = stage + 1 == G::STAGES ? 0 : stage + 1;
+              there = mbar_test_wait(&full[after], after ? phase : phase ^ 1u);
               mma_block<1>(d + BN, sw + G::W_BYTES, sx, idesc);
               mma_commit(&empty[stage]);
-              if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
+              stage = after;
+              if (!after) phase ^= 1u;
             }
             if (!ok) break;
             mma_commit(&tfull[buf]);
