@@ -9,6 +9,13 @@
 // shares of K and add their partial tiles up through distributed shared memory,
 // in rank order.
 //
+// 256 rows over 128 experts, 2048 -> 2 x 768: 53 us for the 83 experts that are
+// reached, 261 MB = 4.9 TB/s; 144 items of 256 weight rows of 4096, one for each
+// CTA, 29.7 us = 5.1 TB/s. A CTA streams a block of K (34 KB) in 0.45 us at best:
+// its eight MMAs take 0.32 us (75 cycles each, whatever their width), and issuing
+// the copies about as long; so the last round of items counts, and 5 us for
+// setting up, the first loads and the last sums.
+//
 // The MMAs' width is the item's rows, rounded up to 16, so that a tile that an
 // expert does not fill costs no more than its rows.
 //
