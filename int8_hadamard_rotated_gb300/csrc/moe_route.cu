@@ -270,39 +270,33 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 8 : 1) moe_route_
   // The choice. A first turn goes by the fp32 values and takes one more than
   // top_k; where two neighbours of that list are near, a second one compares
   // what is near the largest in 64 bits.
-  int chosen;  // lane j: the j-th expert, its logit and its value's key
-  float logit;
-  uint32_t taken, place_key;
+  int chosen;          // lane j: the j-th expert
+  uint32_t place_key;  // and its value's key
   auto choose = [&](bool exact, int count) {
     chosen = -1;
-    logit = -INFINITY;
-    taken = place_key = 0u;
-    // each lane's largest key that is left, and the first place that has it
-    uint32_t best_key;
-    int best_r;
-    auto look = [&]() {
-      best_key = 0u;
-      best_r = 0;
+    place_key = 0u;
+    uint32_t left[EPL], most = 0u;  // what is left, and the lane's largest of it
 #pragma unroll
-      for (int r = EPL - 1; r >= 0; --r) {
-        const uint32_t k = taken >> r & 1u ? 0u : key[r];
-        if (k >= best_key) {
-          best_key = k;
-          best_r = r;
-        }
-      }
-    };
-    look();
+    for (int r = 0; r < EPL; ++r) {
+      left[r] = key[r];
+      most = max(most, key[r]);
+    }
     for (int j = 0; j < count; ++j) {
-      const uint32_t top = __reduce_max_sync(ALL, best_key);
+      const uint32_t top = __reduce_max_sync(ALL, most);
       if (top == 0u) break;
-      uint32_t e = __reduce_min_sync(ALL, best_key == top ? static_cast<uint32_t>(lane + 32 * best_r) : 0xffffu);
+      uint32_t e = 0xffffu;
+      if (most == top) {
+#pragma unroll
+        for (int r = EPL - 1; r >= 0; --r)
+          if (left[r] == top) e = lane + 32 * r;
+      }
+      e = __reduce_min_sync(ALL, e);
       if (exact) {
         const float v = value_of(top), lo = v - 2.5f * error_at(v);
         uint32_t near = 0u;
 #pragma unroll
         for (int r = 0; r < EPL; ++r)
-          if (key[r] != 0u && !(taken >> r & 1u) && (key[r] == top || value_of(key[r]) >= lo)) near |= 1u << r;
+          if (left[r] != 0u && (left[r] == top || value_of(left[r]) >= lo)) near |= 1u << r;
         if (__reduce_add_sync(ALL, __popc(near)) > 1) {
           need_total64();
           double best = -INFINITY;
@@ -322,18 +316,16 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 8 : 1) moe_route_
           e = warp_argmax(best, at);
         }
       }
-      float of = 0.0f;
       if ((e & 31u) == static_cast<uint32_t>(lane)) {
+        most = 0u;
 #pragma unroll
-        for (int r = 0; r < EPL; ++r)
-          if (e >> 5 == static_cast<uint32_t>(r)) of = l[r];
-        taken |= 1u << (e >> 5);
-        look();
+        for (int r = 0; r < EPL; ++r) {
+          if (e >> 5 == static_cast<uint32_t>(r)) left[r] = 0u;
+          most = max(most, left[r]);
+        }
       }
-      of = __shfl_sync(ALL, of, e & 31);
       if (lane == j) {
         chosen = static_cast<int>(e);
-        logit = of;
         place_key = top;
       }
     }
@@ -347,7 +339,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 8 : 1) moe_route_
     if (__any_sync(ALL, near)) choose(true, p.top_k);
     if (lane >= p.top_k) chosen = -1;
   }
-  if (chosen < 0) logit = -INFINITY;
+  const float logit = chosen < 0 ? -INFINITY : to_f32(row[chosen]);
   // The weights from the logits: where they are renormalised, relative to the
   // largest chosen one, so that scores too small for fp32 keep their ratios.
   const float most = p.renormalise ? value_of(__reduce_max_sync(ALL, key_of(logit))) : 0.0f;
