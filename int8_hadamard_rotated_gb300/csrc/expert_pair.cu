@@ -13,10 +13,10 @@
 // row. It forms h there; the two threads of a row exchange their maxima through
 // shared memory, and codes and scale leave from registers.
 //
-// 8192 rows of eight experts, 4096 -> 2 x 2432: 160 us = 2.0 PFLOP/s; a linear of
+// 8192 rows of eight experts, 4096 -> 2 x 2432: 156 us = 2.1 PFLOP/s; a linear of
 // as many products 141 us, the dense kernel 130 us. A tile costs 0.47 us for each
 // block of K (operand delivery and the accumulator's hand-over, as there), and 2
-// to 4 us for the epilogue beyond the two blocks that the MMAs run ahead (SwiGLU:
+// to 3 us for the epilogue beyond the two blocks that the MMAs run ahead (SwiGLU:
 // 128 exponentials and reciprocals a thread take 1.1 us of it). Experts of 512
 // uneven rows leave a fifth of the tiles' rows empty.
 #include "expert_common.cuh"

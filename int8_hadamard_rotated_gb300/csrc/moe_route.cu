@@ -28,8 +28,8 @@ namespace {
 // One token per warp, its logits read once; expert i is on lane i % 32. The
 // work is a chain of warp-wide maxima over order-preserving 32-bit keys
 // (redux), so a token costs instructions and latency, not bandwidth: 4096 x 256
-// logits, eight of four groups by sigmoid and bias, 1960 instructions a warp,
-// 15 us; one token 3.7 us, most of it a launch.
+// logits, eight of four groups by sigmoid and bias, 1850 instructions a warp,
+// 14 us; one token 3.7 us, most of it a launch.
 //
 // Which of two values is larger must not hang on the rounding of exp: values
 // are formed in fp32 with a bound on their error, and where more than one is

@@ -264,6 +264,31 @@ def test_expert_swiglu(ops, T, E, k, only, I, K):  # noqa: E741
     assert ops.convrot_device_status() == ops.OK
 
 
+@pytest.mark.parametrize("T,E,k,N,I,K", [(1, 1, 1, 1, 16, 48), (130, 1, 1, 1, 144, 272), (20, 1024, 4, 40, 32, 144),
+                                          (2, 300, 8, 7, 48, 16), (6, 2, 1, 260, 144, 4240), (400, 2, 2, 33, 272, 4240)])
+def test_expert_extremes(ops, T, E, k, N, I, K):  # noqa: E741
+    """One expert and the most experts, one output feature, long K."""
+    _, _, (order, _, offsets), (d_order, _, d_offsets) = planned(T, T, E, k, None, 0.0)
+    dw, hw = matrices(1, E, N, K, True)
+    dg, hg = matrices(2, E, I, K, True)
+    du, hu = matrices(3, E, I, K, False)
+    Q, s = bo.fp8_pack(activations(T, T, K).numpy())
+    x, sx = dev_codes(Q), torch.from_numpy(s).cuda()
+    src = order // k
+    ref, mag = mo.expert_linear(Q, s, src, offsets, *hw)
+    y = ops.fp8_expert_linear(x, sx, d_offsets, dw, order=d_order, top_k=k, out_dtype=torch.float32)
+    assert_within(y, ref, mo.linear_error(mag, K))
+    g, ga = mo.expert_linear(Q, s, src, offsets, *hg)
+    u, ua = mo.expert_linear(Q, s, src, offsets, *hu)
+    h, dh = mo.swiglu(g, u, mo.linear_error(ga, K), mo.linear_error(ua, K))
+    Qh, sh = ops.fp8_expert_swiglu(x, sx, d_order, d_offsets, k, dg, du)
+    S = bo.widen(host(sh), T * k, I)
+    value = bo.e4m3_values()[codes(Qh)] * S
+    half = np.maximum(2.0 ** -4 * np.maximum(np.abs(value), np.abs(h)), 2.0 ** -10 * S)
+    assert (np.abs(value - h) <= half * (1 + 1e-6) + dh + np.abs(h) * 4 * U24).all()
+    assert ops.convrot_device_status() == ops.OK
+
+
 def test_expert_strides(ops):
     """Gate and up as halves of one array, experts apart; a Y with rows apart and at odd offsets."""
     E, I, K, T, k = 5, 144, 272, 70, 2  # noqa: E741
