@@ -370,8 +370,9 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 8 : 1) moe_route_
 // through all choices for them, twice: every warp has a contiguous part; the
 // first turn counts its choices of each of the CTA's experts and those of lower
 // ones, the second hands the places out, by ballots. Nothing passes between
-// CTAs, but every SM looks at every choice: 512 of 128 experts take 2.7 us,
-// 65536 of 256 experts 32 us.
+// CTAs, but every SM looks at every choice: 512 of 128 experts take 3.2 us, 12000
+// of 64 experts 5.7 us (in two launches 6.4 us), 16384 7.0 us (6.4 us), 65536 of 256
+// experts 33 us.
 //
 // Many: two launches. The choices are dealt out in contiguous parts; the first
 // launch counts a part's choices of every expert, the second sums the parts
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 8 : 1) moe_route_
 
 constexpr int PLAN_WARPS = 32;
 constexpr int PLAN_STEP = 4;          // choices per lane and turn
-constexpr int64_t PLAN_ONE = 4096;    // most choices of the one launch
+constexpr int64_t PLAN_ONE = 12288;   // most choices of the one launch
 constexpr int PART_WARPS = 16;        // the two launches: warps of a CTA
 constexpr int64_t PLAN_PARTS = 32;    // most parts
 constexpr int64_t PART_LEAST = 1024;  // fewest choices of a part
