@@ -121,12 +121,12 @@ __device__ __forceinline__ int first_block(int expert, int col, int n_cols, int 
   return vec ? at % (blocks / 4) * 4 : at * 5 % blocks;
 }
 
-// warp_wait for what the CTAs of a cluster have handed over: what they wrote
-// before is seen.
+// warp_wait for what the CTAs of a cluster (or this CTA's warps alone) have
+// handed over: what they wrote before is seen.
 __device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
-                                             uint64_t limit_ns) {
+                                             uint64_t limit_ns, int ctas) {
   const bool ok = warp_wait(bar, parity, abort_flag, err, limit_ns);
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  if (ctas > 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
   return ok;
 }
 
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
       for (int part_row = 0; part_row < BN; part_row += G::PART_ROWS) {
         if (part_row >= valid) break;
         // the partial tile, once the one before it has been read everywhere
-        ok = cluster_wait(pempty, (seq & 1u) ^ 1u, abort_flag, err, p.wait_ns);
+        ok = cluster_wait(pempty, (seq & 1u) ^ 1u, abort_flag, err, p.wait_ns, split);
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < G::PART_ROWS / 2; ++i) {
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
           part[(2 * i + 1) * W_ROWS + 32 * warp + lane] = b;
         }
         arrive_everywhere(pfull);
-        ok = cluster_wait(pfull, seq & 1u, abort_flag, err, p.wait_ns);
+        ok = cluster_wait(pfull, seq & 1u, abort_flag, err, p.wait_ns, split);
         if (!ok) break;
         ++seq;
         const int rows = min(G::PART_ROWS, valid - part_row);
