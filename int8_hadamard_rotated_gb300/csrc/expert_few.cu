@@ -9,9 +9,9 @@
 // shares of K and add their partial tiles up through distributed shared memory,
 // in rank order.
 //
-// 256 rows over 128 experts, 2048 -> 2 x 768: 53 us for the 83 experts that are
-// reached, 261 MB = 4.9 TB/s; 144 items of 256 weight rows of 4096, one for each
-// CTA, 29.7 us = 5.1 TB/s. A CTA streams a block of K (34 KB) in 0.45 us at best:
+// 256 rows over 128 experts, 2048 -> 2 x 768: 50 us for the 83 experts that are
+// reached, 261 MB = 5.3 TB/s; 144 items of 256 weight rows of 4096, one for each
+// CTA, 30 us = 5.0 TB/s. A CTA streams a block of K (34 KB) in 0.45 us at best:
 // its eight MMAs take 0.32 us (75 cycles each, whatever their width), and issuing
 // the copies about as long; so the last round of items counts, and 5 us for
 // setting up, the first loads and the last sums.
@@ -611,9 +611,9 @@ int launch_expert_few(const ExpertCall& c, cudaStream_t stream) {
   // Items of the rows that an expert has on average: narrower ones cost less
   // while the expert's rows are one item, and read its weights once more for
   // every further item. 64 experts of 3 x 1024 x 2048 (16 of 3 x 1536 x 4096),
-  // gate and up: 16 rows each 54, 59 and 63 us (41, 50 and 58) with 16, 32 and 64
-  // columns; 24 rows 64, 68 and 67 us (54, 48 and 57); 32 rows 80, 74 and 71 us
-  // (69, 64 and 59).
+  // gate, up and down: 16 rows each 80, 80 and 86 us (67, 70 and 79) with 16, 32
+  // and 64 columns; 24 rows 100, 87 and 92 us (85, 68 and 79); 32 rows 125, 99 and
+  // 96 us (106, 88 and 82).
   const int64_t per = c.rows.n / c.rows.E;
   if (per <= 16) return launch_columns<16>(c, stream);
   if (per <= 24) return launch_columns<32>(c, stream);

@@ -12,10 +12,10 @@ namespace convrot {
 namespace moe {
 
 // By the rows that an expert has on average. 64 experts of 3 x 1024 x 2048 (16 of
-// 3 x 1536 x 4096), gate and up plus down: 48 rows each take 140 us (91) with
-// the few-row kernel and 130 us (100) with the other, 64 rows 143 us (103) and 132
-// us (100), 128 rows 247 us (175) and 148 us (103).
-bool many_rows(int64_t n, int E) { return n / E > 56; }
+// 3 x 1536 x 4096), gate and up plus down: 48 rows each take 120 us (85) with
+// the few-row kernel and 129 us (99) with the other, 64 rows 125 us (94) and 129
+// us (100), 80 rows 146 us (128) and 129 us (100).
+bool many_rows(int64_t n, int E) { return n / E > 64; }
 
 int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& gate,
                          const convrot_experts& up, uint8_t* Q_h, float* s_h, cudaStream_t stream,
