@@ -32,11 +32,12 @@ namespace {
 // 14 us; one token 3.7 us, most of it a launch.
 //
 // Which of two values is larger must not hang on the rounding of exp: values
-// are formed in fp32 with a bound on their error, and where more than one is
-// within twice the bound of the largest (about one token in a few hundred),
-// those alone are formed again in 64 bits and compared there. So the choice is
-// that of 64-bit arithmetic at the price of fp32. (All values in 64 bits would
-// take some 50 us for 4096 x 256 logits at this GPU's fp64 rate.)
+// are formed in fp32 with a bound on their error (a group's: the bounds of its
+// summands), and where more than one may be the largest by it (about one token
+// in a few hundred), those alone are formed again in 64 bits and compared there.
+// So the choice is that of 64-bit arithmetic at the price of fp32. (All values
+// in 64 bits would take some 50 us for 4096 x 256 logits at this GPU's fp64
+// rate.)
 
 constexpr int ROUTE_WARPS = 4;
 
@@ -225,22 +226,29 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 8 : 1) moe_route_
       a = fmaxf(a, oa);
     }
     const bool two = p.group_top == 2 && b > -INFINITY;
-    const float value = two ? a + b : a;
-    uint32_t gkey = mine && value > -INFINITY ? key_of(value) : 0u;
+    // (half of the value where it is not exact: a sum of two need not fit fp32)
+    const float value = exact ? a : two ? fmaf(0.5f, a, 0.5f * b) : 0.5f * a;
+    // What it may be off by is what its summands are, whose sum may cancel; and
+    // the roundings of the sum and of the bounds.
+    const float off = exact || value == INFINITY
+                          ? 0.0f
+                          : fmaf(0x1p-22f, fabsf(value), 0.5f * (error_at(a) + (two ? error_at(b) : 0.0f)));
+    const float least_value = value - off, most_value = value + off;
+    uint32_t gkey = mine && a > -INFINITY ? key_of(value) : 0u;
     uint32_t open = 0;  // the chosen groups
     for (int j = 0; j < p.top_groups; ++j) {
       const uint32_t top = __reduce_max_sync(ALL, gkey);
       if (top == 0u) break;
       int best = static_cast<int>(__reduce_min_sync(ALL, gkey == top ? static_cast<uint32_t>(g) : 0xffffu));
       if (!exact) {
-        const float v = value_of(top), lo = v - 5.0f * error_at(v);
-        const bool near = gkey != 0u && (gkey == top || value >= lo);
+        const float least = __shfl_sync(ALL, least_value, best * P);
+        const bool near = gkey != 0u && most_value >= least;
         if (__popc(__ballot_sync(ALL, near && sub == 0)) > 1) {
           need_total64();
           double a64 = -INFINITY, b64 = -INFINITY;
           if (near) {
-            const float least = two ? b : a;
-            const float from = least - 2.5f * error_at(least);
+            const float last = two ? b : a;
+            const float from = last - 2.5f * error_at(last);
             for (int i = sub; i < p.per_group; i += P) {
               const float w = sv[g * pitch + i];
               if (w == -INFINITY || !(w >= from || w == a)) continue;

@@ -119,6 +119,31 @@ def test_route_near_ties(ops):
         check_route(ops, L.cuda(), 8, score=score, n_groups=4, top_groups=2, group_top=2)
 
 
+@pytest.mark.parametrize("score,spread", [("sigmoid", 2.0 ** -22), ("softmax", 2.0 ** -16)])
+@pytest.mark.parametrize("size", [4.0, 16.0, 60.0, 1000.0])
+def test_route_groups_biases_of_opposite_sign(ops, size, score, spread):
+    """Groups whose two largest values cancel: the sum is near 0, what their
+    roundings may be off by is not. The groups' values lie about such a rounding
+    apart."""
+    E = 64
+    bias = torch.full((E,), -4 * size)
+    bias[0::8], bias[1::8] = size, -size
+    L = size * spread * torch.randn(500, E, generator=gen(int(size)))
+    for top, k in ((1, 2), (3, 6)):
+        check_route(ops, L.cuda(), k, bias=bias, score=score, n_groups=8, top_groups=top, group_top=2)
+
+
+def test_route_groups_whose_sum_overflows(ops):
+    """Sums of two values past the fp32 range, next to one at its end."""
+    bias = torch.zeros(40)
+    for g, (a, b) in enumerate(((3.0e38, 3.0e38), (3.3e38, 3.2e38), (3.4e38, 2.0e31), (3.4e38, 1.0e31), (-3.0e38, -3.0e38))):
+        bias[8 * g:8 * g + 8] = -3.2e38
+        bias[8 * g + 3], bias[8 * g + 5] = b, a
+    L = torch.randn(20, 40, generator=gen(12))
+    for top in range(1, 6):
+        check_route(ops, L.cuda(), 2 * top, bias=bias, score="sigmoid", n_groups=5, top_groups=top, group_top=2)
+
+
 def test_route_closed_and_bad(ops):
     E = 24
     L = torch.randn(12, E, generator=gen(4))
