@@ -130,14 +130,10 @@ __device__ __forceinline__ unsigned long long f32x2_add(unsigned long long a, un
   return r;
 }
 
-// silu(g) u = g u / (1 + exp(-g)), with exp(-g) and the reciprocal from the
-// hardware's approximations (ex2.approx, rcp.approx, within 2^-22 each): the
-// relative error is a few 1e-7 and |g| 2^-24 from the exponent's rounding.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * g));
-  return g * rcp_approx(1.0f + e) * u;
-}
+// silu(g) u = g u sigmoid(g): a relative error of a few 1e-7 and |g| 2^-24 from
+// the exponent's rounding while the sigmoid is a normal number (g > -87.3);
+// below, it is off by up to 2^-149.
+__device__ __forceinline__ float silu_mul(float g, float u) { return g * sigmoid_fast(g) * u; }
 
 // Rows that only moe_combine reads, on the way to a bf16 output: binary16
 // with a power of two per row and 128 features that brings the largest

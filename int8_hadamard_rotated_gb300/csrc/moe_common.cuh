@@ -10,6 +10,16 @@ namespace moe {
 constexpr int MAX_EXPERTS = CONVROT_MOE_MAX_EXPERTS;
 constexpr int MAX_TOP_K = CONVROT_MOE_MAX_TOP_K;
 
+// 1 / (1 + exp(-l)) from the hardware's base-2 exponential and reciprocal
+// (ex2.approx, rcp.approx, within 2^-22 and one ulp): the exponential of -|l|, so
+// that nothing overflows and the reciprocal of 1 to 2 is not flushed to zero,
+// and not its .ftz form, so that neither is the result.
+__device__ __forceinline__ float sigmoid_fast(float l) {
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * fabsf(l)));
+  return rcp_approx(1.0f + e) * (l >= 0.0f ? 1.0f : e);
+}
+
 // Rows sorted by expert, as moe_plan leaves them.
 struct Rows {
   const int32_t* order;    // [n] the choice (token * top_k + slot) of a row, or null: row i of the activation

@@ -95,14 +95,6 @@ __device__ __noinline__ double score64(float l, float m, double total, bool sigm
   return sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : exp64(l, m) / total;
 }
 
-// The sigmoid to choose by: the hardware's base-2 exponential and reciprocal,
-// within the bound on the values' error below.
-__device__ __forceinline__ float sigmoid_fast(float l) {
-  float e;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * fabsf(l)));
-  return rcp_approx(1.0f + e) * (l >= 0.0f ? 1.0f : e);
-}
-
 // exp(-c) / (1 + exp(-l)) for c = 0, or l <= c < 0: without underflow in the
 // latter case where l is near c.
 __device__ __forceinline__ float sigmoid_from(float l, float c) {

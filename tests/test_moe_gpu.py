@@ -337,6 +337,33 @@ def test_expert_strides(ops):
         assert (host(base[:, :off].float()) == 0).all() and (host(base[:, off + I:].float()) == 0).all()
 
 
+@pytest.mark.parametrize("rows", [[3] * 8, [130] * 8])
+def test_swiglu_gates_far_below_zero(ops, rows):
+    """Gates around where their sigmoid leaves the normal fp32 range (-87.3), next
+    to up values that bring the products back: activations of zeros, so that g
+    and u are the biases."""
+    base = (-20.0, -60.0, -80.0, -87.0, -88.0, -90.0, -95.0, -101.0)
+    E, K, I = len(base), 128, 144  # noqa: E741
+    r = np.random.default_rng(1)
+    g = (np.array(base)[:, None] - r.random((E, I))).astype(np.float32)
+    u = (r.choice([-1.0, 1.0], (E, I)) * (1 + r.random((E, I))) * 1e30).astype(np.float32)
+    q, s, _ = matrices(1, E, I, K, False)[0]
+    n = sum(rows)
+    x, sx = ops.fp8_pack_activations(torch.zeros(n, K, device="cuda"))
+    offsets = torch.tensor([0] + rows).cumsum(0).to(torch.int32).cuda()
+    Qh, sh = ops.fp8_expert_swiglu(x, sx, None, offsets, 1, (q, s, torch.from_numpy(g).cuda()),
+                                   (q, s, torch.from_numpy(u).cuda()))
+    S = bo.widen(host(sh), n, I)
+    value = bo.e4m3_values()[codes(Qh)] * S
+    which = np.repeat(np.arange(E), rows)
+    zero = np.zeros((n, I))
+    h, dh = mo.swiglu(g[which].astype(np.float64), u[which].astype(np.float64), zero, zero)
+    # a sigmoid below 2^-126 is a multiple of 2^-149: half a step of its rounding, and of the exponential's
+    dh = dh + np.abs(g[which].astype(np.float64) * u[which]) * 2.0 ** -149
+    half = np.maximum(2.0 ** -4 * np.maximum(np.abs(value), np.abs(h)), 2.0 ** -10 * S)
+    assert (np.abs(value - h) <= half * (1 + 1e-6) + dh + np.abs(h) * 4 * U24).all()
+
+
 def test_prepare_experts(ops):
     W = torch.randn(3, 130, 272, generator=gen(1)).cuda()
     Q, s = ops.fp8_prepare_experts(W)
