@@ -783,7 +783,8 @@ size_t fp8_expert_workspace_size(int64_t n, int64_t K, int n_experts);
  *   Y[i,:] = X[m,:] W_e^T + bias_e,
  * X as codes Q_x [T,K] and scales s_x [T, ceil(K/128)], summed as by
  * fp8_linear_packed, one rounding to y_dtype. Rows of Y from offsets[E] on are
- * left as they are. Results repeat bit for bit.
+ * left as they are. Results repeat bit for bit, wherever the arrays lie; calls
+ * of other n or n_experts may sum a row's blocks of K in another order.
  *   order, offsets  of moe_plan for n choices; T >= n where order is NULL.
  *   workspace  with order: at least fp8_expert_workspace_size(n, K, n_experts)
  *              bytes, 16-byte aligned (NULL where that is 0): many rows per

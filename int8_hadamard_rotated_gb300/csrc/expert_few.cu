@@ -113,12 +113,12 @@ __device__ __forceinline__ void drain_columns(unsigned long long (&acc)[BN / 2],
 // Where an item's walk over the blocks of K starts: not at the first one for
 // all. Rows of K = 4096 codes lie 4 KB apart, and CTAs that read the same block
 // of their rows at the same time meet in a few of the memory's channels: 144
-// items, one per CTA, were read at 3.7 TB/s. A multiple of four where the
-// scales are read four at a time. By the matrix' place alone, so that an
-// output's sum has the same order in every call.
-__device__ __forceinline__ int first_block(int expert, int col, int n_cols, int blocks, bool vec) {
+// items, one per CTA, were read at 3.7 TB/s. By the matrix' place and the CTA's
+// blocks alone, not by where the arrays lie in memory: in fours (the scales'
+// wide loads) wherever the blocks are, also for scales that are loaded singly.
+__device__ __forceinline__ int first_block(int expert, int col, int n_cols, int blocks, bool fours) {
   const int at = expert * n_cols + col;
-  return vec ? at % (blocks / 4) * 4 : at * 5 % blocks;
+  return fours ? at % (blocks / 4) * 4 : at * 5 % blocks;
 }
 
 // warp_wait for what the CTAs of a cluster (or this CTA's warps alone) have
@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
   const int unit = static_cast<int>(blockIdx.x) / split, n_units = static_cast<int>(gridDim.x) / split;
   const int kb_begin = p.KB * rank / split, kb_end = p.KB * (rank + 1) / split;  // this CTA's blocks of K
   const int blocks = kb_end - kb_begin;
-  const bool vec = p.vec_scales && kb_begin % 4 == 0 && blocks % 4 == 0;
+  const bool fours = p.KB % 4 == 0 && kb_begin % 4 == 0 && blocks % 4 == 0;
+  const bool vec = p.vec_scales && fours;  // their scales are loaded together
 
   if (threadIdx.x == EPI_WARPS * 32) {
     for (int s = 0; s < G::STAGES; ++s) {
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
         for (int t = unit; ok && t < total; t += n_units) {
           const Source c = next;
           const int f = c.col * FEATURES;
-          int kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, vec);
+          int kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, fours);
           for (int i = 0; i < blocks; ++i) {
             if (i == min(blocks, G::STAGES) - 1 && t + n_units < total) next = look_up(t + n_units);
             if (p.withhold && t == total - 1 && rank == split - 1 && i == blocks - 1) break;
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
         Source s;
         s.row = range.x + c.tile * BN;
         s.width = (min(BN, range.y - s.row) + 15) & ~15;
-        s.kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, vec);
+        s.kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, fours);
         s.rows = make_int4(0, 0, 0, 0);
         if (gather && lane < BN / 4) {
           const int i = s.row + 4 * lane, last = range.y - 1;
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) expert_few_kernel(const __grid
       i.valid = min(BN, range.y - i.row);
       i.col = c.col;
       i.expert = c.expert;
-      i.kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, vec);
+      i.kb = kb_begin + first_block(c.expert, c.col, p.n_cols, blocks, fours);
 #pragma unroll
       for (int k = 0; k < XR; ++k)
         i.xs[k] = p.s_x + static_cast<int64_t>(source_row(p.rows, min(i.row + (32 * k + lane) % BN, range.y - 1))) * p.KB;

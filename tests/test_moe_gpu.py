@@ -364,6 +364,40 @@ def test_swiglu_gates_far_below_zero(ops, rows):
     assert (np.abs(value - h) <= half * (1 + 1e-6) + dh + np.abs(h) * 4 * U24).all()
 
 
+@pytest.mark.parametrize("E,rows", [(1, 5), (3, 4), (40, 3), (60, 20), (12, 40), (4, 100)])
+@pytest.mark.parametrize("K", [512, 2048, 4096])
+def test_results_whatever_the_scales_alignment(ops, E, rows, K):
+    """The same values in scale arrays that start on 16 bytes, and on 4, with
+    experts an odd distance apart: the same bits."""
+    n, N = E * rows, 272
+    r = np.random.default_rng(E)
+
+    def codes_(*shape):
+        return torch.from_numpy(r.integers(0, 0x70, shape).astype(np.uint8) | r.integers(0, 2, shape).astype(np.uint8) << 7)
+
+    def scales(*shape):
+        return torch.from_numpy((2.0 ** r.uniform(-6, 2, shape)).astype(np.float32)).cuda()
+
+    def odd(t):  # the same, 4 bytes past a 16-byte boundary, the first axis apart by one more
+        base = torch.zeros(1 + t.shape[0] * (t[0].numel() + 1), device="cuda")
+        v = base[1:].view(t.shape[0], -1)[:, :-1].view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 16 == 4
+        return v
+
+    x, q, q2 = (codes_(*d).cuda().view(torch.float8_e4m3fn) for d in ((n, K), (E, N, K), (E, N, K)))
+    sx, s, s2 = scales(n, K // 128), scales(E, 3, K // 128), scales(E, 3, K // 128)
+    offsets = (torch.arange(E + 1, dtype=torch.int32) * rows).cuda()
+    base = torch.zeros(1 + sx.numel(), device="cuda")
+    sx_odd = base[1:].view(sx.shape).copy_(sx)
+    y = ops.fp8_expert_linear(x, sx, offsets, (q, s), out_dtype=torch.float32)
+    h = ops.fp8_expert_swiglu(x, sx, None, offsets, 1, (q, s), (q2, s2))
+    for args in ((sx_odd, s, s2), (sx, odd(s), odd(s2)), (sx_odd, odd(s), s2)):
+        assert torch.equal(ops.fp8_expert_linear(x, args[0], offsets, (q, args[1]), out_dtype=torch.float32), y)
+        z = ops.fp8_expert_swiglu(x, args[0], None, offsets, 1, (q, args[1]), (q2, args[2]))
+        assert (codes(z[0]) == codes(h[0])).all() and torch.equal(z[1], h[1])
+
+
 def test_prepare_experts(ops):
     W = torch.randn(3, 130, 272, generator=gen(1)).cuda()
     Q, s = ops.fp8_prepare_experts(W)
