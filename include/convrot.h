@@ -785,13 +785,15 @@ size_t fp8_expert_workspace_size(int64_t n, int64_t K, int n_experts);
  * fp8_linear_packed, one rounding to y_dtype. Rows of Y from offsets[E] on are
  * left as they are. Results repeat bit for bit, wherever the arrays lie; calls
  * of other n or n_experts may sum a row's blocks of K in another order.
- *   order, offsets  of moe_plan for n choices; T >= n where order is NULL.
+ *   order, offsets  of moe_plan for n <= T * top_k choices; n <= T where order
+ *              is NULL (top_k then has no meaning).
  *   workspace  with order: at least fp8_expert_workspace_size(n, K, n_experts)
  *              bytes, 16-byte aligned (NULL where that is 0): many rows per
  *              expert are sorted there first.
- * Errors: those of fp8_linear_packed; ERR_WORKSPACE; ERR_ARG (also n_experts or top_k below
- *         1), ERR_ALIGN (also q_stride % 16), ERR_UNSUPPORTED (more experts
- *         than CONVROT_MOE_MAX_EXPERTS).
+ * Errors: those of fp8_linear_packed; ERR_WORKSPACE; ERR_ARG (also n_experts or
+ *         top_k below 1, more rows than T tokens have), ERR_ALIGN (also
+ *         q_stride % 16), ERR_UNSUPPORTED (more experts than
+ *         CONVROT_MOE_MAX_EXPERTS).
  */
 int fp8_expert_linear(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
                       const int32_t* offsets, int64_t n, int n_experts, int top_k,

@@ -63,7 +63,8 @@ int experts_checks(const convrot_experts& w, int64_t E, int64_t K) {
 int expert_checks(const uint8_t* Q_x, const float* s_x, int64_t T, int64_t K, const int32_t* order,
                   const int32_t* offsets, int64_t n, int E, int top_k, const convrot_experts* w) {
   if (T < 0 || n < 0 || K <= 0 || E < 1 || top_k < 1 || !w || w->N < 0) return CONVROT_ERR_ARG;
-  if (n > 0 && (T == 0 || (!order && T < n))) return CONVROT_ERR_ARG;
+  // n choices are of rows up to (n - 1) / top_k
+  if (n > 0 && T <= (n - 1) / (order ? top_k : 1)) return CONVROT_ERR_ARG;
   if (E > MAX_EXPERTS) return CONVROT_ERR_UNSUPPORTED;
   if (n == 0 || w->N == 0) return CONVROT_OK;
   if (!Q_x || !s_x || !offsets) return CONVROT_ERR_ARG;

@@ -1142,9 +1142,10 @@ def fp8_expert_linear(Q_x: torch.Tensor, s_x: torch.Tensor, offsets: torch.Tenso
                       stream=None) -> torch.Tensor:
     """Rows in the order of a moe_plan, each through its expert's matrix:
     Y[i] = X[m] W_e^T + b_e, with m = i, or, given the plan's order,
-    m = order[i] // top_k. weight: (codes [E,N,K], scales, biases or None) as
-    fp8_prepare_experts gives them. Rows from offsets[E] on are left as they
-    are (in a new Y: uninitialised)."""
+    m = order[i] // top_k (an order of more than T * top_k rows is refused).
+    weight: (codes [E,N,K], scales, biases or None) as fp8_prepare_experts gives
+    them. Rows from offsets[E] on are left as they are (in a new Y:
+    uninitialised)."""
     device, handle = _start(Q_x, stream)
     w, E, N = _experts(weight, "weight", device, _matrix(Q_x, "Q_x")[1])
     T, K, n, q, s, o, f = _plan_of(Q_x, s_x, order, offsets, E, device)

@@ -148,6 +148,24 @@ def test_swiglu_refusals(ops):
     assert call(n=0, T=0) == ops.OK
 
 
+def test_more_choices_than_the_tokens_have(ops):
+    """An order of more choices than T tokens make: a top_k left out or too
+    small, which would read other tokens' rows."""
+    assert linear(ops, k=1) == linear(ops, k=2) == ops.ERR_ARG
+    assert linear(ops, n=121) == ops.ERR_ARG
+    assert linear(ops, T=1 << 30, n=(1 << 30) + 1, k=1) == ops.ERR_ARG
+    # as many choices as there are, fewer, and products past 31 bits, are taken (as far as the missing workspace)
+    assert linear(ops, T=1000, n=3000) == linear(ops, T=1000, n=2900) == ops.ERR_WORKSPACE
+    assert linear(ops, T=1000, n=3000, k=2 ** 31 - 1) == ops.ERR_WORKSPACE
+    assert linear(ops, T=1 << 28, n=(1 << 28) + 1, k=1 << 30) == ops.ERR_ALIAS  # (Y reaches over the other arrays)
+    # without an order top_k has no meaning
+    assert linear(ops, T=3000, n=3000, order=None, k=1, Y=at(0)) == ops.ERR_ALIAS
+    g, u = experts(ops, 8), experts(ops, 9)
+    for k, status in ((1, ops.ERR_ARG), (2, ops.ERR_ARG), (3, ops.ERR_WORKSPACE)):
+        assert ops.lib().fp8_expert_swiglu(at(0), at(1), 1000, 512, at(2), at(3), 3000, 8, k, ctypes.byref(g), ctypes.byref(u),
+                                           at(4), at(5), None, 0, None) == status
+
+
 def test_combine_refusals(ops):
     def call(**kw):
         a = dict(rows=at(0), rt=ops.BF16, ldr=256, n=120, place=at(1), w=at(2), T=40, k=3, N=256, res=at(3), ldres=256,
