@@ -210,6 +210,25 @@ def test_plan(ops, n, E):
     assert ops.convrot_device_status() == ops.OK
 
 
+@pytest.mark.parametrize("n,E", [(3000, 151), (3000, 152), (3000, 303), (3000, 304), (3000, 400), (5000, 607), (5000, 608),
+                                 (9000, 1024), (12288, 64), (12288, 500), (12288, 1024), (12289, 64), (12289, 500),
+                                 (12289, 1024), (300000, 130)])
+def test_plan_at_its_borders(ops, n, E):
+    """Where the experts per CTA change, and at the most choices of one launch."""
+    r = np.random.default_rng(n + E)
+    e = np.where(r.random(n) < 0.3, r.integers(0, 9, size=n), r.integers(-1, E, size=n)).astype(np.int32)
+    e[e == E // 2] = -1
+    order, place, offsets = (host(t) for t in ops.moe_plan(torch.from_numpy(e).cuda(), E))
+    flat = np.where(e < 0, E, e)
+    sort = np.argsort(flat, kind="stable").astype(np.int32)
+    np.testing.assert_array_equal(offsets, np.searchsorted(flat[sort], np.arange(E + 1)))
+    np.testing.assert_array_equal(order, np.where(np.arange(n) < offsets[E], sort, -1))
+    back = np.empty(n, np.int32)
+    back[sort] = np.arange(n)
+    np.testing.assert_array_equal(place, np.where(e < 0, -1, back))
+    assert ops.convrot_device_status() == ops.OK
+
+
 def test_plan_out_of_range(ops):
     """Experts outside [-1, E) are dropped and reported."""
     for bad in (-2, 4, 2 ** 31 - 1, -2 ** 31):
@@ -398,6 +417,46 @@ def test_results_whatever_the_scales_alignment(ops, E, rows, K):
         assert (codes(z[0]) == codes(h[0])).all() and torch.equal(z[1], h[1])
 
 
+@pytest.mark.parametrize("E", [9, 20, 70, 300])
+def test_many_rows_of_many_experts(ops, E):
+    """The kernel for many rows per expert past its first eight and its first 32
+    experts: uneven ones, whole eights without rows, several tiles of one."""
+    r = np.random.default_rng(E)
+    counts = r.integers(1, 180, size=E)
+    counts[r.random(E) < 0.2] = 0
+    counts[8:16] = 0
+    counts[-3] = 700
+    if E > 60:
+        counts[24:48] = 0
+        counts[64:66] = 256, 257
+    short = 66 * E - counts.sum()  # over 64 rows on average
+    if short > 0:
+        counts[E - 2] += short
+    e = r.permutation(np.repeat(np.arange(E), counts)).astype(np.int32)
+    n, N, I, K = e.size, 40, 48, 144  # noqa: E741
+    assert n // E > 64
+    order = np.argsort(e, kind="stable").astype(np.int32)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    d_order, d_offsets = torch.from_numpy(order).cuda(), torch.from_numpy(offsets).cuda()
+    dw, hw = matrices(1, E, N, K, True)
+    dg, hg = matrices(2, E, I, K, True)
+    du, hu = matrices(3, E, I, K, False)
+    Q, s = bo.fp8_pack(activations(E, n, K).numpy())
+    x, sx = dev_codes(Q), torch.from_numpy(s).cuda()
+    for src, d in ((order, d_order), (np.arange(n), None)):
+        ref, mag = mo.expert_linear(Q, s, src, offsets, *hw)
+        assert_within(ops.fp8_expert_linear(x, sx, d_offsets, dw, order=d), ref, mo.linear_error(mag, K))
+        g, ga = mo.expert_linear(Q, s, src, offsets, *hg)
+        u, ua = mo.expert_linear(Q, s, src, offsets, *hu)
+        h, dh = mo.swiglu(g, u, mo.linear_error(ga, K), mo.linear_error(ua, K))
+        Qh, sh = ops.fp8_expert_swiglu(x, sx, d, d_offsets, 1, dg, du)
+        S = bo.widen(host(sh), n, I)
+        value = bo.e4m3_values()[codes(Qh)] * S
+        half = np.maximum(2.0 ** -4 * np.maximum(np.abs(value), np.abs(h)), 2.0 ** -10 * S)
+        assert (np.abs(value - h) <= half * (1 + 1e-6) + dh + np.abs(h) * 4 * U24).all()
+    assert ops.convrot_device_status() == ops.OK
+
+
 def test_prepare_experts(ops):
     W = torch.randn(3, 130, 272, generator=gen(1)).cuda()
     Q, s = ops.fp8_prepare_experts(W)
@@ -451,6 +510,63 @@ def test_moe(ops, T, E, k, only, K, I, N, dtype, out):  # noqa: E741
                     Y=torch.full((T, N), float("nan"), dtype=DT[out], device="cuda"))
     assert_within(y, ref, bound)
     assert ops.convrot_device_status() == ops.OK
+
+
+@pytest.mark.parametrize("T,E,k,out,dtype", [(5, 200, 8, "bf16", "bf16"), (40, 200, 4, "f32", "f16"), (30, 303, 6, "bf16", "f32"),
+                                             (30, 304, 6, "bf16", "bf16"), (60, 700, 8, "f16", "f16"), (25, 1024, 8, "f32", "f32"),
+                                             (3300, 400, 4, "bf16", "bf16"), (3080, 300, 4, "f32", "f32")])
+def test_moe_many_experts(ops, T, E, k, out, dtype):
+    """The plans of more experts and choices inside fp8_moe."""
+    K, I, N = 48, 32, 24  # noqa: E741
+    e, w = choices(T, T, E, k, 0.1)
+    dg, hg = matrices(1, E, I, K, True)
+    du, hu = matrices(2, E, I, K, True)
+    dd, hd = matrices(3, E, N, I, True)
+    X = activations(T, T, K, dtype)
+    ref, bound = mo.moe(X.float().numpy(), e, w, hg, hu, hd, rows_error=2.0 ** -11 if out == "bf16" else 0.0)
+    y = ops.fp8_moe(X.cuda(), torch.from_numpy(e).cuda(), torch.from_numpy(w).cuda(), dg, du, dd, out_dtype=DT[out])
+    assert_within(y, ref, bound)
+    assert ops.convrot_device_status() == ops.OK
+
+
+@pytest.mark.parametrize("k", [9, 12, 32])
+@pytest.mark.parametrize("T", [3, 200])
+def test_moe_many_choices_of_a_token(ops, T, k):
+    """More rows than the weighted sum takes at once, with their powers of two."""
+    E, K, I, N = 36, 144, 48, 264  # noqa: E741
+    e, w = choices(T, T, E, k, 0.2)
+    dg, hg = matrices(1, E, I, K, True)
+    du, hu = matrices(2, E, I, K, True)
+    dd, hd = matrices(3, E, N, I, True)
+    X = activations(T, T, K, "bf16")
+    ref, bound = mo.moe(X.float().numpy(), e, w, hg, hu, hd, rows_error=2.0 ** -11)
+    y = ops.fp8_moe(X.cuda(), torch.from_numpy(e).cuda(), torch.from_numpy(w).cuda(), dg, du, dd)
+    assert_within(y, ref, bound)
+
+
+@pytest.mark.parametrize("T", [1, 40, 900])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_moe_strides(ops, T, dtype):
+    """Rows of X, Y and the residual apart and at odd offsets, the residual in
+    place: the results of dense arrays, and nothing written beside them."""
+    E, k, K, I, N = 8, 2, 272, 144, 200  # noqa: E741
+    X, e, w, gate, up, down = block(ops, T, E, k, K, I, N, T)
+    X = X.to(DT[dtype])
+    res = torch.randn(T, N, generator=gen(T)).to(DT[dtype]).cuda()
+    want = ops.fp8_moe(X, e, w, gate, up, down, residual=res)
+    plain = ops.fp8_moe(X, e, w, gate, up, down)
+    for off in (1, 8):
+        wide = torch.full((T, K + 25), 100.0, dtype=DT[dtype], device="cuda")
+        wide[:, off:off + K] = X
+        x = wide[:, off:off + K]
+        y = torch.full((T, N + 19), 5.0, dtype=DT[dtype], device="cuda")
+        y[:, off:off + N] = res
+        z = y[:, off:off + N]
+        assert torch.equal(ops.fp8_moe(x, e, w, gate, up, down), plain)
+        assert torch.equal(ops.fp8_moe(x, e, w, gate, up, down, residual=z, Y=z), want)
+        assert (y[:, :off] == 5).all() and (y[:, off + N:] == 5).all()
+    z = res.clone()
+    assert torch.equal(ops.fp8_moe(X, e, w, gate, up, down, residual=z, Y=z), want)
 
 
 # ---------------------------------------------------------------------------
