@@ -857,9 +857,12 @@ size_t fp8_moe_workspace_size(int64_t T, int64_t K, int64_t I, int64_t N, int to
  *   Y[t] = residual[t] + sum_j weights[t,j] D_e(silu(G_e(x_t)) * U_e(x_t)), e = experts[t,j],
  * X and the hidden rows quantized as by fp8_pack_activations, sums in fp32, one
  * rounding to y_dtype. With a bf16 Y the rows that D_e gives pass to the sum in
- * binary16 with a power of two per 128 features: a relative error of 2^-11 each
- * at most, an eighth of a rounding to bf16, for half the bytes. Choices of -1 add nothing. A choice outside [-1, E)
- * counts as -1 and is reported as by moe_plan.
+ * binary16 with a power of two per 128 features, for half the bytes: each value
+ * is off by 2^-11 of itself at most, an eighth of a rounding to bf16, or, where
+ * that is more, by 2^-39 of the largest magnitude among its 128 features (by
+ * 2^-151 where that is below 2^-112). fp32 and fp16 outputs keep fp32 rows.
+ * Choices of -1 add nothing. A choice outside [-1, E) counts as -1 and is
+ * reported as by moe_plan.
  *   workspace  at least fp8_moe_workspace_size(...) bytes, 16-byte aligned, not
  *              used by another call that may run at the same time.
  * Errors: those of the operators above, and ERR_WORKSPACE.

@@ -138,7 +138,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g * sigmoid
 // Rows that only moe_combine reads, on the way to a bf16 output: binary16
 // with a power of two per row and 128 features that brings the largest
 // magnitude just below 2^15, so that every value within 2^-29 of it keeps 11
-// bits (a row's rounding is an eighth of bf16's) and none overflows.
+// bits (a row's rounding is an eighth of bf16's) and none overflows; smaller
+// ones are subnormal, off by up to 2^-39 of the largest.
 struct ScaledHalf {};
 template <typename TY> constexpr bool SCALED = false;
 template <> inline constexpr bool SCALED<ScaledHalf> = true;

@@ -1241,7 +1241,8 @@ def fp8_moe(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, gate,
     expert, and the experts' linears, SwiGLU and the weighted sum follow. gate,
     up, down: (codes, scales, biases or None) as fp8_prepare_experts gives them,
     of matrices [I,K], [I,K] and [N,I]. New outputs are of out_dtype (X's own by
-    default); a residual has the type of Y, and may be Y."""
+    default); a residual has the type of Y, and may be Y. For a bfloat16 Y the
+    experts' rows pass to the sum in binary16, scaled per 128 features."""
     device, handle = _start(X, stream)
     T, K = shape = _matrix(X, "X")
     ldx = _rows(X, "X", device, shape)

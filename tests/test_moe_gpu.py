@@ -707,6 +707,30 @@ def test_bf16_rows_keep_their_precision(ops):
         assert (np.abs(host(got.float()).astype(np.float64) - host(want)) <= bound).all(), factor
 
 
+@pytest.mark.parametrize("T", [20, 700])
+@pytest.mark.parametrize("size", [1.0, 1e30, 1e-30])
+def test_bf16_rows_of_a_wide_range(ops, T, size):
+    """Rows whose features differ by up to 2^60 within their block of 128: each is
+    off by half a step of binary16, or by 2^-39 of the block's largest where that
+    is more. Down matrices of zeros: the rows are the biases."""
+    E, k, K, I, N = 6, 3, 128, 128, 272  # noqa: E741
+    X, e, w, gate, up, down = block(ops, T, E, k, K, I, N, 5)
+    r = np.random.default_rng(3)
+    bias = (r.choice([-1.0, 1.0], (E, N)) * 2.0 ** r.uniform(-60, 0, (E, N)) * size).astype(np.float32)
+    y = ops.fp8_moe(X, e, w, gate, up, (torch.zeros(E, N, I, device="cuda").to(torch.float8_e4m3fn),
+                                        torch.ones(E, bo.n_blocks(N), 1, device="cuda"), torch.from_numpy(bias).cuda()))
+    b = bias.astype(np.float64)
+    top = bo.widen(np.stack([np.abs(b[:, j:j + 128]).max(1) for j in range(0, N, 128)], 1), E, N)
+    off = np.maximum(2.0 ** -11 * np.abs(b), 2.0 ** -39 * top)
+    rows = host(e).reshape(-1)  # a choice's row is its expert's
+    place = np.arange(T * k, dtype=np.int32).reshape(T, k)
+    ref, mag = mo.combine(b[rows], place, host(w))
+    bound, _ = mo.combine(off[rows], place, host(w))
+    # below 2^-126 bf16 values are multiples of 2^-126 2^-7: half a step is 2^-134,
+    # where half a step relative to the value would be less
+    assert_within(y, ref, bound + (k + 2) * U24 * mag + 2.0 ** -134)
+
+
 def test_rows_past_31_bits(ops):
     """Sorted codes, outputs and rows of more than 2^31 bytes and elements."""
     T, k, E, K, N = 37500, 8, 4, 8192, 16
