@@ -10,7 +10,7 @@
 // in rank order.
 //
 // 256 rows over 128 experts, 2048 -> 2 x 768: 50 us for the 83 experts that are
-// reached, 261 MB = 5.3 TB/s; 144 items of 256 weight rows of 4096, one for each
+// reached, 261 MB = 5.2 TB/s; 144 items of 256 weight rows of 4096, one for each
 // CTA, 30 us = 5.0 TB/s. A CTA streams a block of K (34 KB) in 0.45 us at best:
 // its eight MMAs take 0.32 us (75 cycles each, whatever their width), and issuing
 // the copies about as long; so the last round of items counts, and 5 us for
@@ -571,8 +571,8 @@ int launch_as(const ExpertCall& c, cudaStream_t stream) {
   auto kernel = expert_few_kernel<BN, SWIGLU, TY>;
   if (int st = allow_smem(kernel, G::smem(MAX_EXPERTS), done, mu, LAUNCH_REGS)) return st;
   // K is split over as many CTAs as give each item of evenly spread choices a
-  // cluster of its own at the same time: one CTA streams some 60 GB/s a
-  // microsecond at most, but a second round of a cluster's exchange costs more
+  // cluster of its own at the same time: one CTA streams 75 GB/s at most (a
+  // block of 34 KB in 0.45 us), but a second round of a cluster's exchange costs more
   // than it gains. SwiGLU of 2 x 1536 x 4096 matrices: 36 items (three experts)
   // take 22.2, 15.7 and 14.1 us unsplit, in two and in four, 72 items 22.6, 19.7
   // and 20.5 us, 96 items 23.5, 28.2 and 27.5 us.
@@ -612,9 +612,13 @@ int launch_expert_few(const ExpertCall& c, cudaStream_t stream) {
   // Items of the rows that an expert has on average: narrower ones cost less
   // while the expert's rows are one item, and read its weights once more for
   // every further item. 64 experts of 3 x 1024 x 2048 (16 of 3 x 1536 x 4096),
-  // gate, up and down: 16 rows each 80, 80 and 86 us (67, 70 and 79) with 16, 32
-  // and 64 columns; 24 rows 100, 87 and 92 us (85, 68 and 79); 32 rows 125, 99 and
-  // 96 us (106, 88 and 82).
+  // gate, up and down: 16 rows each 80, 80 and 87 us (67, 70 and 80) with 16, 32
+  // and 64 columns; 24 rows 100, 89 and 92 us (85, 68 and 79); 32 rows 125, 100 and
+  // 98 us (106, 88 and 83). By the average alone, since the counts are on the
+  // device: where a few experts have most of the rows, a tile that reads weights
+  // again costs little less than one that reads new ones (1024 choices of 128
+  // experts, 2048 -> 2 x 768: evenly 72 us for 129 tiles, with 47 experts reached
+  // and up to 121 rows each 41 us for 93).
   const int64_t per = c.rows.n / c.rows.E;
   if (per <= 16) return launch_columns<16>(c, stream);
   if (per <= 24) return launch_columns<32>(c, stream);

@@ -12,9 +12,9 @@ namespace convrot {
 namespace moe {
 
 // By the rows that an expert has on average. 64 experts of 3 x 1024 x 2048 (16 of
-// 3 x 1536 x 4096), gate and up plus down: 48 rows each take 120 us (85) with
-// the few-row kernel and 129 us (99) with the other, 64 rows 125 us (94) and 129
-// us (100), 80 rows 146 us (128) and 129 us (100).
+// 3 x 1536 x 4096), gate and up plus down: 48 rows each take 121 us (85) with
+// the few-row kernel and 124 us (96) with the other, 64 rows 126 us (95) and 124
+// us (96), 80 rows 149 us (129) and 125 us (96).
 bool many_rows(int64_t n, int E) { return n / E > 64; }
 
 int launch_expert_swiglu(const uint8_t* Q, const float* s, int64_t K, const Rows& r, const convrot_experts& gate,

@@ -13,11 +13,11 @@
 // row. It forms h there; the two threads of a row exchange their maxima through
 // shared memory, and codes and scale leave from registers.
 //
-// 8192 rows of eight experts, 4096 -> 2 x 2432: 156 us = 2.1 PFLOP/s; a linear of
-// as many products 141 us, the dense kernel 130 us. A tile costs 0.47 us for each
+// 8192 rows of eight experts, 4096 -> 2 x 2432: 148 us = 2.2 PFLOP/s; a linear of
+// as many products 139 us, the dense kernel 129 us. A tile costs 0.47 us for each
 // block of K (operand delivery and the accumulator's hand-over, as there), and 2
 // to 3 us for the epilogue beyond the two blocks that the MMAs run ahead (SwiGLU:
-// 128 exponentials and reciprocals a thread take 1.1 us of it). Experts of 512
+// 64 exponentials and as many reciprocals a thread among it). Experts of 512
 // uneven rows leave a fifth of the tiles' rows empty.
 #include "expert_common.cuh"
 
@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) expert_pair_kernel(const __gr
         }
         // the next tile's info and first scales, while the last block's MMAs run
         // (in the linears that store their sums as they are, the loop would
-        // spill registers for it: 54 us instead of 49 us for eight-block tiles)
+        // spill more registers for it than the epilogue does now, 32 bytes and
+        // 84 in fp32: 54 us instead of 49 us for eight-block tiles)
         if (EARLY && kb == p.KB - 1 && t + n_units < total && !start(seq + 1)) { ok = false; break; }
         if (!warp_wait(&tfull[buf], bphase, abort_flag, err, p.wait_ns)) { ok = false; break; }
         tc_fence_after();
